@@ -52,6 +52,9 @@ typedef struct mlora_pool* mlora_pool_t;
 typedef struct mlora_meta* mlora_meta_t;
 typedef struct mlora_slot_cache* mlora_slot_cache_t;
 typedef struct mlora_adapter_cache* mlora_adapter_cache_t;
+typedef struct mlora_kv* mlora_kv_t;
+typedef struct mlora_rope* mlora_rope_t;
+typedef struct mlora_seq* mlora_seq_t;
 
 enum {
   MLORA_OK = 0,
@@ -66,7 +69,8 @@ enum {
   MLORA_ERR_DEVICE_TIMEOUT = 9,   /* a kernel's bounded wait gave up (the GPU stays usable)  */
   MLORA_ERR_MISMATCH = 10,        /* pool and metadata or pool and operands do not fit     */
   MLORA_ERR_NO_FREE_SLOT = 11,    /* a step needs more adapters resident than slots allow  */
-  MLORA_ERR_BAD_TOKEN_ID = 12     /* a token id outside [0, vocab) of an embedding table     */
+  MLORA_ERR_BAD_TOKEN_ID = 12,    /* a token id outside [0, vocab) of an embedding table     */
+  MLORA_ERR_BAD_SEQUENCE = 13     /* a step's sequence names tokens, a length or pages that do not hold */
 };
 
 /* Limits of this build. */
@@ -76,6 +80,8 @@ enum {
 #define MLORA_MAX_TOKENS 65535
 #define MLORA_MAX_SLICES 8            /* output slices of one fused linear (mlora_load_adapter_sliced) */
 #define MLORA_MAX_CLASSES 8           /* rank classes of one pool (mlora_pool_create_classes) */
+#define MLORA_MAX_SEQS 8192           /* sequences of one step (mlora_seq_create) */
+#define MLORA_MAX_HEADS 256           /* query heads, key/value heads of one attention layer */
 
 /* ------------------------------------------------------------------ adapter pool ----- */
 
@@ -315,6 +321,114 @@ MLORA_API mlora_status mlora_embedding_pool_create(int n_classes, const int* cla
 MLORA_API mlora_status mlora_embedding(mlora_pool_t pool, mlora_meta_t meta, const int32_t* ids, const mlora_bf16* E,
                                        float* y, void* stream);
 
+/* ------------------------------------------------------------------ attention step ---- */
+
+/* The attention between the qkv linear and the o linear of a step (an addition with no counterpart on
+ * the pages, which name the qkv and o linears and leave what lies between them to the serving engine):
+ *
+ *   mlora_linear (qkv)  ->  mlora_qkv_write  ->  mlora_attention  ->  mlora_linear (o)
+ *
+ * over a paged cache of each layer's keys and values. One mlora_build_seq serves every layer of a step. */
+
+/* Element types of a cache. */
+enum { MLORA_KV_BF16 = 0, MLORA_KV_E4M3 = 1 };
+
+/* Creates the paged cache of one attention layer: n_pages pages of page_size tokens (8, 16, 32, 64, 128 or
+ * 256), n_kv_heads heads of head_dim (64 or 128) elements.
+ *   K, V: [n_pages, n_kv_heads, page_size, head_dim], bf16, or e4m3 codes with one fp32 scale for each
+ *   token and head (k_scale, v_scale: [n_pages, n_kv_heads, page_size]; an element is code * scale).
+ * The arrays are the caller's (device, 16-byte aligned, valid until the cache is destroyed; the scales NULL
+ * for MLORA_KV_BF16), or, with all four NULL, allocated here and zeroed.
+ * n_pages * page_size * n_kv_heads must stay below 2^31. Other sizes: MLORA_ERR_INVALID_ARG. */
+MLORA_API mlora_status mlora_kv_create(int n_pages, int page_size, int n_kv_heads, int head_dim, int type, void* K,
+                                       void* V, float* k_scale, float* v_scale, mlora_kv_t* out);
+/* Frees the cache (and its arrays where it allocated them: the caller has synchronised). NULL is accepted. */
+MLORA_API mlora_status mlora_kv_destroy(mlora_kv_t kv);
+/* Sizes and device pointers of the cache (any pointer may be NULL). */
+MLORA_API mlora_status mlora_kv_info(mlora_kv_t kv, int* n_pages, int* page_size, int* n_kv_heads, int* head_dim,
+                                     int* type, void** K, void** V, void** k_scale, void** v_scale);
+/* Bytes of a cache's arrays; 0 for invalid sizes. */
+MLORA_API size_t mlora_kv_bytes(int n_pages, int page_size, int n_kv_heads, int head_dim, int type);
+
+/* Rotary frequencies, radians per position, of rot_dim / 2 pairs (host arithmetic in double): theta^(-2i / rot_dim),
+ * and for contexts longer than the original_len tokens of training by `factor`:
+ *   MLORA_ROPE_LINEAR  every frequency divided by factor;
+ *   MLORA_ROPE_BASE    theta multiplied by factor^(rot_dim / (rot_dim - 2)): the fastest pair stays, the
+ *                      slowest is divided by factor;
+ *   MLORA_ROPE_WAVES   a pair that turns at most `low` times over original_len is divided by factor, one that
+ *                      turns at least `high` times stays, linear in the number of turns between them;
+ *   MLORA_ROPE_RAMP    the same two ends, linear in the pair's index between the (whole) indices at which a
+ *                      pair turns `high` and `low` times.
+ * original_len, low and high are read by the last two only. */
+enum { MLORA_ROPE_PLAIN = 0, MLORA_ROPE_LINEAR = 1, MLORA_ROPE_BASE = 2, MLORA_ROPE_WAVES = 3, MLORA_ROPE_RAMP = 4 };
+MLORA_API mlora_status mlora_rope_frequencies(int rot_dim, double theta, int scaling, double factor,
+                                              double original_len, double low, double high, double* freq);
+/* A rotation of the first rot_dim elements of a head (a multiple of 8, at most 128): pair i is elements
+ * (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved; freq: host, rot_dim / 2 radians per position
+ * (mlora_rope_frequencies, or any others of magnitude up to 1e6); mscale multiplies cos and sin (1 where the
+ * scaling has no such factor). */
+MLORA_API mlora_status mlora_rope_create(int rot_dim, int interleaved, const double* freq, float mscale,
+                                         mlora_rope_t* out);
+MLORA_API mlora_status mlora_rope_destroy(mlora_rope_t rope);
+
+/* Metadata and workspace of steps of at most max_seqs sequences, max_tokens new tokens in all and max_pages
+ * pages per sequence, for layers of n_q_heads query heads and n_kv_heads key/value heads (a divisor) of
+ * head_dim. */
+MLORA_API mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n_q_heads, int n_kv_heads,
+                                        int head_dim, mlora_seq_t* out);
+MLORA_API mlora_status mlora_seq_destroy(mlora_seq_t seq);
+
+/* Describes one step (asynchronous on `stream`; the arrays may change once it has run there):
+ *   q_start: device int32 [n_seqs + 1], ascending: the new tokens of sequence s are the step's rows
+ *            q_start[s] .. q_start[s + 1] - 1 (none, one, or many).
+ *   kv_len:  device int32 [n_seqs]: the sequence's length with its new tokens, which are its last ones: the
+ *            last new token has position kv_len[s] - 1. 0 marks a padding sequence, which is skipped.
+ *   pages:   device int32, rows of pages_ld entries: page pages[s * pages_ld + i] holds positions
+ *            i * page_size .. of sequence s; entries past its length are not read.
+ *   T:       rows of the step (rows before q_start[0] and from q_start[n_seqs] on belong to no sequence).
+ *   max_new: an upper bound of every sequence's new tokens, known to the host (1 for a decode step): it
+ *            chooses the attention's kernels.
+ * A sequence with descending or outlying bounds, more than max_new new tokens, fewer cached than new tokens,
+ * a length above max_pages pages or a page outside the cache is skipped like padding and reported by
+ * mlora_seq_status as MLORA_ERR_BAD_SEQUENCE with the first one's number. Caches used with the step have this
+ * one's sizes (MLORA_ERR_MISMATCH otherwise); their element types may differ.
+ * Calls that share a seq must be ordered on one stream. */
+MLORA_API mlora_status mlora_build_seq(mlora_seq_t seq, const int32_t* q_start, const int32_t* kv_len,
+                                       const int32_t* pages, int pages_ld, int n_seqs, int T, int max_new,
+                                       mlora_kv_t kv, void* stream);
+/* Synchronises with the last call that used this object and reports its device-side errors, which it clears. */
+MLORA_API mlora_status mlora_seq_status(mlora_seq_t seq);
+
+/* The step's qkv rows on their way to the attention:
+ *   qkv: device fp32, rows of ld elements (a multiple of 4): n_q_heads query heads, n_kv_heads key heads and
+ *        n_kv_heads value heads of head_dim, as the qkv linear leaves them.
+ *   q_norm, k_norm: device bf16 [head_dim] or NULL: each query (key) head x becomes x / sqrt(mean(x^2) + eps) * w.
+ *   rope: the rotation of queries and keys after the norm, or NULL; the angles are those of the tokens' positions,
+ *        or of positions[t] (device int32 [T]; exact up to 2^24) where positions is not NULL.
+ *   q_out: device bf16 [T, n_q_heads, head_dim], overwritten (zero rows for tokens in no sequence).
+ * Keys and values go to the tokens' rows of the cache: rounded to bf16, or as e4m3 with the scale
+ * max(largest magnitude, 2^-60) / 448 (a row with an infinity or a NaN: scale NaN, so that it reads as NaN).
+ * All arithmetic is fp32; angles are accurate to about 1e-7. Every value is a fixed sequence of operations. */
+MLORA_API mlora_status mlora_qkv_write(mlora_kv_t kv, mlora_seq_t seq, const float* qkv, int64_t ld,
+                                       const mlora_bf16* q_norm, const mlora_bf16* k_norm, float eps,
+                                       mlora_rope_t rope, const int32_t* positions, mlora_bf16* q_out, void* stream);
+
+/* Causal attention of the step's new tokens over the cache, which already holds them:
+ *     out[t, h, :] = sum_{j <= p} softmax_j(scale query[t, h] . K[j, h / G]) V[j, h / G],  p = position of t,
+ * G = n_q_heads / n_kv_heads; query, out: device bf16 [T, n_q_heads, head_dim], 16-byte aligned, not the same
+ * array. Rows of tokens in no sequence are zero. Scores, maxima and sums are fp32; the weights are rounded to
+ * bf16 (f16 over an e4m3 cache) for the product with V. Cache rows past a sequence's length have no effect,
+ * whatever they hold. Deterministic: a repeated call gives the same bits. */
+MLORA_API mlora_status mlora_attention(mlora_kv_t kv, mlora_seq_t seq, const mlora_bf16* query, float scale,
+                                       mlora_bf16* out, void* stream);
+
+/* Reads the step's sequences back as dense rows: position p of sequence s is row row_start[s] + p (device int32
+ * [n_seqs]) of k_out and v_out (device bf16 [rows, n_kv_heads, head_dim]); an e4m3 element is code * scale in fp32,
+ * rounded once. Rows named by no sequence are left as they are; a sequence whose rows would lie outside
+ * [0, rows) is not (wholly) written and reported by mlora_seq_status as MLORA_ERR_INVALID_ARG. */
+MLORA_API mlora_status mlora_kv_read(mlora_kv_t kv, mlora_seq_t seq, const int32_t* row_start, int64_t rows,
+                                     mlora_bf16* k_out, mlora_bf16* v_out, void* stream);
+
 /* ------------------------------------------------------------------ slot residency ---- */
 
 /* Which adapter id sits in which of n_slots GPU slots ("LoRA Serving", section 5: the LRU cache
@@ -379,7 +493,7 @@ MLORA_API mlora_status mlora_check_wait_timeout(void* stream);
  * on its own stream (at most `capacity` launches are kept). mlora_trace_read synchronises
  * and returns, for each kernel kind, the number of launches and their summed device time in
  * milliseconds; kinds: 0 meta, 1 base GEMM, 2 shrink, 3 expand, 4 slot bookkeeping, 5 embedding
- * lookup. */
+ * lookup, 6 sequence metadata, 7 cache write and read, 8 attention. */
 MLORA_API mlora_status mlora_trace_enable(int capacity);
 MLORA_API mlora_status mlora_trace_disable(void);
 MLORA_API mlora_status mlora_trace_read(int n_kinds, int* launches, double* total_ms);

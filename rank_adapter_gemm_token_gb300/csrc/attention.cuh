@@ -1,0 +1,90 @@
+// Device helpers shared by the attention step's kernels: 16-bit and e4m3 packing, and the searches
+// over a step's prefix sums.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <cstdint>
+
+namespace mlora {
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two e4m3 codes (low byte: lo), round to nearest even, saturating.
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two e4m3 codes (low 16 bits) as two halves: exact, every e4m3 value is an f16 value.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+// Eight e4m3 codes times a scale, as bf16 (each product rounded to fp32, then to bf16).
+__device__ __forceinline__ uint4 e4m3_times(uint2 c, float scale) {
+  uint4 out;
+  const uint32_t in[2] = {c.x, c.y};
+  uint32_t* o = &out.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t h = e4m3x2_f16x2(in[i >> 1] >> (16 * (i & 1)));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    o[i] = pack_bf16(f.x * scale, f.y * scale);
+  }
+  return out;
+}
+
+// The last i in [0, n) with pre[i] <= x, for ascending prefix sums with pre[0] <= x (one warp, all lanes).
+template <typename T>
+__device__ __forceinline__ int last_at_most(const T* pre, int n, T x) {
+  int lo = 0, len = n;                                   // the answer lies in [lo, lo + len)
+  while (len > 1) {
+    const int step = (len + 31) / 32;
+    const int at = lo + min(static_cast<int>(threadIdx.x & 31) * step, len - 1);
+    const uint32_t below = __ballot_sync(0xffffffffu, pre[at] <= x);
+    const int next = min((31 - __clz(below | 1u)) * step, len - 1);
+    len = min(step, len - next);
+    lo += next;
+  }
+  return lo;
+}
+
+// An equal share of a list of work items for each of n CTAs. The items' units (keys of 64 or 128) lie one
+// after another, total in all; CTA c takes units [cut(c), cut(c + 1)), so an item that lies across a cut
+// is split and its parts are joined. A cut within `snap` units of an item's end moves there: a split
+// costs more than that imbalance.
+struct Shares {
+  int64_t total;
+  int n;
+  int snap;
+  __device__ __forceinline__ int64_t raw(int64_t c) const { return total * c / n; }
+  // cut(c) when it falls into the item of units [a, b)
+  __device__ __forceinline__ int64_t snapped(int64_t x, int64_t a, int64_t b) const {
+    return x - a <= snap ? a : b - x <= snap ? b : x;
+  }
+  // The cuts that split the item [a, b): CTAs first + 1 ... first + count begin inside it.
+  __device__ __forceinline__ void inside(int64_t a, int64_t b, int* first, int* count) const {
+    const int64_t lo = a + snap + 1, hi = b - snap - 1;      // raw cuts in [lo, hi] stay inside
+    if (lo > hi) {
+      *first = 0, *count = 0;
+      return;
+    }
+    const int64_t c0 = (lo * n + total - 1) / total;          // least c with raw(c) >= lo
+    const int64_t c1 = ((hi + 1) * n - 1) / total;            // largest c with raw(c) <= hi
+    *first = static_cast<int>(c0) - 1;
+    *count = static_cast<int>(c1 >= c0 ? c1 - c0 + 1 : 0);
+  }
+};
+
+}  // namespace mlora

@@ -1,0 +1,538 @@
+// Attention of sequences with few query rows (single tokens, short chunks) over the paged cache:
+//
+//     o_r = sum_{j <= p_r} softmax_j(scale q_r . k_j) v_j
+//
+// for the rows r = (token i, head of the group) of one key/value head, p_r the token's position.
+// Bound: HBM. Each cached row is read once and meets at most 16 query rows (2 to 4 flops a byte), so the
+// work is to keep loads in flight and the split even:
+//   - work = (sequence, key/value head) items of 64-key units, laid out one after another; every CTA takes an
+//     equal share of the units whatever the sequences' lengths (Shares), so one long sequence and many short
+//     ones both fill the GPU. An item across a cut leaves partial sums (with their maximum) in the step's
+//     workspace and the CTA that comes last joins them in key order: the result does not depend on arrival.
+//   - a warp takes 16 keys of each unit, through its own ring of stages filled by cp.async (the next item's
+//     keys are already on their way while one item is finished), with no barrier between warps inside an item.
+//   - the products run on the warp-level tensor instructions with the keys as the M side: S^T = K Q^T and
+//     O^T = V^T P^T with the query rows as N = 8 (or 16), so few rows waste few lanes. (The tcgen05 shapes need
+//     128 rows; here the tensor time is a fraction of the load time either way.)
+//   - softmax in one pass in base 2; the running maximum moves only when a score passes it by 2^8, so most
+//     chunks need no shuffles and no rescaling. P is at most 2^8, which f16 and bf16 hold.
+//   - e4m3: codes become f16 (exact) in registers. The key scale multiplies the score, and the value scale goes
+//     into the exponent: with t_j = score_j + log2 vs_j, P_j = 2^(t_j - max t) is the weight times the scale
+//     and at most 2^8 whatever the scales' magnitude; the denominator sums P_j / vs_j. Query rows are divided
+//     by their largest element, so f16 holds them too.
+// Keys at or past a row's limit are replaced by -inf by selection, and rows past the cached length are
+// zero-filled on load, so what lies there (NaN included) has no effect.
+#include <algorithm>
+
+#include "attention.h"
+#include "attention.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace mlora {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kChunk = 16;                  // keys of a warp's chunk
+constexpr int kRingBytes = 96 * 1024;       // of the CTA's stages: two CTAs per SM
+constexpr float kLazy = 8.0f;               // log2 of the largest P
+
+template <int HD, int NQ, bool E4M3>
+struct RowsCfg {
+  static constexpr int kRowBytes = E4M3 ? HD : 2 * HD;
+  static constexpr int kSegs = kRowBytes / 16;                     // 16-byte segments of a cached row
+  static constexpr int kTile = kChunk * kRowBytes;
+  static constexpr int kScales = E4M3 ? 2 * kChunk * 4 : 0;        // key and value scales of a chunk
+  static constexpr int kStage = 2 * kTile + kScales;
+  static constexpr int kRing = NQ == 1 ? kRingBytes : kRingBytes / 3 * 2;
+  static constexpr int kStages = kRing / (kWarps * kStage) > 8 ? 8 : kRing / (kWarps * kStage);
+  static constexpr int kRows = 8 * NQ;
+  static constexpr int kLd = HD + 4;                               // floats of a row of the joined sums
+  static constexpr int kOOff = kWarps * kStages * kStage;
+  static constexpr int kMlOff = kOOff + kWarps * kRows * kLd * 4;
+  static constexpr int kBytes = kMlOff + kWarps * kRows * 2 * 4 + 16;
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool full) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(full ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool full) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(full ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t mat_trans(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8)
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A place in the list of units: unit u of head kvh of sequence s.
+struct Place {
+  int s, kvh, u, units, len;
+  const int32_t* table;
+  __device__ __forceinline__ void load(const SeqView& v, int seq) {
+    s = seq;
+    len = v.len[seq];
+    units = (len + kRowUnit - 1) / kRowUnit;
+    table = v.table + static_cast<size_t>(seq) * v.max_pages;
+  }
+  __device__ __forceinline__ void at(const SeqView& v, int64_t x) {
+    load(v, last_at_most(v.row_pre, v.S, x));
+    const int rel = static_cast<int>(x - v.row_pre[s]);
+    kvh = rel / units;
+    u = rel - kvh * units;
+  }
+  // the next unit; the caller knows that there is one
+  __device__ __forceinline__ void next(const SeqView& v) {
+    if (++u < units) return;
+    u = 0;
+    if (++kvh < v.Hkv) return;
+    kvh = 0;
+    int q = s + 1;
+    const int64_t here = v.row_pre[q];
+    while (v.row_pre[q + 1] == here) ++q;
+    load(v, q);
+  }
+};
+
+template <int HD, int NQ, bool E4M3>
+__global__ void __launch_bounds__(kThreads, 2)
+attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, float scale_log2, KvView kv, SeqView v) {
+  using C = RowsCfg<HD, NQ, E4M3>;
+  constexpr int kSteps = HD / 16;             // k-steps of S^T, M tiles of O^T
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  float* o_sh = reinterpret_cast<float*>(smem + C::kOOff);
+  float* ml_sh = reinterpret_cast<float*>(smem + C::kMlOff);
+  int* last_sh = reinterpret_cast<int*>(ml_sh + kWarps * C::kRows * 2);
+
+  // rows of tokens in no sequence are zero
+  for (int t0 = blockIdx.x * 32; t0 < v.T; t0 += gridDim.x * 32) {
+    const int tok = t0 + lane;
+    uint32_t none = __ballot_sync(0xffffffffu, tok < v.T && v.tok_seq[tok] < 0);
+    none &= 0x11111111u << warp;
+    while (none) {
+      const int b = __ffs(none) - 1;
+      none &= none - 1;
+      uint4* row = reinterpret_cast<uint4*>(o + static_cast<int64_t>(t0 + b) * v.Hq * HD);
+      for (int i = lane; i < v.Hq * HD / 8; i += 32) row[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+
+  Shares sh;
+  sh.total = v.row_pre[v.S];
+  if (sh.total == 0) return;
+  sh.n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), sh.total));
+  sh.snap = 0;
+  if (static_cast<int>(blockIdx.x) >= sh.n) return;
+  const int64_t x0 = sh.raw(blockIdx.x), x1 = sh.raw(blockIdx.x + 1);
+
+  // ---- the warp's loads: chunk i of the CTA's share goes to stage i % kStages
+  const uint32_t ring = ptx::smem_u32(smem) + warp * (C::kStages * C::kStage);
+  Place src;
+  src.at(v, x0);
+  const int n_chunks = static_cast<int>(x1 - x0);
+  int issued = 0;
+  int page_a = 0, page_b = 0;                 // pages of the next chunk's first and second 8 keys
+  auto look = [&]() {
+    const int k0 = src.u * kRowUnit + warp * kChunk;
+    page_a = src.table[min(k0, src.len - 1) >> kv.page_log2];
+    page_b = kv.page_log2 < 4 ? src.table[min(k0 + 8, src.len - 1) >> kv.page_log2] : page_a;
+  };
+  look();
+  auto issue = [&]() {
+    if (issued < n_chunks) {
+      const int k0 = src.u * kRowUnit + warp * kChunk;
+      if (k0 < src.len) {
+        const uint32_t st = ring + (issued % C::kStages) * C::kStage;
+        constexpr int kStep = 32 / C::kSegs;  // rows of one copy of all lanes
+#pragma unroll
+        for (int i = 0; i < kChunk / kStep; ++i) {
+          const int r = i * kStep + lane / C::kSegs, seg = lane % C::kSegs;
+          const int64_t at = ((static_cast<int64_t>(r < 8 ? page_a : page_b) * v.Hkv + src.kvh) << kv.page_log2) +
+                             ((k0 + r) & (kv.page - 1));
+          const int phys = C::kSegs >= 8 ? seg ^ (r & 7) : seg ^ ((r >> 1) & 3);
+          const uint32_t dst = st + r * C::kRowBytes + phys * 16;
+          const bool in = k0 + r < src.len;
+          cp16(dst, static_cast<const uint8_t*>(kv.K) + at * C::kRowBytes + seg * 16, in);
+          cp16(dst + C::kTile, static_cast<const uint8_t*>(kv.V) + at * C::kRowBytes + seg * 16, in);
+        }
+        if (E4M3) {
+          const int r = lane & 15;
+          const int64_t at = ((static_cast<int64_t>(r < 8 ? page_a : page_b) * v.Hkv + src.kvh) << kv.page_log2) +
+                             ((k0 + r) & (kv.page - 1));
+          cp4(st + 2 * C::kTile + lane * 4, (lane < 16 ? kv.k_scale : kv.v_scale) + at, k0 + r < src.len);
+        }
+      }
+      ++issued;
+      if (issued < n_chunks) {
+        src.next(v);
+        look();
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i) issue();
+
+  // ---- the CTA's items
+  Place at;
+  at.at(v, x0);
+  int done = 0;
+  while (done < n_chunks) {
+    const int u_end = min(at.units, at.u + (n_chunks - done));
+    const int n = v.n[at.s], first = v.start[at.s];
+    const int rows = n * v.G;
+    const int base = at.len - n;               // position of the first new token
+    uint32_t bq[NQ][kSteps][2];
+    float cq[NQ][2];
+    int lim[NQ][2];
+#pragma unroll
+    for (int z = 0; z < NQ; ++z) {
+      const int r = z * 8 + g;
+      const uint16_t* row = q + (static_cast<int64_t>(first + (r < rows ? r / v.G : 0)) * v.Hq + at.kvh * v.G + (r < rows ? r % v.G : 0)) * HD;
+      if (E4M3) {
+        uint4 w[kSteps / 2];
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSteps / 2; ++i) {
+          w[i] = r < rows ? *reinterpret_cast<const uint4*>(row + t * (HD / 4) + i * 8) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t* p = &w[i].x;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) most = fmaxf(most, fmaxf(fabsf(ptx::bf16_lo(p[k])), fabsf(ptx::bf16_hi(p[k]))));
+        }
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        if (!(most > 0.f)) most = 1.f;
+        const float inv = 1.0f / most;
+#pragma unroll
+        for (int i = 0; i < kSteps / 2; ++i) {
+          const uint32_t* p = &w[i].x;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) bq[z][2 * i + (k >> 1)][k & 1] = pack_f16(ptx::bf16_lo(p[k]) * inv, ptx::bf16_hi(p[k]) * inv);
+        }
+        cq[z][0] = scale_log2 * __shfl_sync(0xffffffffu, most, (2 * t) * 4);
+        cq[z][1] = scale_log2 * __shfl_sync(0xffffffffu, most, (2 * t + 1) * 4);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          bq[z][i][0] = r < rows ? *reinterpret_cast<const uint32_t*>(row + 16 * i + 2 * t) : 0u;
+          bq[z][i][1] = r < rows ? *reinterpret_cast<const uint32_t*>(row + 16 * i + 2 * t + 8) : 0u;
+        }
+        cq[z][0] = cq[z][1] = scale_log2;
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int rc = z * 8 + 2 * t + c;
+        lim[z][c] = rc < rows ? base + rc / v.G : -1;
+      }
+    }
+    float acc[NQ][kSteps][4], m[NQ][2], l[NQ][2];
+#pragma unroll
+    for (int z = 0; z < NQ; ++z) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[z][i][k] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) m[z][c] = -INFINITY, l[z][c] = 0.f;
+    }
+
+    for (int u = at.u; u < u_end; ++u, ++done) {
+      cp_wait<C::kStages - 2>();
+      __syncwarp();
+      issue();
+      const int k0 = u * kRowUnit + warp * kChunk;
+      if (k0 >= at.len) continue;
+      const uint32_t st = ring + (done % C::kStages) * C::kStage;
+      float ks[2] = {1.f, 1.f}, lvs[2] = {0.f, 0.f}, rvs[2] = {1.f, 1.f};
+      if (E4M3) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ks[h] = lds_f(st + 2 * C::kTile + (g + 8 * h) * 4);
+          const float vs = lds_f(st + 2 * C::kTile + 64 + (g + 8 * h) * 4);
+          lvs[h] = __log2f(vs);
+          rvs[h] = vs > 0.f ? __fdividef(1.0f, vs) : 0.f;      // a NaN scale counts in the exponent alone
+        }
+      }
+      float sc[NQ][4];
+#pragma unroll
+      for (int z = 0; z < NQ; ++z)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sc[z][k] = 0.f;
+      if (E4M3) {
+        // lane (g, t): bytes t HD/4 ... of key rows g and g + 8; byte 4 i + j is k index (2 t + (j & 1) + 8 (j >> 1))
+        // of step i, for the query rows alike
+        uint4 w[2][HD / 64];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < HD / 64; ++i) {
+            const int r = g + 8 * h, seg = t * (HD / 64) + i;
+            w[h][i] = lds16(st + r * C::kRowBytes + (C::kSegs >= 8 ? seg ^ (r & 7) : seg ^ ((r >> 1) & 3)) * 16);
+          }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const uint32_t x = (&w[0][i >> 2].x)[i & 3], y = (&w[1][i >> 2].x)[i & 3];
+          const uint32_t a[4] = {e4m3x2_f16x2(x), e4m3x2_f16x2(y), e4m3x2_f16x2(x >> 16), e4m3x2_f16x2(y >> 16)};
+#pragma unroll
+          for (int z = 0; z < NQ; ++z) mma<true>(sc[z], a, bq[z][i][0], bq[z][i][1]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          uint32_t a[4];
+          const int r = lane & 15, seg = 2 * i + (lane >> 4);
+          ldsm4(a, st + r * C::kRowBytes + (seg ^ (r & 7)) * 16);
+#pragma unroll
+          for (int z = 0; z < NQ; ++z) mma<false>(sc[z], a, bq[z][i][0], bq[z][i][1]);
+        }
+      }
+      uint32_t pb[NQ][2];
+      const bool edge = k0 + kChunk > base + 1;
+#pragma unroll
+      for (int z = 0; z < NQ; ++z) {
+        bool grow = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = k & 1, h = k >> 1;
+          float x = E4M3 ? fmaf(sc[z][k] * ks[h], cq[z][c], lvs[h]) : sc[z][k] * cq[z][c];
+          if (edge && k0 + g + 8 * h > lim[z][c]) x = -INFINITY;
+          sc[z][k] = x;
+          grow = grow || x > m[z][c] + kLazy;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float top = fmaxf(sc[z][c], sc[z][2 + c]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            top = fmaxf(top, m[z][c]);
+            const float f = top == m[z][c] ? 1.f : exp2_approx(m[z][c] - top);
+            m[z][c] = top;
+            l[z][c] *= f;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) acc[z][i][c] *= f, acc[z][i][2 + c] *= f;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = k & 1;
+          const float p = exp2_approx(sc[z][k] - (m[z][c] == -INFINITY ? 0.f : m[z][c]));
+          l[z][c] = E4M3 ? fmaf(p, rvs[k >> 1], l[z][c]) : l[z][c] + p;
+          sc[z][k] = p;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          pb[z][h] = mat_trans(E4M3 ? pack_f16(sc[z][2 * h], sc[z][2 * h + 1]) : pack_bf16(sc[z][2 * h], sc[z][2 * h + 1]));
+      }
+      const uint32_t vt = st + C::kTile;
+      if (E4M3) {
+        // lane (g, t): bytes g HD/8 ... of value rows 2t, 2t + 1, 2t + 8, 2t + 9; byte 2 i (+ 1) is row g (+ 8) of M tile i
+        uint32_t w[4][HD / 32];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int r = 2 * t + (h & 1) + 8 * (h >> 1);
+          if (HD == 128) {
+            *reinterpret_cast<uint4*>(w[h]) = lds16(vt + r * C::kRowBytes + (g ^ (r & 7)) * 16);
+          } else {
+            *reinterpret_cast<uint2*>(w[h]) = lds8(vt + r * C::kRowBytes + ((g >> 1) ^ ((r >> 1) & 3)) * 16 + (g & 1) * 8);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < HD / 32; ++j) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const uint32_t x = __byte_perm(w[0][j], w[1][j], b ? 0x7362 : 0x5140);
+            const uint32_t y = __byte_perm(w[2][j], w[3][j], b ? 0x7362 : 0x5140);
+            const uint32_t a[4] = {e4m3x2_f16x2(x), e4m3x2_f16x2(x >> 16), e4m3x2_f16x2(y), e4m3x2_f16x2(y >> 16)};
+#pragma unroll
+            for (int z = 0; z < NQ; ++z) mma<true>(acc[z][2 * j + b], a, pb[z][0], pb[z][1]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          uint32_t a[4];
+          const int r = (lane & 7) + ((lane >> 4) & 1) * 8, seg = 2 * i + ((lane >> 3) & 1);
+          ldsm4t(a, vt + r * C::kRowBytes + (seg ^ (r & 7)) * 16);
+#pragma unroll
+          for (int z = 0; z < NQ; ++z) mma<false>(acc[z][i], a, pb[z][0], pb[z][1]);
+        }
+      }
+    }
+
+    // ---- the warps' sums joined
+#pragma unroll
+    for (int z = 0; z < NQ; ++z)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[z][c] += __shfl_xor_sync(0xffffffffu, l[z][c], d);
+        const int r = z * 8 + 2 * t + c;
+        if (g == 0) {
+          ml_sh[(warp * C::kRows + r) * 2] = m[z][c];
+          ml_sh[(warp * C::kRows + r) * 2 + 1] = l[z][c];
+        }
+        float* row = o_sh + (warp * C::kRows + r) * C::kLd;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const int h0 = E4M3 ? (HD / 8) * g + 2 * i : 16 * i + g, h1 = E4M3 ? h0 + 1 : h0 + 8;
+          row[h0] = acc[z][i][c];
+          row[h1] = acc[z][i][2 + c];
+        }
+      }
+    __syncthreads();
+    const int64_t a = v.row_pre[at.s] + static_cast<int64_t>(at.kvh) * at.units;
+    int c0, cuts;
+    sh.inside(a, a + at.units, &c0, &cuts);
+    constexpr int kGroups = HD / 8;
+    float* slots = v.part;
+    constexpr int kSlot = C::kRows * (HD + 2);
+    auto write_out = [&](int r, int h, const float* x, float total) {
+      const float inv = total > 0.f ? 1.0f / total : total == 0.f ? 0.f : total;   // an empty row is zero; NaN stays
+      uint4 w;
+      w.x = pack_bf16(x[0] * inv, x[1] * inv);
+      w.y = pack_bf16(x[2] * inv, x[3] * inv);
+      w.z = pack_bf16(x[4] * inv, x[5] * inv);
+      w.w = pack_bf16(x[6] * inv, x[7] * inv);
+      *reinterpret_cast<uint4*>(o + (static_cast<int64_t>(first + r / v.G) * v.Hq + at.kvh * v.G + r % v.G) * HD + h) = w;
+    };
+    const bool whole = cuts == 0;
+    float* slot = slots + (2 * static_cast<int64_t>(blockIdx.x) + (at.u == 0 ? 1 : 0)) * kSlot;
+    for (int i = threadIdx.x; i < rows * kGroups; i += kThreads) {
+      const int r = i / kGroups, h = (i % kGroups) * 8;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml_sh[(w * C::kRows + r) * 2]);
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, total = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = ml_sh[(w * C::kRows + r) * 2];
+        const float f = mw == -INFINITY ? 0.f : exp2_approx(mw - top);
+        total = fmaf(f, ml_sh[(w * C::kRows + r) * 2 + 1], total);
+        const float* row = o_sh + (w * C::kRows + r) * C::kLd + h;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = fmaf(f, row[k], x[k]);
+      }
+      if (whole) {
+        write_out(r, h, x, total);
+      } else {
+        float* p = slot + r * (HD + 2);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p[h + k] = x[k];
+        if (h == 0) p[HD] = top, p[HD + 1] = total;
+      }
+    }
+    if (!whole) {
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) *last_sh = atomicAdd(&v.sync[c0], 1u) == static_cast<uint32_t>(cuts);
+      __syncthreads();
+      if (*last_sh) {
+        __threadfence();
+        for (int i = threadIdx.x; i < rows * kGroups; i += kThreads) {
+          const int r = i / kGroups, h = (i % kGroups) * 8;
+          float top = -INFINITY;
+          for (int k = 0; k <= cuts; ++k)
+            top = fmaxf(top, __ldcg(slots + (2 * static_cast<int64_t>(c0 + k) + (k == 0)) * kSlot + r * (HD + 2) + HD));
+          float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, total = 0.f;
+          for (int k = 0; k <= cuts; ++k) {
+            const float* p = slots + (2 * static_cast<int64_t>(c0 + k) + (k == 0)) * kSlot + r * (HD + 2);
+            const float mk = __ldcg(p + HD);
+            const float f = mk == -INFINITY ? 0.f : exp2_approx(mk - top);
+            total = fmaf(f, __ldcg(p + HD + 1), total);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const float2 y = __ldcg(reinterpret_cast<const float2*>(p + h + e));
+              x[e] = fmaf(f, y.x, x[e]);
+              x[e + 1] = fmaf(f, y.y, x[e + 1]);
+            }
+          }
+          write_out(r, h, x, total);
+        }
+        if (threadIdx.x == 0) v.sync[c0] = 0;
+      }
+    }
+    __syncthreads();
+    if (done < n_chunks) {
+      at.u = u_end - 1;
+      at.next(v);
+    }
+  }
+  cp_wait<0>();
+}
+
+template <int HD, int NQ, bool E4M3>
+cudaError_t launch_as(const uint16_t* q, uint16_t* o, float scale_log2, const KvView& kv, const SeqView& s, cudaStream_t st) {
+  using C = RowsCfg<HD, NQ, E4M3>;
+  static cudaError_t once = cudaFuncSetAttribute(attention_rows_kernel<HD, NQ, E4M3>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  if (once != cudaSuccess) return once;
+  note_launch_begin(kKindAttn, st);
+  attention_rows_kernel<HD, NQ, E4M3><<<s.row_ctas, kThreads, C::kBytes, st>>>(q, o, scale_log2, kv, s);
+  const cudaError_t e = cudaGetLastError();
+  note_launch_end(kKindAttn, st);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_attention_rows(const uint16_t* q, uint16_t* o, float scale, const KvView& kv, const SeqView& s,
+                                  cudaStream_t st) {
+  const float c = scale * 1.4426950408889634f;
+  const bool two = s.row_limit > 8, f8 = kv.type == kKvE4m3;
+  if (s.hd == 128) {
+    if (two) return f8 ? launch_as<128, 2, true>(q, o, c, kv, s, st) : launch_as<128, 2, false>(q, o, c, kv, s, st);
+    return f8 ? launch_as<128, 1, true>(q, o, c, kv, s, st) : launch_as<128, 1, false>(q, o, c, kv, s, st);
+  }
+  if (two) return f8 ? launch_as<64, 2, true>(q, o, c, kv, s, st) : launch_as<64, 2, false>(q, o, c, kv, s, st);
+  return f8 ? launch_as<64, 1, true>(q, o, c, kv, s, st) : launch_as<64, 1, false>(q, o, c, kv, s, st);
+}
+
+}  // namespace mlora

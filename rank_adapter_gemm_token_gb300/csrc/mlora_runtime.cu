@@ -148,6 +148,12 @@ namespace mlora {
 
 int report_error(int status, const char* message) { return fail(status, "%s", message); }
 int report_cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+int device_sms(int* num_sms) {
+  DeviceState* ds = nullptr;
+  if (mlora_status st = device_state(&ds)) return st;
+  *num_sms = ds->num_sms;
+  return MLORA_OK;
+}
 int gemm_tile_n() { return g_gemm_tile_n.load(std::memory_order_relaxed); }
 int skinny_form() { return g_skinny_form.load(std::memory_order_relaxed); }
 
@@ -325,12 +331,14 @@ const char* mlora_status_string(mlora_status s) {
     case MLORA_ERR_MISMATCH: return "pool, metadata and operands do not fit together";
     case MLORA_ERR_NO_FREE_SLOT: return "more adapters needed at once than free or evictable slots";
     case MLORA_ERR_BAD_TOKEN_ID: return "a token id outside the embedding table";
+    case MLORA_ERR_BAD_SEQUENCE: return "a sequence whose tokens, length or pages do not hold";
     default: return "unknown status";
   }
 }
 
 const char* mlora_kernel_kind_name(int kind) {
-  static const char* names[kNumKinds] = {"meta", "base_gemm", "shrink", "expand", "slot", "embedding"};
+  static const char* names[kNumKinds] = {"meta", "base_gemm", "shrink", "expand", "slot", "embedding",
+                                          "sequences", "kv_cache", "attention"};
   return (kind >= 0 && kind < kNumKinds) ? names[kind] : "?";
 }
 

@@ -13,6 +13,8 @@ constexpr uint32_t kErrWaitTimeout = 1u << 0;   // a bounded mbarrier wait gave 
 constexpr uint32_t kErrBadSlot = 1u << 1;       // a token named an invalid or empty slot
 constexpr uint32_t kErrShape = 1u << 2;         // a launch saw sizes it cannot handle
 constexpr uint32_t kErrBadId = 1u << 3;         // a token id outside the embedding table
+constexpr uint32_t kErrBadSeq = 1u << 4;        // a sequence's bounds or page table do not hold
+constexpr uint32_t kErrBadRow = 1u << 5;        // a cache read's rows lie outside its output
 
 // A wait gives up after this many nanoseconds of %globaltimer (2 s): far above any
 // legitimate wait of these kernels, short enough to leave the GPU usable.

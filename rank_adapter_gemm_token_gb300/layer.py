@@ -165,3 +165,148 @@ def base_gemm(x: torch.Tensor, W: torch.Tensor, y: torch.Tensor | None = None, s
         y = torch.empty((T, D), dtype=torch.float32, device=x.device)
     mlora.mlora_base_gemm(x, W, y, T, K, D, _stream(stream))
     return y
+
+
+# --------------------------------------------------------------------------------------- attention step
+class KVCache:
+    """The paged cache of one attention layer: k, v [n_pages, n_kv_heads, page_size, head_dim], bf16 or
+    float8_e4m3fn with fp32 scales k_scale, v_scale [n_pages, n_kv_heads, page_size]. The tensors may be given
+    (they then decide the type); otherwise they are made here, zeroed, of `dtype`."""
+
+    def __init__(self, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, dtype=torch.bfloat16, k=None,
+                 v=None, k_scale=None, v_scale=None, device="cuda"):
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        if k is None:
+            assert v is None and k_scale is None and v_scale is None
+            k, v = (torch.zeros(shape, dtype=torch.bfloat16, device=device) if dtype == torch.bfloat16 else
+                    torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) for _ in range(2))
+            if dtype == torch.float8_e4m3fn:
+                k_scale, v_scale = (torch.zeros(shape[:3], dtype=torch.float32, device=device) for _ in range(2))
+        assert k.dtype in (torch.bfloat16, torch.float8_e4m3fn) and v.dtype == k.dtype
+        for x in (k, v):
+            assert x.is_cuda and x.is_contiguous() and x.shape == shape
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        assert (k_scale is not None) == e4m3 and (v_scale is not None) == e4m3
+        for x in (k_scale, v_scale):
+            assert x is None or (x.is_cuda and x.is_contiguous() and x.dtype == torch.float32 and x.shape == shape[:3])
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = n_pages, page_size, n_kv_heads, head_dim
+        self.handle = mlora.mlora_kv_create(n_pages, page_size, n_kv_heads, head_dim,
+                                            mlora.MLORA_KV_E4M3 if e4m3 else mlora.MLORA_KV_BF16, k, v, k_scale, v_scale)
+
+    def close(self) -> None:
+        if self.handle:
+            mlora.mlora_kv_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Rope:
+    """Rotary positions over the first rot_dim elements of each head: frequencies theta^(-2i / rot_dim), scaled by
+    `scaling` = one of mlora.MLORA_ROPE_* with its keyword arguments (factor, original_len, low, high), or given whole
+    as `freq` (radians per position)."""
+
+    def __init__(self, rot_dim: int, theta: float = 10000.0, interleaved: bool = False, scaling: int = 0,
+                 mscale: float = 1.0, freq=None, **kw):
+        self.freq = mlora.mlora_rope_frequencies(rot_dim, theta, scaling, **kw) if freq is None else list(freq)
+        self.rot_dim, self.interleaved, self.mscale = rot_dim, interleaved, mscale
+        self.handle = mlora.mlora_rope_create(rot_dim, interleaved, self.freq, mscale)
+
+    def close(self) -> None:
+        if self.handle:
+            mlora.mlora_rope_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class SeqMeta:
+    """One step's sequences (token rows, cached lengths, page tables) and the attention's workspace, for layers of
+    n_q_heads query heads over n_kv_heads key/value heads."""
+
+    def __init__(self, max_seqs: int, max_tokens: int, max_pages: int, n_q_heads: int, n_kv_heads: int, head_dim: int):
+        self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
+        self.handle = mlora.mlora_seq_create(max_seqs, max_tokens, max_pages, n_q_heads, n_kv_heads, head_dim)
+        self.T = 0
+        self.n_seqs = 0
+
+    def build(self, q_start: torch.Tensor, kv_len: torch.Tensor, pages: torch.Tensor, T: int, cache: KVCache,
+              max_new: int, stream=None) -> None:
+        """q_start int32 [n_seqs + 1], kv_len int32 [n_seqs], pages int32 [n_seqs, >= max_pages], all on the GPU."""
+        for x in (q_start, kv_len, pages):
+            assert x.is_cuda and x.dtype == torch.int32 and x.is_contiguous()
+        n = kv_len.shape[0]
+        assert q_start.shape == (n + 1,) and pages.dim() == 2 and pages.shape[0] == n
+        mlora.mlora_build_seq(self.handle, q_start, kv_len, pages, pages.shape[1], n, T, max_new, cache.handle,
+                              _stream(stream))
+        self.T, self.n_seqs = T, n
+
+    def status(self) -> None:
+        mlora.mlora_seq_status(self.handle)
+
+    def close(self) -> None:
+        if self.handle:
+            mlora.mlora_seq_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def qkv_write(cache: KVCache, seq: SeqMeta, qkv: torch.Tensor, q: torch.Tensor | None = None, q_norm=None, k_norm=None,
+              eps: float = 1e-6, rope: Rope | None = None, positions=None, stream=None) -> torch.Tensor:
+    """Norm and rotation of the step's qkv rows (fp32 [T, (Hq + 2 Hkv) hd], rows may be strided); keys and values to
+    the cache, queries bf16 [T, Hq, hd]."""
+    hq, hkv, hd = seq.n_q_heads, seq.n_kv_heads, seq.head_dim
+    assert qkv.is_cuda and qkv.dtype == torch.float32 and qkv.shape == (seq.T, (hq + 2 * hkv) * hd) and qkv.stride(1) == 1
+    for x in (q_norm, k_norm):
+        assert x is None or (x.is_cuda and x.dtype == torch.bfloat16 and x.shape == (hd,) and x.is_contiguous())
+    assert positions is None or (positions.is_cuda and positions.dtype == torch.int32 and positions.shape == (seq.T,)
+                                 and positions.is_contiguous())
+    if q is None:
+        q = torch.empty((seq.T, hq, hd), dtype=torch.bfloat16, device=qkv.device)
+    assert q.dtype == torch.bfloat16 and q.shape == (seq.T, hq, hd) and q.is_contiguous()
+    mlora.mlora_qkv_write(cache.handle, seq.handle, qkv, qkv.stride(0) if seq.T > 1 else qkv.shape[1], q_norm, k_norm,
+                          eps, rope.handle if rope is not None else None, positions, q, _stream(stream))
+    return q
+
+
+def attention(cache: KVCache, seq: SeqMeta, q: torch.Tensor, o: torch.Tensor | None = None, scale: float | None = None,
+              stream=None) -> torch.Tensor:
+    """Causal attention of the step's queries (bf16 [T, Hq, hd]) over the cache: bf16 [T, Hq * hd], the o linear's
+    input. scale: 1 / sqrt(hd) by default."""
+    hq, hd = seq.n_q_heads, seq.head_dim
+    assert q.is_cuda and q.dtype == torch.bfloat16 and q.shape == (seq.T, hq, hd) and q.is_contiguous()
+    if o is None:
+        o = torch.empty((seq.T, hq * hd), dtype=torch.bfloat16, device=q.device)
+    assert o.dtype == torch.bfloat16 and o.shape == (seq.T, hq * hd) and o.is_contiguous()
+    mlora.mlora_attention(cache.handle, seq.handle, q, hd ** -0.5 if scale is None else scale, o, _stream(stream))
+    return o
+
+
+def kv_read(cache: KVCache, seq: SeqMeta, row_start: torch.Tensor, rows: int, k=None, v=None, stream=None) -> tuple:
+    """The step's sequences as dense rows: position p of sequence s is row row_start[s] + p of k, v (bf16
+    [rows, Hkv, hd]). row_start: int32, at least one entry for each sequence."""
+    assert row_start.is_cuda and row_start.dtype == torch.int32 and row_start.is_contiguous()
+    assert row_start.numel() >= seq.n_seqs
+    shape = (rows, cache.n_kv_heads, cache.head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=row_start.device)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=row_start.device)
+    for x in (k, v):
+        assert x.dtype == torch.bfloat16 and x.shape == shape and x.is_contiguous()
+    mlora.mlora_kv_read(cache.handle, seq.handle, row_start, rows, k, v, _stream(stream))
+    return k, v

@@ -27,8 +27,17 @@ MLORA_ERR_DEVICE_TIMEOUT = 9
 MLORA_ERR_MISMATCH = 10
 MLORA_ERR_NO_FREE_SLOT = 11
 MLORA_ERR_BAD_TOKEN_ID = 12
+MLORA_ERR_BAD_SEQUENCE = 13
 
-KERNEL_KINDS = ("meta", "base_gemm", "shrink", "expand", "slot", "embedding")
+MLORA_KV_BF16 = 0
+MLORA_KV_E4M3 = 1
+MLORA_ROPE_PLAIN = 0
+MLORA_ROPE_LINEAR = 1
+MLORA_ROPE_BASE = 2
+MLORA_ROPE_WAVES = 3
+MLORA_ROPE_RAMP = 4
+
+KERNEL_KINDS = ("meta", "base_gemm", "shrink", "expand", "slot", "embedding", "sequences", "kv_cache", "attention")
 
 EXPORTS = (
     "mlora_pool_create", "mlora_pool_destroy", "mlora_load_adapter", "mlora_clear_slot", "mlora_pool_sync",
@@ -42,6 +51,9 @@ EXPORTS = (
     "mlora_adapter_cache_destroy", "mlora_adapter_cache_register", "mlora_adapter_cache_unregister",
     "mlora_adapter_cache_pin", "mlora_adapter_cache_map", "mlora_pool_create_classes", "mlora_pool_layout",
     "mlora_set_path", "mlora_embedding_pool_create", "mlora_embedding",
+    "mlora_kv_create", "mlora_kv_destroy", "mlora_kv_info", "mlora_kv_bytes", "mlora_rope_frequencies",
+    "mlora_rope_create", "mlora_rope_destroy", "mlora_seq_create", "mlora_seq_destroy", "mlora_build_seq",
+    "mlora_seq_status", "mlora_qkv_write", "mlora_attention", "mlora_kv_read",
 )
 
 
@@ -70,6 +82,7 @@ def load(path: str | None = None):
             raise FileNotFoundError(f"{p} is missing: build it with rank_adapter_gemm_token_gb300.build.build()")
         lib = ctypes.CDLL(p)
         vp, i32, f32, u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_uint64
+        i64, f64 = ctypes.c_int64, ctypes.c_double
         sig = {
             "mlora_pool_create": [i32, i32, i32, i32, vp, vp],
             "mlora_pool_create_classes": [i32, vp, vp, i32, i32, vp, vp],
@@ -111,6 +124,19 @@ def load(path: str | None = None):
             "mlora_adapter_cache_unregister": [vp, ctypes.c_int64],
             "mlora_adapter_cache_pin": [vp, ctypes.c_int64, i32],
             "mlora_adapter_cache_map": [vp, vp, i32, vp, vp],
+            "mlora_kv_create": [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp],
+            "mlora_kv_destroy": [vp],
+            "mlora_kv_info": [vp] * 10,
+            "mlora_rope_frequencies": [i32, f64, i32, f64, f64, f64, f64, vp],
+            "mlora_rope_create": [i32, i32, vp, f32, vp],
+            "mlora_rope_destroy": [vp],
+            "mlora_seq_create": [i32, i32, i32, i32, i32, i32, vp],
+            "mlora_seq_destroy": [vp],
+            "mlora_build_seq": [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp],
+            "mlora_seq_status": [vp],
+            "mlora_qkv_write": [vp, vp, vp, i64, vp, vp, f32, vp, vp, vp, vp],
+            "mlora_attention": [vp, vp, vp, f32, vp, vp],
+            "mlora_kv_read": [vp, vp, vp, i64, vp, vp, vp],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -118,6 +144,8 @@ def load(path: str | None = None):
             fn.restype = i32
         lib.mlora_pool_bytes.argtypes = [i32, i32, i32, i32]
         lib.mlora_pool_bytes.restype = ctypes.c_size_t
+        lib.mlora_kv_bytes.argtypes = [i32, i32, i32, i32, i32]
+        lib.mlora_kv_bytes.restype = ctypes.c_size_t
         lib.mlora_status_string.argtypes = [i32]
         lib.mlora_status_string.restype = ctypes.c_char_p
         lib.mlora_last_error.argtypes = []
@@ -321,6 +349,92 @@ def mlora_set_gemm_tile_n(n: int) -> None:
 def mlora_set_skinny_form(form: int) -> None:
     """Small-batch GEMM form: 0 and 1 split-K (CTA pairs), 2 token-split whenever it fits one wave."""
     _check(load().mlora_set_skinny_form(form), "mlora_set_skinny_form")
+
+
+# ------------------------------------------------------------------------- attention step
+def mlora_kv_create(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, type: int, K=None, V=None,
+                    k_scale=None, v_scale=None) -> int:
+    """The paged cache of one attention layer, over the given arrays or (all None) over its own."""
+    out = ctypes.c_void_p()
+    _check(load().mlora_kv_create(n_pages, page_size, n_kv_heads, head_dim, type, _ptr(K), _ptr(V), _ptr(k_scale),
+                                  _ptr(v_scale), ctypes.byref(out)), "mlora_kv_create")
+    return out.value
+
+
+def mlora_kv_destroy(kv: int) -> None:
+    _check(load().mlora_kv_destroy(kv), "mlora_kv_destroy")
+
+
+def mlora_kv_info(kv: int) -> dict:
+    i = [ctypes.c_int() for _ in range(5)]
+    p = [ctypes.c_void_p() for _ in range(4)]
+    _check(load().mlora_kv_info(kv, *(ctypes.byref(v) for v in i), *(ctypes.byref(v) for v in p)), "mlora_kv_info")
+    return dict(zip(("n_pages", "page_size", "n_kv_heads", "head_dim", "type", "K", "V", "k_scale", "v_scale"),
+                    [v.value for v in i + p]))
+
+
+def mlora_kv_bytes(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, type: int) -> int:
+    return int(load().mlora_kv_bytes(n_pages, page_size, n_kv_heads, head_dim, type))
+
+
+def mlora_rope_frequencies(rot_dim: int, theta: float, scaling: int = MLORA_ROPE_PLAIN, factor: float = 1.0,
+                           original_len: float = 0.0, low: float = 0.0, high: float = 0.0) -> list:
+    """Radians per position of the rot_dim / 2 pairs."""
+    out = (ctypes.c_double * max(rot_dim // 2, 1))()
+    _check(load().mlora_rope_frequencies(rot_dim, theta, scaling, factor, original_len, low, high, out),
+           "mlora_rope_frequencies")
+    return list(out)
+
+
+def mlora_rope_create(rot_dim: int, interleaved: bool, freq, mscale: float = 1.0) -> int:
+    freq = [float(f) for f in freq]
+    assert len(freq) == rot_dim // 2
+    arr = (ctypes.c_double * max(len(freq), 1))(*freq)
+    out = ctypes.c_void_p()
+    _check(load().mlora_rope_create(rot_dim, int(bool(interleaved)), arr, mscale, ctypes.byref(out)),
+           "mlora_rope_create")
+    return out.value
+
+
+def mlora_rope_destroy(rope: int) -> None:
+    _check(load().mlora_rope_destroy(rope), "mlora_rope_destroy")
+
+
+def mlora_seq_create(max_seqs: int, max_tokens: int, max_pages: int, n_q_heads: int, n_kv_heads: int,
+                     head_dim: int) -> int:
+    out = ctypes.c_void_p()
+    _check(load().mlora_seq_create(max_seqs, max_tokens, max_pages, n_q_heads, n_kv_heads, head_dim,
+                                   ctypes.byref(out)), "mlora_seq_create")
+    return out.value
+
+
+def mlora_seq_destroy(seq: int) -> None:
+    _check(load().mlora_seq_destroy(seq), "mlora_seq_destroy")
+
+
+def mlora_build_seq(seq: int, q_start, kv_len, pages, pages_ld: int, n_seqs: int, T: int, max_new: int, kv: int,
+                    stream=None) -> None:
+    _check(load().mlora_build_seq(seq, _ptr(q_start), _ptr(kv_len), _ptr(pages), pages_ld, n_seqs, T, max_new, kv,
+                                  _stream(stream)), "mlora_build_seq")
+
+
+def mlora_seq_status(seq: int) -> None:
+    _check(load().mlora_seq_status(seq), "mlora_seq_status")
+
+
+def mlora_qkv_write(kv: int, seq: int, qkv, ld: int, q_norm, k_norm, eps: float, rope, positions, q_out,
+                    stream=None) -> None:
+    _check(load().mlora_qkv_write(kv, seq, _ptr(qkv), ld, _ptr(q_norm), _ptr(k_norm), eps, rope, _ptr(positions),
+                                  _ptr(q_out), _stream(stream)), "mlora_qkv_write")
+
+
+def mlora_attention(kv: int, seq: int, query, scale: float, out, stream=None) -> None:
+    _check(load().mlora_attention(kv, seq, _ptr(query), scale, _ptr(out), _stream(stream)), "mlora_attention")
+
+
+def mlora_kv_read(kv: int, seq: int, row_start, rows: int, k_out, v_out, stream=None) -> None:
+    _check(load().mlora_kv_read(kv, seq, _ptr(row_start), rows, _ptr(k_out), _ptr(v_out), _stream(stream)),
+           "mlora_kv_read")
 
 
 # ------------------------------------------------------------------------- slot residency
