@@ -416,7 +416,7 @@ MLORA_API mlora_status mlora_qkv_write(mlora_kv_t kv, mlora_seq_t seq, const flo
 /* Causal attention of the step's new tokens over the cache, which already holds them:
  *     out[t, h, :] = sum_{j <= p} softmax_j(scale query[t, h] . K[j, h / G]) V[j, h / G],  p = position of t,
  * G = n_q_heads / n_kv_heads; query, out: device bf16 [T, n_q_heads, head_dim], 16-byte aligned, not the same
- * array. Rows of tokens in no sequence are zero. Scores, maxima and sums are fp32; the weights are rounded to
+ * array; scale positive. Rows of tokens in no sequence are zero. Scores, maxima and sums are fp32; the weights are rounded to
  * bf16 (f16 over an e4m3 cache) for the product with V. Cache rows past a sequence's length have no effect,
  * whatever they hold. Deterministic: a repeated call gives the same bits. */
 MLORA_API mlora_status mlora_attention(mlora_kv_t kv, mlora_seq_t seq, const mlora_bf16* query, float scale,

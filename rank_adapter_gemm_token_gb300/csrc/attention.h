@@ -38,9 +38,11 @@ struct SeqView {
   int32_t* blk_row;     // [blocks]   its first row (token * G + head of the group) in the sequence
   int64_t* blk_pre;     // [blocks + 1] key tiles of the blocks before each (one kv head)
   int32_t* counts;      // [0] blocks of the tile kernel, [1] first rejected sequence (INT32_MAX if none)
-  uint32_t* sync;       // arrivals of split items (zero between launches)
+  uint32_t* sync;       // [row_ctas] arrivals of the row kernel's split items (zero between launches)
+  uint32_t* tile_sync;  // [2 tile_ctas] of the tile kernel's, one for each 128-row tile
   uint32_t* err;        // device error word (ptx::kErr* bits)
-  float* part;          // partial results of split items (row kernel, then tile kernel)
+  float* part;          // partial results of the row kernel's split items
+  float* tile_part;     // of the tile kernel's
   int S, T, max_pages, Hq, Hkv, G, hd;
   int row_limit;        // rows (new tokens * G) up to which a sequence takes the row kernel
   int row_ctas, tile_ctas;
@@ -71,12 +73,14 @@ cudaError_t launch_kv_read(const int32_t* row_start, int64_t rows, uint16_t* k, 
 // tokens in no sequence.
 cudaError_t launch_attention_rows(const uint16_t* q, uint16_t* o, float scale, const KvView& kv, const SeqView& s,
                                   cudaStream_t st);
-// The other sequences.
-cudaError_t launch_attention_tiles(const uint16_t* q, uint16_t* o, float scale, const KvView& kv, const SeqView& s,
-                                   cudaStream_t st);
-// Bytes of SeqView::part: two partial results of 16 rows for each CTA of the row kernel.
-inline size_t attention_part_bytes(const SeqView& s) {
-  return static_cast<size_t>(s.row_ctas) * 2 * 16 * (s.hd + 2) * 4;
-}
+// The other sequences; tk and tv: the maps of a bf16 cache's K and V (make_kv_maps; not read for e4m3).
+cudaError_t launch_attention_tiles(const CUtensorMap& tk, const CUtensorMap& tv, const uint16_t* q, uint16_t* o,
+                                   float scale, const KvView& kv, const SeqView& s, cudaStream_t st);
+// K and V as matrices [n_pages * Hkv * page, hd] in boxes of min(page, 128) rows x 64 columns.
+bool make_kv_maps(const KvView& kv, CUtensorMap* k, CUtensorMap* v);
+// Bytes of the partial results: two of 16 rows for each CTA of the row kernel, two of two 128-row tiles for each
+// CTA of the tile kernel.
+inline size_t row_part_bytes(const SeqView& s) { return static_cast<size_t>(s.row_ctas) * 2 * 16 * (s.hd + 2) * 4; }
+inline size_t tile_part_bytes(const SeqView& s) { return static_cast<size_t>(s.tile_ctas) * 2 * 2 * 128 * (s.hd + 2) * 4; }
 
 }  // namespace mlora

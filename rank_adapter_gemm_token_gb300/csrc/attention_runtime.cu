@@ -54,6 +54,7 @@ mlora_status check_cache_sizes(int n_pages, int page, int n_kv_heads, int hd, in
 struct mlora_kv {
   KvView view{};
   bool own = false;
+  CUtensorMap map_k{}, map_v{};       // of a bf16 cache
 };
 
 struct mlora_rope {
@@ -124,6 +125,10 @@ mlora_status mlora_kv_create(int n_pages, int page_size, int n_kv_heads, int hea
       mlora_kv_destroy(kv);
       return created(e, "KV cache");
     }
+  }
+  if (!scales && !make_kv_maps(w, &kv->map_k, &kv->map_v)) {
+    mlora_kv_destroy(kv);
+    return fail(MLORA_ERR_CUDA, "tensor maps of the cache");
   }
   *out = kv;
   return MLORA_OK;
@@ -272,7 +277,8 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
                o_seq = take(T * 4), o_pos = take(T * 4), o_row = take(T * 4), o_pp = take((S + 1) * 4),
                o_rp = take((S + 1) * 8), o_bs = take(J * 4), o_br = take(J * 4), o_bp = take((J + 1) * 8),
                o_counts = take(8 * 4), o_sync = take(static_cast<size_t>(v.row_ctas + 2 * v.tile_ctas) * 4), o_err = take(4),
-               o_part = take(attention_part_bytes(v));
+               o_part = take(row_part_bytes(v)),
+               o_tile_part = take(tile_part_bytes(v));
   cudaError_t e = cudaMalloc(&q->mem, at);
   if (e == cudaSuccess) {
     char* b = static_cast<char*>(q->mem);
@@ -291,7 +297,9 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
     v.counts = reinterpret_cast<int32_t*>(b + o_counts);
     v.sync = reinterpret_cast<uint32_t*>(b + o_sync);
     v.err = reinterpret_cast<uint32_t*>(b + o_err);
+    v.tile_sync = v.sync + v.row_ctas;
     v.part = reinterpret_cast<float*>(b + o_part);
+    v.tile_part = reinterpret_cast<float*>(b + o_tile_part);
     const int32_t counts[8] = {0, INT32_MAX, 0, 0, 0, 0, 0, 0};
     e = cudaMemset(v.sync, 0, static_cast<size_t>(v.row_ctas + 2 * v.tile_ctas) * 4);
     if (e == cudaSuccess) e = cudaMemset(v.err, 0, 4);
@@ -405,11 +413,11 @@ mlora_status mlora_attention(mlora_kv_t kv, mlora_seq_t q, const mlora_bf16* que
   const SeqView& v = q->view;
   if (v.T > 0 && (!query || !out)) return fail(MLORA_ERR_INVALID_ARG, "query or out is NULL");
   if (!aligned(query, 16) || !aligned(out, 16)) return fail(MLORA_ERR_INVALID_ARG, "query and out must be 16-byte aligned");
-  if (!std::isfinite(scale)) return fail(MLORA_ERR_INVALID_ARG, "scale must be finite");
+  if (!(scale > 0.f && std::isfinite(scale))) return fail(MLORA_ERR_INVALID_ARG, "scale must be positive and finite");
   if (v.T == 0) return MLORA_OK;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_attention_rows(query, out, scale, kv->view, v, s);
-  if (e == cudaSuccess && q->tiles) e = launch_attention_tiles(query, out, scale, kv->view, v, s);
+  if (e == cudaSuccess && q->tiles) e = launch_attention_tiles(kv->map_k, kv->map_v, query, out, scale, kv->view, v, s);
   if (e != cudaSuccess) return report_cuda_error(e, "attention launch");
   q->last_stream = s;
   return MLORA_OK;
