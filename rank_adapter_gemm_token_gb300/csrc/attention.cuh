@@ -62,20 +62,21 @@ __device__ __forceinline__ int last_at_most(const T* pre, int n, T x) {
 
 // An equal share of a list of work items for each of n CTAs. The items' units (keys of 64 or 128) lie one
 // after another, total in all; CTA c takes units [cut(c), cut(c + 1)), so an item that lies across a cut
-// is split and its parts are joined. A cut within `snap` units of an item's end moves there: a split
-// costs more than that imbalance.
+// is split and its parts are joined. An item's first `head` units stand for its fixed costs, the others for
+// its keys. A cut in the head, or within `snap` units of the keys' ends, moves to the item's end: a split costs
+// more than that imbalance.
 struct Shares {
   int64_t total;
   int n;
-  int snap;
+  int head, snap;
   __device__ __forceinline__ int64_t raw(int64_t c) const { return total * c / n; }
   // cut(c) when it falls into the item of units [a, b)
   __device__ __forceinline__ int64_t snapped(int64_t x, int64_t a, int64_t b) const {
-    return x - a <= snap ? a : b - x <= snap ? b : x;
+    return x - a <= head + snap ? a : b - x <= snap ? b : x;
   }
   // The cuts that split the item [a, b): CTAs first + 1 ... first + count begin inside it.
   __device__ __forceinline__ void inside(int64_t a, int64_t b, int* first, int* count) const {
-    const int64_t lo = a + snap + 1, hi = b - snap - 1;      // raw cuts in [lo, hi] stay inside
+    const int64_t lo = a + head + snap + 1, hi = b - snap - 1;      // raw cuts in [lo, hi] stay inside
     if (lo > hi) {
       *first = 0, *count = 0;
       return;

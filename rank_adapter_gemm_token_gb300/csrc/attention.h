@@ -23,6 +23,27 @@ struct KvView {
   int n_pages, page, page_log2, Hkv, hd, type;
 };
 
+// A sequence of the row kernel's list, and a CTA's share of the list: `units` units from unit `unit` of head kvh
+// of list entry `item` on.
+struct RowSeq {
+  int32_t seq, n, len, start;
+};
+struct RowShare {
+  int32_t item, kvh, unit, units;
+};
+// A 256-row block of the tile kernel's list: rows r0 ... (token * G + head of the group) of sequence seq, `tiles`
+// key tiles. A CTA's share: `units` units from key tile `tile` of head kvh of block `blk` on.
+struct alignas(32) TileBlk {
+  int32_t seq, n, len, start, r0, tiles;
+};
+struct TileShare {
+  int32_t blk, kvh, tile, units;
+};
+// An item (list entry, head) that lies across cuts: CTAs cta ... cta + parts - 1 each hold a part (parts = 0: none).
+struct JoinTask {
+  int32_t item, kvh, cta, parts;
+};
+
 // Device arrays of one step's sequences, written by launch_build_seq.
 struct SeqView {
   int32_t* start;       // [S] first token row of each sequence
@@ -33,15 +54,17 @@ struct SeqView {
   int32_t* tok_pos;     // [T] position of each token
   int32_t* tok_row;     // [T] page * page size + offset of the token's cache row (-1: none)
   int32_t* page_pre;    // [S + 1] cached pages of the sequences before each
-  int64_t* row_pre;     // [S + 1] key units of the row kernel's sequences before each (one kv head)
-  int32_t* blk_seq;     // [blocks] sequence of each 256-row block of the tile kernel
-  int32_t* blk_row;     // [blocks]   its first row (token * G + head of the group) in the sequence
-  int64_t* blk_pre;     // [blocks + 1] key tiles of the blocks before each (one kv head)
-  int32_t* counts;      // [0] blocks of the tile kernel, [1] first rejected sequence (INT32_MAX if none)
-  uint32_t* sync;       // [row_ctas] arrivals of the row kernel's split items (zero between launches)
-  uint32_t* tile_sync;  // [2 tile_ctas] of the tile kernel's, one for each 128-row tile
+  RowSeq* row_seq;      // [S] the row kernel's sequences
+  int64_t* row_pre;     // [S + 1] units (64 keys, for each kv head) before each of them
+  TileBlk* blk;         // [blocks] the tile kernel's blocks
+  int64_t* blk_pre;     // [blocks + 1] units (kTileHead and the key tiles, for each kv head) before each of them
+  RowShare* row_share;  // [row_ctas]
+  TileShare* tile_share;// [tile_ctas]
+  JoinTask* row_join;   // [row_ctas] the item that CTA i + 1 is the first to continue, if any
+  JoinTask* tile_join;  // [tile_ctas]
+  int32_t* counts;      // [1] first rejected sequence (INT32_MAX if none)
   uint32_t* err;        // device error word (ptx::kErr* bits)
-  float* part;          // partial results of the row kernel's split items
+  float* row_part;      // partial results of the row kernel's split items
   float* tile_part;     // of the tile kernel's
   int S, T, max_pages, Hq, Hkv, G, hd;
   int row_limit;        // rows (new tokens * G) up to which a sequence takes the row kernel
@@ -53,6 +76,8 @@ struct SeqView {
 constexpr int kRowUnit = 64;
 constexpr int kTileKeys = 128;
 constexpr int kBlockRows = 256;
+constexpr int kTileSnap = 2;          // key tiles that a split costs at least
+constexpr int kTileHead = 3;          // key tiles that an item's fixed costs (queries, first products, output) are worth
 
 // Per-pair rotation frequencies in turns per position, each as a sum of two floats.
 struct RopeView {
@@ -69,18 +94,22 @@ cudaError_t launch_qkv_write(const float* qkv, int64_t ld, const uint16_t* q_nor
                              const SeqView& s, int num_sms, cudaStream_t st);
 cudaError_t launch_kv_read(const int32_t* row_start, int64_t rows, uint16_t* k, uint16_t* v, const KvView& kv,
                            const SeqView& s, int num_sms, cudaStream_t st);
-// Sequences of at most SeqView::row_limit rows (single tokens and short chunks), and the zero rows of
-// tokens in no sequence.
+// Attention in up to three launches, each a programmatic dependent of the one before: the row kernel (sequences of at
+// most SeqView::row_limit rows, and the zero rows of tokens in no sequence), with `tiles` the tile kernel (the other
+// sequences; tk and tv: the maps of a bf16 cache's K and V), and the join of the items that were split among CTAs.
 cudaError_t launch_attention_rows(const uint16_t* q, uint16_t* o, float scale, const KvView& kv, const SeqView& s,
                                   cudaStream_t st);
-// The other sequences; tk and tv: the maps of a bf16 cache's K and V (make_kv_maps; not read for e4m3).
 cudaError_t launch_attention_tiles(const CUtensorMap& tk, const CUtensorMap& tv, const uint16_t* q, uint16_t* o,
                                    float scale, const KvView& kv, const SeqView& s, cudaStream_t st);
+cudaError_t launch_attention_join(uint16_t* o, const SeqView& s, bool tiles, cudaStream_t st);
 // K and V as matrices [n_pages * Hkv * page, hd] in boxes of min(page, 128) rows x 64 columns.
 bool make_kv_maps(const KvView& kv, CUtensorMap* k, CUtensorMap* v);
-// Bytes of the partial results: two of 16 rows for each CTA of the row kernel, two of two 128-row tiles for each
-// CTA of the tile kernel.
+// Parts of split items: 2 c + 0 is the part that CTA c continues, 2 c + 1 the one that it begins.
+// Row kernel: [rows][hd] sums, then [rows] (maximum, sum of weights), rows = row_limit.
+// Tile kernel: two 128-row tiles, each [hd / 4][128] four sums, then [128] maxima and [128] sums of weights.
+__host__ __device__ inline int64_t row_slot(const SeqView& s) { return static_cast<int64_t>(s.row_limit) * (s.hd + 2); }
+__host__ __device__ inline int64_t tile_slot(const SeqView& s) { return static_cast<int64_t>(128) * (s.hd + 2); }
 inline size_t row_part_bytes(const SeqView& s) { return static_cast<size_t>(s.row_ctas) * 2 * 16 * (s.hd + 2) * 4; }
-inline size_t tile_part_bytes(const SeqView& s) { return static_cast<size_t>(s.tile_ctas) * 2 * 2 * 128 * (s.hd + 2) * 4; }
+inline size_t tile_part_bytes(const SeqView& s) { return static_cast<size_t>(s.tile_ctas) * 2 * 2 * tile_slot(s) * 4; }
 
 }  // namespace mlora

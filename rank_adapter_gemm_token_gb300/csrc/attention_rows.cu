@@ -51,7 +51,7 @@ struct RowsCfg {
   static constexpr int kLd = HD + 4;                               // floats of a row of the joined sums
   static constexpr int kOOff = kWarps * kStages * kStage;
   static constexpr int kMlOff = kOOff + kWarps * kRows * kLd * 4;
-  static constexpr int kBytes = kMlOff + kWarps * kRows * 2 * 4 + 16;
+  static constexpr int kBytes = kMlOff + kWarps * kRows * 2 * 4;
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool full) {
@@ -110,21 +110,16 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// A place in the list of units: unit u of head kvh of sequence s.
+// A place in the list of units: unit u of head kvh of list entry i.
 struct Place {
-  int s, kvh, u, units, len;
+  int i, kvh, u, units;
+  RowSeq s;
   const int32_t* table;
-  __device__ __forceinline__ void load(const SeqView& v, int seq) {
-    s = seq;
-    len = v.len[seq];
-    units = (len + kRowUnit - 1) / kRowUnit;
-    table = v.table + static_cast<size_t>(seq) * v.max_pages;
-  }
-  __device__ __forceinline__ void at(const SeqView& v, int64_t x) {
-    load(v, last_at_most(v.row_pre, v.S, x));
-    const int rel = static_cast<int>(x - v.row_pre[s]);
-    kvh = rel / units;
-    u = rel - kvh * units;
+  __device__ __forceinline__ void load(const SeqView& v) {
+    const int4 x = *reinterpret_cast<const int4*>(v.row_seq + i);
+    s = RowSeq{x.x, x.y, x.z, x.w};
+    units = (s.len + kRowUnit - 1) / kRowUnit;
+    table = v.table + static_cast<size_t>(s.seq) * v.max_pages;
   }
   // the next unit; the caller knows that there is one
   __device__ __forceinline__ void next(const SeqView& v) {
@@ -132,10 +127,8 @@ struct Place {
     u = 0;
     if (++kvh < v.Hkv) return;
     kvh = 0;
-    int q = s + 1;
-    const int64_t here = v.row_pre[q];
-    while (v.row_pre[q + 1] == here) ++q;
-    load(v, q);
+    ++i;
+    load(v);
   }
 };
 
@@ -149,7 +142,58 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
   const int g = lane >> 2, t = lane & 3;
   float* o_sh = reinterpret_cast<float*>(smem + C::kOOff);
   float* ml_sh = reinterpret_cast<float*>(smem + C::kMlOff);
-  int* last_sh = reinterpret_cast<int*>(ml_sh + kWarps * C::kRows * 2);
+  ptx::grid_dependents_launch();
+
+  const int4 share = *reinterpret_cast<const int4*>(v.row_share + blockIdx.x);
+  const int n_chunks = share.w;
+  // ---- the warp's loads: chunk i of the CTA's share goes to stage i % kStages
+  const uint32_t ring = ptx::smem_u32(smem) + warp * (C::kStages * C::kStage);
+  Place src{share.x, share.y, share.z, 0, {}, nullptr};
+  int issued = 0;
+  int page_a = 0, page_b = 0;                 // pages of the next chunk's first and second 8 keys
+  auto look = [&]() {
+    const int k0 = src.u * kRowUnit + warp * kChunk;
+    page_a = src.table[min(k0, src.s.len - 1) >> kv.page_log2];
+    page_b = kv.page_log2 < 4 ? src.table[min(k0 + 8, src.s.len - 1) >> kv.page_log2] : page_a;
+  };
+  if (n_chunks > 0) {
+    src.load(v);
+    look();
+  }
+  auto issue = [&]() {
+    if (issued < n_chunks) {
+      const int k0 = src.u * kRowUnit + warp * kChunk;
+      if (k0 < src.s.len) {
+        const uint32_t st = ring + (issued % C::kStages) * C::kStage;
+        constexpr int kStep = 32 / C::kSegs;  // rows of one copy of all lanes
+#pragma unroll
+        for (int i = 0; i < kChunk / kStep; ++i) {
+          const int r = i * kStep + lane / C::kSegs, seg = lane % C::kSegs;
+          const int64_t at = ((static_cast<int64_t>(r < 8 ? page_a : page_b) * v.Hkv + src.kvh) << kv.page_log2) +
+                             ((k0 + r) & (kv.page - 1));
+          const int phys = C::kSegs >= 8 ? seg ^ (r & 7) : seg ^ ((r >> 1) & 3);
+          const uint32_t dst = st + r * C::kRowBytes + phys * 16;
+          const bool in = k0 + r < src.s.len;
+          cp16(dst, static_cast<const uint8_t*>(kv.K) + at * C::kRowBytes + seg * 16, in);
+          cp16(dst + C::kTile, static_cast<const uint8_t*>(kv.V) + at * C::kRowBytes + seg * 16, in);
+        }
+        if (E4M3) {
+          const int r = lane & 15;
+          const int64_t at = ((static_cast<int64_t>(r < 8 ? page_a : page_b) * v.Hkv + src.kvh) << kv.page_log2) +
+                             ((k0 + r) & (kv.page - 1));
+          cp4(st + 2 * C::kTile + lane * 4, (lane < 16 ? kv.k_scale : kv.v_scale) + at, k0 + r < src.s.len);
+        }
+      }
+      ++issued;
+      if (issued < n_chunks) {
+        src.next(v);
+        look();
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i) issue();
 
   // rows of tokens in no sequence are zero
   for (int t0 = blockIdx.x * 32; t0 < v.T; t0 += gridDim.x * 32) {
@@ -164,71 +208,15 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
     }
   }
 
-  Shares sh;
-  sh.total = v.row_pre[v.S];
-  if (sh.total == 0) return;
-  sh.n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), sh.total));
-  sh.snap = 0;
-  if (static_cast<int>(blockIdx.x) >= sh.n) return;
-  const int64_t x0 = sh.raw(blockIdx.x), x1 = sh.raw(blockIdx.x + 1);
-
-  // ---- the warp's loads: chunk i of the CTA's share goes to stage i % kStages
-  const uint32_t ring = ptx::smem_u32(smem) + warp * (C::kStages * C::kStage);
-  Place src;
-  src.at(v, x0);
-  const int n_chunks = static_cast<int>(x1 - x0);
-  int issued = 0;
-  int page_a = 0, page_b = 0;                 // pages of the next chunk's first and second 8 keys
-  auto look = [&]() {
-    const int k0 = src.u * kRowUnit + warp * kChunk;
-    page_a = src.table[min(k0, src.len - 1) >> kv.page_log2];
-    page_b = kv.page_log2 < 4 ? src.table[min(k0 + 8, src.len - 1) >> kv.page_log2] : page_a;
-  };
-  look();
-  auto issue = [&]() {
-    if (issued < n_chunks) {
-      const int k0 = src.u * kRowUnit + warp * kChunk;
-      if (k0 < src.len) {
-        const uint32_t st = ring + (issued % C::kStages) * C::kStage;
-        constexpr int kStep = 32 / C::kSegs;  // rows of one copy of all lanes
-#pragma unroll
-        for (int i = 0; i < kChunk / kStep; ++i) {
-          const int r = i * kStep + lane / C::kSegs, seg = lane % C::kSegs;
-          const int64_t at = ((static_cast<int64_t>(r < 8 ? page_a : page_b) * v.Hkv + src.kvh) << kv.page_log2) +
-                             ((k0 + r) & (kv.page - 1));
-          const int phys = C::kSegs >= 8 ? seg ^ (r & 7) : seg ^ ((r >> 1) & 3);
-          const uint32_t dst = st + r * C::kRowBytes + phys * 16;
-          const bool in = k0 + r < src.len;
-          cp16(dst, static_cast<const uint8_t*>(kv.K) + at * C::kRowBytes + seg * 16, in);
-          cp16(dst + C::kTile, static_cast<const uint8_t*>(kv.V) + at * C::kRowBytes + seg * 16, in);
-        }
-        if (E4M3) {
-          const int r = lane & 15;
-          const int64_t at = ((static_cast<int64_t>(r < 8 ? page_a : page_b) * v.Hkv + src.kvh) << kv.page_log2) +
-                             ((k0 + r) & (kv.page - 1));
-          cp4(st + 2 * C::kTile + lane * 4, (lane < 16 ? kv.k_scale : kv.v_scale) + at, k0 + r < src.len);
-        }
-      }
-      ++issued;
-      if (issued < n_chunks) {
-        src.next(v);
-        look();
-      }
-    }
-    cp_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < C::kStages - 1; ++i) issue();
-
   // ---- the CTA's items
-  Place at;
-  at.at(v, x0);
+  Place at{share.x, share.y, share.z, 0, {}, nullptr};
+  if (n_chunks > 0) at.load(v);
   int done = 0;
   while (done < n_chunks) {
     const int u_end = min(at.units, at.u + (n_chunks - done));
-    const int n = v.n[at.s], first = v.start[at.s];
+    const int n = at.s.n, first = at.s.start, len = at.s.len;
     const int rows = n * v.G;
-    const int base = at.len - n;               // position of the first new token
+    const int base = len - n;                  // position of the first new token
     uint32_t bq[NQ][kSteps][2];
     float cq[NQ][2];
     int lim[NQ][2];
@@ -288,7 +276,7 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
       __syncwarp();
       issue();
       const int k0 = u * kRowUnit + warp * kChunk;
-      if (k0 >= at.len) continue;
+      if (k0 >= len) continue;
       const uint32_t st = ring + (done % C::kStages) * C::kStage;
       float ks[2] = {1.f, 1.f}, lvs[2] = {0.f, 0.f}, rvs[2] = {1.f, 1.f};
       if (E4M3) {
@@ -428,12 +416,7 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
         }
       }
     __syncthreads();
-    const int64_t a = v.row_pre[at.s] + static_cast<int64_t>(at.kvh) * at.units;
-    int c0, cuts;
-    sh.inside(a, a + at.units, &c0, &cuts);
     constexpr int kGroups = HD / 8;
-    float* slots = v.part;
-    constexpr int kSlot = C::kRows * (HD + 2);
     auto write_out = [&](int r, int h, const float* x, float total) {
       const float inv = total > 0.f ? 1.0f / total : total == 0.f ? 0.f : total;   // an empty row is zero; NaN stays
       uint4 w;
@@ -443,8 +426,8 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
       w.w = pack_bf16(x[6] * inv, x[7] * inv);
       *reinterpret_cast<uint4*>(o + (static_cast<int64_t>(first + r / v.G) * v.Hq + at.kvh * v.G + r % v.G) * HD + h) = w;
     };
-    const bool whole = cuts == 0;
-    float* slot = slots + (2 * static_cast<int64_t>(blockIdx.x) + (at.u == 0 ? 1 : 0)) * kSlot;
+    const bool whole = at.u == 0 && u_end == at.units;
+    float* slot = v.row_part + (2 * static_cast<int64_t>(blockIdx.x) + (at.u == 0 ? 1 : 0)) * row_slot(v);
     for (int i = threadIdx.x; i < rows * kGroups; i += kThreads) {
       const int r = i / kGroups, h = (i % kGroups) * 8;
       float top = -INFINITY;
@@ -463,40 +446,10 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
       if (whole) {
         write_out(r, h, x, total);
       } else {
-        float* p = slot + r * (HD + 2);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) p[h + k] = x[k];
-        if (h == 0) p[HD] = top, p[HD + 1] = total;
-      }
-    }
-    if (!whole) {
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) *last_sh = atomicAdd(&v.sync[c0], 1u) == static_cast<uint32_t>(cuts);
-      __syncthreads();
-      if (*last_sh) {
-        __threadfence();
-        for (int i = threadIdx.x; i < rows * kGroups; i += kThreads) {
-          const int r = i / kGroups, h = (i % kGroups) * 8;
-          float top = -INFINITY;
-          for (int k = 0; k <= cuts; ++k)
-            top = fmaxf(top, __ldcg(slots + (2 * static_cast<int64_t>(c0 + k) + (k == 0)) * kSlot + r * (HD + 2) + HD));
-          float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, total = 0.f;
-          for (int k = 0; k <= cuts; ++k) {
-            const float* p = slots + (2 * static_cast<int64_t>(c0 + k) + (k == 0)) * kSlot + r * (HD + 2);
-            const float mk = __ldcg(p + HD);
-            const float f = mk == -INFINITY ? 0.f : exp2_approx(mk - top);
-            total = fmaf(f, __ldcg(p + HD + 1), total);
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float2 y = __ldcg(reinterpret_cast<const float2*>(p + h + e));
-              x[e] = fmaf(f, y.x, x[e]);
-              x[e + 1] = fmaf(f, y.y, x[e + 1]);
-            }
-          }
-          write_out(r, h, x, total);
-        }
-        if (threadIdx.x == 0) v.sync[c0] = 0;
+        float4* p = reinterpret_cast<float4*>(slot + r * HD + h);
+        p[0] = make_float4(x[0], x[1], x[2], x[3]);
+        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+        if (h == 0) *reinterpret_cast<float2*>(slot + C::kRows * HD + 2 * r) = make_float2(top, total);
       }
     }
     __syncthreads();

@@ -273,12 +273,13 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
     at += (bytes + 255) / 256 * 256;
     return here;
   };
+  const size_t R = v.row_ctas, C = v.tile_ctas;
   const size_t o_start = take(S * 4), o_n = take(S * 4), o_len = take(S * 4), o_table = take(S * max_pages * 4),
                o_seq = take(T * 4), o_pos = take(T * 4), o_row = take(T * 4), o_pp = take((S + 1) * 4),
-               o_rp = take((S + 1) * 8), o_bs = take(J * 4), o_br = take(J * 4), o_bp = take((J + 1) * 8),
-               o_counts = take(8 * 4), o_sync = take(static_cast<size_t>(v.row_ctas + 2 * v.tile_ctas) * 4), o_err = take(4),
-               o_part = take(row_part_bytes(v)),
-               o_tile_part = take(tile_part_bytes(v));
+               o_rs = take(S * sizeof(RowSeq)), o_rp = take((S + 1) * 8), o_blk = take(J * sizeof(TileBlk)),
+               o_bp = take((J + 1) * 8), o_rsh = take(R * sizeof(RowShare)), o_tsh = take(C * sizeof(TileShare)),
+               o_rj = take(R * sizeof(JoinTask)), o_tj = take(C * sizeof(JoinTask)), o_counts = take(8 * 4),
+               o_err = take(4), o_part = take(row_part_bytes(v)), o_tile_part = take(tile_part_bytes(v));
   cudaError_t e = cudaMalloc(&q->mem, at);
   if (e == cudaSuccess) {
     char* b = static_cast<char*>(q->mem);
@@ -290,19 +291,20 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
     v.tok_pos = reinterpret_cast<int32_t*>(b + o_pos);
     v.tok_row = reinterpret_cast<int32_t*>(b + o_row);
     v.page_pre = reinterpret_cast<int32_t*>(b + o_pp);
+    v.row_seq = reinterpret_cast<RowSeq*>(b + o_rs);
     v.row_pre = reinterpret_cast<int64_t*>(b + o_rp);
-    v.blk_seq = reinterpret_cast<int32_t*>(b + o_bs);
-    v.blk_row = reinterpret_cast<int32_t*>(b + o_br);
+    v.blk = reinterpret_cast<TileBlk*>(b + o_blk);
     v.blk_pre = reinterpret_cast<int64_t*>(b + o_bp);
+    v.row_share = reinterpret_cast<RowShare*>(b + o_rsh);
+    v.tile_share = reinterpret_cast<TileShare*>(b + o_tsh);
+    v.row_join = reinterpret_cast<JoinTask*>(b + o_rj);
+    v.tile_join = reinterpret_cast<JoinTask*>(b + o_tj);
     v.counts = reinterpret_cast<int32_t*>(b + o_counts);
-    v.sync = reinterpret_cast<uint32_t*>(b + o_sync);
     v.err = reinterpret_cast<uint32_t*>(b + o_err);
-    v.tile_sync = v.sync + v.row_ctas;
-    v.part = reinterpret_cast<float*>(b + o_part);
+    v.row_part = reinterpret_cast<float*>(b + o_part);
     v.tile_part = reinterpret_cast<float*>(b + o_tile_part);
     const int32_t counts[8] = {0, INT32_MAX, 0, 0, 0, 0, 0, 0};
-    e = cudaMemset(v.sync, 0, static_cast<size_t>(v.row_ctas + 2 * v.tile_ctas) * 4);
-    if (e == cudaSuccess) e = cudaMemset(v.err, 0, 4);
+    e = cudaMemset(v.err, 0, 4);
     if (e == cudaSuccess) e = cudaMemcpy(v.counts, counts, sizeof counts, cudaMemcpyHostToDevice);
   }
   if (e == cudaSuccess) e = cudaEventCreateWithFlags(&q->done, cudaEventDisableTiming);
@@ -418,6 +420,7 @@ mlora_status mlora_attention(mlora_kv_t kv, mlora_seq_t q, const mlora_bf16* que
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_attention_rows(query, out, scale, kv->view, v, s);
   if (e == cudaSuccess && q->tiles) e = launch_attention_tiles(kv->map_k, kv->map_v, query, out, scale, kv->view, v, s);
+  if (e == cudaSuccess) e = launch_attention_join(out, v, q->tiles, s);
   if (e != cudaSuccess) return report_cuda_error(e, "attention launch");
   q->last_stream = s;
   return MLORA_OK;

@@ -6,19 +6,21 @@
 // other's products:
 //   warps 0-3, 4-7  one softmax warpgroup for each tile, a thread for each row: S from TMEM, running maximum and
 //                   sum in base 2, P back to TMEM as 16-bit in place of S, at the end O / sum to global memory.
-//                   The maximum moves only when a score passes it by 2^8, so O is rescaled rarely. They also
-//                   bring the tile's query rows to shared memory.
+//                   The maximum moves only when a score passes it by 2^8, so O is rescaled rarely.
 //   warps 8-11      keys and values of 128 tokens at a time into a ring of shared-memory tiles. bf16: one warp
 //                   issues TMA boxes of whole pages (a lane for each page). e4m3: all four copy codes by cp.async
 //                   into a ring of their own and turn them into f16 (exact) in the tiles; each thread converts
 //                   what it copied, so no barrier lies between.
-//   warp 12         one thread issues tcgen05.mma: S = Q K^T (both from shared memory, K-major) and O += P V with
-//                   P from TMEM and V as the N-major operand. TMEM: S/P 2 x 128 columns, O 2 x hd columns.
+//   warp 12         tcgen05.mma: S = Q K^T (both from shared memory, K-major) and O += P V with P from TMEM and V as
+//                   the N-major operand. TMEM: S/P 2 x 128 columns, O 2 x hd columns. The instructions are issued
+//                   under a predicate in uniform control flow: issued inside a divergent branch each took 120
+//                   cycles, twice its execution.
+//   warps 13-15     the query rows of the next item, while the last products of this one run.
 // e4m3: the key scale multiplies the score, log2 of the value scale is added to it (P then is the weight times the
 // scale, at most 2^8 whatever the scales), the sum takes P / value scale; query rows are divided by their largest
 // element so that f16 holds them.
-// Work: (block, key/value head) items of 128-key tiles one after another, an equal share to each CTA (Shares);
-// parts of a split item are joined in key order by the CTA that comes last.
+// Work: (block, key/value head) items of 128-key tiles one after another, an equal share to each CTA (seq_meta.cu);
+// parts of a split item are joined by attention_join.cu.
 // Value rows past the cached length are zeroed in shared memory, scores past a row's limit are replaced by -inf:
 // what lies there has no effect. Every wait is bounded: after 2 s a role records the timeout, stops waiting and
 // runs on to the end.
@@ -32,11 +34,11 @@
 namespace mlora {
 namespace {
 
-constexpr int kThreads = 512;               // 128 registers each at launch, shared out again by role: 184, 80, 64
+constexpr int kThreads = 512;               // 128 registers each at launch, shared out again by role: 168, 96, 80
 constexpr int kKeys = kTileKeys;              // 128
 constexpr int kHalf = kKeys * 128;            // bytes of 128 rows of 64 16-bit elements (one swizzled half tile)
 constexpr float kLazy = 8.0f;                 // log2 of the largest P
-constexpr int kSnap = 2;
+constexpr int kQThreads = 96;                 // threads that bring the query rows
 
 template <int HD, bool E4M3>
 struct TilesCfg {
@@ -53,28 +55,42 @@ struct TilesCfg {
   static constexpr int kRawScaleOff = kCodeOff + (E4M3 ? kStages * kCodes : 0);  // scales on their way: [kStages][2][128]
   static constexpr int kScaleOff = kRawScaleOff + (E4M3 ? kStages * 2 * kKeys * 4 : 0);   // [kScaleBufs][3][128] floats
   static constexpr int kBarOff = kScaleOff + (E4M3 ? kScaleBufs * 3 * kKeys * 4 : 0);
-  static constexpr int kBytes = kBarOff + 512 + 1024;
+  static constexpr int kQScaleOff = kBarOff + 512;                 // e4m3: [2][tile][128] scales of the query rows
+  static constexpr int kWalkOff = kQScaleOff + (E4M3 ? 2 * 2 * 128 * 4 : 0);
+  static constexpr int kBytes = kWalkOff + 20 * 128 + 1024;
 };
 
-// tcgen05.mma with A from TMEM.
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// tcgen05.mma, A from shared memory or from TMEM, and the commit, for the lane whose `on` is set.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t on) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"(accumulate), "r"(on)
       : "memory");
 }
-// Shared-memory descriptor of an N-major operand: rows (keys) of 128 bytes holding 64 elements of N, 128-byte
-// swizzle; 8-row groups 1024 bytes apart, the next 64 elements of N one half tile further.
-__device__ __forceinline__ uint64_t sw128_nmajor_desc(uint32_t addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(kHalf >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "r"(accumulate), "r"(on)
+      : "memory");
 }
+__device__ __forceinline__ void umma_commit_on(uint64_t* bar, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(ptx::smem_u32(bar)), "r"(on)
+      : "memory");
+}
+// Shared-memory descriptors (128-byte swizzle, 8-row groups 1024 bytes apart) without the address: the K-major form of
+// ptx::sw128_kmajor_desc, and an N-major operand: rows (keys) of 128 bytes holding 64 elements of N, the next 64 one half
+// tile further. Addresses (in 16 bytes) are added; shared memory ends before their field does.
+constexpr uint64_t kDescK = (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+constexpr uint64_t kDescN = (uint64_t(kHalf >> 4) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 // Instruction descriptor of kind::f16 (fp32 D; A and B bf16, or f16), B N-major on request.
 __host__ __device__ constexpr uint32_t idesc16(bool f16, int M, int N, bool b_nmajor) {
   return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_nmajor ? 1u << 16 : 0u) |
@@ -92,11 +108,41 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// Barrier of tile w's softmax warpgroup.
-__device__ __forceinline__ void tile_sync(int w) {
-  if (w == 0) asm volatile("bar.sync 1, 128;" ::: "memory");
-  else asm volatile("bar.sync 2, 128;" ::: "memory");
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair_u(uint32_t x, uint32_t y) { return pair(__uint_as_float(x), __uint_as_float(y)); }
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -109,81 +155,56 @@ __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool full) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(full ? 4 : 0) : "memory");
 }
 
-// One item (256-row block, key/value head) and the part [ka, kb) of its key tiles that this CTA takes.
-struct Item {
-  int blk, kvh, tiles;          // block, head, key tiles of the whole item
-  int ka, kb;
-  int s, r0, n, len, first, base, rows;
-  int end[2];                   // key tiles that tile w of the block works on: [ka, end[w])
+// The CTA's walk over its share of the items (256-row block, key/value head), with the part [ka, kb) of the item's key
+// tiles that the CTA takes. Every role walks on its own.
+struct alignas(128) Walk {
+  int left;                     // units left in the share
+  int blk, kvh;
+  int ka, kb, tiles;
+  int n, len, first, r0;        // the block's sequence, and its first row
+  int base, rows;               // position of the sequence's first new token; its rows
+  int end[2];                   // tile w of the block works on key tiles [ka, end[w])
   const int32_t* table;
   __device__ __forceinline__ bool present(int w) const { return r0 + 128 * w < rows; }
-};
-
-// The CTA's walk over its share of the items; every role runs its own copy.
-struct Walk {
-  Shares sh;
-  int64_t x, x1;                // next unit, end of the share
-  Item it;
-  __device__ __forceinline__ void block(const SeqView& v, int j) {
-    it.blk = j;
-    it.s = v.blk_seq[j];
-    it.r0 = v.blk_row[j];
-    it.n = v.n[it.s];
-    it.len = v.len[it.s];
-    it.first = v.start[it.s];
-    it.table = v.table + static_cast<size_t>(it.s) * v.max_pages;
-    it.base = it.len - it.n;
-    it.rows = it.n * v.G;
-    it.tiles = static_cast<int>((v.blk_pre[j + 1] - v.blk_pre[j]) / v.Hkv);
+  __device__ __forceinline__ bool whole() const { return ka == 0 && kb == tiles; }
+  __device__ __forceinline__ void block(const SeqView& v) {
+    const TileBlk b = v.blk[blk];
+    n = b.n, len = b.len, first = b.start, r0 = b.r0, tiles = b.tiles;
+    table = v.table + static_cast<size_t>(b.seq) * v.max_pages;
+    base = len - n;
+    rows = n * v.G;
   }
-  __device__ __forceinline__ int64_t cut(const SeqView& v, int J, int64_t c) {
-    const int64_t y = sh.raw(c);
-    if (y >= sh.total) return sh.total;
-    const int j = last_at_most(v.blk_pre, J, y);
-    const int64_t p = v.blk_pre[j];
-    const int tiles = static_cast<int>((v.blk_pre[j + 1] - p) / v.Hkv);
-    const int64_t a = p + static_cast<int64_t>(static_cast<int>(y - p) / tiles) * tiles;
-    return sh.snapped(y, a, a + tiles);
-  }
-  __device__ __forceinline__ bool begin(const SeqView& v) {
-    const int J = v.counts[0];
-    sh.total = J > 0 ? v.blk_pre[J] : 0;
-    if (sh.total == 0) return false;
-    sh.n = static_cast<int>(min(static_cast<int64_t>(gridDim.x), sh.total));
-    sh.snap = kSnap;
-    if (static_cast<int>(blockIdx.x) >= sh.n) return false;
-    x = cut(v, J, blockIdx.x);
-    x1 = cut(v, J, blockIdx.x + 1);
-    if (x >= x1) return false;
-    block(v, last_at_most(v.blk_pre, J, x));
-    const int rel = static_cast<int>(x - v.blk_pre[it.blk]);
-    it.kvh = rel / it.tiles;
-    part(v, rel - it.kvh * it.tiles);
-    return true;
-  }
-  __device__ __forceinline__ void part(const SeqView& v, int ka) {
-    it.ka = ka;
-    it.kb = static_cast<int>(min(static_cast<int64_t>(it.tiles), ka + (x1 - x)));
+  __device__ __forceinline__ void part(const SeqView& v, int from) {
+    ka = from;
+    kb = min(tiles, ka + left - (ka == 0 ? kTileHead : 0));       // (a cut inside an item lies past its head)
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      const int last = (min(it.r0 + 128 * (w + 1), it.rows) - 1) / v.G;
-      const int need = (it.base + last) / kKeys + 1;
-      it.end[w] = it.present(w) ? min(it.kb, need) : it.ka;
-      if (it.end[w] < it.ka) it.end[w] = it.ka;
+      const int last = (min(r0 + 128 * (w + 1), rows) - 1) / v.G;
+      end[w] = present(w) ? max(ka, min(kb, (base + last) / kKeys + 1)) : ka;
     }
   }
-  // Moves to the next item of the share; false at its end.
+  __device__ __forceinline__ bool begin(const SeqView& v) {
+    const int4 s = *reinterpret_cast<const int4*>(v.tile_share + blockIdx.x);
+    left = s.w;
+    if (left <= 0) return false;
+    blk = s.x, kvh = s.y;
+    block(v);
+    part(v, s.z);
+    return true;
+  }
   __device__ __forceinline__ bool next(const SeqView& v) {
-    x += it.kb - it.ka;
-    if (x >= x1) return false;
-    if (++it.kvh == v.Hkv) {
-      it.kvh = 0;
-      block(v, it.blk + 1);
+    left -= kb - ka + (ka == 0 ? kTileHead : 0);
+    if (left <= 0) return false;
+    if (++kvh == v.Hkv) {
+      kvh = 0;
+      ++blk;
+      block(v);
     }
     part(v, 0);
     return true;
   }
 };
+static_assert(sizeof(Walk) <= 128, "a walk's place in shared memory");
 
 template <int HD, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -197,12 +218,13 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* kv_empty = kv_full + C::kRing;
   uint64_t* q_full = kv_empty + C::kRing;
-  uint64_t* s_full = q_full + 2;
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* s_full = q_empty + 2;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
   uint64_t* sc_full = o_full + 2;                     // [kScaleBufs]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sc_full + C::kScaleBufs);
-  int* last_sh = reinterpret_cast<int*>(tmem_slot + 2);   // [2]
+  float* q_scale = reinterpret_cast<float*>(smem + C::kQScaleOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* err = v.err;
 
@@ -212,7 +234,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       ptx::mbar_init(&kv_empty[i], 1);
     }
     for (int w = 0; w < 2; ++w) {
-      ptx::mbar_init(&q_full[w], 128);
+      ptx::mbar_init(&q_full[w], kQThreads);
+      ptx::mbar_init(&q_empty[w], 1);
       ptx::mbar_init(&s_full[w], 1);
       ptx::mbar_init(&p_full[w], 128);
       ptx::mbar_init(&o_full[w], 1);
@@ -225,13 +248,32 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     ptx::tmem_alloc(tmem_slot, 512);
     ptx::tmem_relinquish();
   }
+  ptx::grid_dependents_launch();
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;                   // S/P of tile w at 128 w, O at 256 + 128 w
 
-  Walk walk;
-  const bool any = walk.begin(v);
+  // Each warp's walk lives in shared memory, moved by its first lane: the fields are read a few times an item, and
+  // a softmax thread has no registers to keep them in.
+  Walk* walks = reinterpret_cast<Walk*>(smem + C::kWalkOff);   // [13], and [16 ..]: the loads' own
+  Walk& walk = walks[warp];
+  bool any;
+  {
+    Walk first{};
+    any = first.begin(v);
+    if (lane == 0) walk = first;
+    if (lane == 0 && warp >= 8 && warp < 12) walks[warp + 8] = first;
+    __syncwarp();
+  }
+  auto advance = [&](Walk& w) {
+    __syncwarp();
+    int go = 0;
+    if (lane == 0) go = w.next(v);
+    go = __shfl_sync(0xffffffffu, go, 0);
+    __syncwarp();
+    return go != 0;
+  };
   bool dead = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!dead && !ptx::mbar_wait(bar, parity, err)) dead = true;
@@ -239,52 +281,21 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
 
   if (warp < 8) {
     // ------------------------------------------------------------------ softmax of tile w
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     const int w = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
     uint32_t n_s = 0, n_o = 0;                        // waits done on s_full, o_full
     uint32_t n_sc = 0;                                // key tiles of the CTA so far (scale buffers)
-    for (bool go = any; go; go = walk.next(v)) {
-      const Item& it = walk.it;
+    for (bool go = any; go; go = advance(walk)) {
+      const Walk& it = walk;
       const int r = it.r0 + 128 * w + row;
       const bool valid = r < it.rows;
       const int tok = valid ? r / v.G : 0;
-      const int64_t at = (static_cast<int64_t>(it.first + tok) * v.Hq + it.kvh * v.G + (valid ? r - tok * v.G : 0)) * HD;
       const int lim = valid ? it.base + tok : -1;
-      const int first_lim = it.base + (it.r0 + 128 * w) / v.G;      // of the tile's first row: no key past it is free of masks
+      const int first_lim = it.base + (it.r0 + 128 * w) / v.G;      // the tile's first row sees the fewest keys
       float c = scale_log2;
       const int end = it.end[w];
-      if (end > it.ka) {
-        uint8_t* dst = smem + C::kQ + w * C::kTile + row * 128;
-        uint4 x[HD / 8];
-#pragma unroll
-        for (int i = 0; i < HD / 8; ++i)
-          x[i] = valid ? *reinterpret_cast<const uint4*>(q + at + i * 8) : make_uint4(0u, 0u, 0u, 0u);
-        if (E4M3) {
-          float most = 0.f;
-#pragma unroll
-          for (int i = 0; i < HD / 8; ++i) {
-            const uint32_t* p = &x[i].x;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) most = fmaxf(most, fmaxf(fabsf(ptx::bf16_lo(p[k])), fabsf(ptx::bf16_hi(p[k]))));
-          }
-          if (!(most > 0.f)) most = 1.f;
-          const float inv = 1.0f / most;
-          c *= most;
-#pragma unroll
-          for (int i = 0; i < HD / 8; ++i) {
-            uint32_t* p = &x[i].x;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) p[k] = pack_f16(ptx::bf16_lo(p[k]) * inv, ptx::bf16_hi(p[k]) * inv);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < HD / 8; ++i)
-          *reinterpret_cast<uint4*>(dst + (i >> 3) * kHalf + (((i & 7) ^ (row & 7)) * 16)) = x[i];
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(&q_full[w]);
-      }
       float m = -INFINITY, l = 0.f;
       for (int j = it.ka; j < end; ++j) {
         const float* sc = nullptr;
@@ -296,34 +307,56 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         wait(&s_full[w], n_s & 1);
         ++n_s;
         ptx::tc_fence_after();
-        float s[kKeys];
-        uint32_t(&u)[4][32] = *reinterpret_cast<uint32_t(*)[4][32]>(s);
+        // (the query rows and their scales were there before the products that s_full stands for)
+        if (E4M3 && j == it.ka) c *= q_scale[((n_o & 1) * 2 + w) * 128 + row];
+        // Two passes over S, 32 columns at a time: the maximum, then the weights. Reading S from TMEM twice costs
+        // less than holding 128 scores in registers (which spilled).
+        const bool masked = (j + 1) * kKeys - 1 > first_lim;
+        const uint64_t cc = pair(c, c);
+        const int seen = lim - j * kKeys;             // keys 0 .. seen of the tile are visible
+        auto scores = [&](uint32_t (&x)[32], int h) {  // columns 32 h ...: scaled (e4m3) and masked
+          if (E4M3) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ptx::tmem_ld_32x32b_x32(ts + 32 * i, u[i]);
-        ptx::tmem_ld_wait();
-        if (E4M3) {
-#pragma unroll
-          for (int i = 0; i < kKeys; i += 4) {
-            const float4 ks = *reinterpret_cast<const float4*>(sc + i);
-            const float4 lv = *reinterpret_cast<const float4*>(sc + kKeys + i);
-            s[i] = fmaf(s[i] * ks.x, c, lv.x);
-            s[i + 1] = fmaf(s[i + 1] * ks.y, c, lv.y);
-            s[i + 2] = fmaf(s[i + 2] * ks.z, c, lv.z);
-            s[i + 3] = fmaf(s[i + 3] * ks.w, c, lv.w);
+            for (int i = 0; i < 32; i += 4) {
+              const float4 ks = *reinterpret_cast<const float4*>(sc + 32 * h + i);
+              const float4 lv = *reinterpret_cast<const float4*>(sc + kKeys + 32 * h + i);
+              const float2 y = unpair(fma_pair(mul_pair(pair_u(x[i], x[i + 1]), pair(ks.x, ks.y)), cc, pair(lv.x, lv.y)));
+              const float2 z = unpair(fma_pair(mul_pair(pair_u(x[i + 2], x[i + 3]), pair(ks.z, ks.w)), cc, pair(lv.z, lv.w)));
+              x[i] = __float_as_uint(y.x), x[i + 1] = __float_as_uint(y.y);
+              x[i + 2] = __float_as_uint(z.x), x[i + 3] = __float_as_uint(z.y);
+            }
           }
-        }
-        if ((j + 1) * kKeys - 1 > first_lim) {
-          const int k = lim - j * kKeys;              // keys 0 .. k of the tile are visible
+          if (masked) {
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i) s[i] = i > k ? -INFINITY : s[i];
-        }
-        float t4[4] = {s[0], s[1], s[2], s[3]};
+            for (int i = 0; i < 32; ++i) x[i] = 32 * h + i > seen ? 0xff800000u : x[i];
+          }
+        };
+        auto largest = [&](const uint32_t (&x)[32], float t) {
+          float u = __uint_as_float(x[0]);
 #pragma unroll
-        for (int i = 4; i < kKeys; i += 4) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) t4[k] = fmaxf(t4[k], s[i + k]);
-        }
-        float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+          for (int i = 1; i < 16; ++i) {
+            u = fmaxf(u, __uint_as_float(x[i]));
+            t = fmaxf(t, __uint_as_float(x[i + 16]));
+          }
+          return fmaxf(fmaxf(t, __uint_as_float(x[16])), u);
+        };
+        uint32_t xa[32], xb[32];
+        ptx::tmem_ld_32x32b_x32(ts, xa);
+        ptx::tmem_ld_32x32b_x32(ts + 32, xb);
+        ptx::tmem_ld_wait();
+        scores(xa, 0);
+        float top = largest(xa, -INFINITY);
+        ptx::tmem_ld_32x32b_x32(ts + 64, xa);
+        scores(xb, 1);
+        top = largest(xb, top);
+        ptx::tmem_ld_wait();
+        ptx::tmem_ld_32x32b_x32(ts + 96, xb);
+        scores(xa, 2);
+        top = largest(xa, top);
+        ptx::tmem_ld_wait();
+        ptx::tmem_ld_32x32b_x32(ts, xa);
+        scores(xb, 3);
+        top = largest(xb, top);
         if (!E4M3) top *= c;
         if (j == it.ka) {
           m = top;
@@ -332,48 +365,57 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           const float f = up == m ? 1.f : exp2_approx(m - up);
           m = up;
           l *= f;
-#pragma unroll
+          ptx::tmem_ld_wait();                        // the columns read ahead
+#pragma unroll 1
           for (int i = 0; i < HD / 32; ++i) {
-            uint32_t y[32];
-            ptx::tmem_ld_32x32b_x32(to + 32 * i, y);
+            ptx::tmem_ld_32x32b_x32(to + 32 * i, xb);
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
-            tmem_st_x32(to + 32 * i, y);
+            for (int k = 0; k < 32; ++k) xb[k] = __float_as_uint(__uint_as_float(xb[k]) * f);
+            tmem_st_x32(to + 32 * i, xb);
           }
-          tmem_st_wait();
         }
         const float mm = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t neg = pair(-mm, -mm);
+        uint64_t sum = 0, sum1 = 0;                   // two zeros each
+        auto weights = [&](uint32_t (&x)[32], int h) {
+          scores(x, h);
+          uint32_t p[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t p[32];
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int e = 64 * h + 2 * i + k;
-              s[e] = exp2_approx(E4M3 ? s[e] - mm : fmaf(s[e], c, -mm));
-            }
-            const int e = 64 * h + 2 * i;
+          for (int i = 0; i < 32; i += 4) {
+            const uint64_t y0 = pair_u(x[i], x[i + 1]), y1 = pair_u(x[i + 2], x[i + 3]);
+            float2 e0 = unpair(E4M3 ? add_pair(y0, neg) : fma_pair(y0, cc, neg));
+            float2 e1 = unpair(E4M3 ? add_pair(y1, neg) : fma_pair(y1, cc, neg));
+            e0.x = exp2_approx(e0.x), e0.y = exp2_approx(e0.y);
+            e1.x = exp2_approx(e1.x), e1.y = exp2_approx(e1.y);
             if (E4M3) {
-              const float4 rv = *reinterpret_cast<const float4*>(sc + 2 * kKeys + e);
-              sum[0] = fmaf(s[e], rv.x, sum[0]);
-              sum[1] = fmaf(s[e + 1], rv.y, sum[1]);
-              sum[2] = fmaf(s[e + 2], rv.z, sum[2]);
-              sum[3] = fmaf(s[e + 3], rv.w, sum[3]);
-              p[i] = pack_f16(s[e], s[e + 1]);
-              p[i + 1] = pack_f16(s[e + 2], s[e + 3]);
+              const float4 rv = *reinterpret_cast<const float4*>(sc + 2 * kKeys + 32 * h + i);
+              sum = fma_pair(pair(e0.x, e0.y), pair(rv.x, rv.y), sum);
+              sum1 = fma_pair(pair(e1.x, e1.y), pair(rv.z, rv.w), sum1);
+              p[i / 2] = pack_f16(e0.x, e0.y);
+              p[i / 2 + 1] = pack_f16(e1.x, e1.y);
             } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) sum[k] += s[e + k];
-              p[i] = pack_bf16(s[e], s[e + 1]);
-              p[i + 1] = pack_bf16(s[e + 2], s[e + 3]);
+              sum = add_pair(sum, pair(e0.x, e0.y));
+              sum1 = add_pair(sum1, pair(e1.x, e1.y));
+              p[i / 2] = pack_bf16(e0.x, e0.y);
+              p[i / 2 + 1] = pack_bf16(e1.x, e1.y);
             }
           }
-          tmem_st_x32(ts + 32 * h, p);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_x16(ts + 16 * h, p);
+        };
+        ptx::tmem_ld_wait();
+        ptx::tmem_ld_32x32b_x32(ts + 32, xb);
+        weights(xa, 0);
+        ptx::tmem_ld_wait();
+        ptx::tmem_ld_32x32b_x32(ts + 64, xa);
+        weights(xb, 1);
+        ptx::tmem_ld_wait();
+        ptx::tmem_ld_32x32b_x32(ts + 96, xb);
+        weights(xa, 2);
+        ptx::tmem_ld_wait();
+        weights(xb, 3);
+        const float2 total = unpair(add_pair(sum, sum1));
+        l += total.x + total.y;
         tmem_st_wait();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&p_full[w]);
@@ -386,11 +428,9 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       }
 
       if (it.present(w)) {
-        const int64_t a = v.blk_pre[it.blk] + static_cast<int64_t>(it.kvh) * it.tiles;
-        int c0, cuts;
-        walk.sh.inside(a, a + it.tiles, &c0, &cuts);
-        if (cuts == 0) {
-          const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;
+        if (it.whole()) {
+          const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;      // NaN stays
+          uint16_t* dst = o + (static_cast<int64_t>(it.first + tok) * v.Hq + it.kvh * v.G + (r - tok * v.G)) * HD;
 #pragma unroll
           for (int i = 0; i < HD / 32; ++i) {
             uint32_t y[32];
@@ -404,16 +444,12 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                 z.y = pack_bf16(__uint_as_float(y[8 * k + 2]) * inv, __uint_as_float(y[8 * k + 3]) * inv);
                 z.z = pack_bf16(__uint_as_float(y[8 * k + 4]) * inv, __uint_as_float(y[8 * k + 5]) * inv);
                 z.w = pack_bf16(__uint_as_float(y[8 * k + 6]) * inv, __uint_as_float(y[8 * k + 7]) * inv);
-                *reinterpret_cast<uint4*>(o + at + 32 * i + 8 * k) = z;
+                *reinterpret_cast<uint4*>(dst + 32 * i + 8 * k) = z;
               }
             }
           }
         } else {
-          // a part: sums and maximum to the workspace, [slot][tile][hd / 4][row] float4 and [2][row]
-          constexpr int64_t kSlot = static_cast<int64_t>(128) * (HD + 2);
-          float* parts = v.tile_part;
-          auto slot_of = [&](int k) { return parts + ((2 * static_cast<int64_t>(c0 + k) + (k == 0)) * 2 + w) * kSlot; };
-          float* mine = slot_of(static_cast<int>(blockIdx.x) - c0);
+          float* mine = v.tile_part + ((2 * static_cast<int64_t>(blockIdx.x) + (it.ka == 0)) * 2 + w) * tile_slot(v);
           if (end > it.ka) {
 #pragma unroll
             for (int i = 0; i < HD / 32; ++i) {
@@ -427,62 +463,19 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           }
           mine[128 * HD + row] = m;
           mine[128 * HD + 128 + row] = l;
-          __threadfence();
-          tile_sync(w);
-          if (row == 0) last_sh[w] = atomicAdd(&v.tile_sync[2 * c0 + w], 1u) == static_cast<uint32_t>(cuts);
-          tile_sync(w);
-          if (last_sh[w]) {
-            __threadfence();
-            float top = -INFINITY, total = 0.f;
-            for (int k = 0; k <= cuts; ++k) top = fmaxf(top, __ldcg(slot_of(k) + 128 * HD + row));
-            for (int k = 0; k <= cuts; ++k) {
-              const float mk = __ldcg(slot_of(k) + 128 * HD + row);
-              if (mk != -INFINITY) total = fmaf(exp2_approx(mk - top), __ldcg(slot_of(k) + 128 * HD + 128 + row), total);
-            }
-            const float inv = total > 0.f ? 1.0f / total : total == 0.f ? 0.f : total;
-#pragma unroll 1
-            for (int i = 0; i < HD / 16; ++i) {
-              float y[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) y[e] = 0.f;
-              for (int k = 0; k <= cuts; ++k) {
-                const float* p = slot_of(k);
-                const float mk = __ldcg(p + 128 * HD + row);
-                if (mk == -INFINITY) continue;
-                const float f = exp2_approx(mk - top) * inv;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float4 z = __ldcg(reinterpret_cast<const float4*>(p) + (4 * i + e) * 128 + row);
-                  y[4 * e] = fmaf(f, z.x, y[4 * e]);
-                  y[4 * e + 1] = fmaf(f, z.y, y[4 * e + 1]);
-                  y[4 * e + 2] = fmaf(f, z.z, y[4 * e + 2]);
-                  y[4 * e + 3] = fmaf(f, z.w, y[4 * e + 3]);
-                }
-              }
-              if (valid) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  *reinterpret_cast<uint4*>(o + at + 16 * i + 8 * e) =
-                      make_uint4(pack_bf16(y[8 * e], y[8 * e + 1]), pack_bf16(y[8 * e + 2], y[8 * e + 3]),
-                                 pack_bf16(y[8 * e + 4], y[8 * e + 5]), pack_bf16(y[8 * e + 6], y[8 * e + 7]));
-              }
-            }
-            if (row == 0) v.tile_sync[2 * c0 + w] = 0;
-          }
-          tile_sync(w);
         }
       }
       ptx::tc_fence_before();
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------------ keys and values
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (!E4M3) {
       if (warp == 8) {
         const int box = min(kv.page, kKeys), boxes = kKeys / box;
         uint32_t n = 0;                               // tiles brought so far
-        for (bool go = any; go; go = walk.next(v)) {
-          const Item& it = walk.it;
+        for (bool go = any; go; go = advance(walk)) {
+          const Walk& it = walk;
           for (int j = it.ka; j < it.kb; ++j) {
             const int key = j * kKeys + lane * box;
             const bool mine = lane < boxes && key < it.len;
@@ -514,13 +507,13 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       const uint32_t codes = base + C::kCodeOff + tid * 16;
       const uint32_t raw = base + C::kRawScaleOff + tid * 4;
       // loads run kStages - 1 tiles ahead of the conversion, over a walk of their own
-      Walk ahead = walk;
+      Walk& ahead = walks[warp + 8];
       bool more = any;
-      int aj = any ? ahead.it.ka : 0, ah = 0;         // next tile to load: key tile, keys (0) or values (1)
+      int aj = any ? ahead.ka : 0, ah = 0;         // next tile to load: key tile, keys (0) or values (1)
       uint32_t n_ld = 0;
       auto load = [&]() {
         if (more) {
-          const Item& it = ahead.it;
+          const Walk& it = ahead;
           const int st = n_ld % C::kStages;
           const uint8_t* src = static_cast<const uint8_t*>(ah ? kv.V : kv.K);
 #pragma unroll
@@ -547,8 +540,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           } else {
             ah = 0;
             if (++aj == it.kb) {
-              more = ahead.next(v);
-              aj = more ? ahead.it.ka : 0;
+              more = advance(ahead);
+              aj = more ? ahead.ka : 0;
             }
           }
         }
@@ -557,8 +550,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
 #pragma unroll
       for (int i = 0; i < C::kStages - 1; ++i) load();
       uint32_t n = 0;
-      for (bool go = any; go; go = walk.next(v)) {
-        const Item& it = walk.it;
+      for (bool go = any; go; go = advance(walk)) {
+        const Walk& it = walk;
         for (int j = it.ka; j < it.kb; ++j) {
 #pragma unroll 1
           for (int h = 0; h < 2; ++h, ++n) {
@@ -596,69 +589,121 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 12) {
     // ------------------------------------------------------------------ products
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     const uint32_t id_s = idesc16(E4M3, 128, kKeys, false), id_o = idesc16(E4M3, 128, HD, true);
+    const uint32_t on = lane == 0;
     uint32_t n = 0;                                   // ring position of the item's first key tile
     uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
-    for (bool go = any && warp == 12; go; go = walk.next(v)) {
-      const Item& it = walk.it;
-      for (int j = it.ka; j <= it.kb; ++j) {
-        const uint32_t nk = n + 2 * (j - it.ka), nv = nk - 1;      // ring positions of K_j and V_{j-1}
-        if (j > it.ka) {
-          const int st = nv % C::kRing;
-          wait(&kv_full[st], (nv / C::kRing) & 1);
-          const int cut = it.len - (j - 1) * kKeys;
+    for (bool go = any; go; go = advance(walk)) {
+      const int ka = walk.ka, kb = walk.kb, len = walk.len;
+      const int end[2] = {walk.end[0], walk.end[1]};
+      for (int j = ka; j <= kb; ++j) {
+        const uint32_t nk = n + 2 * (j - ka), nv = nk - 1;         // ring positions of K_j and V_{j-1}
+        const uint32_t vs = nv % C::kRing, ks = nk % C::kRing;
+        if (j > ka) {
+          wait(&kv_full[vs], (nv / C::kRing) & 1);
+          const int cut = len - (j - 1) * kKeys;
           if (!E4M3 && cut < kKeys) {                 // value rows past the length
-            uint8_t* t = smem + C::kRingOff + st * C::kTile;
+            uint8_t* t = smem + C::kRingOff + vs * C::kTile;
             for (int r = cut; r < kKeys; ++r)
               if (lane < HD / 8) *reinterpret_cast<uint4*>(t + (lane >> 3) * kHalf + r * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
             ptx::fence_proxy_async_smem();
             __syncwarp();
           }
         }
-        if (j < it.kb) wait(&kv_full[nk % C::kRing], (nk / C::kRing) & 1);
+        if (j < kb) wait(&kv_full[ks], (nk / C::kRing) & 1);
+        const uint64_t dv = kDescN + ((base + C::kRingOff + vs * C::kTile) >> 4);
+        const uint64_t dk = kDescK + ((base + C::kRingOff + ks * C::kTile) >> 4);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          if (j > it.ka && j - 1 < it.end[w]) {
+          if (j > ka && j - 1 < end[w]) {
             wait(&p_full[w], n_p[w] & 1);
             ++n_p[w];
             ptx::tc_fence_after();
-            if (lane == 0) {
-              const uint32_t vt = base + C::kRingOff + (nv % C::kRing) * C::kTile;
 #pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k)
-                umma_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k, sw128_nmajor_desc(vt + k * 2048), id_o,
-                        j - 1 > it.ka || k > 0);
-              if (j == it.end[w]) ptx::umma_commit(&o_full[w]);
-            }
+            for (int k = 0; k < kKeys / 16; ++k)
+              umma_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k, dv + k * (2048 >> 4), id_o, j - 1 > ka || k > 0, on);
+            if (j == end[w]) umma_commit_on(&o_full[w], on);
           }
-          if (j < it.end[w]) {
-            if (j == it.ka) {
+          if (j < end[w]) {
+            if (j == ka) {
               wait(&q_full[w], n_q[w] & 1);
               ++n_q[w];
               ptx::tc_fence_after();
             }
-            if (lane == 0) {
-              const uint32_t qt = base + C::kQ + w * C::kTile, kt = base + C::kRingOff + (nk % C::kRing) * C::kTile;
+            const uint64_t dq = kDescK + ((base + C::kQ + w * C::kTile) >> 4);
 #pragma unroll
-              for (int k = 0; k < kSteps; ++k) {
-                const uint32_t off = (k >> 2) * kHalf + (k & 3) * 32;
-                ptx::umma_bf16(tmem + 128 * w, ptx::sw128_kmajor_desc(qt + off), ptx::sw128_kmajor_desc(kt + off), id_s, k > 0);
-              }
-              ptx::umma_commit(&s_full[w]);
+            for (int k = 0; k < kSteps; ++k) {
+              const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+              umma_ss(tmem + 128 * w, dq + off, dk + off, id_s, k > 0, on);
             }
+            umma_commit_on(&s_full[w], on);
+            if (j + 1 == end[w]) umma_commit_on(&q_empty[w], on);
           }
         }
-        if (lane == 0) {
-          if (j > it.ka) ptx::umma_commit(&kv_empty[nv % C::kRing]);
-          if (j < it.kb) ptx::umma_commit(&kv_empty[nk % C::kRing]);
-        }
-        __syncwarp();
+        if (j > ka) umma_commit_on(&kv_empty[vs], on);
+        if (j < kb) umma_commit_on(&kv_empty[ks], on);
       }
-      n += 2 * (it.kb - it.ka);
+      n += 2 * (kb - ka);
+    }
+    } else {
+    // ------------------------------------------------------------------ queries
+    const int tid = threadIdx.x - 13 * 32;
+    uint32_t n_q[2] = {0, 0};
+    for (bool go = any; go; go = advance(walk)) {
+      const Walk& it = walk;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (it.end[w] <= it.ka) continue;
+        wait(&q_empty[w], (n_q[w] & 1) ^ 1);
+        uint8_t* tile = smem + C::kQ + w * C::kTile;
+        const int r0 = it.r0 + 128 * w, rows = it.rows;
+        const uint16_t* src = q + (static_cast<int64_t>(it.first) * v.Hq + it.kvh * v.G) * HD;
+        if (!E4M3) {
+          constexpr int kRowSegs = HD / 8;
+          for (int i = tid; i < 128 * kRowSegs; i += kQThreads) {
+            const int row = i / kRowSegs, seg = i % kRowSegs, r = r0 + row;
+            const int tok = r < rows ? r / v.G : 0;
+            cp16(base + C::kQ + w * C::kTile + (seg >> 3) * kHalf + row * 128 + (((seg & 7) ^ (row & 7)) * 16),
+                 src + (static_cast<int64_t>(tok) * v.Hq + (r < rows ? r - tok * v.G : 0)) * HD + seg * 8, r < rows);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+        } else {
+          for (int row = tid; row < 128; row += kQThreads) {
+            const int r = r0 + row, tok = r < rows ? r / v.G : 0;
+            const uint4* x = reinterpret_cast<const uint4*>(src + (static_cast<int64_t>(tok) * v.Hq + (r < rows ? r - tok * v.G : 0)) * HD);
+            float most = 0.f;
+#pragma unroll 8
+            for (int i = 0; i < HD / 8; ++i) {
+              const uint4 y = __ldg(x + i);
+              const uint32_t p[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) most = fmaxf(most, fmaxf(fabsf(ptx::bf16_lo(p[k])), fabsf(ptx::bf16_hi(p[k]))));
+            }
+            if (!(most > 0.f)) most = 1.f;
+            const float inv = r < rows ? 1.0f / most : 0.f;
+#pragma unroll 8
+            for (int i = 0; i < HD / 8; ++i) {
+              const uint4 y = __ldg(x + i);
+              uint32_t p[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) p[k] = r < rows ? pack_f16(ptx::bf16_lo(p[k]) * inv, ptx::bf16_hi(p[k]) * inv) : 0u;
+              *reinterpret_cast<uint4*>(tile + (i >> 3) * kHalf + row * 128 + (((i & 7) ^ (row & 7)) * 16)) = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+            q_scale[((n_q[w] & 1) * 2 + w) * 128 + row] = most;
+          }
+        }
+        ++n_q[w];
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(&q_full[w]);
+      }
     }
   }
+  }
+  ptx::grid_dependency_wait();                        // this grid's end stands for the row kernel's too
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 12) {
@@ -675,8 +720,17 @@ cudaError_t launch_as(const CUtensorMap& tk, const CUtensorMap& tv, const uint16
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (once != cudaSuccess) return once;
   note_launch_begin(kKindAttn, st);
-  attention_tiles_kernel<HD, E4M3><<<s.tile_ctas, kThreads, C::kBytes, st>>>(tk, tv, q, o, scale_log2, kv, s);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(s.tile_ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_tiles_kernel<HD, E4M3>, tk, tv, q, o, scale_log2, kv, s);
   note_launch_end(kKindAttn, st);
   return e;
 }

@@ -11,6 +11,7 @@
 #include <algorithm>
 
 #include "attention.h"
+#include "attention.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -73,10 +74,48 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* warp_sums, int
   return x + (warp > 0 ? before : 0);
 }
 
+// The last i in [0, n) with pre[i] <= x, by one thread.
+__device__ int last_below(const int64_t* pre, int n, int64_t x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// One cut of a list of `n` entries with prefix sums pre: where it falls (entry, head, unit of the item), and the item
+// if the cut is the first inside it.
+struct Cut {
+  int item, kvh, unit;
+  int64_t at;
+  JoinTask join;
+};
+__device__ Cut cut_at(const Shares& sh, const int64_t* pre, int n, int Hkv, int64_t c) {
+  Cut r{n, 0, 0, sh.total, JoinTask{0, 0, 0, 0}};
+  const int64_t y = sh.raw(c);
+  if (y >= sh.total) return r;
+  r.item = last_below(pre, n, y);
+  const int units = static_cast<int>((pre[r.item + 1] - pre[r.item]) / Hkv);
+  r.kvh = static_cast<int>(y - pre[r.item]) / units;
+  const int64_t a = pre[r.item] + static_cast<int64_t>(r.kvh) * units, b = a + units;
+  r.at = sh.snapped(y, a, b);
+  if (r.at > a && r.at < b) {
+    int first, cuts;
+    sh.inside(a, b, &first, &cuts);
+    if (c == first + 1) r.join = JoinTask{r.item, r.kvh, first, cuts + 1};
+    r.unit = static_cast<int>(r.at - a);
+  } else if (r.at == b) {              // the next item
+    if (++r.kvh == Hkv) r.kvh = 0, ++r.item;
+  }
+  return r;
+}
+
 __device__ void plan(const SeqView& v, int page_log2) {
   __shared__ int64_t sums[32];
+  __shared__ int64_t row_total, tile_total;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t tokens = 0, units = 0, cached = 0, blocks = 0;      // totals of the sequences before this chunk
+  int64_t tokens = 0, units = 0, entries = 0, cached = 0, blocks = 0;      // totals of the sequences before this chunk
   for (int s0 = 0; s0 < v.S; s0 += kPlanThreads) {
     const int s = s0 + threadIdx.x;
     int n = s < v.S ? v.n[s] : 0;
@@ -90,28 +129,35 @@ __device__ void plan(const SeqView& v, int page_log2) {
       atomicMin(&v.counts[1], s);
     }
     const int64_t rows = static_cast<int64_t>(n) * v.G;
-    const bool some = rows > 0 && L > 0;
-    const int64_t u = some && rows <= v.row_limit ? (L + kRowUnit - 1) / kRowUnit : 0;
+    const bool some = rows > 0 && L > 0, few = rows <= v.row_limit;
+    const int64_t u = some && few ? (L + kRowUnit - 1) / kRowUnit : 0;
     const int64_t p = (L + (1 << page_log2) - 1) >> page_log2;
-    const int64_t b = some && rows > v.row_limit ? (rows + kBlockRows - 1) / kBlockRows : 0;
-    int64_t tu, tp, tb;
-    const int64_t iu = block_scan(u, sums, &tu), ip = block_scan(p, sums, &tp), ib = block_scan(b, sums, &tb);
-    if (s < v.S) {
-      v.row_pre[s + 1] = (units + iu) * v.Hkv;
-      v.page_pre[s + 1] = static_cast<int32_t>(cached + ip);
+    const int64_t b = some && !few ? (rows + kBlockRows - 1) / kBlockRows : 0;
+    int64_t tu, te, tp, tb;
+    const int64_t iu = block_scan(u, sums, &tu), ie = block_scan(u > 0, sums, &te), ip = block_scan(p, sums, &tp),
+                  ib = block_scan(b, sums, &tb);
+    if (s < v.S) v.page_pre[s + 1] = static_cast<int32_t>(cached + ip);
+    if (u > 0) {
+      v.row_seq[entries + ie - 1] = RowSeq{s, n, L, v.start[s]};
+      v.row_pre[entries + ie] = (units + iu) * v.Hkv;
     }
     // the chunk's tile blocks, a warp for each sequence
     const int64_t first = blocks + ib - b;
     for (int i = 0; i < 32; ++i) {
       const int nb = static_cast<int>(__shfl_sync(0xffffffffu, b, i));
       const int64_t f = __shfl_sync(0xffffffffu, first, i);
+      const int bn = __shfl_sync(0xffffffffu, n, i), bl = __shfl_sync(0xffffffffu, L, i);
+      if (nb == 0) continue;
+      const int bs = s0 + warp * 32 + i, start = v.start[bs];
       for (int k = lane; k < nb; k += 32) {
-        v.blk_seq[f + k] = s0 + warp * 32 + i;
-        v.blk_row[f + k] = k * kBlockRows;
+        const int64_t last = min(static_cast<int64_t>(k + 1) * kBlockRows, static_cast<int64_t>(bn) * v.G) - 1;
+        const int tiles = static_cast<int>((bl - bn + last / v.G) / kTileKeys + 1);
+        v.blk[f + k] = TileBlk{bs, bn, bl, start, k * kBlockRows, tiles};
       }
     }
     tokens += tn;
     units += tu;
+    entries += te;
     cached += tp;
     blocks += tb;
   }
@@ -119,23 +165,45 @@ __device__ void plan(const SeqView& v, int page_log2) {
     v.row_pre[0] = 0;
     v.page_pre[0] = 0;
     v.blk_pre[0] = 0;
-    v.counts[0] = static_cast<int32_t>(blocks);
   }
   __syncthreads();
   int64_t tiles = 0;
   for (int64_t j0 = 0; j0 < blocks; j0 += kPlanThreads) {
     const int64_t j = j0 + threadIdx.x;
-    int64_t kt = 0;
-    if (j < blocks) {
-      const int s = v.blk_seq[j];
-      const int n = v.n[s], L = v.len[s];
-      const int64_t last = min(static_cast<int64_t>(v.blk_row[j]) + kBlockRows, static_cast<int64_t>(n) * v.G) - 1;
-      kt = (L - n + last / v.G + 1 + kTileKeys - 1) / kTileKeys;
-    }
     int64_t total;
-    const int64_t inc = block_scan(kt, sums, &total);
+    const int64_t inc = block_scan(j < blocks ? kTileHead + v.blk[j].tiles : 0, sums, &total);
     if (j < blocks) v.blk_pre[j + 1] = (tiles + inc) * v.Hkv;
     tiles += total;
+  }
+  if (threadIdx.x == 0) row_total = units * v.Hkv, tile_total = tiles * v.Hkv;
+  __syncthreads();
+  // the CTAs' shares: thread c handles cut c and the share after it (cut c + 1 is found again)
+  const int c = threadIdx.x;
+  if (c < v.row_ctas) {
+    Shares sh{row_total, static_cast<int>(min(static_cast<int64_t>(v.row_ctas), row_total)), 0, 0};
+    RowShare share{0, 0, 0, 0};
+    JoinTask join{0, 0, 0, 0};
+    if (c < sh.n) {
+      const Cut a = cut_at(sh, v.row_pre, static_cast<int>(entries), v.Hkv, c);
+      const Cut b = cut_at(sh, v.row_pre, static_cast<int>(entries), v.Hkv, c + 1);
+      share = RowShare{a.item, a.kvh, a.unit, static_cast<int>(b.at - a.at)};
+      join = b.join;
+    }
+    v.row_share[c] = share;
+    v.row_join[c] = join;
+  }
+  if (c < v.tile_ctas) {
+    Shares sh{tile_total, static_cast<int>(min(static_cast<int64_t>(v.tile_ctas), tile_total)), kTileHead, kTileSnap};
+    TileShare share{0, 0, 0, 0};
+    JoinTask join{0, 0, 0, 0};
+    if (c < sh.n) {
+      const Cut a = cut_at(sh, v.blk_pre, static_cast<int>(blocks), v.Hkv, c);
+      const Cut b = cut_at(sh, v.blk_pre, static_cast<int>(blocks), v.Hkv, c + 1);
+      share = TileShare{a.item, a.kvh, max(a.unit - kTileHead, 0), static_cast<int>(b.at - a.at)};
+      join = b.join;
+    }
+    v.tile_share[c] = share;
+    v.tile_join[c] = join;
   }
 }
 
