@@ -372,8 +372,8 @@ MLORA_API mlora_status mlora_rope_create(int rot_dim, int interleaved, const dou
 MLORA_API mlora_status mlora_rope_destroy(mlora_rope_t rope);
 
 /* Metadata and workspace of steps of at most max_seqs sequences, max_tokens new tokens in all and max_pages
- * pages per sequence, for layers of n_q_heads query heads and n_kv_heads key/value heads (a divisor) of
- * head_dim. */
+ * pages per sequence, for layers of n_q_heads query heads and n_kv_heads key/value heads (a divisor, at least one for
+ * 128 query heads) of head_dim. */
 MLORA_API mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n_q_heads, int n_kv_heads,
                                         int head_dim, mlora_seq_t* out);
 MLORA_API mlora_status mlora_seq_destroy(mlora_seq_t seq);

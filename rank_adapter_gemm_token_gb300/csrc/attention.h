@@ -31,10 +31,10 @@ struct RowSeq {
 struct RowShare {
   int32_t item, kvh, unit, units;
 };
-// A 256-row block of the tile kernel's list: rows r0 ... (token * G + head of the group) of sequence seq, `tiles`
-// key tiles. A CTA's share: `units` units from key tile `tile` of head kvh of block `blk` on.
+// A block of the tile kernel's list: tokens t0 ... (two tiles of SeqView::tile_tokens) of sequence seq, `tiles` key
+// tiles. A CTA's share: `units` units from key tile `tile` of head kvh of block `blk` on.
 struct alignas(32) TileBlk {
-  int32_t seq, n, len, start, r0, tiles;
+  int32_t seq, n, len, start, t0, tiles;
 };
 struct TileShare {
   int32_t blk, kvh, tile, units;
@@ -67,15 +67,14 @@ struct SeqView {
   float* row_part;      // partial results of the row kernel's split items
   float* tile_part;     // of the tile kernel's
   int S, T, max_pages, Hq, Hkv, G, hd;
+  int tile_tokens;      // tokens of one 128-row tile of the tile kernel (128 / G)
   int row_limit;        // rows (new tokens * G) up to which a sequence takes the row kernel
   int row_ctas, tile_ctas;
 };
 
-// Keys of one unit of the row kernel (four warps x 16 keys) and of one tile of the tile kernel;
-// rows of one block of the tile kernel.
+// Keys of one unit of the row kernel (four warps x 16 keys) and of one tile of the tile kernel.
 constexpr int kRowUnit = 64;
 constexpr int kTileKeys = 128;
-constexpr int kBlockRows = 256;
 constexpr int kTileSnap = 2;          // key tiles that a split costs at least
 constexpr int kTileHead = 3;          // key tiles that an item's fixed costs (queries, first products, output) are worth
 
@@ -96,13 +95,14 @@ cudaError_t launch_kv_read(const int32_t* row_start, int64_t rows, uint16_t* k, 
                            const SeqView& s, int num_sms, cudaStream_t st);
 // Attention in up to three launches, each a programmatic dependent of the one before: the row kernel (sequences of at
 // most SeqView::row_limit rows, and the zero rows of tokens in no sequence), with `tiles` the tile kernel (the other
-// sequences; tk and tv: the maps of a bf16 cache's K and V), and the join of the items that were split among CTAs.
+// sequences; tk and tv: the maps of the cache's K and V), and the join of the items that were split among CTAs.
 cudaError_t launch_attention_rows(const uint16_t* q, uint16_t* o, float scale, const KvView& kv, const SeqView& s,
                                   cudaStream_t st);
 cudaError_t launch_attention_tiles(const CUtensorMap& tk, const CUtensorMap& tv, const uint16_t* q, uint16_t* o,
                                    float scale, const KvView& kv, const SeqView& s, cudaStream_t st);
 cudaError_t launch_attention_join(uint16_t* o, const SeqView& s, bool tiles, cudaStream_t st);
-// K and V as matrices [n_pages * Hkv * page, hd] in boxes of min(page, 128) rows x 64 columns.
+// K and V as matrices [n_pages * Hkv * page, hd] in boxes of min(page, 128) rows x 64 columns (bf16, swizzled) or
+// whole rows (e4m3).
 bool make_kv_maps(const KvView& kv, CUtensorMap* k, CUtensorMap* v);
 // Parts of split items: 2 c + 0 is the part that CTA c continues, 2 c + 1 the one that it begins.
 // Row kernel: [rows][hd] sums, then [rows] (maximum, sum of weights), rows = row_limit.

@@ -14,7 +14,7 @@ namespace mlora {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kSlices = 8;            // of a 256-row block
+constexpr int kSlices = 8;            // of a block
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -78,8 +78,8 @@ attention_join_kernel(uint16_t* __restrict__ o, SeqView v) {
   }
   const TileBlk b = v.blk[task.x];
   const int slice = idx % kSlices, w = slice / 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tr = (slice & 3) * 32 + lane, r = b.r0 + 128 * w + tr;
-  const bool valid = r < b.n * v.G;
+  const int tr = (slice & 3) * 32 + lane, tok = b.t0 + v.tile_tokens * w + tr / v.G;
+  const bool valid = tr < v.tile_tokens * v.G && tok < b.n;
   const int64_t slot = tile_slot(v);
   auto part = [&](int k) { return v.tile_part + ((2 * static_cast<int64_t>(cta + k) + (k == 0)) * 2 + w) * slot; };
   ptx::grid_dependency_wait();
@@ -124,8 +124,7 @@ attention_join_kernel(uint16_t* __restrict__ o, SeqView v) {
     }
   }
   if (!valid) return;
-  const int tok = r / v.G;
-  uint16_t* dst = o + (static_cast<int64_t>(b.start + tok) * v.Hq + kvh * v.G + r - tok * v.G) * HD;
+  uint16_t* dst = o + (static_cast<int64_t>(b.start + tok) * v.Hq + kvh * v.G + tr % v.G) * HD;
 #pragma unroll
   for (int c = 0; c < kCols; ++c)
     *reinterpret_cast<uint2*>(dst + 4 * (warp + 4 * c)) = make_uint2(pack_bf16(x[c].x, x[c].y), pack_bf16(x[c].z, x[c].w));

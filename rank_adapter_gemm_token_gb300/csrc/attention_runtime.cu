@@ -54,7 +54,7 @@ mlora_status check_cache_sizes(int n_pages, int page, int n_kv_heads, int hd, in
 struct mlora_kv {
   KvView view{};
   bool own = false;
-  CUtensorMap map_k{}, map_v{};       // of a bf16 cache
+  CUtensorMap map_k{}, map_v{};
 };
 
 struct mlora_rope {
@@ -126,7 +126,7 @@ mlora_status mlora_kv_create(int n_pages, int page_size, int n_kv_heads, int hea
       return created(e, "KV cache");
     }
   }
-  if (!scales && !make_kv_maps(w, &kv->map_k, &kv->map_v)) {
+  if (!make_kv_maps(w, &kv->map_k, &kv->map_v)) {
     mlora_kv_destroy(kv);
     return fail(MLORA_ERR_CUDA, "tensor maps of the cache");
   }
@@ -249,6 +249,8 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
   if (head_dim != 64 && head_dim != 128) return fail(MLORA_ERR_INVALID_ARG, "head size %d must be 64 or 128", head_dim);
   if (n_kv_heads < 1 || n_kv_heads > MLORA_MAX_HEADS || n_q_heads < n_kv_heads || n_q_heads > MLORA_MAX_HEADS || n_q_heads % n_kv_heads)
     return fail(MLORA_ERR_INVALID_ARG, "%d query heads must be a multiple of %d key/value heads, both in [1, %d]", n_q_heads, n_kv_heads, MLORA_MAX_HEADS);
+  if (n_q_heads / n_kv_heads > 128)
+    return fail(MLORA_ERR_INVALID_ARG, "%d query heads for each key/value head, at most 128", n_q_heads / n_kv_heads);
   int sms = 0;
   if (mlora_status st = device_sms(&sms)) return st;
   mlora_seq* q = new (std::nothrow) mlora_seq();
@@ -261,11 +263,12 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
   v.Hq = n_q_heads;
   v.Hkv = n_kv_heads;
   v.G = n_q_heads / n_kv_heads;
+  v.tile_tokens = 128 / v.G;
   v.hd = head_dim;
   v.row_ctas = 2 * sms;
   v.tile_ctas = sms;
   const size_t S = max_seqs, T = max_tokens;
-  q->max_blocks = static_cast<int64_t>(T) * v.G / kBlockRows + static_cast<int64_t>(S);
+  q->max_blocks = static_cast<int64_t>(T) / (2 * v.tile_tokens) + static_cast<int64_t>(S);
   const size_t J = q->max_blocks;
   size_t at = 0;
   auto take = [&](size_t bytes) {

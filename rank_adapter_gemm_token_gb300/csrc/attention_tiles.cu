@@ -1,24 +1,26 @@
 // Attention of sequences with many query rows (chunks of a prompt, whole prompts, groups of many heads) over
 // the paged cache, the formula of attention_rows.cu. Bound: the tensor cores and, next to them, the exponentials.
 //
-// Rows are (token, head of the group) pairs of one key/value head, 256 to a block: all heads of a group share
-// its keys. A persistent CTA works on two 128-row tiles at once, so that one tile's softmax runs beside the
-// other's products:
+// Rows are (token, head of the group) pairs of one key/value head: all heads of a group share its keys. A tile holds the
+// rows of as many whole tokens as fit 128 rows (128 / G), a block two tiles. A persistent CTA works on both tiles of a
+// block at once, so that one tile's softmax runs beside the other's products:
 //   warps 0-3, 4-7  one softmax warpgroup for each tile, a thread for each row: S from TMEM, running maximum and
 //                   sum in base 2, P back to TMEM as 16-bit in place of S, at the end O / sum to global memory.
 //                   The maximum moves only when a score passes it by 2^8, so O is rescaled rarely.
-//   warps 8-11      keys and values of 128 tokens at a time into a ring of shared-memory tiles. bf16: one warp
-//                   issues TMA boxes of whole pages (a lane for each page). e4m3: all four copy codes by cp.async
-//                   into a ring of their own and turn them into f16 (exact) in the tiles; each thread converts
-//                   what it copied, so no barrier lies between.
+//   warps 8-11      bf16: the first brings keys and values of 128 tokens at a time into a ring of shared-memory tiles
+//                   by TMA boxes of whole pages (a lane for each page), the second clears value rows past the
+//                   sequence's length. e4m3: warp 14 brings the codes, all four turn them into f16 in the ring's tiles.
 //   warp 12         tcgen05.mma: S = Q K^T (both from shared memory, K-major) and O += P V with P from TMEM and V as
-//                   the N-major operand. TMEM: S/P 2 x 128 columns, O 2 x hd columns. The instructions are issued
-//                   under a predicate in uniform control flow: issued inside a divergent branch each took 120
-//                   cycles, twice its execution.
-//   warps 13-15     the query rows of the next item, while the last products of this one run.
-// e4m3: the key scale multiplies the score, log2 of the value scale is added to it (P then is the weight times the
-// scale, at most 2^8 whatever the scales), the sum takes P / value scale; query rows are divided by their largest
-// element so that f16 holds them.
+//                   the N-major operand. TMEM: S/P 2 x 128 columns, O 2 x hd columns. One elected thread issues them:
+//                   chosen by its lane number instead, each instruction took 120 cycles to issue, twice its execution;
+//                   with a warp for each tile, their instructions alternate and the rate falls by a third.
+//   warp 15         the next item's queries by TMA, while the last products of this one run (e4m3: and their f16 form).
+// e4m3: a tile's key rows become f16 as code * (scale / largest scale of the tile), rounded once (2^-12 on average, as the
+// queries are), and that largest scale multiplies the tile's scores. Its value rows become code * 2^k, exact: with
+// scale = f 2^(E + k), 1 <= f < 2 and 2^E the binary power of the tile's largest scale, f multiplies P before its rounding,
+// E is added to the scores (P then is the weight times the scale, at most 2^9 whatever the scales) and 2^-E multiplies the
+// sum. So the softmax reads one factor a key from shared memory; with both scales and the sum's factor of each key it took
+// 5000 cycles a tile against 1400 for bf16. Query rows are divided by their largest element so that f16 holds them.
 // Work: (block, key/value head) items of 128-key tiles one after another, an equal share to each CTA (seq_meta.cu);
 // parts of a split item are joined by attention_join.cu.
 // Value rows past the cached length are zeroed in shared memory, scores past a row's limit are replaced by -inf:
@@ -34,11 +36,11 @@
 namespace mlora {
 namespace {
 
-constexpr int kThreads = 512;               // 128 registers each at launch, shared out again by role: 168, 96, 80
+constexpr int kThreads = 512;               // 128 registers each at launch, shared out again by role: 152, 104, 104
 constexpr int kKeys = kTileKeys;              // 128
 constexpr int kHalf = kKeys * 128;            // bytes of 128 rows of 64 16-bit elements (one swizzled half tile)
-constexpr float kLazy = 8.0f;                 // log2 of the largest P
-constexpr int kQThreads = 96;                 // threads that bring the query rows
+constexpr float kLazy = 8.0f;                 // log2 of the largest exponential
+constexpr float kLeastScale = 1.17549435e-38f;   // value scales below the normal numbers count as zero
 
 template <int HD, bool E4M3>
 struct TilesCfg {
@@ -53,38 +55,32 @@ struct TilesCfg {
   static constexpr int kRingOff = 2 * kTile;
   static constexpr int kCodeOff = kRingOff + kRing * kTile;
   static constexpr int kRawScaleOff = kCodeOff + (E4M3 ? kStages * kCodes : 0);  // scales on their way: [kStages][2][128]
-  static constexpr int kScaleOff = kRawScaleOff + (E4M3 ? kStages * 2 * kKeys * 4 : 0);   // [kScaleBufs][3][128] floats
-  static constexpr int kBarOff = kScaleOff + (E4M3 ? kScaleBufs * 3 * kKeys * 4 : 0);
+  static constexpr int kScaleOff = kRawScaleOff + (E4M3 ? kStages * 2 * kKeys * 4 : 0);   // float4 of each scale buffer
+  static constexpr int kMantOff = kScaleOff + (E4M3 ? kScaleBufs * 16 : 0);                // [kScaleBufs][128] f of the value rows
+  static constexpr int kFactorOff = kMantOff + (E4M3 ? kScaleBufs * kKeys * 4 : 0);        // [2][128] half2, [8] maxima
+  static constexpr int kBarOff = kFactorOff + (E4M3 ? 2 * kKeys * 4 + 32 : 0);
   static constexpr int kQScaleOff = kBarOff + 512;                 // e4m3: [2][tile][128] scales of the query rows
   static constexpr int kWalkOff = kQScaleOff + (E4M3 ? 2 * 2 * 128 * 4 : 0);
-  static constexpr int kBytes = kWalkOff + 20 * 128 + 1024;
+  static constexpr int kBytes = kWalkOff + 16 * 128 + 1024;
 };
 
-// tcgen05.mma, A from shared memory or from TMEM, and the commit, for the lane whose `on` is set.
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t on) {
+// tcgen05.mma with A from TMEM.
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-      "r"(accumulate), "r"(on)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t on) {
+// True in one lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-      "r"(accumulate), "r"(on)
-      : "memory");
-}
-__device__ __forceinline__ void umma_commit_on(uint64_t* bar, uint32_t on) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(ptx::smem_u32(bar)), "r"(on)
-      : "memory");
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(on));
+  return on != 0;
 }
 // Shared-memory descriptors (128-byte swizzle, 8-row groups 1024 bytes apart) without the address: the K-major form of
 // ptx::sw128_kmajor_desc, and an N-major operand: rows (keys) of 128 bytes holding 64 elements of N, the next 64 one half
@@ -108,13 +104,6 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-      : "memory");
-}
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pair(float x, float y) {
   uint64_t r;
@@ -143,16 +132,32 @@ __device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint64_t pair_u(uint32_t x, uint32_t y) { return pair(__uint_as_float(x), __uint_as_float(y)); }
 
+// Barrier of the four warps that turn codes into f16.
+__device__ __forceinline__ void converters_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Two e4m3 codes as f16, times a factor.
+__device__ __forceinline__ uint32_t scaled(uint32_t two, __half2 f) {
+  const uint32_t h = e4m3x2_f16x2(two);
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h), f);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool full) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(full ? 16 : 0) : "memory");
+// 3-D tiled load; c0 is the innermost coordinate.
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          ptx::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
 }
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool full) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(full ? 4 : 0) : "memory");
+// Untiled bulk copy (both addresses and the size multiples of 16 bytes).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, int bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(ptx::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+               : "memory");
 }
 
 // The CTA's walk over its share of the items (256-row block, key/value head), with the part [ka, kb) of the item's key
@@ -161,26 +166,24 @@ struct alignas(128) Walk {
   int left;                     // units left in the share
   int blk, kvh;
   int ka, kb, tiles;
-  int n, len, first, r0;        // the block's sequence, and its first row
-  int base, rows;               // position of the sequence's first new token; its rows
+  int n, len, first, t0;        // the block's sequence, and the first of its tokens
+  int base;                     // position of the sequence's first new token
   int end[2];                   // tile w of the block works on key tiles [ka, end[w])
   const int32_t* table;
-  __device__ __forceinline__ bool present(int w) const { return r0 + 128 * w < rows; }
   __device__ __forceinline__ bool whole() const { return ka == 0 && kb == tiles; }
   __device__ __forceinline__ void block(const SeqView& v) {
     const TileBlk b = v.blk[blk];
-    n = b.n, len = b.len, first = b.start, r0 = b.r0, tiles = b.tiles;
+    n = b.n, len = b.len, first = b.start, t0 = b.t0, tiles = b.tiles;
     table = v.table + static_cast<size_t>(b.seq) * v.max_pages;
     base = len - n;
-    rows = n * v.G;
   }
   __device__ __forceinline__ void part(const SeqView& v, int from) {
     ka = from;
     kb = min(tiles, ka + left - (ka == 0 ? kTileHead : 0));       // (a cut inside an item lies past its head)
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      const int last = (min(r0 + 128 * (w + 1), rows) - 1) / v.G;
-      end[w] = present(w) ? max(ka, min(kb, (base + last) / kKeys + 1)) : ka;
+      const int last = min(t0 + v.tile_tokens * (w + 1), n) - 1;
+      end[w] = t0 + v.tile_tokens * w < n ? max(ka, min(kb, (base + last) / kKeys + 1)) : ka;
     }
   }
   __device__ __forceinline__ bool begin(const SeqView& v) {
@@ -209,7 +212,7 @@ static_assert(sizeof(Walk) <= 128, "a walk's place in shared memory");
 template <int HD, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                       const uint16_t* __restrict__ q, uint16_t* __restrict__ o, float scale_log2, KvView kv, SeqView v) {
+                       const __grid_constant__ CUtensorMap tmap_q, uint16_t* __restrict__ o, float scale_log2, KvView kv, SeqView v) {
   using C = TilesCfg<HD, E4M3>;
   constexpr int kSteps = HD / 16;
   extern __shared__ uint8_t smem_raw[];
@@ -219,11 +222,16 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
   uint64_t* kv_empty = kv_full + C::kRing;
   uint64_t* q_full = kv_empty + C::kRing;
   uint64_t* q_empty = q_full + 2;
-  uint64_t* s_full = q_empty + 2;
+  uint64_t* q_raw = q_empty + 2;                      // e4m3: bf16 queries that are not f16 yet
+  uint64_t* s_full = q_raw + 2;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
   uint64_t* sc_full = o_full + 2;                     // [kScaleBufs]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sc_full + C::kScaleBufs);
+  uint64_t* v_short = sc_full + C::kScaleBufs;        // bf16: a value tile with rows past the length is there, and
+  uint64_t* v_clean = v_short + 1;                    // those rows are zero
+  uint64_t* raw_full = v_clean + 1;                   // [kStages], e4m3
+  uint64_t* raw_empty = raw_full + C::kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_empty + C::kStages);
   float* q_scale = reinterpret_cast<float*>(smem + C::kQScaleOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* err = v.err;
@@ -234,13 +242,20 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       ptx::mbar_init(&kv_empty[i], 1);
     }
     for (int w = 0; w < 2; ++w) {
-      ptx::mbar_init(&q_full[w], kQThreads);
+      ptx::mbar_init(&q_full[w], E4M3 ? 32 : 1);
+      ptx::mbar_init(&q_raw[w], 1);
       ptx::mbar_init(&q_empty[w], 1);
       ptx::mbar_init(&s_full[w], 1);
       ptx::mbar_init(&p_full[w], 128);
       ptx::mbar_init(&o_full[w], 1);
     }
     for (int i = 0; i < C::kScaleBufs; ++i) ptx::mbar_init(&sc_full[i], 128);
+    ptx::mbar_init(v_short, 1);
+    ptx::mbar_init(v_clean, 32);
+    for (int i = 0; i < C::kStages; ++i) {
+      ptx::mbar_init(&raw_full[i], 1);
+      ptx::mbar_init(&raw_empty[i], 128);
+    }
     ptx::fence_barrier_init();
     ptx::fence_proxy_async_smem();
   }
@@ -256,14 +271,13 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
 
   // Each warp's walk lives in shared memory, moved by its first lane: the fields are read a few times an item, and
   // a softmax thread has no registers to keep them in.
-  Walk* walks = reinterpret_cast<Walk*>(smem + C::kWalkOff);   // [13], and [16 ..]: the loads' own
+  Walk* walks = reinterpret_cast<Walk*>(smem + C::kWalkOff);   // [16]
   Walk& walk = walks[warp];
   bool any;
   {
     Walk first{};
     any = first.begin(v);
     if (lane == 0) walk = first;
-    if (lane == 0 && warp >= 8 && warp < 12) walks[warp + 8] = first;
     __syncwarp();
   }
   auto advance = [&](Walk& w) {
@@ -279,143 +293,176 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     if (!dead && !ptx::mbar_wait(bar, parity, err)) dead = true;
   };
 
+  // Keys and values of the share's tiles into the ring (bf16), or codes and scales into the stages (e4m3): one warp, a
+  // lane for each page of a tile.
+  auto bring = [&]() {
+    uint64_t* full = E4M3 ? raw_full : kv_full;
+    uint64_t* empty = E4M3 ? raw_empty : kv_empty;
+    constexpr int kDepth = E4M3 ? C::kStages : C::kRing;
+    const int box = min(kv.page, kKeys), boxes = kKeys / box;
+    uint32_t n = 0;                                   // tiles brought so far
+    for (bool go = any; go; go = advance(walk)) {
+      const Walk& it = walk;
+      for (int j = it.ka; j < it.kb; ++j) {
+        const int key = j * kKeys + lane * box;
+        const bool mine = lane < boxes && key < it.len;
+        int at = 0;
+        if (mine) at = ((it.table[key >> kv.page_log2] * v.Hkv + it.kvh) << kv.page_log2) + (key & (kv.page - 1));
+        const int count = __popc(__ballot_sync(0xffffffffu, mine));
+#pragma unroll
+        for (int h = 0; h < 2; ++h, ++n) {            // the keys (and both scales), then the values
+          const int st = n % kDepth;
+          wait(&empty[st], ((n / kDepth) & 1) ^ 1);
+          if (lane == 0)
+            ptx::mbar_arrive_expect_tx(&full[st], count * box * (!E4M3 ? 2 * HD : h == 0 ? HD + 8 : HD));
+          __syncwarp();
+          if (!mine) continue;
+          if (E4M3) {
+            ptx::tma_load_2d(smem + C::kCodeOff + st * C::kCodes + lane * box * HD, h ? &tmap_v : &tmap_k, &full[st], 0, at);
+            if (h == 0) {
+              uint8_t* dst = smem + C::kRawScaleOff + st * 2 * kKeys * 4 + lane * box * 4;
+              bulk_load(dst, kv.k_scale + at, box * 4, &full[st]);
+              bulk_load(dst + kKeys * 4, kv.v_scale + at, box * 4, &full[st]);
+            }
+          } else {
+            uint8_t* dst = smem + C::kRingOff + st * C::kTile + lane * box * 128;
+#pragma unroll
+            for (int x = 0; x < C::kHalves; ++x)
+              ptx::tma_load_2d(dst + x * kHalf, h ? &tmap_v : &tmap_k, &full[st], 64 * x, at);
+          }
+        }
+      }
+    }
+  };
+
   if (warp < 8) {
     // ------------------------------------------------------------------ softmax of tile w
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     const int w = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
+    const int row_tok = row / v.G, row_head = row - row_tok * v.G;
     uint32_t n_s = 0, n_o = 0;                        // waits done on s_full, o_full
     uint32_t n_sc = 0;                                // key tiles of the CTA so far (scale buffers)
     for (bool go = any; go; go = advance(walk)) {
       const Walk& it = walk;
-      const int r = it.r0 + 128 * w + row;
-      const bool valid = r < it.rows;
-      const int tok = valid ? r / v.G : 0;
+      const int tok0 = it.t0 + v.tile_tokens * w, tok = tok0 + row_tok;
+      const bool valid = row_tok < v.tile_tokens && tok < it.n;
       const int lim = valid ? it.base + tok : -1;
-      const int first_lim = it.base + (it.r0 + 128 * w) / v.G;      // the tile's first row sees the fewest keys
+      const int first_lim = it.base + tok0;           // the tile's first row sees the fewest keys
       float c = scale_log2;
       const int end = it.end[w];
       float m = -INFINITY, l = 0.f;
       for (int j = it.ka; j < end; ++j) {
-        const float* sc = nullptr;
+        float ct = c, off = 0.f, rv = 1.f;            // score = S ct + off; the sum takes rv times the exponentials
+        const float* mant = nullptr;
         if (E4M3) {
           const uint32_t t = n_sc + (j - it.ka);
           wait(&sc_full[t % C::kScaleBufs], (t / C::kScaleBufs) & 1);
-          sc = reinterpret_cast<const float*>(smem + C::kScaleOff) + (t % C::kScaleBufs) * 3 * kKeys;
+          const float4 f = reinterpret_cast<const float4*>(smem + C::kScaleOff)[t % C::kScaleBufs];
+          ct = f.x, off = f.y, rv = f.z;
+          mant = reinterpret_cast<const float*>(smem + C::kMantOff) + (t % C::kScaleBufs) * kKeys;
         }
         wait(&s_full[w], n_s & 1);
         ++n_s;
         ptx::tc_fence_after();
         // (the query rows and their scales were there before the products that s_full stands for)
-        if (E4M3 && j == it.ka) c *= q_scale[((n_o & 1) * 2 + w) * 128 + row];
-        // Two passes over S, 32 columns at a time: the maximum, then the weights. Reading S from TMEM twice costs
-        // less than holding 128 scores in registers (which spilled).
+        if (E4M3) {
+          if (j == it.ka) c *= q_scale[((n_o & 1) * 2 + w) * 128 + row];
+          ct *= c;
+        }
         const bool masked = (j + 1) * kKeys - 1 > first_lim;
-        const uint64_t cc = pair(c, c);
+        const uint64_t cc = pair(ct, ct);
         const int seen = lim - j * kKeys;             // keys 0 .. seen of the tile are visible
-        auto scores = [&](uint32_t (&x)[32], int h) {  // columns 32 h ...: scaled (e4m3) and masked
-          if (E4M3) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 ks = *reinterpret_cast<const float4*>(sc + 32 * h + i);
-              const float4 lv = *reinterpret_cast<const float4*>(sc + kKeys + 32 * h + i);
-              const float2 y = unpair(fma_pair(mul_pair(pair_u(x[i], x[i + 1]), pair(ks.x, ks.y)), cc, pair(lv.x, lv.y)));
-              const float2 z = unpair(fma_pair(mul_pair(pair_u(x[i + 2], x[i + 3]), pair(ks.z, ks.w)), cc, pair(lv.z, lv.w)));
-              x[i] = __float_as_uint(y.x), x[i + 1] = __float_as_uint(y.y);
-              x[i + 2] = __float_as_uint(z.x), x[i + 3] = __float_as_uint(z.y);
-            }
-          }
+        constexpr int W = 32;                         // columns at a time
+        auto mask = [&](uint32_t (&x)[W], int h) {    // of columns W h ...
           if (masked) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = 32 * h + i > seen ? 0xff800000u : x[i];
+            for (int i = 0; i < W; ++i) x[i] = W * h + i > seen ? 0xff800000u : x[i];
           }
         };
-        auto largest = [&](const uint32_t (&x)[32], float t) {
+        auto largest = [&](const uint32_t (&x)[W], float t) {
           float u = __uint_as_float(x[0]);
 #pragma unroll
-          for (int i = 1; i < 16; ++i) {
+          for (int i = 1; i < W / 2; ++i) {
             u = fmaxf(u, __uint_as_float(x[i]));
-            t = fmaxf(t, __uint_as_float(x[i + 16]));
+            t = fmaxf(t, __uint_as_float(x[i + W / 2]));
           }
-          return fmaxf(fmaxf(t, __uint_as_float(x[16])), u);
+          return fmaxf(fmaxf(t, __uint_as_float(x[W / 2])), u);
         };
-        uint32_t xa[32], xb[32];
-        ptx::tmem_ld_32x32b_x32(ts, xa);
-        ptx::tmem_ld_32x32b_x32(ts + 32, xb);
-        ptx::tmem_ld_wait();
-        scores(xa, 0);
-        float top = largest(xa, -INFINITY);
-        ptx::tmem_ld_32x32b_x32(ts + 64, xa);
-        scores(xb, 1);
-        top = largest(xb, top);
-        ptx::tmem_ld_wait();
-        ptx::tmem_ld_32x32b_x32(ts + 96, xb);
-        scores(xa, 2);
-        top = largest(xa, top);
-        ptx::tmem_ld_wait();
-        ptx::tmem_ld_32x32b_x32(ts, xa);
-        scores(xb, 3);
-        top = largest(xb, top);
-        if (!E4M3) top *= c;
-        if (j == it.ka) {
-          m = top;
-        } else if (__any_sync(0xffffffffu, top > m + kLazy)) {
+        uint32_t xa[W], xb[W];
+        float top = -INFINITY;
+        if (j == it.ka) {                             // the first tile's maximum
+#pragma unroll
+          for (int h = 0; h < kKeys / W; h += 2) {
+            ptx::tmem_ld_32x32b_x32(ts + W * h, xa);
+            ptx::tmem_ld_32x32b_x32(ts + W * h + W, xb);
+            ptx::tmem_ld_wait();
+            mask(xa, h);
+            top = largest(xa, top);
+            mask(xb, h + 1);
+            top = largest(xb, top);
+          }
+          m = fmaf(top, ct, off);
+        }
+        // One pass over S, 32 columns at a time: weights against the maximum so far, and the tile's own maximum. P
+        // waits in registers: where the tile's maximum is above the lazy limit, S is still there for another pass.
+        uint32_t p[64];
+        uint64_t sum, sum1;
+        for (;;) {
+          const float mm = m == -INFINITY ? 0.f : m;
+          const uint64_t neg = pair(off - mm, off - mm);
+          top = -INFINITY;
+          sum = 0, sum1 = 0;                          // two zeros each
+          auto weights = [&](uint32_t (&x)[W], int h) {
+            mask(x, h);
+            top = largest(x, top);
+#pragma unroll
+            for (int i = 0; i < W; i += 4) {
+              float2 e0 = unpair(fma_pair(pair_u(x[i], x[i + 1]), cc, neg));
+              float2 e1 = unpair(fma_pair(pair_u(x[i + 2], x[i + 3]), cc, neg));
+              e0.x = exp2_approx(e0.x), e0.y = exp2_approx(e0.y);
+              e1.x = exp2_approx(e1.x), e1.y = exp2_approx(e1.y);
+              sum = add_pair(sum, pair(e0.x, e0.y));
+              sum1 = add_pair(sum1, pair(e1.x, e1.y));
+              if (E4M3) {
+                const float4 f = *reinterpret_cast<const float4*>(mant + W * h + i);
+                e0 = unpair(mul_pair(pair(e0.x, e0.y), pair(f.x, f.y)));
+                e1 = unpair(mul_pair(pair(e1.x, e1.y), pair(f.z, f.w)));
+              }
+              p[W / 2 * h + i / 2] = E4M3 ? pack_f16(e0.x, e0.y) : pack_bf16(e0.x, e0.y);
+              p[W / 2 * h + i / 2 + 1] = E4M3 ? pack_f16(e1.x, e1.y) : pack_bf16(e1.x, e1.y);
+            }
+          };
+          ptx::tmem_ld_32x32b_x32(ts, xa);
+#pragma unroll
+          for (int h = 0; h < kKeys / W; h += 2) {
+            ptx::tmem_ld_wait();
+            ptx::tmem_ld_32x32b_x32(ts + W * h + W, xb);
+            weights(xa, h);
+            ptx::tmem_ld_wait();
+            if (h + 2 < kKeys / W) ptx::tmem_ld_32x32b_x32(ts + W * h + 2 * W, xa);
+            weights(xb, h + 1);
+          }
+          top = fmaf(top, ct, off);
+          if (!__any_sync(0xffffffffu, top > m + kLazy)) break;
           const float up = top > m + kLazy ? top : m;
           const float f = up == m ? 1.f : exp2_approx(m - up);
           m = up;
           l *= f;
-          ptx::tmem_ld_wait();                        // the columns read ahead
 #pragma unroll 1
-          for (int i = 0; i < HD / 32; ++i) {
-            ptx::tmem_ld_32x32b_x32(to + 32 * i, xb);
+          for (int i = 0; i < HD / W; ++i) {
+            ptx::tmem_ld_32x32b_x32(to + W * i, xb);
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) xb[k] = __float_as_uint(__uint_as_float(xb[k]) * f);
-            tmem_st_x32(to + 32 * i, xb);
+            for (int k = 0; k < W; ++k) xb[k] = __float_as_uint(__uint_as_float(xb[k]) * f);
+            tmem_st_x32(to + W * i, xb);
           }
         }
-        const float mm = m == -INFINITY ? 0.f : m;
-        const uint64_t neg = pair(-mm, -mm);
-        uint64_t sum = 0, sum1 = 0;                   // two zeros each
-        auto weights = [&](uint32_t (&x)[32], int h) {
-          scores(x, h);
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const uint64_t y0 = pair_u(x[i], x[i + 1]), y1 = pair_u(x[i + 2], x[i + 3]);
-            float2 e0 = unpair(E4M3 ? add_pair(y0, neg) : fma_pair(y0, cc, neg));
-            float2 e1 = unpair(E4M3 ? add_pair(y1, neg) : fma_pair(y1, cc, neg));
-            e0.x = exp2_approx(e0.x), e0.y = exp2_approx(e0.y);
-            e1.x = exp2_approx(e1.x), e1.y = exp2_approx(e1.y);
-            if (E4M3) {
-              const float4 rv = *reinterpret_cast<const float4*>(sc + 2 * kKeys + 32 * h + i);
-              sum = fma_pair(pair(e0.x, e0.y), pair(rv.x, rv.y), sum);
-              sum1 = fma_pair(pair(e1.x, e1.y), pair(rv.z, rv.w), sum1);
-              p[i / 2] = pack_f16(e0.x, e0.y);
-              p[i / 2 + 1] = pack_f16(e1.x, e1.y);
-            } else {
-              sum = add_pair(sum, pair(e0.x, e0.y));
-              sum1 = add_pair(sum1, pair(e1.x, e1.y));
-              p[i / 2] = pack_bf16(e0.x, e0.y);
-              p[i / 2 + 1] = pack_bf16(e1.x, e1.y);
-            }
-          }
-          tmem_st_x16(ts + 16 * h, p);
-        };
-        ptx::tmem_ld_wait();
-        ptx::tmem_ld_32x32b_x32(ts + 32, xb);
-        weights(xa, 0);
-        ptx::tmem_ld_wait();
-        ptx::tmem_ld_32x32b_x32(ts + 64, xa);
-        weights(xb, 1);
-        ptx::tmem_ld_wait();
-        ptx::tmem_ld_32x32b_x32(ts + 96, xb);
-        weights(xa, 2);
-        ptx::tmem_ld_wait();
-        weights(xb, 3);
         const float2 total = unpair(add_pair(sum, sum1));
-        l += total.x + total.y;
+        l = fmaf(total.x + total.y, rv, l);
+        tmem_st_x32(ts, p);
+        tmem_st_x32(ts + 32, p + 32);
         tmem_st_wait();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&p_full[w]);
@@ -427,10 +474,10 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         ptx::tc_fence_after();
       }
 
-      if (it.present(w)) {
+      if (tok0 < it.n) {
         if (it.whole()) {
           const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;      // NaN stays
-          uint16_t* dst = o + (static_cast<int64_t>(it.first + tok) * v.Hq + it.kvh * v.G + (r - tok * v.G)) * HD;
+          uint16_t* dst = o + (static_cast<int64_t>(it.first + tok) * v.Hq + it.kvh * v.G + row_head) * HD;
 #pragma unroll
           for (int i = 0; i < HD / 32; ++i) {
             uint32_t y[32];
@@ -469,239 +516,222 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------------ keys and values
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (!E4M3) {
       if (warp == 8) {
-        const int box = min(kv.page, kKeys), boxes = kKeys / box;
-        uint32_t n = 0;                               // tiles brought so far
+        bring();
+      } else if (warp == 9) {
+        // value rows past the length, in the one tile of an item that may hold any, when the products have come to it
+        uint32_t n = 1, par = 0;                      // ring position of the item's first value tile; tiles so far
         for (bool go = any; go; go = advance(walk)) {
           const Walk& it = walk;
-          for (int j = it.ka; j < it.kb; ++j) {
-            const int key = j * kKeys + lane * box;
-            const bool mine = lane < boxes && key < it.len;
-            int at = 0;
-            if (mine) at = ((it.table[key >> kv.page_log2] * v.Hkv + it.kvh) << kv.page_log2) + (key & (kv.page - 1));
-            const int count = __popc(__ballot_sync(0xffffffffu, mine));
-#pragma unroll
-            for (int h = 0; h < 2; ++h, ++n) {        // the keys, then the values
-              const int st = n % C::kRing;
-              wait(&kv_empty[st], ((n / C::kRing) & 1) ^ 1);
-              uint8_t* dst = smem + C::kRingOff + st * C::kTile + lane * box * 128;
-              if (lane == 0) ptx::mbar_arrive_expect_tx(&kv_full[st], count * box * 128 * C::kHalves);
-              __syncwarp();
-              if (mine) {
-#pragma unroll
-                for (int x = 0; x < C::kHalves; ++x)
-                  ptx::tma_load_2d(dst + x * kHalf, h ? &tmap_v : &tmap_k, &kv_full[st], 64 * x, at);
-              }
-            }
+          if (it.kb * kKeys > it.len) {
+            wait(v_short, par);
+            par ^= 1;
+            uint8_t* t = smem + C::kRingOff + (n + 2 * (it.kb - 1 - it.ka)) % C::kRing * C::kTile;
+            for (int i = (it.len - (it.kb - 1) * kKeys) * (HD / 8) + lane; i < kKeys * (HD / 8); i += 32)
+              *reinterpret_cast<uint4*>(t + (i % (HD / 8) >> 3) * kHalf + i / (HD / 8) * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(v_clean);
           }
+          n += 2 * (it.kb - it.ka);
         }
-        // the copies of an abandoned run are waited for by the kernel's end
       }
     } else {
       const int tid = threadIdx.x - 256;
-      constexpr int kStep = 128 / C::kSegs;           // rows of one copy of all threads
+      constexpr int kStep = 128 / C::kSegs;           // rows that the threads take at a time, 16 codes each
       constexpr int kCopies = kKeys / kStep;
-      const int seg = tid % C::kSegs, r_in = tid / C::kSegs;
-      const uint32_t codes = base + C::kCodeOff + tid * 16;
-      const uint32_t raw = base + C::kRawScaleOff + tid * 4;
-      // loads run kStages - 1 tiles ahead of the conversion, over a walk of their own
-      Walk& ahead = walks[warp + 8];
-      bool more = any;
-      int aj = any ? ahead.ka : 0, ah = 0;         // next tile to load: key tile, keys (0) or values (1)
-      uint32_t n_ld = 0;
-      auto load = [&]() {
-        if (more) {
-          const Walk& it = ahead;
-          const int st = n_ld % C::kStages;
-          const uint8_t* src = static_cast<const uint8_t*>(ah ? kv.V : kv.K);
-#pragma unroll
-          for (int i = 0; i < kCopies; ++i) {
-            const int key = aj * kKeys + i * kStep + r_in;
-            const bool in = key < it.len;
-            const int page = it.table[min(key, it.len - 1) >> kv.page_log2];
-            const int64_t at = ((static_cast<int64_t>(page) * v.Hkv + it.kvh) << kv.page_log2) + (key & (kv.page - 1));
-            cp16(codes + st * C::kCodes + i * 2048, src + at * HD + seg * 16, in);
-          }
-          {
-            const int key = aj * kKeys + tid;
-            const bool in = key < it.len;
-            const int page = it.table[min(key, it.len - 1) >> kv.page_log2];
-            const int64_t at = ((static_cast<int64_t>(page) * v.Hkv + it.kvh) << kv.page_log2) + (key & (kv.page - 1));
-            if (ah == 0) {                            // both scales come with the keys: the scores need them
-              cp4(raw + st * 2 * kKeys * 4, kv.k_scale + at, in);
-              cp4(raw + st * 2 * kKeys * 4 + kKeys * 4, kv.v_scale + at, in);
-            }
-          }
-          ++n_ld;
-          if (ah == 0) {
-            ah = 1;
-          } else {
-            ah = 0;
-            if (++aj == it.kb) {
-              more = advance(ahead);
-              aj = more ? ahead.ka : 0;
-            }
-          }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      };
-#pragma unroll
-      for (int i = 0; i < C::kStages - 1; ++i) load();
+      const int seg = tid % C::kSegs, r_in = tid / C::kSegs, even = (seg & 3) * 2;
+      const bool odd = seg >= 4;                      // the second half tile's lanes write their two segments in the
+                                                      // other order: different banks
+      __half2* factors = reinterpret_cast<__half2*>(smem + C::kFactorOff);           // keys' rows, values' rows
+      float* maxima = reinterpret_cast<float*>(smem + C::kFactorOff + 2 * kKeys * 4);
       uint32_t n = 0;
       for (bool go = any; go; go = advance(walk)) {
         const Walk& it = walk;
         for (int j = it.ka; j < it.kb; ++j) {
+          const int cut = it.len - j * kKeys;         // rows of the tile inside the sequence (any number)
 #pragma unroll 1
           for (int h = 0; h < 2; ++h, ++n) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
             const int st = n % C::kRing, cs = n % C::kStages;
-            wait(&kv_empty[st], ((n / C::kRing) & 1) ^ 1);
-            if (h == 0) {
-              const uint32_t t = n / 2;
-              float* sc = reinterpret_cast<float*>(smem + C::kScaleOff) + (t % C::kScaleBufs) * 3 * kKeys + tid;
-              const float* rw = reinterpret_cast<const float*>(smem + C::kRawScaleOff) + cs * 2 * kKeys + tid;
-              const float ks = rw[0], vs = rw[kKeys];
-              sc[0] = ks;
-              sc[kKeys] = __log2f(vs);
-              sc[2 * kKeys] = vs > 0.f ? __fdividef(1.0f, vs) : 0.f;      // a NaN scale counts in the exponent alone
-              ptx::mbar_arrive(&sc_full[t % C::kScaleBufs]);
-            }
-            uint8_t* dst = smem + C::kRingOff + st * C::kTile + (seg >> 2) * kHalf;
+            wait(&raw_full[cs], (n / C::kStages) & 1);
             const uint8_t* src = smem + C::kCodeOff + tid * 16 + cs * C::kCodes;
+            uint4 cd[kCopies];
 #pragma unroll
             for (int i = 0; i < kCopies; ++i) {
-              const uint4 cd = *reinterpret_cast<const uint4*>(src + i * 2048);
-              const uint4 lo = make_uint4(e4m3x2_f16x2(cd.x), e4m3x2_f16x2(cd.x >> 16), e4m3x2_f16x2(cd.y), e4m3x2_f16x2(cd.y >> 16));
-              const uint4 hi = make_uint4(e4m3x2_f16x2(cd.z), e4m3x2_f16x2(cd.z >> 16), e4m3x2_f16x2(cd.w), e4m3x2_f16x2(cd.w >> 16));
-              const int r = i * kStep + r_in, p = (seg & 3) * 2;
-              const bool odd = seg >= 4;              // the halves' lanes take different banks
-              *reinterpret_cast<uint4*>(dst + r * 128 + (((p + (odd ? 1 : 0)) ^ (r & 7)) * 16)) = odd ? hi : lo;
-              *reinterpret_cast<uint4*>(dst + r * 128 + (((p + (odd ? 0 : 1)) ^ (r & 7)) * 16)) = odd ? lo : hi;
+              cd[i] = *reinterpret_cast<const uint4*>(src + i * 2048);
+              if (i * kStep + r_in >= cut) cd[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (h == 0) {
+              // the tile's largest scales, and every row's share of them
+              const float* rw = reinterpret_cast<const float*>(smem + C::kRawScaleOff) + cs * 2 * kKeys + tid;
+              const float ks = tid < cut ? rw[0] : 0.f, vs = tid < cut ? rw[kKeys] : 0.f;
+              float km = ks, vm = vs;                 // (the maximum passes over NaN)
+#pragma unroll
+              for (int d = 16; d > 0; d >>= 1) {
+                km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, d));
+                vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, d));
+              }
+              if (lane == 0) maxima[warp - 8] = km, maxima[warp - 4] = vm;
+              converters_sync();
+              km = fmaxf(fmaxf(maxima[0], maxima[1]), fmaxf(maxima[2], maxima[3]));
+              vm = fmaxf(fmaxf(maxima[4], maxima[5]), fmaxf(maxima[6], maxima[7]));
+              if (!(km > 0.f)) km = 1.f;
+              if (!(vm >= kLeastScale)) vm = 1.f;
+              // a row with a NaN scale is NaN in its scores alone: its values would reach rows that do not see it
+              factors[tid] = __half2half2(__float2half_rn(ks != ks || vs != vs ? __int_as_float(0x7fffffff) : __fdividef(ks, km)));
+              const uint32_t t = n / 2;
+              const float top2 = __int_as_float(__float_as_int(vm) & 0x7f800000);               // 2^E
+              const float row2 = vs >= kLeastScale ? __int_as_float(__float_as_int(vs) & 0x7f800000) : 0.f;
+              const float inv2 = 1.0f / top2;
+              factors[kKeys + tid] = __half2half2(__float2half_rn(row2 * inv2));
+              (reinterpret_cast<float*>(smem + C::kMantOff) + (t % C::kScaleBufs) * kKeys)[tid] = row2 > 0.f ? vs / row2 : 1.f;
+              if (tid == 0)
+                reinterpret_cast<float4*>(smem + C::kScaleOff)[t % C::kScaleBufs] =
+                    make_float4(km, static_cast<float>((__float_as_int(vm) >> 23) - 127), inv2, 0.f);
+              ptx::mbar_arrive(&sc_full[t % C::kScaleBufs]);
+              converters_sync();
+            }
+            ptx::mbar_arrive(&raw_empty[cs]);
+            wait(&kv_empty[st], ((n / C::kRing) & 1) ^ 1);
+            uint8_t* dst = smem + C::kRingOff + st * C::kTile + (seg >> 2) * kHalf;
+            __half2 f[kCopies];
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) f[i] = factors[h * kKeys + i * kStep + r_in];
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+              const uint4 lo = make_uint4(scaled(cd[i].x, f[i]), scaled(cd[i].x >> 16, f[i]), scaled(cd[i].y, f[i]), scaled(cd[i].y >> 16, f[i]));
+              const uint4 hi = make_uint4(scaled(cd[i].z, f[i]), scaled(cd[i].z >> 16, f[i]), scaled(cd[i].w, f[i]), scaled(cd[i].w >> 16, f[i]));
+              const int r = i * kStep + r_in;
+              *reinterpret_cast<uint4*>(dst + r * 128 + (((even + (odd ? 1 : 0)) ^ (r & 7)) * 16)) = odd ? hi : lo;
+              *reinterpret_cast<uint4*>(dst + r * 128 + (((even + (odd ? 0 : 1)) ^ (r & 7)) * 16)) = odd ? lo : hi;
             }
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(&kv_full[st]);
-            load();
           }
         }
       }
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 12) {
-    // ------------------------------------------------------------------ products
-    const uint32_t id_s = idesc16(E4M3, 128, kKeys, false), id_o = idesc16(E4M3, 128, HD, true);
-    const uint32_t on = lane == 0;
-    uint32_t n = 0;                                   // ring position of the item's first key tile
-    uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
-    for (bool go = any; go; go = advance(walk)) {
-      const int ka = walk.ka, kb = walk.kb, len = walk.len;
-      const int end[2] = {walk.end[0], walk.end[1]};
-      for (int j = ka; j <= kb; ++j) {
-        const uint32_t nk = n + 2 * (j - ka), nv = nk - 1;         // ring positions of K_j and V_{j-1}
-        const uint32_t vs = nv % C::kRing, ks = nk % C::kRing;
-        if (j > ka) {
-          wait(&kv_full[vs], (nv / C::kRing) & 1);
-          const int cut = len - (j - 1) * kKeys;
-          if (!E4M3 && cut < kKeys) {                 // value rows past the length
-            uint8_t* t = smem + C::kRingOff + vs * C::kTile;
-            for (int r = cut; r < kKeys; ++r)
-              if (lane < HD / 8) *reinterpret_cast<uint4*>(t + (lane >> 3) * kHalf + r * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
+      // ---------------------------------------------------------------- products
+      if (elect_one()) {
+        const uint32_t id_s = idesc16(E4M3, 128, kKeys, false), id_o = idesc16(E4M3, 128, HD, true);
+        uint32_t ks = 0, ks_par = 0, vs = 0, vs_par = 0;           // ring slots of K_j and V_{j-1}, their phases
+        uint32_t q_par[2] = {0, 0}, p_par[2] = {0, 0}, clean_par = 0;
+        bool go = any;
+        while (go) {
+          const int ka = walk.ka, kb = walk.kb, end0 = walk.end[0], end1 = walk.end[1];
+          const bool short_tile = !E4M3 && kb * kKeys > walk.len;
+          for (int j = ka; j <= kb; ++j) {
+            if (j > ka) {
+              vs = ks, vs_par = ks_par;               // the tile after K_{j-1}
+              if (++vs == C::kRing) vs = 0, vs_par ^= 1;
+              ks = vs, ks_par = vs_par;
+              if (++ks == C::kRing) ks = 0, ks_par ^= 1;
+              wait(&kv_full[vs], vs_par);
+              if (short_tile && j == kb) {
+                ptx::mbar_arrive(v_short);
+                wait(v_clean, clean_par);
+                clean_par ^= 1;
+              }
+            }
+            if (j < kb) wait(&kv_full[ks], ks_par);
+            const uint64_t dv = kDescN + ((base + C::kRingOff + vs * C::kTile) >> 4);
+            const uint64_t dk = kDescK + ((base + C::kRingOff + ks * C::kTile) >> 4);
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const int end = w ? end1 : end0;
+              if (j > ka && j - 1 < end) {
+                wait(&p_full[w], p_par[w]);
+                p_par[w] ^= 1;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                  umma_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k, dv + k * (2048 >> 4), id_o, j - 1 > ka || k > 0);
+                if (j == end) ptx::umma_commit(&o_full[w]);
+              }
+              if (j < end) {
+                if (j == ka) {
+                  wait(&q_full[w], q_par[w]);
+                  q_par[w] ^= 1;
+                  ptx::tc_fence_after();
+                }
+                const uint64_t dq = kDescK + ((base + C::kQ + w * C::kTile) >> 4);
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                  const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+                  ptx::umma_bf16(tmem + 128 * w, dq + off, dk + off, id_s, k > 0);
+                }
+                ptx::umma_commit(&s_full[w]);
+                if (j + 1 == end) ptx::umma_commit(&q_empty[w]);
+              }
+            }
+            if (j > ka) ptx::umma_commit(&kv_empty[vs]);
+            if (j < kb) ptx::umma_commit(&kv_empty[ks]);
           }
+          // (ks is now the slot of the next item's first key tile)
+          go = walk.next(v);
         }
-        if (j < kb) wait(&kv_full[ks], (nk / C::kRing) & 1);
-        const uint64_t dv = kDescN + ((base + C::kRingOff + vs * C::kTile) >> 4);
-        const uint64_t dk = kDescK + ((base + C::kRingOff + ks * C::kTile) >> 4);
+      }
+      __syncwarp();
+    } else if (warp == 14) {
+      if (E4M3) bring();
+    } else if (warp == 15) {
+      // ---------------------------------------------------------------- queries
+      // TMA boxes of whole tokens (rows past the tile's last token keep what was there, rows of other sequences may come
+      // along: their results are not used)
+      uint32_t par = 0;                               // a bit for each tile
+      const uint32_t bytes = static_cast<uint32_t>(v.tile_tokens * v.G * HD * 2);
+      for (bool go = any; go; go = advance(walk)) {
+        const Walk& it = walk;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          if (j > ka && j - 1 < end[w]) {
-            wait(&p_full[w], n_p[w] & 1);
-            ++n_p[w];
-            ptx::tc_fence_after();
+          if (it.end[w] <= it.ka) continue;
+          wait(&q_empty[w], ((par >> w) & 1) ^ 1);
+          uint8_t* tile = smem + C::kQ + w * C::kTile;
+          uint64_t* full = E4M3 ? &q_raw[w] : &q_full[w];
+          if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(full, bytes);
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              umma_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k, dv + k * (2048 >> 4), id_o, j - 1 > ka || k > 0, on);
-            if (j == end[w]) umma_commit_on(&o_full[w], on);
+            for (int x = 0; x < C::kHalves; ++x)
+              tma_load_3d(tile + x * kHalf, &tmap_q, full, 64 * x, it.kvh * v.G, it.first + it.t0 + v.tile_tokens * w);
           }
-          if (j < end[w]) {
-            if (j == ka) {
-              wait(&q_full[w], n_q[w] & 1);
-              ++n_q[w];
-              ptx::tc_fence_after();
-            }
-            const uint64_t dq = kDescK + ((base + C::kQ + w * C::kTile) >> 4);
+          __syncwarp();
+          if (E4M3) {
+            // to f16, each row divided by its largest element
+            wait(full, (par >> w) & 1);
+#pragma unroll 1
+            for (int row = lane; row < 128; row += 32) {
+              auto seg = [&](int i) { return reinterpret_cast<uint4*>(tile + (i >> 3) * kHalf + row * 128 + (((i & 7) ^ (row & 7)) * 16)); };
+              float most = 0.f;
+#pragma unroll 4
+              for (int i = 0; i < HD / 8; ++i) {
+                const uint4 x = *seg(i);
+                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-              const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-              umma_ss(tmem + 128 * w, dq + off, dk + off, id_s, k > 0, on);
+                for (int k = 0; k < 4; ++k) most = fmaxf(most, fmaxf(fabsf(ptx::bf16_lo(y[k])), fabsf(ptx::bf16_hi(y[k]))));
+              }
+              if (!(most > 0.f)) most = 1.f;
+              const float inv = 1.0f / most;
+#pragma unroll 4
+              for (int i = 0; i < HD / 8; ++i) {
+                const uint4 x = *seg(i);
+                uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = pack_f16(ptx::bf16_lo(y[k]) * inv, ptx::bf16_hi(y[k]) * inv);
+                *seg(i) = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+              q_scale[(((par >> w) & 1) * 2 + w) * 128 + row] = most;
             }
-            umma_commit_on(&s_full[w], on);
-            if (j + 1 == end[w]) umma_commit_on(&q_empty[w], on);
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(&q_full[w]);
           }
+          par ^= 1u << w;
         }
-        if (j > ka) umma_commit_on(&kv_empty[vs], on);
-        if (j < kb) umma_commit_on(&kv_empty[ks], on);
-      }
-      n += 2 * (kb - ka);
-    }
-    } else {
-    // ------------------------------------------------------------------ queries
-    const int tid = threadIdx.x - 13 * 32;
-    uint32_t n_q[2] = {0, 0};
-    for (bool go = any; go; go = advance(walk)) {
-      const Walk& it = walk;
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        if (it.end[w] <= it.ka) continue;
-        wait(&q_empty[w], (n_q[w] & 1) ^ 1);
-        uint8_t* tile = smem + C::kQ + w * C::kTile;
-        const int r0 = it.r0 + 128 * w, rows = it.rows;
-        const uint16_t* src = q + (static_cast<int64_t>(it.first) * v.Hq + it.kvh * v.G) * HD;
-        if (!E4M3) {
-          constexpr int kRowSegs = HD / 8;
-          for (int i = tid; i < 128 * kRowSegs; i += kQThreads) {
-            const int row = i / kRowSegs, seg = i % kRowSegs, r = r0 + row;
-            const int tok = r < rows ? r / v.G : 0;
-            cp16(base + C::kQ + w * C::kTile + (seg >> 3) * kHalf + row * 128 + (((seg & 7) ^ (row & 7)) * 16),
-                 src + (static_cast<int64_t>(tok) * v.Hq + (r < rows ? r - tok * v.G : 0)) * HD + seg * 8, r < rows);
-          }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
-        } else {
-          for (int row = tid; row < 128; row += kQThreads) {
-            const int r = r0 + row, tok = r < rows ? r / v.G : 0;
-            const uint4* x = reinterpret_cast<const uint4*>(src + (static_cast<int64_t>(tok) * v.Hq + (r < rows ? r - tok * v.G : 0)) * HD);
-            float most = 0.f;
-#pragma unroll 8
-            for (int i = 0; i < HD / 8; ++i) {
-              const uint4 y = __ldg(x + i);
-              const uint32_t p[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) most = fmaxf(most, fmaxf(fabsf(ptx::bf16_lo(p[k])), fabsf(ptx::bf16_hi(p[k]))));
-            }
-            if (!(most > 0.f)) most = 1.f;
-            const float inv = r < rows ? 1.0f / most : 0.f;
-#pragma unroll 8
-            for (int i = 0; i < HD / 8; ++i) {
-              const uint4 y = __ldg(x + i);
-              uint32_t p[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) p[k] = r < rows ? pack_f16(ptx::bf16_lo(p[k]) * inv, ptx::bf16_hi(p[k]) * inv) : 0u;
-              *reinterpret_cast<uint4*>(tile + (i >> 3) * kHalf + row * 128 + (((i & 7) ^ (row & 7)) * 16)) = make_uint4(p[0], p[1], p[2], p[3]);
-            }
-            q_scale[((n_q[w] & 1) * 2 + w) * 128 + row] = most;
-          }
-        }
-        ++n_q[w];
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(&q_full[w]);
       }
     }
-  }
   }
   ptx::grid_dependency_wait();                        // this grid's end stands for the row kernel's too
   ptx::tc_fence_before();
@@ -715,6 +745,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
 template <int HD, bool E4M3>
 cudaError_t launch_as(const CUtensorMap& tk, const CUtensorMap& tv, const uint16_t* q, uint16_t* o, float scale_log2,
                       const KvView& kv, const SeqView& s, cudaStream_t st) {
+  CUtensorMap tq;
+  if (!make_tmap_heads_bf16(&tq, q, s.T, s.Hq, HD, s.tile_tokens, s.G)) return cudaErrorInvalidValue;
   using C = TilesCfg<HD, E4M3>;
   static cudaError_t once = cudaFuncSetAttribute(attention_tiles_kernel<HD, E4M3>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
@@ -730,7 +762,7 @@ cudaError_t launch_as(const CUtensorMap& tk, const CUtensorMap& tv, const uint16
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_tiles_kernel<HD, E4M3>, tk, tv, q, o, scale_log2, kv, s);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_tiles_kernel<HD, E4M3>, tk, tv, tq, o, scale_log2, kv, s);
   note_launch_end(kKindAttn, st);
   return e;
 }
@@ -740,6 +772,7 @@ cudaError_t launch_as(const CUtensorMap& tk, const CUtensorMap& tv, const uint16
 bool make_kv_maps(const KvView& kv, CUtensorMap* k, CUtensorMap* v) {
   const long rows = static_cast<long>(kv.n_pages) * kv.page * kv.Hkv;
   const int box = std::min(kv.page, kTileKeys);
+  if (kv.type == kKvE4m3) return make_tmap_u8(k, kv.K, rows, kv.hd, box) && make_tmap_u8(v, kv.V, rows, kv.hd, box);
   return make_tmap_bf16(k, kv.K, rows, kv.hd, box, 64) && make_tmap_bf16(v, kv.V, rows, kv.hd, box, 64);
 }
 

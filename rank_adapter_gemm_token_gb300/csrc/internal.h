@@ -111,6 +111,10 @@ void note_launch_end(int kind, cudaStream_t s);
 // Row-major bf16 matrix [rows, cols] as a TMA tensor map with a box of box_rows x box_cols and
 // the 128-byte swizzle (gemm_tc.cu). False if the encoder is unavailable or rejects it.
 bool make_tmap_bf16(CUtensorMap* map, const void* base, long rows, int cols, int box_rows, int box_cols);
+// bf16 [tokens, heads, hd] with a box of box_tokens x box_heads x 64 elements (128-byte rows, 128-byte swizzle).
+bool make_tmap_heads_bf16(CUtensorMap* map, const void* base, long tokens, int heads, int hd, int box_tokens, int box_heads);
+// Row-major byte matrix [rows, cols] with a box of box_rows whole rows (cols a multiple of 16, at most 256), not swizzled.
+bool make_tmap_u8(CUtensorMap* map, const void* base, long rows, int cols, int box_rows);
 // Row-major fp32 matrix [rows, cols] with a box of box_rows x 32 columns (128 bytes, 128-byte
 // swizzle), for tiled stores. False unless cols is a multiple of 4 and base 16-byte aligned.
 bool make_tmap_f32_sw128(CUtensorMap* map, const void* base, long rows, int cols, int box_rows);

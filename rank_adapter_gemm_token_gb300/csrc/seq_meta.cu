@@ -132,7 +132,8 @@ __device__ void plan(const SeqView& v, int page_log2) {
     const bool some = rows > 0 && L > 0, few = rows <= v.row_limit;
     const int64_t u = some && few ? (L + kRowUnit - 1) / kRowUnit : 0;
     const int64_t p = (L + (1 << page_log2) - 1) >> page_log2;
-    const int64_t b = some && !few ? (rows + kBlockRows - 1) / kBlockRows : 0;
+    const int per = 2 * v.tile_tokens;              // tokens of a block
+    const int64_t b = some && !few ? (n + per - 1) / per : 0;
     int64_t tu, te, tp, tb;
     const int64_t iu = block_scan(u, sums, &tu), ie = block_scan(u > 0, sums, &te), ip = block_scan(p, sums, &tp),
                   ib = block_scan(b, sums, &tb);
@@ -150,9 +151,8 @@ __device__ void plan(const SeqView& v, int page_log2) {
       if (nb == 0) continue;
       const int bs = s0 + warp * 32 + i, start = v.start[bs];
       for (int k = lane; k < nb; k += 32) {
-        const int64_t last = min(static_cast<int64_t>(k + 1) * kBlockRows, static_cast<int64_t>(bn) * v.G) - 1;
-        const int tiles = static_cast<int>((bl - bn + last / v.G) / kTileKeys + 1);
-        v.blk[f + k] = TileBlk{bs, bn, bl, start, k * kBlockRows, tiles};
+        const int tiles = (bl - bn + min((k + 1) * per, bn) - 1) / kTileKeys + 1;
+        v.blk[f + k] = TileBlk{bs, bn, bl, start, k * per, tiles};
       }
     }
     tokens += tn;
