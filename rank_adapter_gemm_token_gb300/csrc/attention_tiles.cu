@@ -14,7 +14,8 @@
 //                   the N-major operand. TMEM: S/P 2 x 128 columns, O 2 x hd columns. One elected thread issues them:
 //                   chosen by its lane number instead, each instruction took 120 cycles to issue, twice its execution;
 //                   with a warp for each tile, their instructions alternate and the rate falls by a third.
-//   warp 15         the next item's queries by TMA, while the last products of this one run (e4m3: and their f16 form).
+//   warps 15, 13    the next item's queries of one tile each by TMA, while the last products of this one run (e4m3: and
+//                   their f16 form).
 // e4m3: a tile's key rows become f16 as code * (scale / largest scale of the tile), rounded once (2^-12 on average, as the
 // queries are), and that largest scale multiplies the tile's scores. Its value rows become code * 2^k, exact: with
 // scale = f 2^(E + k), 1 <= f < 2 and 2^E the binary power of the tile's largest scale, f multiplies P before its rounding,
@@ -49,6 +50,7 @@ struct TilesCfg {
   static constexpr int kRing = E4M3 ? 3 : (HD == 128 ? 4 : 6);     // 16-bit key / value tiles
   static constexpr int kCodes = kKeys * HD;                        // e4m3 bytes of a tile
   static constexpr int kStages = HD == 128 ? 3 : 6;                // tiles of codes on their way
+  static constexpr int kCols = E4M3 ? 16 : 32;                     // columns of S that a softmax thread works on at a time
   static constexpr int kSegs = HD / 16;                            // 16-byte segments of a row of codes
   static constexpr int kScaleBufs = 4;
   static constexpr int kQ = 0;
@@ -101,6 +103,22 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* r) {
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
       "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { ptx::tmem_ld_32x32b_x32(taddr, r); }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st_x32(taddr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -374,7 +392,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         const bool masked = (j + 1) * kKeys - 1 > first_lim;
         const uint64_t cc = pair(ct, ct);
         const int seen = lim - j * kKeys;             // keys 0 .. seen of the tile are visible
-        constexpr int W = 32;                         // columns at a time
+        constexpr int W = C::kCols;                   // columns at a time
         auto mask = [&](uint32_t (&x)[W], int h) {    // of columns W h ...
           if (masked) {
 #pragma unroll
@@ -395,8 +413,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         if (j == it.ka) {                             // the first tile's maximum
 #pragma unroll
           for (int h = 0; h < kKeys / W; h += 2) {
-            ptx::tmem_ld_32x32b_x32(ts + W * h, xa);
-            ptx::tmem_ld_32x32b_x32(ts + W * h + W, xb);
+            tmem_ld(ts + W * h, xa);
+            tmem_ld(ts + W * h + W, xb);
             ptx::tmem_ld_wait();
             mask(xa, h);
             top = largest(xa, top);
@@ -434,14 +452,14 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               p[W / 2 * h + i / 2 + 1] = E4M3 ? pack_f16(e1.x, e1.y) : pack_bf16(e1.x, e1.y);
             }
           };
-          ptx::tmem_ld_32x32b_x32(ts, xa);
+          tmem_ld(ts, xa);
 #pragma unroll
           for (int h = 0; h < kKeys / W; h += 2) {
             ptx::tmem_ld_wait();
-            ptx::tmem_ld_32x32b_x32(ts + W * h + W, xb);
+            tmem_ld(ts + W * h + W, xb);
             weights(xa, h);
             ptx::tmem_ld_wait();
-            if (h + 2 < kKeys / W) ptx::tmem_ld_32x32b_x32(ts + W * h + 2 * W, xa);
+            if (h + 2 < kKeys / W) tmem_ld(ts + W * h + 2 * W, xa);
             weights(xb, h + 1);
           }
           top = fmaf(top, ct, off);
@@ -452,11 +470,11 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           l *= f;
 #pragma unroll 1
           for (int i = 0; i < HD / W; ++i) {
-            ptx::tmem_ld_32x32b_x32(to + W * i, xb);
+            tmem_ld(to + W * i, xb);
             ptx::tmem_ld_wait();
 #pragma unroll
             for (int k = 0; k < W; ++k) xb[k] = __float_as_uint(__uint_as_float(xb[k]) * f);
-            tmem_st_x32(to + W * i, xb);
+            tmem_st(to + W * i, xb);
           }
         }
         const float2 total = unpair(add_pair(sum, sum1));
@@ -546,21 +564,28 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                                                       // other order: different banks
       __half2* factors = reinterpret_cast<__half2*>(smem + C::kFactorOff);           // keys' rows, values' rows
       float* maxima = reinterpret_cast<float*>(smem + C::kFactorOff + 2 * kKeys * 4);
+      uint4 cd[kCopies];                              // the tile's codes, read while the tile before it is finished
+      auto fetch = [&](uint32_t tile) {
+        const int cs = tile % C::kStages;
+        wait(&raw_full[cs], (tile / C::kStages) & 1);
+        const uint8_t* src = smem + C::kCodeOff + tid * 16 + cs * C::kCodes;
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) cd[i] = *reinterpret_cast<const uint4*>(src + i * 2048);
+      };
+      if (any) fetch(0);
       uint32_t n = 0;
       for (bool go = any; go; go = advance(walk)) {
         const Walk& it = walk;
+        const bool last_item = it.left <= it.kb - it.ka + (it.ka == 0 ? kTileHead : 0);
         for (int j = it.ka; j < it.kb; ++j) {
           const int cut = it.len - j * kKeys;         // rows of the tile inside the sequence (any number)
 #pragma unroll 1
           for (int h = 0; h < 2; ++h, ++n) {
             const int st = n % C::kRing, cs = n % C::kStages;
-            wait(&raw_full[cs], (n / C::kStages) & 1);
-            const uint8_t* src = smem + C::kCodeOff + tid * 16 + cs * C::kCodes;
-            uint4 cd[kCopies];
+            if (cut < kKeys) {
 #pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-              cd[i] = *reinterpret_cast<const uint4*>(src + i * 2048);
-              if (i * kStep + r_in >= cut) cd[i] = make_uint4(0u, 0u, 0u, 0u);
+              for (int i = 0; i < kCopies; ++i)
+                if (i * kStep + r_in >= cut) cd[i] = make_uint4(0u, 0u, 0u, 0u);
             }
             if (h == 0) {
               // the tile's largest scales, and every row's share of them
@@ -606,6 +631,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               *reinterpret_cast<uint4*>(dst + r * 128 + (((even + (odd ? 1 : 0)) ^ (r & 7)) * 16)) = odd ? hi : lo;
               *reinterpret_cast<uint4*>(dst + r * 128 + (((even + (odd ? 0 : 1)) ^ (r & 7)) * 16)) = odd ? lo : hi;
             }
+            if (!(last_item && h == 1 && j + 1 == it.kb)) fetch(n + 1);
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(&kv_full[st]);
           }
@@ -678,58 +704,60 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       __syncwarp();
     } else if (warp == 14) {
       if (E4M3) bring();
-    } else if (warp == 15) {
+    } else {
       // ---------------------------------------------------------------- queries
       // TMA boxes of whole tokens (rows past the tile's last token keep what was there, rows of other sequences may come
       // along: their results are not used)
-      uint32_t par = 0;                               // a bit for each tile
+      const int w = warp == 13;
+      uint32_t par = 0;
       const uint32_t bytes = static_cast<uint32_t>(v.tile_tokens * v.G * HD * 2);
+      uint8_t* tile = smem + C::kQ + w * C::kTile;
+      uint64_t* full = E4M3 ? &q_raw[w] : &q_full[w];
       for (bool go = any; go; go = advance(walk)) {
         const Walk& it = walk;
+        if (it.end[w] <= it.ka) continue;
+        wait(&q_empty[w], par ^ 1);
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(full, bytes);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (it.end[w] <= it.ka) continue;
-          wait(&q_empty[w], ((par >> w) & 1) ^ 1);
-          uint8_t* tile = smem + C::kQ + w * C::kTile;
-          uint64_t* full = E4M3 ? &q_raw[w] : &q_full[w];
-          if (lane == 0) {
-            ptx::mbar_arrive_expect_tx(full, bytes);
-#pragma unroll
-            for (int x = 0; x < C::kHalves; ++x)
-              tma_load_3d(tile + x * kHalf, &tmap_q, full, 64 * x, it.kvh * v.G, it.first + it.t0 + v.tile_tokens * w);
-          }
-          __syncwarp();
-          if (E4M3) {
-            // to f16, each row divided by its largest element
-            wait(full, (par >> w) & 1);
-#pragma unroll 1
-            for (int row = lane; row < 128; row += 32) {
-              auto seg = [&](int i) { return reinterpret_cast<uint4*>(tile + (i >> 3) * kHalf + row * 128 + (((i & 7) ^ (row & 7)) * 16)); };
-              float most = 0.f;
-#pragma unroll 4
-              for (int i = 0; i < HD / 8; ++i) {
-                const uint4 x = *seg(i);
-                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) most = fmaxf(most, fmaxf(fabsf(ptx::bf16_lo(y[k])), fabsf(ptx::bf16_hi(y[k]))));
-              }
-              if (!(most > 0.f)) most = 1.f;
-              const float inv = 1.0f / most;
-#pragma unroll 4
-              for (int i = 0; i < HD / 8; ++i) {
-                const uint4 x = *seg(i);
-                uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = pack_f16(ptx::bf16_lo(y[k]) * inv, ptx::bf16_hi(y[k]) * inv);
-                *seg(i) = make_uint4(y[0], y[1], y[2], y[3]);
-              }
-              q_scale[(((par >> w) & 1) * 2 + w) * 128 + row] = most;
-            }
-            ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(&q_full[w]);
-          }
-          par ^= 1u << w;
+          for (int x = 0; x < C::kHalves; ++x)
+            tma_load_3d(tile + x * kHalf, &tmap_q, full, 64 * x, it.kvh * v.G, it.first + it.t0 + v.tile_tokens * w);
         }
+        __syncwarp();
+        if (E4M3) {
+          // to f16, each row divided by its largest element: two lanes to a row
+          constexpr int kN = HD / 16;                 // a lane's 16-byte segments
+          wait(full, par);
+#pragma unroll 1
+          for (int r0 = 0; r0 < 128; r0 += 16) {
+            const int row = r0 + (lane >> 1), side = lane & 1;
+            uint4 x[kN];
+            float most = 0.f;
+            auto seg = [&](int i) { return reinterpret_cast<uint4*>(tile + ((i + side * kN) >> 3) * kHalf + row * 128 + ((((i + side * kN) & 7) ^ (row & 7)) * 16)); };
+#pragma unroll
+            for (int i = 0; i < kN; ++i) x[i] = *seg(i);
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+              const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) most = fmaxf(most, fmaxf(fabsf(ptx::bf16_lo(y[k])), fabsf(ptx::bf16_hi(y[k]))));
+            }
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            if (!(most > 0.f)) most = 1.f;
+            const float inv = 1.0f / most;
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+              uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) y[k] = pack_f16(ptx::bf16_lo(y[k]) * inv, ptx::bf16_hi(y[k]) * inv);
+              *seg(i) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+            if (side == 0) q_scale[(par * 2 + w) * 128 + row] = most;
+          }
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive(&q_full[w]);
+        }
+        par ^= 1;
       }
     }
   }
