@@ -391,7 +391,7 @@ MLORA_API mlora_status mlora_seq_destroy(mlora_seq_t seq);
  * A sequence with descending or outlying bounds, more than max_new new tokens, fewer cached than new tokens,
  * a length above max_pages pages or a page outside the cache is skipped like padding and reported by
  * mlora_seq_status as MLORA_ERR_BAD_SEQUENCE with the first one's number. Caches used with the step have this
- * one's sizes (MLORA_ERR_MISMATCH otherwise); their element types may differ.
+ * one's sizes and element type (MLORA_ERR_MISMATCH otherwise).
  * Calls that share a seq must be ordered on one stream. */
 MLORA_API mlora_status mlora_build_seq(mlora_seq_t seq, const int32_t* q_start, const int32_t* kv_len,
                                        const int32_t* pages, int pages_ld, int n_seqs, int T, int max_new,

@@ -39,7 +39,7 @@ struct alignas(32) TileBlk {
 struct TileShare {
   int32_t blk, kvh, tile, units;
 };
-// An item (list entry, head) that lies across cuts: CTAs cta ... cta + parts - 1 each hold a part (parts = 0: none).
+// An item (list entry, head) that lies across cuts: CTAs cta ... cta + parts - 1 each hold a part.
 struct JoinTask {
   int32_t item, kvh, cta, parts;
 };
@@ -60,9 +60,9 @@ struct SeqView {
   int64_t* blk_pre;     // [blocks + 1] units (kTileHead and the key tiles, for each kv head) before each of them
   RowShare* row_share;  // [row_ctas]
   TileShare* tile_share;// [tile_ctas]
-  JoinTask* row_join;   // [row_ctas] the item that CTA i + 1 is the first to continue, if any
-  JoinTask* tile_join;  // [tile_ctas]
-  int32_t* counts;      // [1] first rejected sequence (INT32_MAX if none)
+  JoinTask* row_join;   // [counts[2]] the row kernel's split items
+  JoinTask* tile_join;  // [counts[3]] the tile kernel's
+  int32_t* counts;      // [1] first rejected sequence (INT32_MAX if none), [2], [3] split items
   uint32_t* err;        // device error word (ptx::kErr* bits)
   float* row_part;      // partial results of the row kernel's split items
   float* tile_part;     // of the tile kernel's
@@ -77,6 +77,9 @@ constexpr int kRowUnit = 64;
 constexpr int kTileKeys = 128;
 constexpr int kTileSnap = 2;          // key tiles that a split costs at least
 constexpr int kTileHead = 3;          // key tiles that an item's fixed costs (queries, first products, output) are worth
+
+// CTAs of the row kernel on an SM: by the row limit (16 rather than 8) and the cache's type.
+__host__ __device__ constexpr int rows_ctas_per_sm(bool sixteen, bool e4m3) { return e4m3 && !sixteen ? 3 : 2; }
 
 // Per-pair rotation frequencies in turns per position, each as a sum of two floats.
 struct RopeView {

@@ -1,10 +1,11 @@
 // Joins the parts of attention items that were split among CTAs: with part k's maximum m_k (base 2), weights' sum l_k
 // and weighted value sums x_k,
 //     o = sum_k 2^(m_k - m) x_k / sum_k 2^(m_k - m) l_k,   m = max_k m_k,
-// in the order of the keys, so the result does not depend on which CTA was first. A CTA for each cut that may be the
-// first inside an item (most leave at once): a row item whole, a tile item in slices of 32 rows. Launched as a
-// programmatic dependent: it reads its task while the attention still runs. Bound by the latency of two dependent
-// reads of the L2, where the parts still are.
+// in an order that the split alone fixes, so the result does not depend on which CTA was first. The plan lists the split
+// items; a unit of work is a row item whole, or 8 rows of a tile item, so that a few items with many parts (a chunk on a
+// long context) still spread over the SMs. Launched as a programmatic dependent: it reads its first task while the
+// attention still runs. Bound by the latency of the parts' reads (from L2): eight parts are asked for at once, and where a
+// row item has fewer elements than the CTA threads, its parts are divided among groups of threads.
 #include "attention.h"
 #include "attention.cuh"
 #include "internal.h"
@@ -13,8 +14,10 @@
 namespace mlora {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kSlices = 8;            // of a block
+constexpr int kThreads = 256;
+constexpr int kRows = 8;              // rows of a unit of a tile item
+constexpr int kSlices = 256 / kRows;  // units of a block
+constexpr int kAhead = 8;             // parts asked for at once
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -25,109 +28,117 @@ __device__ __forceinline__ float inverse(float total) {
   return total > 0.f ? 1.0f / total : total == 0.f ? 0.f : total;      // an empty row is zero; NaN stays
 }
 
+// Running maximum, sum of weights and four weighted value sums.
+struct Sums {
+  float top, total;
+  float4 x;
+  __device__ __forceinline__ void add(float m, float l, const float4& y) {
+    if (m == -INFINITY) return;       // (a part that saw none of the row's keys has no sums)
+    const float up = fmaxf(top, m);
+    const float f = exp2_approx(top - up), g = exp2_approx(m - up);
+    top = up;
+    total = total * f + l * g;
+    x.x = x.x * f + y.x * g;
+    x.y = x.y * f + y.y * g;
+    x.z = x.z * f + y.z * g;
+    x.w = x.w * f + y.w * g;
+  }
+};
+
 template <int HD>
 __global__ void __launch_bounds__(kThreads)
 attention_join_kernel(uint16_t* __restrict__ o, SeqView v) {
-  const bool row = static_cast<int>(blockIdx.x) < v.row_ctas;
-  const int idx = static_cast<int>(blockIdx.x) - (row ? 0 : v.row_ctas);
-  const int4 task = *reinterpret_cast<const int4*>(row ? v.row_join + idx : v.tile_join + idx / kSlices);
-  const int kvh = task.y, cta = task.z, parts = task.w;
-  if (parts == 0) {                     // (the grid's end stands for the end of the attention: every CTA waits for it)
-    ptx::grid_dependency_wait();
-    return;
-  }
-  if (row) {
-    const int4 sq = *reinterpret_cast<const int4*>(v.row_seq + task.x);
-    const int rows = sq.y * v.G;
-    const int64_t slot = row_slot(v);
-    const float* first = v.row_part + (2 * static_cast<int64_t>(cta) + 1) * slot;           // part 0; part k: CTA cta + k
-    auto part = [&](int k) { return k == 0 ? first : v.row_part + 2 * static_cast<int64_t>(cta + k) * slot; };
-    ptx::grid_dependency_wait();
-    for (int i = threadIdx.x; i < rows * (HD / 4); i += kThreads) {
-      const int r = i / (HD / 4), h = i % (HD / 4) * 4;
-      float top = -INFINITY, total = 0.f;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      constexpr int kAhead = 8;
-      for (int k0 = 0; k0 < parts; k0 += kAhead) {
-        float2 ml[kAhead];
-        float4 y[kAhead];
+  constexpr int kQuads = HD / 4;       // groups of four columns
+  __shared__ float4 sx[kThreads];
+  __shared__ float2 sm[kThreads];
+  const int row_units = v.counts[2], units = row_units + v.counts[3] * kSlices;
+  bool waited = false;
+  auto wait = [&]() {
+    if (!waited) ptx::grid_dependency_wait();
+    waited = true;
+  };
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    if (u < row_units) {
+      const int4 task = *reinterpret_cast<const int4*>(v.row_join + u);
+      const int4 sq = *reinterpret_cast<const int4*>(v.row_seq + task.x);
+      const int kvh = task.y, parts = task.w, elements = sq.y * v.G * kQuads;
+      const int64_t slot = row_slot(v);
+      const float* base = v.row_part + 2 * static_cast<int64_t>(task.z) * slot;      // part k > 0: base + 2 k slot
+      wait();
+      // threads beyond the elements take a share of the parts
+      const int groups = max(1, kThreads / elements);
+      for (int i0 = 0; i0 < elements; i0 += kThreads) {
+        const int e = groups > 1 ? static_cast<int>(threadIdx.x) % elements : i0 + static_cast<int>(threadIdx.x);
+        const int g = groups > 1 ? static_cast<int>(threadIdx.x) / elements : 0;
+        const bool mine = e < elements && g < groups;
+        const int r = mine ? e / kQuads : 0, h = e % kQuads * 4;
+        Sums z{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (mine) {
+          for (int k0 = g; k0 < parts; k0 += kAhead * groups) {
+            float2 ml[kAhead];
+            float4 y[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const float* p = part(min(k0 + k, parts - 1));
-          ml[k] = __ldcg(reinterpret_cast<const float2*>(p + v.row_limit * HD + 2 * r));
-          y[k] = __ldcg(reinterpret_cast<const float4*>(p + r * HD + h));
+            for (int k = 0; k < kAhead; ++k) {
+              const int part = min(k0 + k * groups, parts - 1);
+              const float* p = base + (part == 0 ? slot : 2 * part * slot);
+              ml[k] = __ldcg(reinterpret_cast<const float2*>(p + v.row_limit * HD + 2 * r));
+              y[k] = __ldcg(reinterpret_cast<const float4*>(p + r * HD + h));
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+              if (k0 + k * groups < parts) z.add(ml[k].x, ml[k].y, y[k]);
+          }
         }
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          if (k0 + k >= parts || ml[k].x == -INFINITY) continue;
-          const float up = fmaxf(top, ml[k].x);
-          const float f = exp2_approx(top - up), g = exp2_approx(ml[k].x - up);
-          top = up;
-          total = total * f + ml[k].y * g;
-          x.x = x.x * f + y[k].x * g;
-          x.y = x.y * f + y[k].y * g;
-          x.z = x.z * f + y[k].z * g;
-          x.w = x.w * f + y[k].w * g;
+        if (groups > 1) {
+          sm[threadIdx.x] = make_float2(z.top, z.total);
+          sx[threadIdx.x] = z.x;
+          __syncthreads();
+          if (mine && g == 0)
+            for (int k = 1; k < groups; ++k) {
+              const float2 ml = sm[threadIdx.x + k * elements];
+              z.add(ml.x, ml.y, sx[threadIdx.x + k * elements]);
+            }
+          __syncthreads();
+        }
+        if (mine && g == 0) {
+          const float inv = inverse(z.total);
+          *reinterpret_cast<uint2*>(o + (static_cast<int64_t>(sq.w + r / v.G) * v.Hq + kvh * v.G + r % v.G) * HD + h) =
+              make_uint2(pack_bf16(z.x.x * inv, z.x.y * inv), pack_bf16(z.x.z * inv, z.x.w * inv));
         }
       }
-      const float inv = inverse(total);
-      *reinterpret_cast<uint2*>(o + (static_cast<int64_t>(sq.w + r / v.G) * v.Hq + kvh * v.G + r % v.G) * HD + h) =
-          make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+      continue;
     }
-    return;
+    const int unit = u - row_units, slice = unit % kSlices, w = slice / (kSlices / 2);
+    const int4 task = *reinterpret_cast<const int4*>(v.tile_join + unit / kSlices);
+    const TileBlk b = v.blk[task.x];
+    const int kvh = task.y, parts = task.w;
+    const int r = slice % (kSlices / 2) * kRows + static_cast<int>(threadIdx.x) % kRows, quad = static_cast<int>(threadIdx.x) / kRows;
+    const int tok = b.t0 + v.tile_tokens * w + r / v.G;
+    if (quad >= kQuads || r >= v.tile_tokens * v.G || tok >= b.n) continue;
+    const int64_t slot = tile_slot(v);
+    const float* base = v.tile_part + (4 * static_cast<int64_t>(task.z) + w) * slot;    // part k > 0: base + 4 k slot
+    wait();
+    Sums z{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int k0 = 0; k0 < parts; k0 += kAhead) {
+      float m[kAhead], l[kAhead];
+      float4 y[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int part = min(k0 + k, parts - 1);
+        const float* p = base + (part == 0 ? 2 * slot : 4 * part * slot);
+        m[k] = __ldcg(p + 128 * HD + r);
+        l[k] = __ldcg(p + 128 * HD + 128 + r);
+        y[k] = __ldcg(reinterpret_cast<const float4*>(p) + quad * 128 + r);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (k0 + k < parts) z.add(m[k], l[k], y[k]);
+    }
+    const float inv = inverse(z.total);
+    *reinterpret_cast<uint2*>(o + (static_cast<int64_t>(b.start + tok) * v.Hq + kvh * v.G + r % v.G) * HD + 4 * quad) =
+        make_uint2(pack_bf16(z.x.x * inv, z.x.y * inv), pack_bf16(z.x.z * inv, z.x.w * inv));
   }
-  const TileBlk b = v.blk[task.x];
-  const int slice = idx % kSlices, w = slice / 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tr = (slice & 3) * 32 + lane, tok = b.t0 + v.tile_tokens * w + tr / v.G;
-  const bool valid = tr < v.tile_tokens * v.G && tok < b.n;
-  const int64_t slot = tile_slot(v);
-  auto part = [&](int k) { return v.tile_part + ((2 * static_cast<int64_t>(cta + k) + (k == 0)) * 2 + w) * slot; };
-  ptx::grid_dependency_wait();
-  if (!__any_sync(0xffffffffu, valid)) return;
-  float top = -INFINITY, total = 0.f;
-  for (int k0 = 0; k0 < parts; k0 += 4) {
-    float m[4], l[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float* p = part(min(k0 + k, parts - 1)) + 128 * HD + tr;
-      m[k] = __ldcg(p);
-      l[k] = __ldcg(p + 128);
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (k0 + k >= parts || m[k] == -INFINITY) continue;
-      const float up = fmaxf(top, m[k]);
-      total = total * exp2_approx(top - up) + l[k] * exp2_approx(m[k] - up);
-      top = up;
-    }
-  }
-  const float inv = inverse(total);
-  constexpr int kCols = HD / 16;                       // four-column groups of a warp: groups warp, warp + 4, ...
-  float4 x[kCols];
-#pragma unroll
-  for (int c = 0; c < kCols; ++c) x[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int k = 0; k < parts; ++k) {
-    const float* p = part(k);
-    const float m = __ldcg(p + 128 * HD + tr);
-    float4 y[kCols];
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) y[c] = __ldcg(reinterpret_cast<const float4*>(p) + (warp + 4 * c) * 128 + tr);
-    if (m == -INFINITY) continue;                      // (a part that saw none of the row's keys has no sums)
-    const float f = exp2_approx(m - top) * inv;
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) {
-      x[c].x = fmaf(f, y[c].x, x[c].x);
-      x[c].y = fmaf(f, y[c].y, x[c].y);
-      x[c].z = fmaf(f, y[c].z, x[c].z);
-      x[c].w = fmaf(f, y[c].w, x[c].w);
-    }
-  }
-  if (!valid) return;
-  uint16_t* dst = o + (static_cast<int64_t>(b.start + tok) * v.Hq + kvh * v.G + tr % v.G) * HD;
-#pragma unroll
-  for (int c = 0; c < kCols; ++c)
-    *reinterpret_cast<uint2*>(dst + 4 * (warp + 4 * c)) = make_uint2(pack_bf16(x[c].x, x[c].y), pack_bf16(x[c].z, x[c].w));
+  wait();                              // the grid's end stands for the end of the attention
 }
 
 }  // namespace
@@ -135,7 +146,7 @@ attention_join_kernel(uint16_t* __restrict__ o, SeqView v) {
 cudaError_t launch_attention_join(uint16_t* o, const SeqView& s, bool tiles, cudaStream_t st) {
   note_launch_begin(kKindAttn, st);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(s.row_ctas + (tiles ? s.tile_ctas * kSlices : 0));
+  cfg.gridDim = dim3((tiles ? 4 : 2) * s.tile_ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr{};

@@ -35,7 +35,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 16;                  // keys of a warp's chunk
-constexpr int kRingBytes = 96 * 1024;       // of the CTA's stages: two CTAs per SM
 constexpr float kLazy = 8.0f;               // log2 of the largest P
 
 template <int HD, int NQ, bool E4M3>
@@ -45,7 +44,10 @@ struct RowsCfg {
   static constexpr int kTile = kChunk * kRowBytes;
   static constexpr int kScales = E4M3 ? 2 * kChunk * 4 : 0;        // key and value scales of a chunk
   static constexpr int kStage = 2 * kTile + kScales;
-  static constexpr int kRing = NQ == 1 ? kRingBytes : kRingBytes / 3 * 2;
+  // CTAs of an SM, and bytes of a CTA's stages: e4m3 chunks are half as long and take more instructions, so they get
+  // more warps.
+  static constexpr int kCtas = rows_ctas_per_sm(NQ == 2, E4M3);
+  static constexpr int kRing = kCtas == 3 ? 54 * 1024 : NQ == 1 ? 96 * 1024 : 64 * 1024;
   static constexpr int kStages = kRing / (kWarps * kStage) > 8 ? 8 : kRing / (kWarps * kStage);
   static constexpr int kRows = 8 * NQ;
   static constexpr int kLd = HD + 4;                               // floats of a row of the joined sums
@@ -133,7 +135,7 @@ struct Place {
 };
 
 template <int HD, int NQ, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, RowsCfg<HD, NQ, E4M3>::kCtas)
 attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, float scale_log2, KvView kv, SeqView v) {
   using C = RowsCfg<HD, NQ, E4M3>;
   constexpr int kSteps = HD / 16;             // k-steps of S^T, M tiles of O^T

@@ -69,7 +69,7 @@ struct mlora_seq {
   int64_t max_blocks = 0;
   void* mem = nullptr;
   bool built = false;
-  int page = 0, n_pages = 0;          // of the cache that the last build checked its tables against
+  int page = 0, n_pages = 0, type = 0;   // of the cache that the last build checked its tables against
   bool tiles = false;                 // the last build may hold sequences above the row limit
   cudaEvent_t done = nullptr;
   cudaStream_t last_stream = nullptr;
@@ -265,7 +265,7 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
   v.G = n_q_heads / n_kv_heads;
   v.tile_tokens = 128 / v.G;
   v.hd = head_dim;
-  v.row_ctas = 2 * sms;
+  v.row_ctas = 3 * sms;               // at most (mlora_build_seq)
   v.tile_ctas = sms;
   const size_t S = max_seqs, T = max_tokens;
   q->max_blocks = static_cast<int64_t>(T) / (2 * v.tile_tokens) + static_cast<int64_t>(S);
@@ -351,9 +351,11 @@ mlora_status mlora_build_seq(mlora_seq_t q, const int32_t* q_start, const int32_
   // or a single token has more than 8.
   const int64_t most = static_cast<int64_t>(max_new) * v.G;
   v.row_limit = most <= 8 ? 8 : most <= 16 || v.G > 8 ? 16 : 8;
+  v.row_ctas = rows_ctas_per_sm(v.row_limit > 8, w.type == kKvE4m3) * q->num_sms;
   q->tiles = most > v.row_limit;
   q->page = w.page;
   q->n_pages = w.n_pages;
+  q->type = w.type;
   const cudaError_t e = launch_build_seq(q_start, kv_len, pages, pages_ld, v, max_new, w, s);
   if (e != cudaSuccess) return report_cuda_error(e, "build_seq launch");
   q->last_stream = s;
@@ -388,6 +390,7 @@ static mlora_status check_step(mlora_kv_t kv, mlora_seq_t q) {
     return fail(MLORA_ERR_MISMATCH, "the cache has %d heads of %d, the sequences' object %d of %d", w.Hkv, w.hd, q->view.Hkv, q->view.hd);
   if (w.page != q->page || w.n_pages != q->n_pages)
     return fail(MLORA_ERR_MISMATCH, "the sequences were built on a cache of %d pages of %d, this one has %d of %d", q->n_pages, q->page, w.n_pages, w.page);
+  if (w.type != q->type) return fail(MLORA_ERR_MISMATCH, "the sequences were built on a cache of another element type");
   return MLORA_OK;
 }
 

@@ -21,6 +21,7 @@ namespace {
 constexpr int kCheckThreads = 256;
 constexpr int kPlanThreads = 1024;
 constexpr int kMapSeqs = 8192;      // MLORA_MAX_SEQS: token starts kept in shared memory by the token map
+constexpr int kPlanPre = kMapSeqs / 2;   // prefix sums kept there by the plan
 
 __global__ void __launch_bounds__(kCheckThreads)
 check_seq_kernel(const int32_t* __restrict__ q_start, const int32_t* __restrict__ kv_len,
@@ -52,26 +53,33 @@ check_seq_kernel(const int32_t* __restrict__ q_start, const int32_t* __restrict_
   }
 }
 
-// Inclusive scan over the block's kPlanThreads threads; *total gets the sum.
-__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* warp_sums, int64_t* total) {
+// Inclusive scans of N values over the block's kPlanThreads threads, in place; total gets the sums.
+template <int N>
+__device__ __forceinline__ void block_scan(int64_t (&x)[N], int64_t (*warp_sums)[32], int64_t (&total)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  int64_t w = warp_sums[lane];
+  for (int i = 0; i < N; ++i) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, w, d);
-    if (lane >= d) w += y;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x[i], d);
+      if (lane >= d) x[i] += y;
+    }
+    if (lane == 31) warp_sums[i][warp] = x[i];
   }
-  *total = __shfl_sync(0xffffffffu, w, 31);
-  const int64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
-  return x + (warp > 0 ? before : 0);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    int64_t w = warp_sums[i][lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, w, d);
+      if (lane >= d) w += y;
+    }
+    total[i] = __shfl_sync(0xffffffffu, w, 31);
+    const int64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    if (warp > 0) x[i] += before;
+  }
+  __syncthreads();
 }
 
 // The last i in [0, n) with pre[i] <= x, by one thread.
@@ -111,111 +119,126 @@ __device__ Cut cut_at(const Shares& sh, const int64_t* pre, int n, int Hkv, int6
   return r;
 }
 
-__device__ void plan(const SeqView& v, int page_log2) {
-  __shared__ int64_t sums[32];
-  __shared__ int64_t row_total, tile_total;
+// The shares and joins of one list of n entries; cuts: a place for kPlanThreads + 1 cuts' positions.
+template <bool TILES>
+__device__ __forceinline__ void share_out(const SeqView& v, const int64_t* pre, int n, const Shares& sh, int ctas, int64_t* cuts,
+                                          int* joins) {
+  const int c = threadIdx.x;
+  Cut cut{n, 0, 0, sh.total, JoinTask{0, 0, 0, 0}};
+  if (c <= sh.n && sh.total > 0) cut = cut_at(sh, pre, n, v.Hkv, c);
+  cuts[c] = cut.at;
+  __syncthreads();
+  if (c < ctas) {
+    const int units = c < sh.n && sh.total > 0 ? static_cast<int>(cuts[c + 1] - cut.at) : 0;
+    if (TILES)
+      v.tile_share[c] = TileShare{cut.item, cut.kvh, max(cut.unit - kTileHead, 0), units};
+    else
+      v.row_share[c] = RowShare{cut.item, cut.kvh, cut.unit, units};
+  }
+  if (cut.join.parts > 0) (TILES ? v.tile_join : v.row_join)[atomicAdd(joins, 1)] = cut.join;
+  __syncthreads();
+}
+
+__device__ void plan(const SeqView& v, int page_log2, int64_t* pre) {
+  __shared__ int64_t sums[5][32];
+  __shared__ int64_t cuts[kPlanThreads];
+  __shared__ int joins[2];                        // split items so far (their order in the lists does not matter)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t tokens = 0, units = 0, entries = 0, cached = 0, blocks = 0;      // totals of the sequences before this chunk
   for (int s0 = 0; s0 < v.S; s0 += kPlanThreads) {
     const int s = s0 + threadIdx.x;
-    int n = s < v.S ? v.n[s] : 0;
-    const int L = s < v.S ? v.len[s] : 0;
+    const int n = s < v.S ? v.n[s] : 0, L = s < v.S ? v.len[s] : 0, start = s < v.S ? v.start[s] : 0;
+    const int64_t rows = static_cast<int64_t>(n) * v.G;
+    const bool some = rows > 0 && L > 0, few = rows <= v.row_limit;
+    const int per = 2 * v.tile_tokens;              // tokens of a block
+    const int64_t u = some && few ? (L + kRowUnit - 1) / kRowUnit : 0;
+    const int64_t b = some && !few ? (n + per - 1) / per : 0;
+    int64_t x[5] = {n, u, u > 0, (static_cast<int64_t>(L) + (1 << page_log2) - 1) >> page_log2, b}, t[5];
+    block_scan(x, sums, t);
     // starts that do not ascend could name more tokens than there are: the lists hold T
-    int64_t tn;
-    const int64_t in = block_scan(n, sums, &tn);
-    if (tokens + in > v.T) {
-      n = 0;
+    const bool over = tokens + x[0] > v.T;
+    if (over && n > 0) {
       atomicOr(v.err, ptx::kErrBadSeq);
       atomicMin(&v.counts[1], s);
     }
-    const int64_t rows = static_cast<int64_t>(n) * v.G;
-    const bool some = rows > 0 && L > 0, few = rows <= v.row_limit;
-    const int64_t u = some && few ? (L + kRowUnit - 1) / kRowUnit : 0;
-    const int64_t p = (L + (1 << page_log2) - 1) >> page_log2;
-    const int per = 2 * v.tile_tokens;              // tokens of a block
-    const int64_t b = some && !few ? (n + per - 1) / per : 0;
-    int64_t tu, te, tp, tb;
-    const int64_t iu = block_scan(u, sums, &tu), ie = block_scan(u > 0, sums, &te), ip = block_scan(p, sums, &tp),
-                  ib = block_scan(b, sums, &tb);
-    if (s < v.S) v.page_pre[s + 1] = static_cast<int32_t>(cached + ip);
+    if (s < v.S) v.page_pre[s + 1] = static_cast<int32_t>(cached + x[3]);
     if (u > 0) {
-      v.row_seq[entries + ie - 1] = RowSeq{s, n, L, v.start[s]};
-      v.row_pre[entries + ie] = (units + iu) * v.Hkv;
+      const int64_t e = entries + x[2];
+      v.row_seq[e - 1] = RowSeq{s, over ? 0 : n, L, start};
+      v.row_pre[e] = (units + x[1]) * v.Hkv;
     }
     // the chunk's tile blocks, a warp for each sequence
-    const int64_t first = blocks + ib - b;
-    for (int i = 0; i < 32; ++i) {
-      const int nb = static_cast<int>(__shfl_sync(0xffffffffu, b, i));
+    const int64_t first = blocks + x[4] - b;
+    uint32_t has = __ballot_sync(0xffffffffu, b > 0);
+    while (has) {
+      const int i = __ffs(has) - 1;
+      has &= has - 1;
+      const int nb = static_cast<int>(__shfl_sync(0xffffffffu, b, i)), bn = __shfl_sync(0xffffffffu, n, i),
+                bl = __shfl_sync(0xffffffffu, L, i), bstart = __shfl_sync(0xffffffffu, start, i);
       const int64_t f = __shfl_sync(0xffffffffu, first, i);
-      const int bn = __shfl_sync(0xffffffffu, n, i), bl = __shfl_sync(0xffffffffu, L, i);
-      if (nb == 0) continue;
-      const int bs = s0 + warp * 32 + i, start = v.start[bs];
+      if (__shfl_sync(0xffffffffu, static_cast<int>(over), i)) continue;
       for (int k = lane; k < nb; k += 32) {
         const int tiles = (bl - bn + min((k + 1) * per, bn) - 1) / kTileKeys + 1;
-        v.blk[f + k] = TileBlk{bs, bn, bl, start, k * per, tiles};
+        v.blk[f + k] = TileBlk{s0 + warp * 32 + i, bn, bl, bstart, k * per, tiles};
       }
     }
-    tokens += tn;
-    units += tu;
-    entries += te;
-    cached += tp;
-    blocks += tb;
+    tokens += t[0];
+    units += t[1];
+    entries += t[2];
+    cached += t[3];
+    blocks += t[4];
+    if (tokens > v.T) {                 // the rejected sequences' blocks are not there: the tile kernel leaves them all out
+      blocks = 0;
+      break;
+    }
   }
   if (threadIdx.x == 0) {
     v.row_pre[0] = 0;
     v.page_pre[0] = 0;
     v.blk_pre[0] = 0;
+    joins[0] = joins[1] = 0;
   }
   __syncthreads();
+  // The prefix sums once more in shared memory, where they fit: the cuts are searched in them.
+  const bool small_rows = entries < kPlanPre;
+  if (small_rows)
+    for (int64_t i = threadIdx.x; i <= entries; i += kPlanThreads) pre[i] = v.row_pre[i];
+  __syncthreads();
+  const int64_t row_total = units * v.Hkv;
+  share_out<false>(v, small_rows ? pre : v.row_pre, static_cast<int>(entries),
+                   Shares{row_total, static_cast<int>(min(static_cast<int64_t>(v.row_ctas), row_total)), 0, 0}, v.row_ctas, cuts,
+                   &joins[0]);
   int64_t tiles = 0;
+  const bool small_tiles = blocks < kPlanPre;
   for (int64_t j0 = 0; j0 < blocks; j0 += kPlanThreads) {
     const int64_t j = j0 + threadIdx.x;
-    int64_t total;
-    const int64_t inc = block_scan(j < blocks ? kTileHead + v.blk[j].tiles : 0, sums, &total);
-    if (j < blocks) v.blk_pre[j + 1] = (tiles + inc) * v.Hkv;
-    tiles += total;
+    int64_t x[1] = {j < blocks ? kTileHead + v.blk[j].tiles : 0}, t[1];
+    block_scan(x, sums, t);
+    if (j < blocks) {
+      const int64_t p = (tiles + x[0]) * v.Hkv;
+      v.blk_pre[j + 1] = p;
+      if (small_tiles) pre[j + 1] = p;
+    }
+    tiles += t[0];
   }
-  if (threadIdx.x == 0) row_total = units * v.Hkv, tile_total = tiles * v.Hkv;
+  if (threadIdx.x == 0) pre[0] = 0;
   __syncthreads();
-  // the CTAs' shares: thread c handles cut c and the share after it (cut c + 1 is found again)
-  const int c = threadIdx.x;
-  if (c < v.row_ctas) {
-    Shares sh{row_total, static_cast<int>(min(static_cast<int64_t>(v.row_ctas), row_total)), 0, 0};
-    RowShare share{0, 0, 0, 0};
-    JoinTask join{0, 0, 0, 0};
-    if (c < sh.n) {
-      const Cut a = cut_at(sh, v.row_pre, static_cast<int>(entries), v.Hkv, c);
-      const Cut b = cut_at(sh, v.row_pre, static_cast<int>(entries), v.Hkv, c + 1);
-      share = RowShare{a.item, a.kvh, a.unit, static_cast<int>(b.at - a.at)};
-      join = b.join;
-    }
-    v.row_share[c] = share;
-    v.row_join[c] = join;
-  }
-  if (c < v.tile_ctas) {
-    Shares sh{tile_total, static_cast<int>(min(static_cast<int64_t>(v.tile_ctas), tile_total)), kTileHead, kTileSnap};
-    TileShare share{0, 0, 0, 0};
-    JoinTask join{0, 0, 0, 0};
-    if (c < sh.n) {
-      const Cut a = cut_at(sh, v.blk_pre, static_cast<int>(blocks), v.Hkv, c);
-      const Cut b = cut_at(sh, v.blk_pre, static_cast<int>(blocks), v.Hkv, c + 1);
-      share = TileShare{a.item, a.kvh, max(a.unit - kTileHead, 0), static_cast<int>(b.at - a.at)};
-      join = b.join;
-    }
-    v.tile_share[c] = share;
-    v.tile_join[c] = join;
-  }
+  const int64_t tile_total = tiles * v.Hkv;
+  share_out<true>(v, small_tiles ? pre : v.blk_pre, static_cast<int>(blocks),
+                  Shares{tile_total, static_cast<int>(min(static_cast<int64_t>(v.tile_ctas), tile_total)), kTileHead, kTileSnap},
+                  v.tile_ctas, cuts, &joins[1]);
+  if (threadIdx.x < 2) v.counts[2 + threadIdx.x] = joins[threadIdx.x];
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
 plan_seq_kernel(const int32_t* __restrict__ q_start, SeqView v, int page_log2) {
-  __shared__ int32_t begin[kMapSeqs + 1];
+  __shared__ alignas(16) int32_t begin[kMapSeqs + 1];
   const int S = v.S;
   if (blockIdx.x > 0)
     for (int i = threadIdx.x; i <= S && S > 0; i += kPlanThreads) begin[i] = q_start[i];
   ptx::grid_dependency_wait();        // the check's results
   if (blockIdx.x == 0) {
-    plan(v, page_log2);
+    plan(v, page_log2, reinterpret_cast<int64_t*>(begin));
     return;
   }
   __syncthreads();

@@ -134,6 +134,19 @@ def _stream(stream):
     return stream
 
 
+# The current stream's raw handle. The attention step's calls take a few microseconds on the GPU for small batches, where
+# making a Stream object for each (about 3 us) is felt.
+_raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, device: torch.device):
+    if stream is not None:
+        return stream
+    if _raw_current_stream is None:
+        return torch.cuda.current_stream(device)
+    return _raw_current_stream(device.index)
+
+
 def linear(pool: AdapterPool, meta: StepMeta, x: torch.Tensor, W: torch.Tensor, y: torch.Tensor | None = None,
            stream=None) -> torch.Tensor:
     """y[T, D] fp32 = x W^T + the step's LoRA side path (x [T, K] and W [D, K] bf16 on the GPU)."""
@@ -235,6 +248,7 @@ class SeqMeta:
 
     def __init__(self, max_seqs: int, max_tokens: int, max_pages: int, n_q_heads: int, n_kv_heads: int, head_dim: int):
         self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
+        self.device = torch.device("cuda", torch.cuda.current_device())
         self.handle = mlora.mlora_seq_create(max_seqs, max_tokens, max_pages, n_q_heads, n_kv_heads, head_dim)
         self.T = 0
         self.n_seqs = 0
@@ -247,7 +261,7 @@ class SeqMeta:
         n = kv_len.shape[0]
         assert q_start.shape == (n + 1,) and pages.dim() == 2 and pages.shape[0] == n
         mlora.mlora_build_seq(self.handle, q_start, kv_len, pages, pages.shape[1], n, T, max_new, cache.handle,
-                              _stream(stream))
+                              _raw_stream(stream, self.device))
         self.T, self.n_seqs = T, n
 
     def status(self) -> None:
@@ -276,10 +290,11 @@ def qkv_write(cache: KVCache, seq: SeqMeta, qkv: torch.Tensor, q: torch.Tensor |
     assert positions is None or (positions.is_cuda and positions.dtype == torch.int32 and positions.shape == (seq.T,)
                                  and positions.is_contiguous())
     if q is None:
-        q = torch.empty((seq.T, hq, hd), dtype=torch.bfloat16, device=qkv.device)
-    assert q.dtype == torch.bfloat16 and q.shape == (seq.T, hq, hd) and q.is_contiguous()
+        q = torch.empty((seq.T, hq, hd), dtype=torch.bfloat16, device=seq.device)
+    else:
+        assert q.dtype == torch.bfloat16 and q.shape == (seq.T, hq, hd) and q.is_contiguous()
     mlora.mlora_qkv_write(cache.handle, seq.handle, qkv, qkv.stride(0) if seq.T > 1 else qkv.shape[1], q_norm, k_norm,
-                          eps, rope.handle if rope is not None else None, positions, q, _stream(stream))
+                          eps, rope.handle if rope is not None else None, positions, q, _raw_stream(stream, seq.device))
     return q
 
 
@@ -290,9 +305,10 @@ def attention(cache: KVCache, seq: SeqMeta, q: torch.Tensor, o: torch.Tensor | N
     hq, hd = seq.n_q_heads, seq.head_dim
     assert q.is_cuda and q.dtype == torch.bfloat16 and q.shape == (seq.T, hq, hd) and q.is_contiguous()
     if o is None:
-        o = torch.empty((seq.T, hq * hd), dtype=torch.bfloat16, device=q.device)
-    assert o.dtype == torch.bfloat16 and o.shape == (seq.T, hq * hd) and o.is_contiguous()
-    mlora.mlora_attention(cache.handle, seq.handle, q, hd ** -0.5 if scale is None else scale, o, _stream(stream))
+        o = torch.empty((seq.T, hq * hd), dtype=torch.bfloat16, device=seq.device)
+    else:
+        assert o.dtype == torch.bfloat16 and o.shape == (seq.T, hq * hd) and o.is_contiguous()
+    mlora.mlora_attention(cache.handle, seq.handle, q, hd ** -0.5 if scale is None else scale, o, _raw_stream(stream, seq.device))
     return o
 
 
@@ -303,10 +319,10 @@ def kv_read(cache: KVCache, seq: SeqMeta, row_start: torch.Tensor, rows: int, k=
     assert row_start.numel() >= seq.n_seqs
     shape = (rows, cache.n_kv_heads, cache.head_dim)
     if k is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=row_start.device)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=seq.device)
     if v is None:
-        v = torch.empty(shape, dtype=torch.bfloat16, device=row_start.device)
-    for x in (k, v):
-        assert x.dtype == torch.bfloat16 and x.shape == shape and x.is_contiguous()
-    mlora.mlora_kv_read(cache.handle, seq.handle, row_start, rows, k, v, _stream(stream))
+        v = torch.empty(shape, dtype=torch.bfloat16, device=seq.device)
+    assert k.shape == shape and v.shape == shape and k.dtype == v.dtype == torch.bfloat16
+    assert k.is_contiguous() and v.is_contiguous()
+    mlora.mlora_kv_read(cache.handle, seq.handle, row_start, rows, k, v, _raw_stream(stream, seq.device))
     return k, v

@@ -74,6 +74,8 @@ def library_path() -> str:
 def load(path: str | None = None):
     """Load libmlora.so (raises FileNotFoundError if it has not been built)."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
