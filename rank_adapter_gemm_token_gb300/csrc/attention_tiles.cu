@@ -28,6 +28,7 @@
 // what lies there has no effect. Every wait is bounded: after 2 s a role records the timeout, stops waiting and
 // runs on to the end.
 #include <algorithm>
+#include <climits>
 
 #include "attention.h"
 #include "attention.cuh"
@@ -367,7 +368,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       const int tok0 = it.t0 + v.tile_tokens * w, tok = tok0 + row_tok;
       const bool valid = row_tok < v.tile_tokens && tok < it.n;
       const int lim = valid ? it.base + tok : -1;
-      const int first_lim = it.base + tok0;           // the tile's first row sees the fewest keys
+      // the fewest and the most keys that a row of the warp sees (rows of no token see none)
+      const int low = __reduce_min_sync(0xffffffffu, valid ? lim : INT_MAX), high = __reduce_max_sync(0xffffffffu, lim);
       float c = scale_log2;
       const int end = it.end[w];
       float m = -INFINITY, l = 0.f;
@@ -389,16 +391,14 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           if (j == it.ka) c *= q_scale[((n_o & 1) * 2 + w) * 128 + row];
           ct *= c;
         }
-        const bool masked = (j + 1) * kKeys - 1 > first_lim;
         const uint64_t cc = pair(ct, ct);
-        const int seen = lim - j * kKeys;             // keys 0 .. seen of the tile are visible
+        const int seen = lim - j * kKeys, seen_low = low - j * kKeys, seen_high = high - j * kKeys;   // keys 0 .. seen are visible
         constexpr int W = C::kCols;                   // columns at a time
         auto mask = [&](uint32_t (&x)[W], int h) {    // of columns W h ...
-          if (masked) {
 #pragma unroll
-            for (int i = 0; i < W; ++i) x[i] = W * h + i > seen ? 0xff800000u : x[i];
-          }
+          for (int i = 0; i < W; ++i) x[i] = W * h + i > seen ? 0xff800000u : x[i];
         };
+        const bool edge = seen_low < kKeys - 1;       // some row of the warp does not see the whole tile
         auto largest = [&](const uint32_t (&x)[W], float t) {
           float u = __uint_as_float(x[0]);
 #pragma unroll
@@ -410,20 +410,13 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         };
         uint32_t xa[W], xb[W];
         float top = -INFINITY;
-        if (j == it.ka) {                             // the first tile's maximum
-#pragma unroll
-          for (int h = 0; h < kKeys / W; h += 2) {
-            tmem_ld(ts + W * h, xa);
-            tmem_ld(ts + W * h + W, xb);
-            ptx::tmem_ld_wait();
-            mask(xa, h);
-            top = largest(xa, top);
-            mask(xb, h + 1);
-            top = largest(xb, top);
-          }
-          m = fmaf(top, ct, off);
+        if (j == it.ka) {                             // a first maximum: that of the first columns
+          tmem_ld(ts, xa);
+          ptx::tmem_ld_wait();
+          if (edge) mask(xa, 0);
+          m = fmaf(largest(xa, top), ct, off);
         }
-        // One pass over S, 32 columns at a time: weights against the maximum so far, and the tile's own maximum. P
+        // One pass over S, W columns at a time: weights against the maximum so far, and the tile's own maximum. P
         // waits in registers: where the tile's maximum is above the lazy limit, S is still there for another pass.
         uint32_t p[64];
         uint64_t sum, sum1;
@@ -433,7 +426,6 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           top = -INFINITY;
           sum = 0, sum1 = 0;                          // two zeros each
           auto weights = [&](uint32_t (&x)[W], int h) {
-            mask(x, h);
             top = largest(x, top);
 #pragma unroll
             for (int i = 0; i < W; i += 4) {
@@ -452,15 +444,31 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               p[W / 2 * h + i / 2 + 1] = E4M3 ? pack_f16(e1.x, e1.y) : pack_bf16(e1.x, e1.y);
             }
           };
-          tmem_ld(ts, xa);
+          if (!edge) {
+            tmem_ld(ts, xa);
 #pragma unroll
-          for (int h = 0; h < kKeys / W; h += 2) {
-            ptx::tmem_ld_wait();
-            tmem_ld(ts + W * h + W, xb);
-            weights(xa, h);
-            ptx::tmem_ld_wait();
-            if (h + 2 < kKeys / W) tmem_ld(ts + W * h + 2 * W, xa);
-            weights(xb, h + 1);
+            for (int h = 0; h < kKeys / W; h += 2) {
+              ptx::tmem_ld_wait();
+              tmem_ld(ts + W * h + W, xb);
+              weights(xa, h);
+              ptx::tmem_ld_wait();
+              if (h + 2 < kKeys / W) tmem_ld(ts + W * h + 2 * W, xa);
+              weights(xb, h + 1);
+            }
+          } else {
+            // columns that no row of the warp sees are left out, the others masked one by one
+#pragma unroll
+            for (int h = 0; h < kKeys / W; ++h) {
+              if (W * h <= seen_high) {
+                tmem_ld(ts + W * h, xa);
+                ptx::tmem_ld_wait();
+                mask(xa, h);
+                weights(xa, h);
+              } else {
+#pragma unroll
+                for (int i = 0; i < W / 2; ++i) p[W / 2 * h + i] = 0u;
+              }
+            }
           }
           top = fmaf(top, ct, off);
           if (!__any_sync(0xffffffffu, top > m + kLazy)) break;
