@@ -151,6 +151,18 @@ __device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint64_t pair_u(uint32_t x, uint32_t y) { return pair(__uint_as_float(x), __uint_as_float(y)); }
 
+// 32 bytes, in one store where the output is 32-byte aligned: a thread writes its own row, and the rows of a warp lie in 32
+// different lines, which the load/store unit takes one by one.
+__device__ __forceinline__ void store32(uint16_t* p, const uint32_t* x, bool wide) {
+  if (!wide) {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+    return;
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
 // Barrier of the four warps that turn codes into f16.
 __device__ __forceinline__ void converters_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // Two e4m3 codes as f16, times a factor.
@@ -360,24 +372,25 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     const int w = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
+    const bool wide = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
     const int row_tok = row / v.G, row_head = row - row_tok * v.G;
     uint32_t n_s = 0, n_o = 0;                        // waits done on s_full, o_full
     uint32_t n_sc = 0;                                // key tiles of the CTA so far (scale buffers)
     for (bool go = any; go; go = advance(walk)) {
       const Walk& it = walk;
-      const int tok0 = it.t0 + v.tile_tokens * w, tok = tok0 + row_tok;
+      const int tok = it.t0 + v.tile_tokens * w + row_tok;
       const bool valid = row_tok < v.tile_tokens && tok < it.n;
       const int lim = valid ? it.base + tok : -1;
       // the fewest and the most keys that a row of the warp sees (rows of no token see none)
       const int low = __reduce_min_sync(0xffffffffu, valid ? lim : INT_MAX), high = __reduce_max_sync(0xffffffffu, lim);
+      const int ka = it.ka, end = it.end[w];
       float c = scale_log2;
-      const int end = it.end[w];
       float m = -INFINITY, l = 0.f;
-      for (int j = it.ka; j < end; ++j) {
+      for (int j = ka; j < end; ++j) {
         float ct = c, off = 0.f, rv = 1.f;            // score = S ct + off; the sum takes rv times the exponentials
         const float* mant = nullptr;
         if (E4M3) {
-          const uint32_t t = n_sc + (j - it.ka);
+          const uint32_t t = n_sc + (j - ka);
           wait(&sc_full[t % C::kScaleBufs], (t / C::kScaleBufs) & 1);
           const float4 f = reinterpret_cast<const float4*>(smem + C::kScaleOff)[t % C::kScaleBufs];
           ct = f.x, off = f.y, rv = f.z;
@@ -388,7 +401,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         ptx::tc_fence_after();
         // (the query rows and their scales were there before the products that s_full stands for)
         if (E4M3) {
-          if (j == it.ka) c *= q_scale[((n_o & 1) * 2 + w) * 128 + row];
+          if (j == ka) c *= q_scale[((n_o & 1) * 2 + w) * 128 + row];
           ct *= c;
         }
         const uint64_t cc = pair(ct, ct);
@@ -410,7 +423,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         };
         uint32_t xa[W], xb[W];
         float top = -INFINITY;
-        if (j == it.ka) {                             // a first maximum: that of the first columns
+        if (j == ka) {                                // a first maximum: that of the first columns
           tmem_ld(ts, xa);
           ptx::tmem_ld_wait();
           if (edge) mask(xa, 0);
@@ -493,49 +506,43 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         ptx::tc_fence_before();
         ptx::mbar_arrive(&p_full[w]);
       }
-      n_sc += it.kb - it.ka;
-      if (end > it.ka) {
+      n_sc += it.kb - ka;
+      if (end > ka) {
         wait(&o_full[w], n_o & 1);
         ++n_o;
         ptx::tc_fence_after();
       }
-
-      if (tok0 < it.n) {
-        if (it.whole()) {
-          const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;      // NaN stays
-          uint16_t* dst = o + (static_cast<int64_t>(it.first + tok) * v.Hq + it.kvh * v.G + row_head) * HD;
+      if (!it.whole() && it.t0 + v.tile_tokens * w < it.n) {
+        // a part of a split item, to the workspace
+        float* mine = v.tile_part + ((2 * static_cast<int64_t>(blockIdx.x) + (ka == 0)) * 2 + w) * tile_slot(v);
+        if (end > ka) {
 #pragma unroll
           for (int i = 0; i < HD / 32; ++i) {
             uint32_t y[32];
             ptx::tmem_ld_32x32b_x32(to + 32 * i, y);
             ptx::tmem_ld_wait();
-            if (valid) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint4 z;
-                z.x = pack_bf16(__uint_as_float(y[8 * k]) * inv, __uint_as_float(y[8 * k + 1]) * inv);
-                z.y = pack_bf16(__uint_as_float(y[8 * k + 2]) * inv, __uint_as_float(y[8 * k + 3]) * inv);
-                z.z = pack_bf16(__uint_as_float(y[8 * k + 4]) * inv, __uint_as_float(y[8 * k + 5]) * inv);
-                z.w = pack_bf16(__uint_as_float(y[8 * k + 6]) * inv, __uint_as_float(y[8 * k + 7]) * inv);
-                *reinterpret_cast<uint4*>(dst + 32 * i + 8 * k) = z;
-              }
-            }
+            for (int k = 0; k < 8; ++k)
+              reinterpret_cast<uint4*>(mine)[(8 * i + k) * 128 + row] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
           }
-        } else {
-          float* mine = v.tile_part + ((2 * static_cast<int64_t>(blockIdx.x) + (it.ka == 0)) * 2 + w) * tile_slot(v);
-          if (end > it.ka) {
+        }
+        mine[128 * HD + row] = m;
+        mine[128 * HD + 128 + row] = l;
+      } else if (end > ka) {
+        const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;          // NaN stays
+        uint16_t* dst = o + (static_cast<int64_t>(it.first + tok) * v.Hq + it.kvh * v.G + row_head) * HD;
 #pragma unroll
-            for (int i = 0; i < HD / 32; ++i) {
-              uint32_t y[32];
-              ptx::tmem_ld_32x32b_x32(to + 32 * i, y);
-              ptx::tmem_ld_wait();
+        for (int i = 0; i < HD / 32; ++i) {
+          uint32_t y[32];
+          ptx::tmem_ld_32x32b_x32(to + 32 * i, y);
+          ptx::tmem_ld_wait();
+          uint32_t z[16];
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                reinterpret_cast<uint4*>(mine)[(8 * i + k) * 128 + row] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-            }
+          for (int k = 0; k < 16; ++k) z[k] = pack_bf16(__uint_as_float(y[2 * k]) * inv, __uint_as_float(y[2 * k + 1]) * inv);
+          if (valid) {
+            store32(dst + 32 * i, z, wide);
+            store32(dst + 32 * i + 16, z + 8, wide);
           }
-          mine[128 * HD + row] = m;
-          mine[128 * HD + 128 + row] = l;
         }
       }
       ptx::tc_fence_before();

@@ -214,6 +214,19 @@ def test_another_stream(layer, kind):
     assert torch.equal(o, o2)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_operands_aligned_to_16_bytes_alone(layer, kind):
+    from rank_adapter_gemm_token_gb300 import mlora
+    st = Step(layer, [1, 40, 2], [300, 100, 0], kind=kind)
+    whole = st.run()
+    wide = torch.empty(st.T * st.hq * st.hd + 8, dtype=torch.bfloat16, device="cuda")
+    q = torch.empty_like(wide)
+    q[8:] = st.q.flatten()
+    mlora.mlora_attention(st.cache.handle, st.seq.handle, q.data_ptr() + 16, st.hd ** -0.5, wide.data_ptr() + 16)
+    torch.cuda.synchronize()
+    assert torch.equal(wide[8:].view_as(whole), whole)
+
+
 def test_offsets_past_32_bits(layer):
     """A cache of 5.2e9 elements each for K and V, the sequences in its last pages."""
     st = Step(layer, [1, 20], [100, 100], 8, 8, page=16, n_pages=320000)
