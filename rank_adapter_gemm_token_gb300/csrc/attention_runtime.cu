@@ -403,7 +403,8 @@ mlora_status mlora_qkv_write(mlora_kv_t kv, mlora_seq_t q, const float* qkv, int
   const int64_t width = static_cast<int64_t>(v.Hq + 2 * v.Hkv) * v.hd;
   if (ld < width || ld % 4) return fail(MLORA_ERR_INVALID_ARG, "qkv rows of %lld elements must be a multiple of 4 and at least %lld", (long long)ld, (long long)width);
   if (v.T > 0 && (!qkv || !q_out)) return fail(MLORA_ERR_INVALID_ARG, "qkv or q_out is NULL");
-  if (!aligned(qkv, 16) || !aligned(q_out, 16)) return fail(MLORA_ERR_INVALID_ARG, "qkv and q_out must be 16-byte aligned");
+  if (!aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(q_norm, 16) || !aligned(k_norm, 16))
+    return fail(MLORA_ERR_INVALID_ARG, "qkv, q_out and the norms' weights must be 16-byte aligned");
   if ((q_norm || k_norm) && !(eps >= 0.f && std::isfinite(eps))) return fail(MLORA_ERR_INVALID_ARG, "eps must be finite and not negative");
   if (rope && rope->rot > v.hd) return fail(MLORA_ERR_MISMATCH, "the rotation turns %d elements of heads of %d", rope->rot, v.hd);
   RopeView r{nullptr, 0, 0, 1.f};
