@@ -25,21 +25,26 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Two e4m3 codes (low 16 bits) as two halves: exact, every e4m3 value is an f16 value.
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
-  return r;
+// Four e4m3 codes as two pairs of halves: exact, every e4m3 value is an f16 value. (Both halves of the register are named, so
+// that the upper one needs no shift.)
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
 }
 // Eight e4m3 codes times a scale, as bf16 (each product rounded to fp32, then to bf16).
 __device__ __forceinline__ uint4 e4m3_times(uint2 c, float scale) {
   uint4 out;
-  const uint32_t in[2] = {c.x, c.y};
+  uint32_t h[4];
+  e4m3x4_f16x4(c.x, h[0], h[1]);
+  e4m3x4_f16x4(c.y, h[2], h[3]);
   uint32_t* o = &out.x;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t h = e4m3x2_f16x2(in[i >> 1] >> (16 * (i & 1)));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
     o[i] = pack_bf16(f.x * scale, f.y * scale);
   }
   return out;

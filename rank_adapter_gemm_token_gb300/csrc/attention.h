@@ -23,8 +23,8 @@ struct KvView {
   int n_pages, page, page_log2, Hkv, hd, type;
 };
 
-// A sequence of the row kernel's list, and a CTA's share of the list: `units` units from unit `unit` of head kvh
-// of list entry `item` on.
+// A sequence of the row kernel's list, and a CTA's share of the list: `units` units of 64 keys, from unit `unit` of head
+// kvh of list entry `item` on.
 struct RowSeq {
   int32_t seq, n, len, start;
 };
@@ -55,7 +55,7 @@ struct SeqView {
   int32_t* tok_row;     // [T] page * page size + offset of the token's cache row (-1: none)
   int32_t* page_pre;    // [S + 1] cached pages of the sequences before each
   RowSeq* row_seq;      // [S] the row kernel's sequences
-  int64_t* row_pre;     // [S + 1] units (64 keys, for each kv head) before each of them
+  int64_t* row_pre;     // [S + 1] units (kRowHead and one for 64 keys, for each kv head) before each of them
   TileBlk* blk;         // [blocks] the tile kernel's blocks
   int64_t* blk_pre;     // [blocks + 1] units (kTileHead and the key tiles, for each kv head) before each of them
   RowShare* row_share;  // [row_ctas]
@@ -74,6 +74,7 @@ struct SeqView {
 
 // Keys of one unit of the row kernel (four warps x 16 keys) and of one tile of the tile kernel.
 constexpr int kRowUnit = 64;
+constexpr int kRowHead = 3;           // units that an item's fixed costs (queries, joining the warps' sums) are worth
 constexpr int kTileKeys = 128;
 constexpr int kTileSnap = 2;          // key tiles that a split costs at least
 constexpr int kTileHead = 3;          // key tiles that an item's fixed costs (queries, first products, output) are worth

@@ -168,22 +168,33 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
       if (k0 < src.s.len) {
         const uint32_t st = ring + (issued % C::kStages) * C::kStage;
         constexpr int kStep = 32 / C::kSegs;  // rows of one copy of all lanes
+        constexpr int kHalf = kChunk / 2 / kStep;                                // copies of eight rows
+        static_assert(kStep * kHalf == 8, "a copy of all lanes takes 2, 4 or 8 rows");
+        // the chunk's first and second eight rows: pages of 16 tokens and more hold them one after the other
+        const int64_t row_a = (static_cast<int64_t>(page_a) * v.Hkv + src.kvh) << kv.page_log2;
+        const int64_t row_b = (static_cast<int64_t>(page_b) * v.Hkv + src.kvh) << kv.page_log2;
+        const int off_a = k0 & (kv.page - 1), off_b = (k0 + 8) & (kv.page - 1);
+        const int lr = lane / C::kSegs, seg = lane % C::kSegs;
+        const bool full = k0 + kChunk <= src.s.len;
 #pragma unroll
-        for (int i = 0; i < kChunk / kStep; ++i) {
-          const int r = i * kStep + lane / C::kSegs, seg = lane % C::kSegs;
-          const int64_t at = ((static_cast<int64_t>(r < 8 ? page_a : page_b) * v.Hkv + src.kvh) << kv.page_log2) +
-                             ((k0 + r) & (kv.page - 1));
-          const int phys = C::kSegs >= 8 ? seg ^ (r & 7) : seg ^ ((r >> 1) & 3);
-          const uint32_t dst = st + r * C::kRowBytes + phys * 16;
-          const bool in = k0 + r < src.s.len;
-          cp16(dst, static_cast<const uint8_t*>(kv.K) + at * C::kRowBytes + seg * 16, in);
-          cp16(dst + C::kTile, static_cast<const uint8_t*>(kv.V) + at * C::kRowBytes + seg * 16, in);
+        for (int half = 0; half < 2; ++half) {
+          const int64_t at = ((half ? row_b + off_b : row_a + off_a) + lr) * C::kRowBytes + seg * 16;
+          const uint8_t* pk = static_cast<const uint8_t*>(kv.K) + at;
+          const uint8_t* pv = static_cast<const uint8_t*>(kv.V) + at;
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i) {
+            const int r = half * 8 + i * kStep + lr;
+            const int phys = C::kSegs >= 8 ? seg ^ (r & 7) : seg ^ ((r >> 1) & 3);
+            const uint32_t dst = st + r * C::kRowBytes + phys * 16;
+            const bool in = full || k0 + r < src.s.len;
+            cp16(dst, pk + i * kStep * C::kRowBytes, in);
+            cp16(dst + C::kTile, pv + i * kStep * C::kRowBytes, in);
+          }
         }
         if (E4M3) {
           const int r = lane & 15;
-          const int64_t at = ((static_cast<int64_t>(r < 8 ? page_a : page_b) * v.Hkv + src.kvh) << kv.page_log2) +
-                             ((k0 + r) & (kv.page - 1));
-          cp4(st + 2 * C::kTile + lane * 4, (lane < 16 ? kv.k_scale : kv.v_scale) + at, k0 + r < src.s.len);
+          const int64_t at = (r < 8 ? row_a + off_a : row_b + off_b) + (r & 7);
+          cp4(st + 2 * C::kTile + lane * 4, (lane < 16 ? kv.k_scale : kv.v_scale) + at, full || k0 + r < src.s.len);
         }
       }
       ++issued;
@@ -290,11 +301,11 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
           rvs[h] = vs > 0.f ? __fdividef(1.0f, vs) : 0.f;      // a NaN scale counts in the exponent alone
         }
       }
-      float sc[NQ][4];
+      float sc[NQ][4], sc1[NQ][4];                // two sums, of the even and odd k-steps: half the chain of products
 #pragma unroll
       for (int z = 0; z < NQ; ++z)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sc[z][k] = 0.f;
+        for (int k = 0; k < 4; ++k) sc[z][k] = sc1[z][k] = 0.f;
       if (E4M3) {
         // lane (g, t): bytes t HD/4 ... of key rows g and g + 8; byte 4 i + j is k index (2 t + (j & 1) + 8 (j >> 1))
         // of step i, for the query rows alike
@@ -309,9 +320,11 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
           const uint32_t x = (&w[0][i >> 2].x)[i & 3], y = (&w[1][i >> 2].x)[i & 3];
-          const uint32_t a[4] = {e4m3x2_f16x2(x), e4m3x2_f16x2(y), e4m3x2_f16x2(x >> 16), e4m3x2_f16x2(y >> 16)};
+          uint32_t a[4];
+          e4m3x4_f16x4(x, a[0], a[2]);
+          e4m3x4_f16x4(y, a[1], a[3]);
 #pragma unroll
-          for (int z = 0; z < NQ; ++z) mma<true>(sc[z], a, bq[z][i][0], bq[z][i][1]);
+          for (int z = 0; z < NQ; ++z) mma<true>(i & 1 ? sc1[z] : sc[z], a, bq[z][i][0], bq[z][i][1]);
         }
       } else {
 #pragma unroll
@@ -320,7 +333,7 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
           const int r = lane & 15, seg = 2 * i + (lane >> 4);
           ldsm4(a, st + r * C::kRowBytes + (seg ^ (r & 7)) * 16);
 #pragma unroll
-          for (int z = 0; z < NQ; ++z) mma<false>(sc[z], a, bq[z][i][0], bq[z][i][1]);
+          for (int z = 0; z < NQ; ++z) mma<false>(i & 1 ? sc1[z] : sc[z], a, bq[z][i][0], bq[z][i][1]);
         }
       }
       uint32_t pb[NQ][2];
@@ -331,7 +344,8 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int c = k & 1, h = k >> 1;
-          float x = E4M3 ? fmaf(sc[z][k] * ks[h], cq[z][c], lvs[h]) : sc[z][k] * cq[z][c];
+          float x = sc[z][k] + sc1[z][k];
+          x = E4M3 ? fmaf(x * ks[h], cq[z][c], lvs[h]) : x * cq[z][c];
           if (edge && k0 + g + 8 * h > lim[z][c]) x = -INFINITY;
           sc[z][k] = x;
           grow = grow || x > m[z][c] + kLazy;
@@ -380,7 +394,9 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
           for (int b = 0; b < 2; ++b) {
             const uint32_t x = __byte_perm(w[0][j], w[1][j], b ? 0x7362 : 0x5140);
             const uint32_t y = __byte_perm(w[2][j], w[3][j], b ? 0x7362 : 0x5140);
-            const uint32_t a[4] = {e4m3x2_f16x2(x), e4m3x2_f16x2(x >> 16), e4m3x2_f16x2(y), e4m3x2_f16x2(y >> 16)};
+            uint32_t a[4];
+            e4m3x4_f16x4(x, a[0], a[1]);
+            e4m3x4_f16x4(y, a[2], a[3]);
 #pragma unroll
             for (int z = 0; z < NQ; ++z) mma<true>(acc[z][2 * j + b], a, pb[z][0], pb[z][1]);
           }

@@ -165,11 +165,17 @@ __device__ __forceinline__ void store32(uint16_t* p, const uint32_t* x, bool wid
 }
 // Barrier of the four warps that turn codes into f16.
 __device__ __forceinline__ void converters_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-// Two e4m3 codes as f16, times a factor.
-__device__ __forceinline__ uint32_t scaled(uint32_t two, __half2 f) {
-  const uint32_t h = e4m3x2_f16x2(two);
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h), f);
-  return *reinterpret_cast<const uint32_t*>(&r);
+// Eight e4m3 codes as f16, times a factor.
+__device__ __forceinline__ uint4 scaled(uint32_t x, uint32_t y, __half2 f) {
+  uint32_t h[4];
+  e4m3x4_f16x4(x, h[0], h[1]);
+  e4m3x4_f16x4(y, h[2], h[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), f);
+    h[i] = *reinterpret_cast<const uint32_t*>(&r);
+  }
+  return make_uint4(h[0], h[1], h[2], h[3]);
 }
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -640,8 +646,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             for (int i = 0; i < kCopies; ++i) f[i] = factors[h * kKeys + i * kStep + r_in];
 #pragma unroll
             for (int i = 0; i < kCopies; ++i) {
-              const uint4 lo = make_uint4(scaled(cd[i].x, f[i]), scaled(cd[i].x >> 16, f[i]), scaled(cd[i].y, f[i]), scaled(cd[i].y >> 16, f[i]));
-              const uint4 hi = make_uint4(scaled(cd[i].z, f[i]), scaled(cd[i].z >> 16, f[i]), scaled(cd[i].w, f[i]), scaled(cd[i].w >> 16, f[i]));
+              const uint4 lo = scaled(cd[i].x, cd[i].y, f[i]), hi = scaled(cd[i].z, cd[i].w, f[i]);
               const int r = i * kStep + r_in;
               *reinterpret_cast<uint4*>(dst + r * 128 + (((even + (odd ? 1 : 0)) ^ (r & 7)) * 16)) = odd ? hi : lo;
               *reinterpret_cast<uint4*>(dst + r * 128 + (((even + (odd ? 0 : 1)) ^ (r & 7)) * 16)) = odd ? lo : hi;

@@ -126,14 +126,15 @@ __device__ __forceinline__ void share_out(const SeqView& v, const int64_t* pre, 
   const int c = threadIdx.x;
   Cut cut{n, 0, 0, sh.total, JoinTask{0, 0, 0, 0}};
   if (c <= sh.n && sh.total > 0) cut = cut_at(sh, pre, n, v.Hkv, c);
-  cuts[c] = cut.at;
+  // (row shares count their keys' units alone: those of an item's head are taken off where the item begins)
+  cuts[c] = TILES ? cut.at : cut.at - static_cast<int64_t>(kRowHead) * (static_cast<int64_t>(cut.item) * v.Hkv + cut.kvh + (cut.unit > 0));
   __syncthreads();
   if (c < ctas) {
-    const int units = c < sh.n && sh.total > 0 ? static_cast<int>(cuts[c + 1] - cut.at) : 0;
+    const int units = c < sh.n && sh.total > 0 ? static_cast<int>(cuts[c + 1] - cuts[c]) : 0;
     if (TILES)
       v.tile_share[c] = TileShare{cut.item, cut.kvh, max(cut.unit - kTileHead, 0), units};
     else
-      v.row_share[c] = RowShare{cut.item, cut.kvh, cut.unit, units};
+      v.row_share[c] = RowShare{cut.item, cut.kvh, max(cut.unit - kRowHead, 0), units};
   }
   if (cut.join.parts > 0) (TILES ? v.tile_join : v.row_join)[atomicAdd(joins, 1)] = cut.join;
   __syncthreads();
@@ -151,7 +152,7 @@ __device__ void plan(const SeqView& v, int page_log2, int64_t* pre) {
     const int64_t rows = static_cast<int64_t>(n) * v.G;
     const bool some = rows > 0 && L > 0, few = rows <= v.row_limit;
     const int per = 2 * v.tile_tokens;              // tokens of a block
-    const int64_t u = some && few ? (L + kRowUnit - 1) / kRowUnit : 0;
+    const int64_t u = some && few ? kRowHead + (L + kRowUnit - 1) / kRowUnit : 0;
     const int64_t b = some && !few ? (n + per - 1) / per : 0;
     int64_t x[5] = {n, u, u > 0, (static_cast<int64_t>(L) + (1 << page_log2) - 1) >> page_log2, b}, t[5];
     block_scan(x, sums, t);
@@ -206,7 +207,7 @@ __device__ void plan(const SeqView& v, int page_log2, int64_t* pre) {
   __syncthreads();
   const int64_t row_total = units * v.Hkv;
   share_out<false>(v, small_rows ? pre : v.row_pre, static_cast<int>(entries),
-                   Shares{row_total, static_cast<int>(min(static_cast<int64_t>(v.row_ctas), row_total)), 0, 0}, v.row_ctas, cuts,
+                   Shares{row_total, static_cast<int>(min(static_cast<int64_t>(v.row_ctas), row_total)), kRowHead, 0}, v.row_ctas, cuts,
                    &joins[0]);
   int64_t tiles = 0;
   const bool small_tiles = blocks < kPlanPre;
