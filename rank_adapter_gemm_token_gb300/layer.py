@@ -326,3 +326,14 @@ def kv_read(cache: KVCache, seq: SeqMeta, row_start: torch.Tensor, rows: int, k=
     assert k.is_contiguous() and v.is_contiguous()
     mlora.mlora_kv_read(cache.handle, seq.handle, row_start, rows, k, v, _raw_stream(stream, seq.device))
     return k, v
+
+
+def attention_block(meta: StepMeta, seq: SeqMeta, cache: KVCache, x: torch.Tensor, qkv_pool: AdapterPool, W_qkv: torch.Tensor,
+                    o_pool: AdapterPool, W_o: torch.Tensor, q_norm=None, k_norm=None, eps: float = 1e-6,
+                    rope: Rope | None = None, scale: float | None = None, stream=None) -> torch.Tensor:
+    """One layer's attention for the step that `meta` (adapters) and `seq` (sequences) describe: the adapted qkv linear of
+    x (bf16 [T, hidden]), the write of its rows, the attention over the cache, and the adapted o linear: fp32
+    [T, W_o.shape[0]]."""
+    qkv = linear(qkv_pool, meta, x, W_qkv, stream=stream)
+    q = qkv_write(cache, seq, qkv, q_norm=q_norm, k_norm=k_norm, eps=eps, rope=rope, stream=stream)
+    return linear(o_pool, meta, attention(cache, seq, q, scale=scale, stream=stream), W_o, stream=stream)

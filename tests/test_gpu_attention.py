@@ -503,3 +503,65 @@ def test_kv_read_outside_its_rows_is_reported(layer):
             st.seq.status()
         assert e.value.status == mlora.MLORA_ERR_INVALID_ARG
         assert (k[rows:] == 7.0).all() and (v[rows:] == 7.0).all()
+
+
+# ------------------------------------------------------------------------------------------- the layer
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_example_stepwise_equals_one_step(kind):
+    """The same keys and values are cached either way; queries and outputs differ by bf16 rounding (2^-8 a value at most, in
+    three places) and, e4m3, by codes that a last-bit difference of the linear's sums moves to the neighbour (rare)."""
+    from examples import attention_serving
+    assert attention_serving.main(kind) <= 3 * 2.0 ** -8
+
+
+def test_attention_block_against_fp64(layer):
+    """The adapted layer in fp64. Rounding to bf16 in five places (queries, keys, values, weights, the attention's output),
+    each 2^-8 relative at most and about 2^-9 in the 2-norm; scores of a few units pass those of queries and keys on: 8
+    roundings of 2^-9 in all."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *shape, std=1.0: (std * torch.randn(*shape, generator=g, device="cuda")).to(torch.bfloat16)  # noqa: E731
+    hidden, hq, hkv, hd, page = 512, 8, 2, 64, 16
+    n, ctx = [40, 1, 1, 7], [0, 30, 100, 12]
+    T, lens = sum(n), [a + b for a, b in zip(n, ctx)]
+    W_qkv, W_o = rand((hq + 2 * hkv) * hd, hidden, std=0.04), rand(hidden, hq * hd, std=0.04)
+    pools = layer.AdapterPool(2, 8, hidden, W_qkv.shape[0]), layer.AdapterPool(2, 8, hq * hd, hidden)
+    ab = [[(rand(8, p.K, std=0.05), rand(p.D, 8, std=0.05)) for _ in range(2)] for p in pools]
+    for p, mats in zip(pools, ab):
+        for slot, (A, B) in enumerate(mats):
+            p.load(slot, A, B, 8, 16.0)
+        p.sync()
+    x, slots = rand(T, hidden), torch.tensor([0] * 40 + [1, -1, 0, 1, 0, 1, 0, 1, -1], dtype=torch.int32)[:T]
+    starts = np.concatenate([[0], np.cumsum(n)]).tolist()
+    cache = layer.KVCache(40, page, hkv, hd)
+    table = torch.arange(40, dtype=torch.int32).reshape(4, 10).cuda()
+    old = [(rand(c, hkv, hd), rand(c, hkv, hd)) for c in ctx]              # what earlier steps cached
+    for s, (k, v) in enumerate(old):
+        for p in range(ctx[s]):
+            cache.k[int(table[s, p // page]), :, p % page] = k[p]
+            cache.v[int(table[s, p // page]), :, p % page] = v[p]
+    meta, seq = layer.StepMeta(T, 1, 8), layer.SeqMeta(4, T, 10, hq, hkv, hd)
+    meta.build(slots.cuda(), None, pools[0])
+    seq.build(torch.tensor(starts, dtype=torch.int32).cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), table, T, cache, max(n))
+    rope = layer.Rope(hd, 10000.0)
+    y = layer.attention_block(meta, seq, cache, x, pools[0], W_qkv, pools[1], W_o, rope=rope)
+    seq.status()
+    d = lambda t: t.double().cpu().numpy()  # noqa: E731
+
+    def linear(z, W, mats):
+        out = z @ d(W).T
+        for t, s in enumerate(slots.tolist()):
+            if s >= 0:
+                out[t] += 2.0 * d(mats[s][1]) @ (d(mats[s][0]) @ z[t])
+        return out
+
+    rows = linear(d(x), W_qkv, ab[0]).reshape(T, hq + 2 * hkv, hd)
+    pos = np.concatenate([np.arange(c, c + m) for c, m in zip(ctx, n)])
+    q, k = ref.rotate(rows[:, :hq], pos, rope.freq, False), ref.rotate(rows[:, hq:hq + hkv], pos, rope.freq, False)
+    keys = [np.concatenate([d(o[0]), k[a:b]]) for o, a, b in zip(old, starts, starts[1:])]
+    values = [np.concatenate([d(o[1]), rows[a:b, hq + hkv:]]) for o, a, b in zip(old, starts, starts[1:])]
+    att, _, _ = ref.attention(q, keys, values, starts, hq // hkv, hd ** -0.5)
+    want = linear(att.reshape(T, hq * hd), W_o, ab[1])
+    err = np.linalg.norm(d(y) - want) / np.linalg.norm(want)
+    assert err <= 8 * 2.0 ** -9, err
+    for p in pools:
+        p.close()
