@@ -16,12 +16,14 @@
 //                   with a warp for each tile, their instructions alternate and the rate falls by a third.
 //   warps 15, 13    the next item's queries of one tile each by TMA, while the last products of this one run (e4m3: and
 //                   their f16 form).
-// e4m3: a tile's key rows become f16 as code * (scale / largest scale of the tile), rounded once (2^-12 on average, as the
-// queries are), and that largest scale multiplies the tile's scores. Its value rows become code * 2^k, exact: with
-// scale = f 2^(E + k), 1 <= f < 2 and 2^E the binary power of the tile's largest scale, f multiplies P before its rounding,
-// E is added to the scores (P then is the weight times the scale, at most 2^9 whatever the scales) and 2^-E multiplies the
-// sum. So the softmax reads one factor a key from shared memory; with both scales and the sum's factor of each key it took
-// 5000 cycles a tile against 1400 for bf16. Query rows are divided by their largest element so that f16 holds them.
+// e4m3: a tile's key rows become f16 as code * 64 (scale / largest scale of the tile), rounded once (2^-12 on average, as
+// the queries are), and 1/64 of that largest scale multiplies the tile's scores. Its value rows become code * 2^k, exact:
+// with scale = f 2^(E + k), 1 <= f < 2 and 2^E 1/64 of the binary power of the tile's largest scale, f multiplies P before
+// its rounding, E is added to the scores (P then is the weight times the scale, below 2^15 whatever the scales) and 2^-E
+// multiplies the sum. So the softmax reads one factor a key from shared memory; with both scales and the sum's factor of
+// each key it took 5000 cycles a tile against 1400 for bf16. The 64 puts a tile's largest row at the top of f16's range:
+// rows of scales 2^20 below it, which may be all that an early token sees of the tile, keep their bits. Query rows are
+// divided by their largest element so that f16 holds them.
 // Work: (block, key/value head) items of 128-key tiles one after another, an equal share to each CTA (seq_meta.cu);
 // parts of a split item are joined by attention_join.cu.
 // Value rows past the cached length are zeroed in shared memory, scores past a row's limit are replaced by -inf:
@@ -42,7 +44,9 @@ constexpr int kThreads = 512;               // 128 registers each at launch, sha
 constexpr int kKeys = kTileKeys;              // 128
 constexpr int kHalf = kKeys * 128;            // bytes of 128 rows of 64 16-bit elements (one swizzled half tile)
 constexpr float kLazy = 8.0f;                 // log2 of the largest exponential
-constexpr float kLeastScale = 1.17549435e-38f;   // value scales below the normal numbers count as zero
+constexpr int kLiftLog2 = 6;                  // e4m3: a tile's largest row is scaled to codes of 64 times their value
+constexpr float kLift = 64.0f;
+constexpr float kLeastScale = 0x1p-100f;      // value scales below count as zero (those written here are above 2^-69)
 
 template <int HD, bool E4M3>
 struct TilesCfg {
@@ -395,18 +399,18 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       for (int j = ka; j < end; ++j) {
         float ct = c, off = 0.f, rv = 1.f;            // score = S ct + off; the sum takes rv times the exponentials
         const float* mant = nullptr;
+        wait(&s_full[w], n_s & 1);
+        ++n_s;
+        ptx::tc_fence_after();
         if (E4M3) {
+          // (The query rows' scales were there before the products that s_full stands for. So were the tile's factors, and
+          // they are not waited for any sooner: a tile without work in an item comes here while the codes of that item are
+          // still on their way, when the factors' barrier may be two phases back, which its parity cannot tell.)
           const uint32_t t = n_sc + (j - ka);
           wait(&sc_full[t % C::kScaleBufs], (t / C::kScaleBufs) & 1);
           const float4 f = reinterpret_cast<const float4*>(smem + C::kScaleOff)[t % C::kScaleBufs];
           ct = f.x, off = f.y, rv = f.z;
           mant = reinterpret_cast<const float*>(smem + C::kMantOff) + (t % C::kScaleBufs) * kKeys;
-        }
-        wait(&s_full[w], n_s & 1);
-        ++n_s;
-        ptx::tc_fence_after();
-        // (the query rows and their scales were there before the products that s_full stands for)
-        if (E4M3) {
           if (j == ka) c *= q_scale[((n_o & 1) * 2 + w) * 128 + row];
           ct *= c;
         }
@@ -441,7 +445,10 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         uint64_t sum, sum1;
         for (;;) {
           const float mm = m == -INFINITY ? 0.f : m;
-          const uint64_t neg = pair(off - mm, off - mm);
+          // e4m3: P is f16, and a weight of 2^-24 may multiply values that much larger than the largest weight's: P is
+          // lifted by 2^6, l with it, which leaves it below 2^15 (2^8 and the scale's mantissa) and O / l as it is
+          constexpr float up = E4M3 ? kLiftLog2 : 0.f;
+          const uint64_t neg = pair(off - mm + up, off - mm + up);
           top = -INFINITY;
           sum = 0, sum1 = 0;                          // two zeros each
           auto weights = [&](uint32_t (&x)[W], int h) {
@@ -491,9 +498,9 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           }
           top = fmaf(top, ct, off);
           if (!__any_sync(0xffffffffu, top > m + kLazy)) break;
-          const float up = top > m + kLazy ? top : m;
-          const float f = up == m ? 1.f : exp2_approx(m - up);
-          m = up;
+          const float next = top > m + kLazy ? top : m;
+          const float f = next == m ? 1.f : exp2_approx(m - next);
+          m = next;
           l *= f;
 #pragma unroll 1
           for (int i = 0; i < HD / W; ++i) {
@@ -625,16 +632,16 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               if (!(km > 0.f)) km = 1.f;
               if (!(vm >= kLeastScale)) vm = 1.f;
               // a row with a NaN scale is NaN in its scores alone: its values would reach rows that do not see it
-              factors[tid] = __half2half2(__float2half_rn(ks != ks || vs != vs ? __int_as_float(0x7fffffff) : __fdividef(ks, km)));
+              factors[tid] = __half2half2(__float2half_rn(ks != ks || vs != vs ? __int_as_float(0x7fffffff) : kLift * __fdividef(ks, km)));
               const uint32_t t = n / 2;
               const float top2 = __int_as_float(__float_as_int(vm) & 0x7f800000);               // 2^E
               const float row2 = vs >= kLeastScale ? __int_as_float(__float_as_int(vs) & 0x7f800000) : 0.f;
               const float inv2 = 1.0f / top2;
-              factors[kKeys + tid] = __half2half2(__float2half_rn(row2 * inv2));
+              factors[kKeys + tid] = __half2half2(__float2half_rn(kLift * row2 * inv2));
               (reinterpret_cast<float*>(smem + C::kMantOff) + (t % C::kScaleBufs) * kKeys)[tid] = row2 > 0.f ? vs / row2 : 1.f;
               if (tid == 0)
                 reinterpret_cast<float4*>(smem + C::kScaleOff)[t % C::kScaleBufs] =
-                    make_float4(km, static_cast<float>((__float_as_int(vm) >> 23) - 127), inv2, 0.f);
+                    make_float4(km / kLift, static_cast<float>((__float_as_int(vm) >> 23) - 127 - kLiftLog2), inv2 * kLift, 0.f);
               ptx::mbar_arrive(&sc_full[t % C::kScaleBufs]);
               converters_sync();
             }

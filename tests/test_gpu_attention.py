@@ -149,6 +149,16 @@ def test_long_axis_is_split_and_joined(layer, n, ctx, hq, hkv, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_blocks_of_one_tile_between_others(layer, kind):
+    """Prompts of 660 tokens: each one's last block has rows in its first tile alone, and its run of six key tiles is followed
+    in the same CTA by the next prompt's first block, where both tiles have rows."""
+    st = Step(layer, [660] * 6, [0] * 6, 32, 8, hd=64, page=64, kind=kind, seed=9)
+    o = st.run()
+    st.seq.status()
+    st.check(o)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_large_scores_and_rising_maxima(layer, kind):
     """Scores of tens to hundreds: the running maximum moves often, and late."""
     for n, ctx in (([1, 2], [900, 300]), ([60], [500])):
