@@ -68,8 +68,8 @@ __device__ __forceinline__ int last_at_most(const T* pre, int n, T x) {
 // An equal share of a list of work items for each of n CTAs. The items' units (keys of 64 or 128) lie one
 // after another, total in all; CTA c takes units [cut(c), cut(c + 1)), so an item that lies across a cut
 // is split and its parts are joined. An item's first `head` units stand for its fixed costs, the others for
-// its keys. A cut in the head, or within `snap` units of the keys' ends, moves to the item's end: a split costs
-// more than that imbalance.
+// its keys. A cut in the head, or within `snap` units of the keys' ends, moves to the item's end, and any cut in an item too
+// short for others moves to the nearer end: a split costs more than that imbalance.
 struct Shares {
   int64_t total;
   int n;
@@ -77,7 +77,9 @@ struct Shares {
   __device__ __forceinline__ int64_t raw(int64_t c) const { return total * c / n; }
   // cut(c) when it falls into the item of units [a, b)
   __device__ __forceinline__ int64_t snapped(int64_t x, int64_t a, int64_t b) const {
-    return x - a <= head + snap ? a : b - x <= snap ? b : x;
+    const int64_t lo = a + head + snap + 1, hi = b - snap - 1;
+    if (lo > hi) return 2 * (x - a) <= b - a ? a : b;
+    return x < lo ? a : x > hi ? b : x;
   }
   // The cuts that split the item [a, b): CTAs first + 1 ... first + count begin inside it.
   __device__ __forceinline__ void inside(int64_t a, int64_t b, int* first, int* count) const {
