@@ -32,12 +32,16 @@ struct RowShare {
   int32_t item, kvh, unit, units;
 };
 // A block of the tile kernel's list: tokens t0 ... (two tiles of SeqView::tile_tokens) of sequence seq, `tiles` key
-// tiles. A CTA's share: `units` units from key tile `tile` of head kvh of block `blk` on.
+// tiles.
 struct alignas(32) TileBlk {
   int32_t seq, n, len, start, t0, tiles;
 };
-struct TileShare {
-  int32_t blk, kvh, tile, units;
+// What a CTA of the tile kernel does next: key tiles [ka, kb) of head kvh of such a block, of which its tile w sees
+// [ka, end[w]); split: not the whole item. A CTA's list begins at tile_share.x and holds tile_share.y of them.
+struct alignas(16) TileWork {
+  int32_t ka, kb, end[2];
+  int32_t len, n, start, t0;
+  int32_t seq, kvh, split, unused;
 };
 // An item (list entry, head) that lies across cuts: CTAs cta ... cta + parts - 1 each hold a part.
 struct JoinTask {
@@ -59,7 +63,8 @@ struct SeqView {
   TileBlk* blk;         // [blocks] the tile kernel's blocks
   int64_t* blk_pre;     // [blocks + 1] units (kTileHead and the key tiles, for each kv head) before each of them
   RowShare* row_share;  // [row_ctas]
-  TileShare* tile_share;// [tile_ctas]
+  int2* tile_share;     // [tile_ctas]
+  TileWork* tile_work;  // [blocks * Hkv + tile_ctas]
   JoinTask* row_join;   // [counts[2]] the row kernel's split items
   JoinTask* tile_join;  // [counts[3]] the tile kernel's
   int32_t* counts;      // [1] first rejected sequence (INT32_MAX if none), [2], [3] split items
@@ -77,6 +82,7 @@ constexpr int kRowUnit = 64;
 constexpr int kRowHead = 3;           // units that an item's fixed costs (queries, joining the warps' sums) are worth
 constexpr int kTileKeys = 128;
 constexpr int kTileSnap = 2;          // key tiles that a split costs at least
+constexpr int kTileDeal = 12;         // key tiles above the mean up to which whole items are dealt out
 constexpr int kTileHead = 3;          // key tiles that an item's fixed costs (queries, first products, output) are worth
 
 // CTAs of the row kernel on an SM: by the row limit (16 rather than 8) and the cache's type.

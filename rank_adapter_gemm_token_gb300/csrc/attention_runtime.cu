@@ -280,7 +280,7 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
   const size_t o_start = take(S * 4), o_n = take(S * 4), o_len = take(S * 4), o_table = take(S * max_pages * 4),
                o_seq = take(T * 4), o_pos = take(T * 4), o_row = take(T * 4), o_pp = take((S + 1) * 4),
                o_rs = take(S * sizeof(RowSeq)), o_rp = take((S + 1) * 8), o_blk = take(J * sizeof(TileBlk)),
-               o_bp = take((J + 1) * 8), o_rsh = take(R * sizeof(RowShare)), o_tsh = take(C * sizeof(TileShare)),
+               o_bp = take((J + 1) * 8), o_rsh = take(R * sizeof(RowShare)), o_tsh = take(C * sizeof(int2)), o_tw = take((J * n_kv_heads + C) * sizeof(TileWork)),
                o_rj = take(R * sizeof(JoinTask)), o_tj = take(C * sizeof(JoinTask)), o_counts = take(8 * 4),
                o_err = take(4), o_part = take(row_part_bytes(v)), o_tile_part = take(tile_part_bytes(v));
   cudaError_t e = cudaMalloc(&q->mem, at);
@@ -299,7 +299,8 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
     v.blk = reinterpret_cast<TileBlk*>(b + o_blk);
     v.blk_pre = reinterpret_cast<int64_t*>(b + o_bp);
     v.row_share = reinterpret_cast<RowShare*>(b + o_rsh);
-    v.tile_share = reinterpret_cast<TileShare*>(b + o_tsh);
+    v.tile_share = reinterpret_cast<int2*>(b + o_tsh);
+    v.tile_work = reinterpret_cast<TileWork*>(b + o_tw);
     v.row_join = reinterpret_cast<JoinTask*>(b + o_rj);
     v.tile_join = reinterpret_cast<JoinTask*>(b + o_tj);
     v.counts = reinterpret_cast<int32_t*>(b + o_counts);

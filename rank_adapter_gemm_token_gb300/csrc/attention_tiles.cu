@@ -24,7 +24,7 @@
 // each key it took 5000 cycles a tile against 1400 for bf16. The 64 puts a tile's largest row at the top of f16's range:
 // rows of scales 2^20 below it, which may be all that an early token sees of the tile, keep their bits. Query rows are
 // divided by their largest element so that f16 holds them.
-// Work: (block, key/value head) items of 128-key tiles one after another, an equal share to each CTA (seq_meta.cu);
+// Work: (block, key/value head) items of 128-key tiles, dealt out whole or in equal shares, a list for each CTA (seq_meta.cu);
 // parts of a split item are joined by attention_join.cu.
 // Value rows past the cached length are zeroed in shared memory, scores past a row's limit are replaced by -inf:
 // what lies there has no effect. Every wait is bounded: after 2 s a role records the timeout, stops waiting and
@@ -67,7 +67,7 @@ struct TilesCfg {
   static constexpr int kBarOff = kFactorOff + (E4M3 ? 2 * kKeys * 4 + 32 : 0);
   static constexpr int kQScaleOff = kBarOff + 512;                 // e4m3: [2][tile][128] scales of the query rows
   static constexpr int kWalkOff = kQScaleOff + (E4M3 ? 2 * 2 * 128 * 4 : 0);
-  static constexpr int kBytes = kWalkOff + 16 * 128 + 1024;
+  static constexpr int kBytes = kWalkOff + 16 * 64 + 1024;
 };
 
 // tcgen05.mma with A from TMEM.
@@ -210,54 +210,11 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, int bytes,
                : "memory");
 }
 
-// The CTA's walk over its share of the items (256-row block, key/value head), with the part [ka, kb) of the item's key
-// tiles that the CTA takes. Every role walks on its own.
-struct alignas(128) Walk {
-  int left;                     // units left in the share
-  int blk, kvh;
-  int ka, kb, tiles;
-  int n, len, first, t0;        // the block's sequence, and the first of its tokens
-  int base;                     // position of the sequence's first new token
-  int end[2];                   // tile w of the block works on key tiles [ka, end[w])
-  const int32_t* table;
-  __device__ __forceinline__ bool whole() const { return ka == 0 && kb == tiles; }
-  __device__ __forceinline__ void block(const SeqView& v) {
-    const TileBlk b = v.blk[blk];
-    n = b.n, len = b.len, first = b.start, t0 = b.t0, tiles = b.tiles;
-    table = v.table + static_cast<size_t>(b.seq) * v.max_pages;
-    base = len - n;
-  }
-  __device__ __forceinline__ void part(const SeqView& v, int from) {
-    ka = from;
-    kb = min(tiles, ka + left - (ka == 0 ? kTileHead : 0));       // (a cut inside an item lies past its head)
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int last = min(t0 + v.tile_tokens * (w + 1), n) - 1;
-      end[w] = t0 + v.tile_tokens * w < n ? max(ka, min(kb, (base + last) / kKeys + 1)) : ka;
-    }
-  }
-  __device__ __forceinline__ bool begin(const SeqView& v) {
-    const int4 s = *reinterpret_cast<const int4*>(v.tile_share + blockIdx.x);
-    left = s.w;
-    if (left <= 0) return false;
-    blk = s.x, kvh = s.y;
-    block(v);
-    part(v, s.z);
-    return true;
-  }
-  __device__ __forceinline__ bool next(const SeqView& v) {
-    left -= kb - ka + (ka == 0 ? kTileHead : 0);
-    if (left <= 0) return false;
-    if (++kvh == v.Hkv) {
-      kvh = 0;
-      ++blk;
-      block(v);
-    }
-    part(v, 0);
-    return true;
-  }
+// Where a warp is in the CTA's list of work: each role walks on its own.
+struct alignas(64) Walk {
+  TileWork it;
+  int at, last;
 };
-static_assert(sizeof(Walk) <= 128, "a walk's place in shared memory");
 
 template <int HD, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -319,24 +276,31 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;                   // S/P of tile w at 128 w, O at 256 + 128 w
 
-  // Each warp's walk lives in shared memory, moved by its first lane: the fields are read a few times an item, and
-  // a softmax thread has no registers to keep them in.
-  Walk* walks = reinterpret_cast<Walk*>(smem + C::kWalkOff);   // [16]
-  Walk& walk = walks[warp];
+  // Each warp's walk lives in shared memory: the fields are read a few times an item, and a softmax thread has no
+  // registers to keep them in.
+  Walk& walk = reinterpret_cast<Walk*>(smem + C::kWalkOff)[warp];      // [16]
+  const TileWork& it = walk.it;
+  auto load = [&](int at) {
+    constexpr int kWords = sizeof(TileWork) / 4;
+    const int x = lane < kWords ? reinterpret_cast<const int*>(v.tile_work + at)[lane] : at;
+    __syncwarp();
+    if (lane <= kWords) reinterpret_cast<int*>(&walk)[lane] = x;
+    __syncwarp();
+  };
   bool any;
   {
-    Walk first{};
-    any = first.begin(v);
-    if (lane == 0) walk = first;
+    const int2 share = v.tile_share[blockIdx.x];
+    any = share.y > 0;
+    if (any) load(share.x);
+    if (lane == 0) walk.last = share.x + share.y - 1;
     __syncwarp();
   }
-  auto advance = [&](Walk& w) {
+  auto advance = [&]() {
     __syncwarp();
-    int go = 0;
-    if (lane == 0) go = w.next(v);
-    go = __shfl_sync(0xffffffffu, go, 0);
-    __syncwarp();
-    return go != 0;
+    const int at = walk.at;
+    if (at == walk.last) return false;
+    load(at + 1);
+    return true;
   };
   bool dead = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -351,13 +315,13 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     constexpr int kDepth = E4M3 ? C::kStages : C::kRing;
     const int box = min(kv.page, kKeys), boxes = kKeys / box;
     uint32_t n = 0;                                   // tiles brought so far
-    for (bool go = any; go; go = advance(walk)) {
-      const Walk& it = walk;
+    for (bool go = any; go; go = advance()) {
+      const int32_t* table = v.table + static_cast<size_t>(it.seq) * v.max_pages;
       for (int j = it.ka; j < it.kb; ++j) {
         const int key = j * kKeys + lane * box;
         const bool mine = lane < boxes && key < it.len;
         int at = 0;
-        if (mine) at = ((it.table[key >> kv.page_log2] * v.Hkv + it.kvh) << kv.page_log2) + (key & (kv.page - 1));
+        if (mine) at = ((table[key >> kv.page_log2] * v.Hkv + it.kvh) << kv.page_log2) + (key & (kv.page - 1));
         const int count = __popc(__ballot_sync(0xffffffffu, mine));
 #pragma unroll
         for (int h = 0; h < 2; ++h, ++n) {            // the keys (and both scales), then the values
@@ -396,10 +360,9 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     uint32_t n_s = 0, n_o = 0;                        // waits done on s_full, o_full
     uint32_t n_sc = 0;                                // key tiles of the CTA so far (scale buffers)
     for (bool go = any; go;) {
-      const Walk& it = walk;
       const int tok = it.t0 + v.tile_tokens * w + row_tok;
       const bool valid = row_tok < v.tile_tokens && tok < it.n;
-      const int lim = valid ? it.base + tok : -1;
+      const int lim = valid ? it.len - it.n + tok : -1;
       // the fewest and the most keys that a row of the warp sees (rows of no token see none)
       const int low = __reduce_min_sync(0xffffffffu, valid ? lim : INT_MAX), high = __reduce_max_sync(0xffffffffu, lim);
       const int ka = it.ka, end = it.end[w];
@@ -478,11 +441,12 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             p[i / 2 + 1] = E4M3 ? pack_f16(e1.x, e1.y) : pack_bf16(e1.x, e1.y);
           }
         };
-        if constexpr (E4M3) {
+        if (E4M3 || edge) {
           // Two passes over S in small loops: the maximum, then the weights, each piece's P over columns of S that were
-          // read. Instructions bound this path: converters and softmax run different code side by side, and held as below,
-          // unrolled, the warps waited for instructions more often than they issued one (8000 tokens 621 us against 568;
-          // two pieces a turn, the next loaded ahead, 625).
+          // read. e4m3: the supply of instructions bounds it, since converters and softmax run different code side by side;
+          // held as below, unrolled, the warps waited for instructions more often than they issued one (8000 tokens 621 us
+          // against 568; two pieces a turn, the next loaded ahead, 625). bf16: for the tiles that some row of the warp
+          // does not see whole, at most two of an item, where a second unrolled copy cost registers (347 us against 335).
           const int pieces = max(0, min(kKeys / W, (seen_high + W) / W));         // that some row of the warp sees
           auto pass = [&](auto&& work) {
 #pragma unroll 1
@@ -516,7 +480,6 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           if (j == ka) {                              // a first maximum: that of the first columns
             tmem_ld(ts, xa);
             ptx::tmem_ld_wait();
-            if (edge) mask(xa, 0);
             m = fmaf(largest(xa, top), ct, off);
           }
           // One pass over S, W columns at a time: weights against the maximum so far, and the tile's own maximum. P
@@ -531,31 +494,15 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               top = largest(x, top);
               weights(x, h, neg, p + W / 2 * h);
             };
-            if (!edge) {
-              tmem_ld(ts, xa);
+            tmem_ld(ts, xa);
 #pragma unroll
-              for (int h = 0; h < kKeys / W; h += 2) {
-                ptx::tmem_ld_wait();
-                tmem_ld(ts + W * h + W, xb);
-                piece(xa, h);
-                ptx::tmem_ld_wait();
-                if (h + 2 < kKeys / W) tmem_ld(ts + W * h + 2 * W, xa);
-                piece(xb, h + 1);
-              }
-            } else {
-              // columns that no row of the warp sees are left out, the others masked one by one
-#pragma unroll
-              for (int h = 0; h < kKeys / W; ++h) {
-                if (W * h <= seen_high) {
-                  tmem_ld(ts + W * h, xa);
-                  ptx::tmem_ld_wait();
-                  mask(xa, h);
-                  piece(xa, h);
-                } else {
-#pragma unroll
-                  for (int i = 0; i < W / 2; ++i) p[W / 2 * h + i] = 0u;
-                }
-              }
+            for (int h = 0; h < kKeys / W; h += 2) {
+              ptx::tmem_ld_wait();
+              tmem_ld(ts + W * h + W, xb);
+              piece(xa, h);
+              ptx::tmem_ld_wait();
+              if (h + 2 < kKeys / W) tmem_ld(ts + W * h + 2 * W, xa);
+              piece(xb, h + 1);
             }
             top = fmaf(top, ct, off);
             if (!__any_sync(0xffffffffu, top > m + kLazy)) break;
@@ -572,9 +519,9 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       }
       n_sc += it.kb - ka;
       // While the last product runs: where the rows go, and the next item.
-      const bool part = !it.whole() && it.t0 + v.tile_tokens * w < it.n;     // of a split item, to the workspace
+      const bool part = it.split != 0 && it.t0 + v.tile_tokens * w < it.n;     // of a split item, to the workspace
       const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;             // NaN stays
-      const int64_t own = (static_cast<int64_t>(it.first + tok) * v.Hq + it.kvh * v.G + row_head) * HD;
+      const int64_t own = (static_cast<int64_t>(it.start + tok) * v.Hq + it.kvh * v.G + row_head) * HD;
       uint16_t* dst[4];                               // of the rows of the thread's four lanes, where the thread stores
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -583,7 +530,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       }
       float* mine = v.tile_part + ((2 * static_cast<int64_t>(blockIdx.x) + (ka == 0)) * 2 + w) * tile_slot(v);
       const bool worked = end > ka;
-      go = advance(walk);
+      go = advance();
       if (worked) {
         wait(&o_full[w], n_o & 1);
         ++n_o;
@@ -638,9 +585,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       } else if (warp == 9) {
         // value rows past the length, in the one tile of an item that may hold any, when the products have come to it
         uint32_t n = 1, par = 0;                      // ring position of the item's first value tile; tiles so far
-        for (bool go = any; go; go = advance(walk)) {
-          const Walk& it = walk;
-          if (it.kb * kKeys > it.len) {
+        for (bool go = any; go; go = advance()) {
+              if (it.kb * kKeys > it.len) {
             wait(v_short, par);
             par ^= 1;
             uint8_t* t = smem + C::kRingOff + (n + 2 * (it.kb - 1 - it.ka)) % C::kRing * C::kTile;
@@ -662,9 +608,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       __half2* factors = reinterpret_cast<__half2*>(smem + C::kFactorOff);           // keys' rows, values' rows
       float* maxima = reinterpret_cast<float*>(smem + C::kFactorOff + 2 * kKeys * 4);
       uint32_t n = 0;
-      for (bool go = any; go; go = advance(walk)) {
-        const Walk& it = walk;
-        for (int j = it.ka; j < it.kb; ++j) {
+      for (bool go = any; go; go = advance()) {
+          for (int j = it.ka; j < it.kb; ++j) {
           const int cut = it.len - j * kKeys;         // rows of the tile inside the sequence (any number)
 #pragma unroll 1
           for (int h = 0; h < 2; ++h, ++n) {
@@ -741,10 +686,16 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         const uint32_t id_s = idesc16(E4M3, 128, kKeys, false), id_o = idesc16(E4M3, 128, HD, true);
         uint32_t ks = 0, ks_par = 0, vs = 0, vs_par = 0;           // ring slots of K_j and V_{j-1}, their phases
         uint32_t q_par[2] = {0, 0}, p_par[2] = {0, 0}, clean_par = 0;
-        bool go = any;
-        while (go) {
-          const int ka = walk.ka, kb = walk.kb, end0 = walk.end[0], end1 = walk.end[1];
-          const bool short_tile = !E4M3 && kb * kKeys > walk.len;
+        int at = any ? walk.at : 0, len = it.len;
+        const int last = any ? walk.last : -1;
+        int4 next = *reinterpret_cast<const int4*>(&it);
+        while (at <= last) {
+          const int ka = next.x, kb = next.y, end0 = next.z, end1 = next.w;
+          const bool short_tile = !E4M3 && kb * kKeys > len;
+          if (++at <= last) {                         // the next item, long before it is wanted
+            next = *reinterpret_cast<const int4*>(v.tile_work + at);
+            len = v.tile_work[at].len;
+          }
           for (int j = ka; j <= kb; ++j) {
             if (j > ka) {
               vs = ks, vs_par = ks_par;               // the tile after K_{j-1}
@@ -793,7 +744,6 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             if (j < kb) ptx::umma_commit(&kv_empty[ks]);
           }
           // (ks is now the slot of the next item's first key tile)
-          go = walk.next(v);
         }
       }
       __syncwarp();
@@ -808,15 +758,14 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       const uint32_t bytes = static_cast<uint32_t>(v.tile_tokens * v.G * HD * 2);
       uint8_t* tile = smem + C::kQ + w * C::kTile;
       uint64_t* full = E4M3 ? &q_raw[w] : &q_full[w];
-      for (bool go = any; go; go = advance(walk)) {
-        const Walk& it = walk;
-        if (it.end[w] <= it.ka) continue;
+      for (bool go = any; go; go = advance()) {
+          if (it.end[w] <= it.ka) continue;
         wait(&q_empty[w], par ^ 1);
         if (lane == 0) {
           ptx::mbar_arrive_expect_tx(full, bytes);
 #pragma unroll
           for (int x = 0; x < C::kHalves; ++x)
-            tma_load_3d(tile + x * kHalf, &tmap_q, full, 64 * x, it.kvh * v.G, it.first + it.t0 + v.tile_tokens * w);
+            tma_load_3d(tile + x * kHalf, &tmap_q, full, 64 * x, it.kvh * v.G, it.start + it.t0 + v.tile_tokens * w);
         }
         __syncwarp();
         if (E4M3) {
