@@ -5,12 +5,13 @@
 //           the caller's may change as soon as this kernel has run. A sequence that fails is skipped
 //           (length 0: nothing is read or written for it, its rows of the attention are zero) and
 //           recorded;
-//   plan    block 0: the work of the attention kernels as prefix sums, over which their CTAs take equal
-//           shares (attention_rows.cu), or whole items dealt out, where there are enough (tile kernel, whose CTAs
-//           get lists); the other blocks: sequence, position and cache row of each token.
+//   plan    blocks 0 and 1: the work of the row kernel and of the tile kernel as prefix sums, over which their CTAs take
+//           equal shares, or whole items dealt out, where there are enough (tile kernel, whose CTAs get lists); the other
+//           blocks: sequence, position and cache row of each token.
 // Bound by latency: a few dependent loads and three block scans; the table is read once.
 #include <algorithm>
 #include <climits>
+#include <cstddef>
 
 #include "attention.h"
 #include "attention.cuh"
@@ -121,16 +122,20 @@ __device__ Cut cut_at(const Shares& sh, const int64_t* pre, int n, int Hkv, int6
   return r;
 }
 
-// Key tiles [ka, kb) of an item.
-__device__ __forceinline__ TileWork work_of(const SeqView& v, const TileBlk& b, int kvh, int ka, int kb) {
-  TileWork k{ka, kb, {ka, ka}, b.len, b.n, b.start, b.t0, b.seq, kvh, ka > 0 || kb < b.tiles, 0};
+// Key tiles [ka, kb) of an item, to a place of a list.
+__device__ __forceinline__ void put_work(const SeqView& v, int64_t place, const TileBlk& b, int kvh, int ka, int kb) {
+  int end[2];
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     const int from = b.t0 + v.tile_tokens * w, last = min(from + v.tile_tokens, b.n) - 1;
-    if (from < b.n) k.end[w] = max(ka, min(kb, (b.len - b.n + last) / kTileKeys + 1));
+    end[w] = from < b.n ? max(ka, min(kb, (b.len - b.n + last) / kTileKeys + 1)) : ka;
   }
-  return k;
+  int4* to = reinterpret_cast<int4*>(v.tile_work + place);
+  to[0] = make_int4(ka, kb, end[0], end[1]);
+  to[1] = make_int4(b.len, b.n, b.start, b.t0);
+  to[2] = make_int4(b.seq, kvh, ka > 0 || kb < b.tiles, 0);
 }
+static_assert(sizeof(TileWork) == 48 && offsetof(TileWork, len) == 16 && offsetof(TileWork, seq) == 32, "written in this order");
 
 // The shares and joins of one list of n entries; cuts: a place for kPlanThreads cuts' positions.
 template <bool TILES>
@@ -158,8 +163,7 @@ __device__ __forceinline__ void share_out(const SeqView& v, const int64_t* pre, 
       const int place = first + k;
       for (int i = threadIdx.x & 31; i < count; i += 32) {
         const TileBlk b = v.blk[(first + i) / v.Hkv];
-        v.tile_work[place + i] =
-            work_of(v, b, (first + i) % v.Hkv, i == 0 ? ka : 0, i == count - 1 && kb > 0 ? kb : b.tiles);
+        put_work(v, place + i, b, (first + i) % v.Hkv, i == 0 ? ka : 0, i == count - 1 && kb > 0 ? kb : b.tiles);
       }
       if ((threadIdx.x & 31) == 0) v.tile_share[k] = make_int2(place, some ? count : 0);
     }
@@ -168,10 +172,11 @@ __device__ __forceinline__ void share_out(const SeqView& v, const int64_t* pre, 
   __syncthreads();
 }
 
-__device__ void plan(const SeqView& v, int page_log2, int64_t* pre) {
+// The row kernel's work, or the tile kernel's (TILES).
+template <bool TILES>
+__device__ void plan(const SeqView& v, int page_log2, int64_t* pre, int64_t* cuts) {
   __shared__ int64_t sums[5][32];
-  __shared__ int64_t cuts[kPlanThreads];
-  __shared__ int joins[2];                        // split items so far (their order in the lists does not matter)
+  __shared__ int joins;                           // split items so far (their order in the lists does not matter)
   __shared__ int most, deepest;                   // key tiles of the largest block; units of the fullest hands
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t tokens = 0, units = 0, entries = 0, cached = 0, blocks = 0;      // totals of the sequences before this chunk
@@ -187,19 +192,19 @@ __device__ void plan(const SeqView& v, int page_log2, int64_t* pre) {
     block_scan(x, sums, t);
     // starts that do not ascend could name more tokens than there are: the lists hold T
     const bool over = tokens + x[0] > v.T;
-    if (over && n > 0) {
+    if (!TILES && over && n > 0) {
       atomicOr(v.err, ptx::kErrBadSeq);
       atomicMin(&v.counts[1], s);
     }
-    if (s < v.S) v.page_pre[s + 1] = static_cast<int32_t>(cached + x[3]);
-    if (u > 0) {
+    if (!TILES && s < v.S) v.page_pre[s + 1] = static_cast<int32_t>(cached + x[3]);
+    if (!TILES && u > 0) {
       const int64_t e = entries + x[2];
       v.row_seq[e - 1] = RowSeq{s, over ? 0 : n, L, start};
       v.row_pre[e] = (units + x[1]) * v.Hkv;
     }
     // the chunk's tile blocks, a warp for each sequence
     const int64_t first = blocks + x[4] - b;
-    uint32_t has = __ballot_sync(0xffffffffu, b > 0);
+    uint32_t has = __ballot_sync(0xffffffffu, TILES && b > 0);
     while (has) {
       const int i = __ffs(has) - 1;
       has &= has - 1;
@@ -223,22 +228,24 @@ __device__ void plan(const SeqView& v, int page_log2, int64_t* pre) {
     }
   }
   if (threadIdx.x == 0) {
-    v.row_pre[0] = 0;
-    v.page_pre[0] = 0;
-    v.blk_pre[0] = 0;
-    joins[0] = joins[1] = 0;
-    most = deepest = 0;
+    if (!TILES) v.row_pre[0] = v.page_pre[0] = 0;
+    if (TILES) v.blk_pre[0] = 0;
+    joins = most = deepest = 0;
   }
   __syncthreads();
   // The prefix sums once more in shared memory, where they fit: the cuts are searched in them.
-  const bool small_rows = entries < kPlanPre;
-  if (small_rows)
-    for (int64_t i = threadIdx.x; i <= entries; i += kPlanThreads) pre[i] = v.row_pre[i];
-  __syncthreads();
-  const int64_t row_total = units * v.Hkv;
-  share_out<false>(v, small_rows ? pre : v.row_pre, static_cast<int>(entries),
-                   Shares{row_total, static_cast<int>(min(static_cast<int64_t>(v.row_ctas), row_total)), kRowHead, 0}, v.row_ctas, cuts,
-                   &joins[0]);
+  if (!TILES) {
+    const bool small_rows = entries < kPlanPre;
+    if (small_rows)
+      for (int64_t i = threadIdx.x; i <= entries; i += kPlanThreads) pre[i] = v.row_pre[i];
+    __syncthreads();
+    const int64_t row_total = units * v.Hkv;
+    share_out<false>(v, small_rows ? pre : v.row_pre, static_cast<int>(entries),
+                     Shares{row_total, static_cast<int>(min(static_cast<int64_t>(v.row_ctas), row_total)), kRowHead, 0}, v.row_ctas,
+                     cuts, &joins);
+    if (threadIdx.x == 0) v.counts[2] = joins;
+    return;
+  }
   int64_t tiles = 0;
   const bool small_tiles = blocks < kPlanPre;
   for (int64_t j0 = 0; j0 < blocks; j0 += kPlanThreads) {
@@ -268,18 +275,32 @@ __device__ void plan(const SeqView& v, int page_log2, int64_t* pre) {
     int* at = reinterpret_cast<int*>(cuts);         // blocks of each class, the larger first; then where they go
     at[threadIdx.x] = 0;
     __syncthreads();
-    for (int64_t j = threadIdx.x; j < blocks; j += kPlanThreads) atomicAdd(&at[1023 - (v.blk[j].tiles >> shift)], 1);
+    // The blocks' next places in their classes; a warp's blocks of one class (often all of them) take theirs together.
+    auto places = [&](int64_t* rank) {
+      for (int64_t j0 = 0; j0 < blocks; j0 += kPlanThreads) {
+        const int64_t j = j0 + threadIdx.x;
+        const int cls = j < blocks ? 1023 - (v.blk[j].tiles >> shift) : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, cls);
+        const int leader = __ffs(same) - 1;
+        int first = 0;
+        if (lane == leader && cls >= 0) first = atomicAdd(&at[cls], __popc(same));
+        first = __shfl_sync(0xffffffffu, first, leader);
+        if (rank != nullptr && cls >= 0) rank[j] = first + __popc(same & ((1u << lane) - 1));
+      }
+    };
+    places(nullptr);
     __syncthreads();
     const int own = at[threadIdx.x], hands = static_cast<int>((items + n - 1) / n);
     int64_t x[1] = {own}, t[1];
     block_scan(x, sums, t);
     at[threadIdx.x] = static_cast<int>(x[0]) - own;
     __syncthreads();
-    auto size = [&](int64_t i) {                    // units of the i-th item by falling size
+    auto size = [&](int i) {                        // units of the i-th item by falling size
+      const int rank = i / v.Hkv;
       int lo = 0, hi = 1024;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (at[mid] <= static_cast<int>(i / v.Hkv)) lo = mid; else hi = mid;
+        if (at[mid] <= rank) lo = mid; else hi = mid;
       }
       return kTileHead + ((1024 - lo) << shift) - 1;
     };
@@ -288,55 +309,59 @@ __device__ void plan(const SeqView& v, int page_log2, int64_t* pre) {
       int64_t sum = 0;
       if (hands <= 8) {
         for (int h = 0; h < hands; ++h) {
-          const int64_t i = static_cast<int64_t>(h) * n + ((h & 1) != 0 ? n - 1 - threadIdx.x : threadIdx.x);
+          const int i = h * n + static_cast<int>((h & 1) != 0 ? n - 1 - threadIdx.x : threadIdx.x);
           if (i < items) sum += size(i);
         }
       } else if (threadIdx.x == 0) {
-        sum = max(static_cast<int64_t>(size(0)), mean + size(static_cast<int64_t>(hands - 1) * n));
+        sum = max(static_cast<int64_t>(size(0)), mean + size((hands - 1) * n));
       }
       atomicMax(&deepest, static_cast<int>(min(sum, static_cast<int64_t>(INT_MAX))));
     }
     __syncthreads();
     if (deepest <= mean + kTileDeal) {
       // (which block of a class comes first changes who does an item, not how it is done)
-      for (int64_t j = threadIdx.x; j < blocks; j += kPlanThreads) {
+      int64_t* rank = small_tiles ? pre : v.blk_pre;           // (its prefix sums are not wanted)
+      places(rank);
+      __syncthreads();
+      for (int i = threadIdx.x; i < static_cast<int>(items); i += kPlanThreads) {
+        const int j = i / v.Hkv, kvh = i - j * v.Hkv, place = static_cast<int>(rank[j]) * v.Hkv + kvh;
+        const int hand = place / n, c = place - hand * n, cta = (hand & 1) != 0 ? n - 1 - c : c;
         const TileBlk b = v.blk[j];
-        const int i0 = atomicAdd(&at[1023 - (b.tiles >> shift)], 1) * v.Hkv;
-        for (int kvh = 0; kvh < v.Hkv; ++kvh) {
-          const int hand = (i0 + kvh) / n, c = (i0 + kvh) % n;
-          const int cta = (hand & 1) != 0 ? n - 1 - c : c;
-          v.tile_work[cta * hands + hand] = work_of(v, b, kvh, 0, b.tiles);
-        }
+        put_work(v, cta * hands + hand, b, kvh, 0, b.tiles);
       }
       const int over = static_cast<int>(items - static_cast<int64_t>(hands - 1) * n);      // items of the last hand
-      __syncthreads();
       for (int cta = threadIdx.x; cta < n; cta += kPlanThreads) {
         const int c = ((hands - 1) & 1) != 0 ? n - 1 - cta : cta;
         v.tile_share[cta] = make_int2(cta * hands, hands - (c < over ? 0 : 1));
       }
-      if (threadIdx.x < 2) v.counts[2 + threadIdx.x] = joins[threadIdx.x];
+      if (threadIdx.x == 0) v.counts[3] = 0;
       return;
     }
   }
   share_out<true>(v, small_tiles ? pre : v.blk_pre, static_cast<int>(blocks),
                   Shares{tile_total, static_cast<int>(min(static_cast<int64_t>(v.tile_ctas), tile_total)), kTileHead, kTileSnap},
-                  v.tile_ctas, cuts, &joins[1]);
-  if (threadIdx.x < 2) v.counts[2 + threadIdx.x] = joins[threadIdx.x];
+                  v.tile_ctas, cuts, &joins);
+  if (threadIdx.x == 0) v.counts[3] = joins;
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
 plan_seq_kernel(const int32_t* __restrict__ q_start, SeqView v, int page_log2) {
   __shared__ alignas(16) int32_t begin[kMapSeqs + 1];
+  __shared__ int64_t cuts[kPlanThreads];
   const int S = v.S;
-  if (blockIdx.x > 0)
+  if (blockIdx.x > 1)
     for (int i = threadIdx.x; i <= S && S > 0; i += kPlanThreads) begin[i] = q_start[i];
   ptx::grid_dependency_wait();        // the check's results
-  if (blockIdx.x == 0) {
-    plan(v, page_log2, reinterpret_cast<int64_t*>(begin));
+  if (blockIdx.x < 2) {
+    int64_t* pre = reinterpret_cast<int64_t*>(begin);
+    if (blockIdx.x == 0)
+      plan<false>(v, page_log2, pre, cuts);
+    else
+      plan<true>(v, page_log2, pre, cuts);
     return;
   }
   __syncthreads();
-  const int t = (blockIdx.x - 1) * kPlanThreads + threadIdx.x;
+  const int t = (blockIdx.x - 2) * kPlanThreads + threadIdx.x;
   if (t >= v.T) return;
   int lo = 0, hi = S;                 // the last s with begin[s] <= t (the starts ascend, or are rejected below)
   while (hi - lo > 1) {
@@ -371,7 +396,7 @@ cudaError_t launch_build_seq(const int32_t* q_start, const int32_t* kv_len, cons
   if (e != cudaSuccess) return e;
   note_launch_begin(kKindSeq, st);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(1 + (s.T + kPlanThreads - 1) / kPlanThreads);
+  cfg.gridDim = dim3(2 + (s.T + kPlanThreads - 1) / kPlanThreads);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
