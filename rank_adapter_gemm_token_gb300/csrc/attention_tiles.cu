@@ -6,7 +6,7 @@
 // block at once, so that one tile's softmax runs beside the other's products:
 //   warps 0-3, 4-7  one softmax warpgroup for each tile, a thread for each row: S from TMEM, running maximum and
 //                   sum in base 2, P back to TMEM as 16-bit in place of S, at the end O / sum to global memory.
-//                   The maximum moves only when a score passes it by 2^8, so O is rescaled rarely.
+//                   The maximum moves only when a score passes it by 2^8 (e4m3: 2^4), so O is rescaled rarely.
 //   warps 8-11      bf16: the first brings keys and values of 128 tokens at a time into a ring of shared-memory tiles
 //                   by TMA boxes of whole pages (a lane for each page), the second clears value rows past the
 //                   sequence's length. e4m3: warp 14 brings the codes, all four turn them into f16 in the ring's tiles.
@@ -43,7 +43,13 @@ namespace {
 constexpr int kThreads = 512;               // 128 registers each at launch, shared out again by role: 152, 104, 104
 constexpr int kKeys = kTileKeys;              // 128
 constexpr int kHalf = kKeys * 128;            // bytes of 128 rows of 64 16-bit elements (one swizzled half tile)
-constexpr float kLazy = 8.0f;                 // log2 of the largest exponential
+// log2 of the largest exponential; e4m3: and of the factor that lifts P in f16, whose normal numbers then reach down to
+// weights of 2^-24 (their values may be that much larger than the others), while P, a scale's mantissa in it, stays below
+// 2^15. (A limit of 4 in place of 8 rescales O more often: 552 us against 548 at 8000 tokens; one of 2 573.)
+template <bool E4M3>
+constexpr float kLazy = E4M3 ? 4.0f : 8.0f;
+template <bool E4M3>
+constexpr float kUp = E4M3 ? 10.0f : 0.0f;
 constexpr int kLiftLog2 = 6;                  // e4m3: a tile's largest row is scaled to codes of 64 times their value
 constexpr float kLift = 64.0f;
 constexpr float kLeastScale = 0x1p-100f;      // value scales below count as zero (those written here are above 2^-69)
@@ -419,9 +425,6 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             tmem_st(to + W * i, xb);
           }
         };
-        // e4m3: P is f16, and a weight of 2^-24 may multiply values that much larger than the largest weight's: P is lifted
-        // by 2^6, l with it, which leaves it below 2^15 (2^8 and the scale's mantissa) and O / l as it is
-        constexpr float up = E4M3 ? kLiftLog2 : 0.f;
         // the weights of columns W h ... against the maximum m, into p
         auto weights = [&](uint32_t (&x)[W], int h, uint64_t neg, uint32_t* p) {
 #pragma unroll
@@ -461,10 +464,10 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           top = fmaf(top, ct, off);
           if (j == ka)
             m = top;
-          else if (__any_sync(0xffffffffu, top > m + kLazy))
-            rescale(top > m + kLazy ? top : m);
+          else if (__any_sync(0xffffffffu, top > m + kLazy<E4M3>))
+            rescale(top > m + kLazy<E4M3> ? top : m);
           const float mm = m == -INFINITY ? 0.f : m;
-          const uint64_t neg = pair(off - mm + up, off - mm + up);
+          const uint64_t neg = pair(off - mm + kUp<E4M3>, off - mm + kUp<E4M3>);
           uint32_t p[W / 2];
           pass([&](uint32_t (&x)[W], int h) {
             weights(x, h, neg, p);
@@ -505,8 +508,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               piece(xb, h + 1);
             }
             top = fmaf(top, ct, off);
-            if (!__any_sync(0xffffffffu, top > m + kLazy)) break;
-            rescale(top > m + kLazy ? top : m);
+            if (!__any_sync(0xffffffffu, top > m + kLazy<E4M3>)) break;
+            rescale(top > m + kLazy<E4M3> ? top : m);
           }
           tmem_st_x32(ts, p);
           tmem_st_x32(ts + 32, p + 32);

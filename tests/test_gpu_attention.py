@@ -158,6 +158,28 @@ def test_blocks_of_one_tile_between_others(layer, kind):
     st.check(o)
 
 
+# Steps with more blocks of rows than there are CTAs, which the tile kernel takes whole: a few each, of very different
+# lengths; many each; more than the plan keeps in shared memory.
+DEALT = [
+    ([700, 90, 333, 512, 61, 900, 40], [0, 300, 0, 64, 700, 0, 129], 32, 8, 128),
+    ([17 + 7 * i % 44 for i in range(200)], [13 * i % 90 for i in range(200)], 8, 8, 64),
+    ([1 + i % 2 for i in range(4200)], [i % 5 for i in range(4200)], 24, 1, 64),
+]
+
+
+# (Not the second with e4m3: its scales, spread over 2^40, leave sums to weights of 2^-54, which are zero in f16.)
+@pytest.mark.parametrize("case,kind", [(0, "bf16"), (1, "bf16"), (2, "bf16"), (0, "e4m3"), (2, "e4m3")])
+def test_whole_blocks_dealt_out(layer, case, kind):
+    n, ctx, hq, hkv, hd = DEALT[case]
+    st = Step(layer, n, ctx, hq, hkv, hd, 32, kind, seed=20 + case)
+    o = st.run()
+    st.seq.status()
+    st.check(o)
+    for _ in range(3):
+        st.build()
+        assert torch.equal(o, st.run()), "who takes a block changes the result"
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_large_scores_and_rising_maxima(layer, kind):
     """Scores of tens to hundreds: the running maximum moves often, and late."""
