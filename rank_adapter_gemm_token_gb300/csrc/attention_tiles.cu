@@ -171,17 +171,6 @@ __device__ __forceinline__ void turn4(uint32_t (&z)[32], int lane) {
     }
   }
 }
-// 32 bytes, in one store where the output is 32-byte aligned.
-__device__ __forceinline__ void store32(uint16_t* p, const uint32_t* x, bool wide) {
-  if (!wide) {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(x[4], x[5], x[6], x[7]);
-    return;
-  }
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
-               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-               : "memory");
-}
 // Barrier of the four warps that turn codes into f16.
 __device__ __forceinline__ void converters_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // Eight e4m3 codes as f16, times a factor.

@@ -18,7 +18,8 @@
 //
 // kv_read: whole sequences' cached rows as dense bf16 rows [token, head, hd]; a copy (bf16) or code * scale
 // rounded once (e4m3). Bound: HBM. A warp takes a run of consecutive (page, head) units, so that only its first one
-// searches for its sequence.
+// searches for its sequence. e4m3: a lane's 16 codes are 32 bytes of output, written in one store: in two, each with half
+// of every sector, 64000 tokens of 8 heads took 81 us in place of 67 (5.6 TB/s of codes, scales and rows together).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -242,6 +243,7 @@ kv_read_kernel(const int32_t* __restrict__ row_start, int64_t rows, uint16_t* __
   const int64_t end = units * (w + 1) / warps;
   if (u >= end) return;
   const int e = lane % kLanes * kE, r0 = lane / kLanes;
+  const bool wide = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
   int g = static_cast<int>(u / kv.Hkv), h = static_cast<int>(u - static_cast<int64_t>(g) * kv.Hkv);
   int sq = last_at_most(s.page_pre, s.S, g);
   while (u < end) {
@@ -273,10 +275,10 @@ kv_read_kernel(const int32_t* __restrict__ row_start, int64_t rows, uint16_t* __
             if (r >= cnt) break;
             const int64_t to = ((dst + r) * kv.Hkv + h) * HD + e;
             if (E4M3) {
-              reinterpret_cast<uint4*>(k_out + to)[0] = e4m3_times(make_uint2(a[k].x, a[k].y), ks[k]);
-              reinterpret_cast<uint4*>(k_out + to)[1] = e4m3_times(make_uint2(a[k].z, a[k].w), ks[k]);
-              reinterpret_cast<uint4*>(v_out + to)[0] = e4m3_times(make_uint2(c[k].x, c[k].y), vs[k]);
-              reinterpret_cast<uint4*>(v_out + to)[1] = e4m3_times(make_uint2(c[k].z, c[k].w), vs[k]);
+              uint4 y[2] = {e4m3_times(make_uint2(a[k].x, a[k].y), ks[k]), e4m3_times(make_uint2(a[k].z, a[k].w), ks[k])};
+              store32(k_out + to, &y[0].x, wide);
+              y[0] = e4m3_times(make_uint2(c[k].x, c[k].y), vs[k]), y[1] = e4m3_times(make_uint2(c[k].z, c[k].w), vs[k]);
+              store32(v_out + to, &y[0].x, wide);
             } else {
               *reinterpret_cast<uint4*>(k_out + to) = a[k];
               *reinterpret_cast<uint4*>(v_out + to) = c[k];
