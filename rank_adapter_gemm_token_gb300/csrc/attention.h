@@ -81,8 +81,8 @@ struct SeqView {
 constexpr int kRowUnit = 64;
 constexpr int kRowHead = 3;           // units that an item's fixed costs (queries, joining the warps' sums) are worth
 constexpr int kTileKeys = 128;
-constexpr int kTileSnap = 2;          // key tiles that a split costs at least
-constexpr int kTileDeal = 12;         // key tiles above the mean up to which whole items are dealt out
+constexpr int kTileSnap = 2;          // key tiles that a split costs at least (1 and 0: a prompt of 3000 tokens in shares 93, 97 us for 87)
+constexpr int kTileDeal = 12;         // key tiles above the mean up to which whole items are dealt out (6: 6 chunks of 300 on 4000 137 us for 108)
 constexpr int kTileHead = 3;          // key tiles that an item's fixed costs (queries, first products, output) are worth
 
 // CTAs of the row kernel on an SM: by the row limit (16 rather than 8) and the cache's type.

@@ -8,7 +8,7 @@
 //   - work = (sequence, key/value head) items of 64-key units, laid out one after another; every CTA takes an
 //     equal share of the units whatever the sequences' lengths (Shares), so one long sequence and many short
 //     ones both fill the GPU. An item across a cut leaves partial sums (with their maximum) in the step's
-//     workspace and the CTA that comes last joins them in key order: the result does not depend on arrival.
+//     workspace, which attention_join.cu joins in the order of the parts.
 //   - a warp takes 16 keys of each unit, through its own ring of stages filled by cp.async (the next item's
 //     keys are already on their way while one item is finished), with no barrier between warps inside an item.
 //   - the products run on the warp-level tensor instructions with the keys as the M side: S^T = K Q^T and
@@ -22,6 +22,9 @@
 //     by their largest element, so f16 holds them too.
 // Keys at or past a row's limit are replaced by -inf by selection, and rows past the cached length are
 // zero-filled on load, so what lies there (NaN included) has no effect.
+// Measured with the join, 32 heads of 128 on 8, the cache's bytes over the time of a call: 256 sequences of 200-2000 tokens
+// bf16 171 us, 6.5 TB/s; e4m3 106 us, 5.8 TB/s; one of 131000 tokens 86 us, 6.2 TB/s (copy: 6.8). One of 500 tokens: 4.5 us
+// and the join's launch.
 #include <algorithm>
 
 #include "attention.h"

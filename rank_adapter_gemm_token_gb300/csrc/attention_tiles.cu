@@ -26,6 +26,10 @@
 // divided by their largest element so that f16 holds them.
 // Work: (block, key/value head) items of 128-key tiles, dealt out whole or in equal shares, a list for each CTA (seq_meta.cu);
 // parts of a split item are joined by attention_join.cu.
+// Measured, 32 heads of 128 on 8: one prompt of 8000 tokens 335 us, 1565 TFLOP/s (tcgen05 busy for 0.6 to 0.7 of the cycles; the
+// rest is a softmax that its own products wait for, TMEM being full with two tiles); 512 tokens on 32000 195 us, 1390;
+// 8 x 512 tokens 33 us, 520: of an item's first and last tile about 4400 cycles, 1.5 tiles, overlap with nothing. e4m3:
+// 8000 tokens 552 us, 950.
 // Value rows past the cached length are zeroed in shared memory, scores past a row's limit are replaced by -inf:
 // what lies there has no effect. Every wait is bounded: after 2 s a role records the timeout, stops waiting and
 // runs on to the end.
