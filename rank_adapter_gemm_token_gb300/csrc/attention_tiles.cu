@@ -67,6 +67,8 @@ struct TilesCfg {
   static constexpr int kStages = HD == 128 ? 3 : 6;                // tiles of codes on their way
   static constexpr int kSegs = HD / 16;                            // 16-byte segments of a row of codes
   static constexpr int kScaleBufs = 4;
+  // registers of a softmax thread and of the others: together those of two threads at launch
+  static constexpr int kSoftmaxRegs = E4M3 ? 136 : 152, kOtherRegs = 256 - kSoftmaxRegs;
   static constexpr int kQ = 0;
   static constexpr int kRingOff = 2 * kTile;
   static constexpr int kCodeOff = kRingOff + kRing * kTile;
@@ -350,7 +352,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
 
   if (warp < 8) {
     // ------------------------------------------------------------------ softmax of tile w
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
     const int w = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + 128 * w, to = tmem + lanes + 256 + 128 * w;
@@ -574,7 +576,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------------ keys and values
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (!E4M3) {
       if (warp == 8) {
         bring();
@@ -582,7 +584,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         // value rows past the length, in the one tile of an item that may hold any, when the products have come to it
         uint32_t n = 1, par = 0;                      // ring position of the item's first value tile; tiles so far
         for (bool go = any; go; go = advance()) {
-              if (it.kb * kKeys > it.len) {
+          if (it.kb * kKeys > it.len) {
             wait(v_short, par);
             par ^= 1;
             uint8_t* t = smem + C::kRingOff + (n + 2 * (it.kb - 1 - it.ka)) % C::kRing * C::kTile;
@@ -605,7 +607,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       float* maxima = reinterpret_cast<float*>(smem + C::kFactorOff + 2 * kKeys * 4);
       uint32_t n = 0;
       for (bool go = any; go; go = advance()) {
-          for (int j = it.ka; j < it.kb; ++j) {
+        for (int j = it.ka; j < it.kb; ++j) {
           const int cut = it.len - j * kKeys;         // rows of the tile inside the sequence (any number)
 #pragma unroll 1
           for (int h = 0; h < 2; ++h, ++n) {
@@ -675,7 +677,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (warp == 12) {
       // ---------------------------------------------------------------- products
       if (elect_one()) {
