@@ -7,6 +7,8 @@
 
 #include <cstdint>
 
+#include "attention.h"
+
 namespace mlora {
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -105,5 +107,85 @@ struct Shares {
     *count = static_cast<int>(c1 >= c0 ? c1 - c0 + 1 : 0);
   }
 };
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Joining the parts of split attention items.
+constexpr int kPartsAhead = 8;           // parts asked for at once
+__device__ __forceinline__ float inverse(float total) {
+  return total > 0.f ? 1.0f / total : total == 0.f ? 0.f : total;      // an empty row is zero; NaN stays
+}
+
+// Running maximum, sum of weights and four weighted value sums.
+struct Sums {
+  float top, total;
+  float4 x;
+  __device__ __forceinline__ void add(float m, float l, const float4& y) {
+    if (m == -INFINITY) return;       // (a part that saw none of the row's keys has no sums)
+    const float up = fmaxf(top, m);
+    const float f = exp2_approx(top - up), g = exp2_approx(m - up);
+    top = up;
+    total = total * f + l * g;
+    x.x = x.x * f + y.x * g;
+    x.y = x.y * f + y.y * g;
+    x.z = x.z * f + y.z * g;
+    x.w = x.w * f + y.w * g;
+  }
+};
+
+// Joins the parts of a row kernel's item, `rows` rows (token, head of the group) from `o` on: parts CTAs from `cta` on hold one.
+// All threads of the block; sx, sm: a place for each.
+template <int HD, int THREADS>
+__device__ __forceinline__ void join_rows(uint16_t* o, const SeqView& v, int rows, int cta, int parts, float4* sx, float2* sm) {
+  constexpr int kQuads = HD / 4;         // groups of four columns
+  const int elements = rows * kQuads;
+  const int64_t slot = row_slot(v);
+  const float* base = v.row_part + 2 * static_cast<int64_t>(cta) * slot;      // part k > 0: base + 2 k slot
+  // threads beyond the elements take a share of the parts
+  const int groups = max(1, THREADS / elements);
+  for (int i0 = 0; i0 < elements; i0 += THREADS) {
+    const int e = groups > 1 ? static_cast<int>(threadIdx.x) % elements : i0 + static_cast<int>(threadIdx.x);
+    const int g = groups > 1 ? static_cast<int>(threadIdx.x) / elements : 0;
+    const bool mine = e < elements && g < groups;
+    const int r = mine ? e / kQuads : 0, h = e % kQuads * 4;
+    Sums z{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (mine) {
+      for (int k0 = g; k0 < parts; k0 += kPartsAhead * groups) {
+        float2 ml[kPartsAhead];
+        float4 y[kPartsAhead];
+#pragma unroll
+        for (int k = 0; k < kPartsAhead; ++k) {
+          const int part = min(k0 + k * groups, parts - 1);
+          const float* p = base + (part == 0 ? slot : 2 * part * slot);
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(p + v.row_limit * HD + 2 * r));
+          y[k] = __ldcg(reinterpret_cast<const float4*>(p + r * HD + h));
+        }
+#pragma unroll
+        for (int k = 0; k < kPartsAhead; ++k)
+          if (k0 + k * groups < parts) z.add(ml[k].x, ml[k].y, y[k]);
+      }
+    }
+    if (groups > 1) {
+      sm[threadIdx.x] = make_float2(z.top, z.total);
+      sx[threadIdx.x] = z.x;
+      __syncthreads();
+      if (mine && g == 0)
+        for (int k = 1; k < groups; ++k) {
+          const float2 ml = sm[threadIdx.x + k * elements];
+          z.add(ml.x, ml.y, sx[threadIdx.x + k * elements]);
+        }
+      __syncthreads();
+    }
+    if (mine && g == 0) {
+      const float inv = inverse(z.total);
+      *reinterpret_cast<uint2*>(o + (static_cast<int64_t>(r / v.G) * v.Hq + r % v.G) * HD + h) =
+          make_uint2(pack_bf16(z.x.x * inv, z.x.y * inv), pack_bf16(z.x.z * inv, z.x.w * inv));
+    }
+  }
+}
 
 }  // namespace mlora

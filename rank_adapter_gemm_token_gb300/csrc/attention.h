@@ -28,8 +28,11 @@ struct KvView {
 struct RowSeq {
   int32_t seq, n, len, start;
 };
-struct RowShare {
+// Where the share begins (ends) inside an item, first_cta (last_cta) is the CTA that has that item's first part, of
+// first_parts (last_parts); otherwise the parts are 0.
+struct alignas(16) RowShare {
   int32_t item, kvh, unit, units;
+  int32_t first_cta, first_parts, last_cta, last_parts;
 };
 // A block of the tile kernel's list: tokens t0 ... (two tiles of SeqView::tile_tokens) of sequence seq, `tiles` key
 // tiles.
@@ -65,9 +68,9 @@ struct SeqView {
   RowShare* row_share;  // [row_ctas]
   int2* tile_share;     // [tile_ctas]
   TileWork* tile_work;  // [blocks * Hkv + tile_ctas]
-  JoinTask* row_join;   // [counts[2]] the row kernel's split items
-  JoinTask* tile_join;  // [counts[3]] the tile kernel's
-  int32_t* counts;      // [1] first rejected sequence (INT32_MAX if none), [2], [3] split items
+  int32_t* row_there;   // [row_ctas] parts there of the item whose first part a CTA has (0 between calls)
+  JoinTask* tile_join;  // [counts[2]] the tile kernel's split items
+  int32_t* counts;      // [1] first rejected sequence (INT32_MAX if none), [2] split items
   uint32_t* err;        // device error word (ptx::kErr* bits)
   float* row_part;      // partial results of the row kernel's split items
   float* tile_part;     // of the tile kernel's
@@ -110,7 +113,7 @@ cudaError_t launch_attention_rows(const uint16_t* q, uint16_t* o, float scale, c
                                   cudaStream_t st);
 cudaError_t launch_attention_tiles(const CUtensorMap& tk, const CUtensorMap& tv, const uint16_t* q, uint16_t* o,
                                    float scale, const KvView& kv, const SeqView& s, cudaStream_t st);
-cudaError_t launch_attention_join(uint16_t* o, const SeqView& s, bool tiles, cudaStream_t st);
+cudaError_t launch_attention_join(uint16_t* o, const SeqView& s, cudaStream_t st);
 // K and V as matrices [n_pages * Hkv * page, hd] in boxes of min(page, 128) rows x 64 columns (bf16, swizzled) or
 // whole rows (e4m3).
 bool make_kv_maps(const KvView& kv, CUtensorMap* k, CUtensorMap* v);

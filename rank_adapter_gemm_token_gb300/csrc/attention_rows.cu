@@ -8,7 +8,8 @@
 //   - work = (sequence, key/value head) items of 64-key units, laid out one after another; every CTA takes an
 //     equal share of the units whatever the sequences' lengths (Shares), so one long sequence and many short
 //     ones both fill the GPU. An item across a cut leaves partial sums (with their maximum) in the step's
-//     workspace, which attention_join.cu joins in the order of the parts.
+//     workspace, and the CTA that comes last with one joins them in their order: the result does not depend on who it is.
+//     (As a launch of its own that took as long on the GPU, and a small call 2 us more: 10.4 us against 8.5 for one token.)
 //   - a warp takes 16 keys of each unit, through its own ring of stages filled by cp.async (the next item's
 //     keys are already on their way while one item is finished), with no barrier between warps inside an item.
 //   - the products run on the warp-level tensor instructions with the keys as the M side: S^T = K Q^T and
@@ -22,9 +23,8 @@
 //     by their largest element, so f16 holds them too.
 // Keys at or past a row's limit are replaced by -inf by selection, and rows past the cached length are
 // zero-filled on load, so what lies there (NaN included) has no effect.
-// Measured with the join, 32 heads of 128 on 8, the cache's bytes over the time of a call: 256 sequences of 200-2000 tokens
-// bf16 171 us, 6.5 TB/s; e4m3 106 us, 5.8 TB/s; one of 131000 tokens 86 us, 6.2 TB/s (copy: 6.8). One of 500 tokens: 4.5 us
-// and the join's launch.
+// Measured, 32 heads of 128 on 8, the cache's bytes over the time of a call: 256 sequences of 200-2000 tokens
+// bf16 171 us, 6.5 TB/s; e4m3 106 us, 5.8 TB/s; one of 131000 tokens 86 us, 6.2 TB/s (copy: 6.8); one of 500 tokens 8.5 us.
 #include <algorithm>
 
 #include "attention.h"
@@ -108,11 +108,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // A place in the list of units: unit u of head kvh of list entry i.
@@ -474,6 +469,23 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
       }
     }
     __syncthreads();
+    if (!whole) {
+      // the CTA that comes last with a part joins them all
+      const int4 ends = reinterpret_cast<const int4*>(v.row_share + blockIdx.x)[1];
+      const int cta = at.u > 0 ? ends.x : ends.z, parts = at.u > 0 ? ends.y : ends.w;
+      if (threadIdx.x == 0) {
+        __threadfence();
+        const bool last = atomicAdd(v.row_there + cta, 1) == parts - 1;
+        if (last) v.row_there[cta] = 0;               // for the next call
+        __threadfence();
+        ml_sh[0] = last ? 1.f : 0.f;
+      }
+      __syncthreads();
+      if (ml_sh[0] != 0.f)
+        join_rows<HD, kThreads>(o + (static_cast<int64_t>(first) * v.Hq + at.kvh * v.G) * HD, v, rows, cta, parts,
+                                reinterpret_cast<float4*>(o_sh), reinterpret_cast<float2*>(o_sh + 4 * kThreads));
+      __syncthreads();
+    }
     if (done < n_chunks) {
       at.u = u_end - 1;
       at.next(v);

@@ -281,7 +281,7 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
                o_seq = take(T * 4), o_pos = take(T * 4), o_row = take(T * 4), o_pp = take((S + 1) * 4),
                o_rs = take(S * sizeof(RowSeq)), o_rp = take((S + 1) * 8), o_blk = take(J * sizeof(TileBlk)),
                o_bp = take((J + 1) * 8), o_rsh = take(R * sizeof(RowShare)), o_tsh = take(C * sizeof(int2)), o_tw = take((J * n_kv_heads + C) * sizeof(TileWork)),
-               o_rj = take(R * sizeof(JoinTask)), o_tj = take(C * sizeof(JoinTask)), o_counts = take(8 * 4),
+               o_there = take(R * 4), o_tj = take(C * sizeof(JoinTask)), o_counts = take(8 * 4),
                o_err = take(4), o_part = take(row_part_bytes(v)), o_tile_part = take(tile_part_bytes(v));
   cudaError_t e = cudaMalloc(&q->mem, at);
   if (e == cudaSuccess) {
@@ -301,7 +301,7 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
     v.row_share = reinterpret_cast<RowShare*>(b + o_rsh);
     v.tile_share = reinterpret_cast<int2*>(b + o_tsh);
     v.tile_work = reinterpret_cast<TileWork*>(b + o_tw);
-    v.row_join = reinterpret_cast<JoinTask*>(b + o_rj);
+    v.row_there = reinterpret_cast<int32_t*>(b + o_there);
     v.tile_join = reinterpret_cast<JoinTask*>(b + o_tj);
     v.counts = reinterpret_cast<int32_t*>(b + o_counts);
     v.err = reinterpret_cast<uint32_t*>(b + o_err);
@@ -428,7 +428,7 @@ mlora_status mlora_attention(mlora_kv_t kv, mlora_seq_t q, const mlora_bf16* que
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_attention_rows(query, out, scale, kv->view, v, s);
   if (e == cudaSuccess && q->tiles) e = launch_attention_tiles(kv->map_k, kv->map_v, query, out, scale, kv->view, v, s);
-  if (e == cudaSuccess) e = launch_attention_join(out, v, q->tiles, s);
+  if (e == cudaSuccess && q->tiles) e = launch_attention_join(out, v, s);
   if (e != cudaSuccess) return report_cuda_error(e, "attention launch");
   q->last_stream = s;
   return MLORA_OK;

@@ -29,7 +29,7 @@
 // Measured, 32 heads of 128 on 8: one prompt of 8000 tokens 335 us, 1565 TFLOP/s (tcgen05 busy for 0.6 to 0.7 of the cycles; the
 // rest is a softmax that its own products wait for, TMEM being full with two tiles); 512 tokens on 32000 195 us, 1390;
 // 8 x 512 tokens 33 us, 520: of an item's first and last tile about 4400 cycles, 1.5 tiles, overlap with nothing. e4m3:
-// 8000 tokens 552 us, 950.
+// 8000 tokens 540 us, 970.
 // Value rows past the cached length are zeroed in shared memory, scores past a row's limit are replaced by -inf:
 // what lies there has no effect. Every wait is bounded: after 2 s a role records the timeout, stops waiting and
 // runs on to the end.
@@ -44,7 +44,7 @@
 namespace mlora {
 namespace {
 
-constexpr int kThreads = 512;               // 128 registers each at launch, shared out again by role: 152, 104, 104
+constexpr int kThreads = 512;               // 128 registers each at launch, shared out again by role (kSoftmaxRegs)
 constexpr int kKeys = kTileKeys;              // 128
 constexpr int kHalf = kKeys * 128;            // bytes of 128 rows of 64 16-bit elements (one swizzled half tile)
 // log2 of the largest exponential; e4m3: and of the factor that lifts P in f16, whose normal numbers then reach down to
@@ -190,11 +190,6 @@ __device__ __forceinline__ uint4 scaled(uint32_t x, uint32_t y, __half2 f) {
     h[i] = *reinterpret_cast<const uint32_t*>(&r);
   }
   return make_uint4(h[0], h[1], h[2], h[3]);
-}
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 // 3-D tiled load; c0 is the innermost coordinate.
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, uint64_t* bar, int c0, int c1, int c2) {

@@ -115,7 +115,7 @@ __device__ Cut cut_at(const Shares& sh, const int64_t* pre, int n, int Hkv, int6
   if (r.at > a && r.at < b) {
     int first, cuts;
     sh.inside(a, b, &first, &cuts);
-    if (c == first + 1) r.join = JoinTask{r.item, r.kvh, first, cuts + 1};
+    r.join = JoinTask{r.item, r.kvh, first, cuts + 1};
     r.unit = static_cast<int>(r.at - a);
   } else if (r.at == b) {              // the next item
     if (++r.kvh == Hkv) r.kvh = 0, ++r.item;
@@ -138,10 +138,10 @@ __device__ __forceinline__ void put_work(const SeqView& v, int64_t place, const 
 }
 static_assert(sizeof(TileWork) == 48 && offsetof(TileWork, len) == 16 && offsetof(TileWork, seq) == 32, "written in this order");
 
-// The shares and joins of one list of n entries; cuts: a place for kPlanThreads cuts' positions.
+// The shares and joins of one list of n entries; cuts, parts: places for kPlanThreads cuts' positions and items' parts.
 template <bool TILES>
 __device__ __forceinline__ void share_out(const SeqView& v, const int64_t* pre, int n, const Shares& sh, int ctas, int64_t* cuts,
-                                          int* joins) {
+                                          int64_t* parts, int* joins) {
   const int c = threadIdx.x;
   Cut cut{n, 0, 0, sh.total, JoinTask{0, 0, 0, 0}};
   if (c <= sh.n && sh.total > 0) cut = cut_at(sh, pre, n, v.Hkv, c);
@@ -150,9 +150,16 @@ __device__ __forceinline__ void share_out(const SeqView& v, const int64_t* pre, 
   const int64_t number = static_cast<int64_t>(cut.item) * v.Hkv + cut.kvh;
   cuts[c] = TILES ? number << 32 | max(cut.unit - kTileHead, 0) : cut.at - kRowHead * (number + (cut.unit > 0));
   __syncthreads();
+  if (!TILES) {                                   // (the prefix sums are not wanted any more)
+    parts[c] = static_cast<int64_t>(cut.join.cta) << 32 | cut.join.parts;
+    __syncthreads();
+  }
   if (!TILES && c < ctas) {
     const int units = c < sh.n && sh.total > 0 ? static_cast<int>(cuts[c + 1] - cuts[c]) : 0;
-    v.row_share[c] = RowShare{cut.item, cut.kvh, max(cut.unit - kRowHead, 0), units};
+    const int64_t next = parts[c + 1];
+    v.row_share[c] = RowShare{cut.item, cut.kvh, max(cut.unit - kRowHead, 0), units, cut.join.cta, cut.join.parts,
+                              static_cast<int>(next >> 32), static_cast<int>(next)};
+    v.row_there[c] = 0;
   }
   if (TILES) {
     // a warp to a CTA's list; before it lie that many items and one place for each cut
@@ -169,7 +176,7 @@ __device__ __forceinline__ void share_out(const SeqView& v, const int64_t* pre, 
       if ((threadIdx.x & 31) == 0) v.tile_share[k] = make_int2(place, some ? count : 0);
     }
   }
-  if (cut.join.parts > 0) (TILES ? v.tile_join : v.row_join)[atomicAdd(joins, 1)] = cut.join;
+  if (TILES && cut.join.parts > 0 && c == cut.join.cta + 1) v.tile_join[atomicAdd(joins, 1)] = cut.join;
   __syncthreads();
 }
 
@@ -243,8 +250,7 @@ __device__ void plan(const SeqView& v, int page_log2, int64_t* pre, int64_t* cut
     const int64_t row_total = units * v.Hkv;
     share_out<false>(v, small_rows ? pre : v.row_pre, static_cast<int>(entries),
                      Shares{row_total, static_cast<int>(min(static_cast<int64_t>(v.row_ctas), row_total)), kRowHead, 0}, v.row_ctas,
-                     cuts, &joins);
-    if (threadIdx.x == 0) v.counts[2] = joins;
+                     cuts, pre, &joins);
     return;
   }
   int64_t tiles = 0;
@@ -335,14 +341,14 @@ __device__ void plan(const SeqView& v, int page_log2, int64_t* pre, int64_t* cut
         const int c = ((hands - 1) & 1) != 0 ? n - 1 - cta : cta;
         v.tile_share[cta] = make_int2(cta * hands, hands - (c < over ? 0 : 1));
       }
-      if (threadIdx.x == 0) v.counts[3] = 0;
+      if (threadIdx.x == 0) v.counts[2] = 0;
       return;
     }
   }
   share_out<true>(v, small_tiles ? pre : v.blk_pre, static_cast<int>(blocks),
                   Shares{tile_total, static_cast<int>(min(static_cast<int64_t>(v.tile_ctas), tile_total)), kTileHead, kTileSnap},
-                  v.tile_ctas, cuts, &joins);
-  if (threadIdx.x == 0) v.counts[3] = joins;
+                  v.tile_ctas, cuts, pre, &joins);
+  if (threadIdx.x == 0) v.counts[2] = joins;
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
