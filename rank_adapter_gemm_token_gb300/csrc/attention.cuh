@@ -137,16 +137,23 @@ struct Sums {
   }
 };
 
-// Joins the parts of a row kernel's item, `rows` rows (token, head of the group) from `o` on: parts CTAs from `cta` on hold one.
-// All threads of the block; sx, sm: a place for each.
+// Joins `count` parts of a row kernel's item of `rows` rows (token, head of the group): those from part `from` on, `step` apart,
+// of the item whose first part CTA `cta` has. The result goes to the output rows from o on, or, without o, to the place of part
+// `from`. All threads of the block; sx, sm: a place for each.
 template <int HD, int THREADS>
-__device__ __forceinline__ void join_rows(uint16_t* o, const SeqView& v, int rows, int cta, int parts, float4* sx, float2* sm) {
+__device__ __forceinline__ void join_rows(uint16_t* o, const SeqView& v, int rows, int cta, int from, int step, int count,
+                                          float4* sx, float2* sm) {
   constexpr int kQuads = HD / 4;         // groups of four columns
   const int elements = rows * kQuads;
   const int64_t slot = row_slot(v);
-  const float* base = v.row_part + 2 * static_cast<int64_t>(cta) * slot;      // part k > 0: base + 2 k slot
+  float* base = v.row_part + 2 * static_cast<int64_t>(cta) * slot;            // part k > 0: base + 2 k slot
+  auto part = [&](int i) {
+    const int k = from + i * step;
+    return base + (k == 0 ? slot : 2 * k * slot);
+  };
   // threads beyond the elements take a share of the parts
   const int groups = max(1, THREADS / elements);
+  float2* done = sm + THREADS;           // m and l of the rows
   for (int i0 = 0; i0 < elements; i0 += THREADS) {
     const int e = groups > 1 ? static_cast<int>(threadIdx.x) % elements : i0 + static_cast<int>(threadIdx.x);
     const int g = groups > 1 ? static_cast<int>(threadIdx.x) / elements : 0;
@@ -154,19 +161,18 @@ __device__ __forceinline__ void join_rows(uint16_t* o, const SeqView& v, int row
     const int r = mine ? e / kQuads : 0, h = e % kQuads * 4;
     Sums z{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     if (mine) {
-      for (int k0 = g; k0 < parts; k0 += kPartsAhead * groups) {
+      for (int k0 = g; k0 < count; k0 += kPartsAhead * groups) {
         float2 ml[kPartsAhead];
         float4 y[kPartsAhead];
 #pragma unroll
         for (int k = 0; k < kPartsAhead; ++k) {
-          const int part = min(k0 + k * groups, parts - 1);
-          const float* p = base + (part == 0 ? slot : 2 * part * slot);
+          const float* p = part(min(k0 + k * groups, count - 1));
           ml[k] = __ldcg(reinterpret_cast<const float2*>(p + v.row_limit * HD + 2 * r));
           y[k] = __ldcg(reinterpret_cast<const float4*>(p + r * HD + h));
         }
 #pragma unroll
         for (int k = 0; k < kPartsAhead; ++k)
-          if (k0 + k * groups < parts) z.add(ml[k].x, ml[k].y, y[k]);
+          if (k0 + k * groups < count) z.add(ml[k].x, ml[k].y, y[k]);
       }
     }
     if (groups > 1) {
@@ -180,11 +186,21 @@ __device__ __forceinline__ void join_rows(uint16_t* o, const SeqView& v, int row
         }
       __syncthreads();
     }
-    if (mine && g == 0) {
+    if (!mine || g > 0) continue;
+    if (o == nullptr) {
+      *reinterpret_cast<float4*>(part(0) + r * HD + h) = z.x;                  // (no other thread reads this element)
+      if (h == 0) done[r] = make_float2(z.top, z.total);
+    } else {
       const float inv = inverse(z.total);
       *reinterpret_cast<uint2*>(o + (static_cast<int64_t>(r / v.G) * v.Hq + r % v.G) * HD + h) =
           make_uint2(pack_bf16(z.x.x * inv, z.x.y * inv), pack_bf16(z.x.z * inv, z.x.w * inv));
     }
+  }
+  if (o == nullptr) {
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < rows)
+      *reinterpret_cast<float2*>(part(0) + v.row_limit * HD + 2 * threadIdx.x) = done[threadIdx.x];
+    __syncthreads();
   }
 }
 

@@ -68,7 +68,8 @@ struct SeqView {
   RowShare* row_share;  // [row_ctas]
   int2* tile_share;     // [tile_ctas]
   TileWork* tile_work;  // [blocks * Hkv + tile_ctas]
-  int32_t* row_there;   // [row_ctas] parts there of the item whose first part a CTA has (0 between calls)
+  int32_t* row_there;   // [3][row_ctas] parts there of the first run of the item that a CTA begins, that item's runs there, parts
+                        // there of a later run that the CTA begins (all 0 between calls)
   JoinTask* tile_join;  // [counts[2]] the tile kernel's split items
   int32_t* counts;      // [1] first rejected sequence (INT32_MAX if none), [2] split items
   uint32_t* err;        // device error word (ptx::kErr* bits)

@@ -470,20 +470,35 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
     }
     __syncthreads();
     if (!whole) {
-      // the CTA that comes last with a part joins them all
+      // The CTA that comes last with a part joins them; of more than eight, runs of eight first, then the runs: with all
+      // parts of a long axis read by one CTA, three sequences of 10000-40000 (38 parts an item, e4m3) took 40 us against 32.
       const int4 ends = reinterpret_cast<const int4*>(v.row_share + blockIdx.x)[1];
       const int cta = at.u > 0 ? ends.x : ends.z, parts = at.u > 0 ? ends.y : ends.w;
-      if (threadIdx.x == 0) {
-        __threadfence();
-        const bool last = atomicAdd(v.row_there + cta, 1) == parts - 1;
-        if (last) v.row_there[cta] = 0;               // for the next call
-        __threadfence();
-        ml_sh[0] = last ? 1.f : 0.f;
+      auto is_last = [&](int32_t* there, int count) {
+        if (threadIdx.x == 0) {
+          __threadfence();
+          const bool last = atomicAdd(there, 1) == count - 1;
+          if (last) *there = 0;                       // for the next call
+          __threadfence();
+          ml_sh[0] = last ? 1.f : 0.f;
+        }
+        __syncthreads();
+        const bool last = ml_sh[0] != 0.f;
+        __syncthreads();
+        return last;
+      };
+      float4* sx = reinterpret_cast<float4*>(o_sh);
+      float2* sm = reinterpret_cast<float2*>(o_sh + 4 * kThreads);
+      uint16_t* out = o + (static_cast<int64_t>(first) * v.Hq + at.kvh * v.G) * HD;
+      const int run = (static_cast<int>(blockIdx.x) - cta) & ~(kPartsAhead - 1), in_run = min(kPartsAhead, parts - run);
+      // (an item's first run and the last of the item before may begin in the same CTA: counters of their own)
+      if (is_last(v.row_there + (run == 0 ? 0 : 2 * v.row_ctas) + cta + run, in_run)) {
+        const bool all = parts <= kPartsAhead;
+        join_rows<HD, kThreads>(all ? out : nullptr, v, rows, cta, run, 1, in_run, sx, sm);
+        const int runs = (parts + kPartsAhead - 1) / kPartsAhead;
+        if (!all && is_last(v.row_there + v.row_ctas + cta, runs))
+          join_rows<HD, kThreads>(out, v, rows, cta, 0, kPartsAhead, runs, sx, sm);
       }
-      __syncthreads();
-      if (ml_sh[0] != 0.f)
-        join_rows<HD, kThreads>(o + (static_cast<int64_t>(first) * v.Hq + at.kvh * v.G) * HD, v, rows, cta, parts,
-                                reinterpret_cast<float4*>(o_sh), reinterpret_cast<float2*>(o_sh + 4 * kThreads));
       __syncthreads();
     }
     if (done < n_chunks) {

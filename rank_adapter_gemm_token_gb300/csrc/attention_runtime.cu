@@ -281,7 +281,7 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
                o_seq = take(T * 4), o_pos = take(T * 4), o_row = take(T * 4), o_pp = take((S + 1) * 4),
                o_rs = take(S * sizeof(RowSeq)), o_rp = take((S + 1) * 8), o_blk = take(J * sizeof(TileBlk)),
                o_bp = take((J + 1) * 8), o_rsh = take(R * sizeof(RowShare)), o_tsh = take(C * sizeof(int2)), o_tw = take((J * n_kv_heads + C) * sizeof(TileWork)),
-               o_there = take(R * 4), o_tj = take(C * sizeof(JoinTask)), o_counts = take(8 * 4),
+               o_there = take(3 * R * 4), o_tj = take(C * sizeof(JoinTask)), o_counts = take(8 * 4),
                o_err = take(4), o_part = take(row_part_bytes(v)), o_tile_part = take(tile_part_bytes(v));
   cudaError_t e = cudaMalloc(&q->mem, at);
   if (e == cudaSuccess) {

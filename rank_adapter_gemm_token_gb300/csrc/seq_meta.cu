@@ -159,7 +159,7 @@ __device__ __forceinline__ void share_out(const SeqView& v, const int64_t* pre, 
     const int64_t next = parts[c + 1];
     v.row_share[c] = RowShare{cut.item, cut.kvh, max(cut.unit - kRowHead, 0), units, cut.join.cta, cut.join.parts,
                               static_cast<int>(next >> 32), static_cast<int>(next)};
-    v.row_there[c] = 0;
+    v.row_there[c] = v.row_there[ctas + c] = v.row_there[2 * ctas + c] = 0;
   }
   if (TILES) {
     // a warp to a CTA's list; before it lie that many items and one place for each cut

@@ -149,6 +149,21 @@ def test_long_axis_is_split_and_joined(layer, n, ctx, hq, hkv, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("seqs,hq,hkv,hd", [(8, 32, 8, 64), (5, 32, 8, 128), (4, 20, 4, 64), (7, 8, 8, 64)])
+def test_items_of_many_parts_side_by_side(layer, seqs, hq, hkv, hd, kind):
+    """A few sequences, so that each one's keys go to nine or more CTAs and most CTAs end one item and begin the next: the parts of
+    neighbours are told apart, whatever their numbers, and a call leaves nothing behind for the next."""
+    for k in range(6):
+        ctx = [752 + 997 * (i + 1) * (k + 1) % 2259 for i in range(seqs)]
+        st = Step(layer, [1] * seqs, ctx, hq, hkv, hd, 64, kind, seed=40 + k)
+        o = st.run()
+        st.seq.status()
+        st.check(o)
+        for _ in range(5):
+            assert torch.equal(o, st.run())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_blocks_of_one_tile_between_others(layer, kind):
     """Prompts of 660 tokens: each one's last block has rows in its first tile alone, and its run of six key tiles is followed
     in the same CTA by the next prompt's first block, where both tiles have rows."""
