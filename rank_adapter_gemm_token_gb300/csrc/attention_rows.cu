@@ -24,7 +24,7 @@
 // Keys at or past a row's limit are replaced by -inf by selection, and rows past the cached length are
 // zero-filled on load, so what lies there (NaN included) has no effect.
 // Measured, 32 heads of 128 on 8, the cache's bytes over the time of a call: 256 sequences of 200-2000 tokens
-// bf16 171 us, 6.5 TB/s; e4m3 106 us, 5.8 TB/s; one of 131000 tokens 86 us, 6.2 TB/s (copy: 6.8); one of 500 tokens 8.5 us.
+// bf16 171 us, 6.5 TB/s; e4m3 106 us, 5.8 TB/s; one of 131000 tokens 85 us, 6.3 TB/s (copy: 6.8); one of 500 tokens 8.5 us.
 #include <algorithm>
 
 #include "attention.h"
