@@ -1,8 +1,9 @@
 // One step's sequences: the metadata that every layer's cache write, attention and cache read of the
 // step share (mlora_build_seq). Two launches:
-//   check   a warp for each sequence: its bounds and its page table (every page of its cached length
-//           inside the cache), the used part of the table copied into the step's own storage, so that
-//           the caller's may change as soon as this kernel has run. A sequence that fails is skipped
+//   check   a warp for each sequence: its bounds (inside the step, not below an earlier start) and its
+//           page table (every page of its cached length inside the cache), the used part of the table
+//           copied into the step's own storage, so that the caller's may change as soon as this kernel
+//           has run. A sequence that fails is skipped
 //           (length 0: nothing is read or written for it, its rows of the attention are zero) and
 //           recorded;
 //   plan    blocks 0 and 1: the work of the row kernel and of the tile kernel as prefix sums, over which their CTAs take
@@ -30,13 +31,23 @@ constexpr int kPlanPre = kMapSeqs / 2;   // prefix sums kept there by the plan
 __global__ void __launch_bounds__(kCheckThreads)
 check_seq_kernel(const int32_t* __restrict__ q_start, const int32_t* __restrict__ kv_len,
                  const int32_t* __restrict__ pages, int table_ld, SeqView v, int max_new, int n_pages, int page_log2) {
+  constexpr int kSeqs = kCheckThreads / 32;
+  __shared__ int32_t tops[kSeqs];
   ptx::grid_dependents_launch();
-  const int lane = threadIdx.x & 31;
-  const int s = blockIdx.x * (kCheckThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int s0 = blockIdx.x * kSeqs, s = s0 + warp;
+  // The largest start up to the sequence's own: one below an earlier start would share tokens with another sequence, and
+  // accepted sequences could have more than T tokens in all, which is what the plan's lists hold.
+  int top = INT_MIN;
+  for (int i = threadIdx.x; i < s0; i += kCheckThreads) top = max(top, q_start[i]);
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) tops[warp] = top;
+  __syncthreads();
   if (s >= v.S) return;
+  top = __reduce_max_sync(0xffffffffu, lane < kSeqs ? max(tops[lane], lane <= warp ? q_start[s0 + lane] : INT_MIN) : INT_MIN);
   const int a = q_start[s], b = q_start[s + 1], L = kv_len[s];
   const int page = 1 << page_log2;
-  bool ok = a >= 0 && a <= b && b <= v.T && b - a <= max_new && L >= 0 &&
+  bool ok = a >= 0 && a == top && a <= b && b <= v.T && b - a <= max_new && L >= 0 &&
             static_cast<int64_t>(L) <= static_cast<int64_t>(v.max_pages) * page && (L == 0 || L >= b - a);
   const int used = ok ? (L + page - 1) >> page_log2 : 0;
   bool fine = true;
@@ -83,6 +94,24 @@ __device__ __forceinline__ void block_scan(int64_t (&x)[N], int64_t (*warp_sums)
     const int64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
     if (warp > 0) x[i] += before;
   }
+  __syncthreads();
+}
+
+// x[i] <- max(x[0], ..., x[i]), i < n, by all threads of the block, a run of elements each; tops: a place for each thread.
+__device__ __noinline__ void running_max(int32_t* x, int n, int32_t* tops) {
+  const int per = (n + kPlanThreads - 1) / kPlanThreads, i0 = min(static_cast<int>(threadIdx.x) * per, n), i1 = min(i0 + per, n);
+  int32_t top = INT_MIN;
+  for (int i = i0; i < i1; ++i) x[i] = top = max(top, x[i]);
+  tops[threadIdx.x] = top;
+  for (int d = 1; d < kPlanThreads; d <<= 1) {
+    __syncthreads();
+    const int32_t before = static_cast<int>(threadIdx.x) >= d ? tops[threadIdx.x - d] : INT_MIN;
+    __syncthreads();
+    tops[threadIdx.x] = max(tops[threadIdx.x], before);
+  }
+  __syncthreads();
+  if (threadIdx.x > 0)
+    for (int i = i0; i < i1; ++i) x[i] = max(x[i], tops[threadIdx.x - 1]);
   __syncthreads();
 }
 
@@ -183,11 +212,11 @@ __device__ __forceinline__ void share_out(const SeqView& v, const int64_t* pre, 
 // The row kernel's work, or the tile kernel's (TILES).
 template <bool TILES>
 __device__ void plan(const SeqView& v, int page_log2, int64_t* pre, int64_t* cuts) {
-  __shared__ int64_t sums[5][32];
+  __shared__ int64_t sums[4][32];
   __shared__ int joins;                           // split items so far (their order in the lists does not matter)
   __shared__ int most, deepest;                   // key tiles of the largest block; units of the fullest hands
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t tokens = 0, units = 0, entries = 0, cached = 0, blocks = 0;      // totals of the sequences before this chunk
+  int64_t units = 0, entries = 0, cached = 0, blocks = 0;      // totals of the sequences before this chunk
   for (int s0 = 0; s0 < v.S; s0 += kPlanThreads) {
     const int s = s0 + threadIdx.x;
     const int n = s < v.S ? v.n[s] : 0, L = s < v.S ? v.len[s] : 0, start = s < v.S ? v.start[s] : 0;
@@ -196,22 +225,16 @@ __device__ void plan(const SeqView& v, int page_log2, int64_t* pre, int64_t* cut
     const int per = 2 * v.tile_tokens;              // tokens of a block
     const int64_t u = some && few ? kRowHead + (L + kRowUnit - 1) / kRowUnit : 0;
     const int64_t b = some && !few ? (n + per - 1) / per : 0;
-    int64_t x[5] = {n, u, u > 0, (static_cast<int64_t>(L) + (1 << page_log2) - 1) >> page_log2, b}, t[5];
+    int64_t x[4] = {u, u > 0, (static_cast<int64_t>(L) + (1 << page_log2) - 1) >> page_log2, b}, t[4];
     block_scan(x, sums, t);
-    // starts that do not ascend could name more tokens than there are: the lists hold T
-    const bool over = tokens + x[0] > v.T;
-    if (!TILES && over && n > 0) {
-      atomicOr(v.err, ptx::kErrBadSeq);
-      atomicMin(&v.counts[1], s);
-    }
-    if (!TILES && s < v.S) v.page_pre[s + 1] = static_cast<int32_t>(cached + x[3]);
+    if (!TILES && s < v.S) v.page_pre[s + 1] = static_cast<int32_t>(cached + x[2]);
     if (!TILES && u > 0) {
-      const int64_t e = entries + x[2];
-      v.row_seq[e - 1] = RowSeq{s, over ? 0 : n, L, start};
-      v.row_pre[e] = (units + x[1]) * v.Hkv;
+      const int64_t e = entries + x[1];
+      v.row_seq[e - 1] = RowSeq{s, n, L, start};
+      v.row_pre[e] = (units + x[0]) * v.Hkv;
     }
     // the chunk's tile blocks, a warp for each sequence
-    const int64_t first = blocks + x[4] - b;
+    const int64_t first = blocks + x[3] - b;
     uint32_t has = __ballot_sync(0xffffffffu, TILES && b > 0);
     while (has) {
       const int i = __ffs(has) - 1;
@@ -219,21 +242,15 @@ __device__ void plan(const SeqView& v, int page_log2, int64_t* pre, int64_t* cut
       const int nb = static_cast<int>(__shfl_sync(0xffffffffu, b, i)), bn = __shfl_sync(0xffffffffu, n, i),
                 bl = __shfl_sync(0xffffffffu, L, i), bstart = __shfl_sync(0xffffffffu, start, i);
       const int64_t f = __shfl_sync(0xffffffffu, first, i);
-      if (__shfl_sync(0xffffffffu, static_cast<int>(over), i)) continue;
       for (int k = lane; k < nb; k += 32) {
         const int tiles = (bl - bn + min((k + 1) * per, bn) - 1) / kTileKeys + 1;
         v.blk[f + k] = TileBlk{s0 + warp * 32 + i, bn, bl, bstart, k * per, tiles};
       }
     }
-    tokens += t[0];
-    units += t[1];
-    entries += t[2];
-    cached += t[3];
-    blocks += t[4];
-    if (tokens > v.T) {                 // the rejected sequences' blocks are not there: the tile kernel leaves them all out
-      blocks = 0;
-      break;
-    }
+    units += t[0];
+    entries += t[1];
+    cached += t[2];
+    blocks += t[3];
   }
   if (threadIdx.x == 0) {
     if (!TILES) v.row_pre[0] = v.page_pre[0] = 0;
@@ -356,8 +373,12 @@ plan_seq_kernel(const int32_t* __restrict__ q_start, SeqView v, int page_log2) {
   __shared__ alignas(16) int32_t begin[kMapSeqs + 1];
   __shared__ int64_t cuts[kPlanThreads];
   const int S = v.S;
+  bool falls = false;
   if (blockIdx.x > 1)
-    for (int i = threadIdx.x; i <= S && S > 0; i += kPlanThreads) begin[i] = q_start[i];
+    for (int i = threadIdx.x; i <= S && S > 0; i += kPlanThreads) {
+      begin[i] = q_start[i];
+      falls = falls || (i > 0 && q_start[i - 1] > begin[i]);
+    }
   ptx::grid_dependency_wait();        // the check's results
   if (blockIdx.x < 2) {
     int64_t* pre = reinterpret_cast<int64_t*>(begin);
@@ -367,10 +388,11 @@ plan_seq_kernel(const int32_t* __restrict__ q_start, SeqView v, int page_log2) {
       plan<true>(v, page_log2, pre, cuts);
     return;
   }
-  __syncthreads();
+  // Starts that fall somewhere: their running maximum takes their place, which is an accepted sequence's own start and its end.
+  if (__syncthreads_or(falls)) running_max(begin, S + 1, reinterpret_cast<int32_t*>(cuts));
   const int t = (blockIdx.x - 2) * kPlanThreads + threadIdx.x;
   if (t >= v.T) return;
-  int lo = 0, hi = S;                 // the last s with begin[s] <= t (the starts ascend, or are rejected below)
+  int lo = 0, hi = S;                 // the last s with begin[s] <= t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (begin[mid] <= t) lo = mid; else hi = mid;

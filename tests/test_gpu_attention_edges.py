@@ -1,0 +1,93 @@
+"""The attention step at its edges: steps whose sequences do not hold, degenerate scales and scores, other streams.
+Tolerances are those of test_gpu_attention.py unless a test derives its own."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from tests.test_gpu_attention import Step  # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def layer():
+    from rank_adapter_gemm_token_gb300 import layer
+    return layer
+
+
+def ints(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------------------------------- starts that fall
+def falling_step(layer, starts, T, hq, hkv, hd):
+    """A step of one-page sequences (length 8, page s for sequence s) with the given starts; returns what the operators make
+    of it: queries written, cache before and after, attention, rows read back, and which sequences must be served."""
+    from rank_adapter_gemm_token_gb300 import mlora
+    S = len(starts) - 1
+    g = torch.Generator(device="cuda").manual_seed(S)
+    n = [b - a for a, b in zip(starts, starts[1:])]
+    most = np.maximum.accumulate(starts)
+    good = [s for s in range(S) if starts[s] == most[s] and 0 <= n[s] <= 8 and starts[s + 1] <= T]
+    cache = layer.KVCache(S, 8, hkv, hd)
+    cache.k.normal_(generator=g)
+    cache.v.normal_(generator=g)
+    seq = layer.SeqMeta(S, T, 1, hq, hkv, hd)
+    seq.build(ints(starts), ints([8] * S), torch.arange(S, dtype=torch.int32, device="cuda")[:, None].contiguous(), T, cache, 8)
+    with pytest.raises(mlora.MloraError) as e:
+        seq.status()
+    assert e.value.status == mlora.MLORA_ERR_BAD_SEQUENCE
+    first = next(s for s in range(S) if s not in set(good))
+    assert f"sequence {first}:" in str(e.value)
+    return cache, seq, good, n, g
+
+
+@pytest.mark.parametrize("hq,hkv,hd", [(4, 2, 64), (32, 1, 64)])   # the row kernel, the tile kernel
+@pytest.mark.parametrize("S,T,starts", [
+    (4, 14, [0, 6, 2, 8, 14]),                                    # the third would share the first one's tokens
+    (2500, 1, [i % 2 for i in range(2501)]),                      # one token, named by 1250 sequences
+    (3000, 2100, [min(i, 1500) if i <= 1500 else 700 + (i - 1501) % 800 if i < 2400 else 1500 + i - 2400 for i in range(3001)]),
+])
+def test_sequences_that_start_below_an_earlier_one_are_skipped(layer, S, T, starts, hq, hkv, hd):
+    assert len(starts) == S + 1
+    cache, seq, good, n, g = falling_step(layer, starts, T, hq, hkv, hd)
+    assert 0 < len(good) < S
+    # the cache: new rows of the served sequences alone
+    k0, v0 = cache.k.clone(), cache.v.clone()
+    qkv = torch.randn(T, (hq + 2 * hkv) * hd, generator=g, device="cuda")
+    q = layer.qkv_write(cache, seq, qkv)
+    want_q = torch.zeros_like(q)
+    rows = qkv.view(T, hq + 2 * hkv, hd).to(torch.bfloat16)
+    for s in good:
+        a, b = starts[s], starts[s + 1]
+        want_q[a:b] = rows[a:b, :hq]
+        k0[s, :, 8 - n[s]:] = rows[a:b, hq:hq + hkv].transpose(0, 1)
+        v0[s, :, 8 - n[s]:] = rows[a:b, hq + hkv:].transpose(0, 1)
+    assert torch.equal(q, want_q) and torch.equal(cache.k, k0) and torch.equal(cache.v, v0)
+    # the attention: their rows, and zeros
+    o = layer.attention(cache, seq, q, torch.full((T, hq * hd), 7.0, dtype=torch.bfloat16, device="cuda"))
+    want, tol = torch.zeros(T, hq, hd, dtype=torch.float64, device="cuda"), torch.zeros(T, hq, hd, dtype=torch.float64, device="cuda")
+    for s in good:
+        a, b = starts[s], starts[s + 1]
+        if a == b:
+            continue
+        k, v = (x[s].double().repeat_interleave(hq // hkv, 0) for x in (cache.k, cache.v))       # [hq, 8, hd]
+        z = torch.einsum("thd,hjd->thj", q[a:b].double(), k) * hd ** -0.5
+        hidden = torch.arange(8, device="cuda")[None] > torch.arange(8 - n[s], 8, device="cuda")[:, None]
+        p = torch.softmax(z.masked_fill(hidden[:, None], float("-inf")), -1)
+        want[a:b] = torch.einsum("thj,hjd->thd", p, v)
+        # weights and the output rounded to bf16, scores (below 64) to 5e-6 of their size
+        tol[a:b] = 2.0 ** -8 * want[a:b].abs() + (2.0 ** -8 + 1e-3) * torch.einsum("thj,hjd->thd", p, v.abs()) + 1e-30
+    assert bool(((o.double().view(T, hq, hd) - want).abs() <= tol).all())
+    # the cache read: their rows, in their places
+    at, start = 0, []
+    for s in range(S):
+        start.append(at)
+        at += 8 if s in set(good) else 0
+    out = [torch.full((S * 8, hkv, hd), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    layer.kv_read(cache, seq, ints(start), S * 8, *out)
+    seq.status()
+    for x, dense in zip((cache.k, cache.v), out):
+        assert torch.equal(dense[:at], x[good].transpose(1, 2).reshape(at, hkv, hd))
+        assert bool((dense[at:] == 7.0).all())
