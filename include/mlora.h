@@ -388,8 +388,9 @@ MLORA_API mlora_status mlora_seq_destroy(mlora_seq_t seq);
  *   T:       rows of the step (rows before q_start[0] and from q_start[n_seqs] on belong to no sequence).
  *   max_new: an upper bound of every sequence's new tokens, known to the host (1 for a decode step): it
  *            chooses the attention's kernels.
- * A sequence with descending or outlying bounds, a start below an earlier entry of q_start, more than max_new new tokens, fewer cached than new tokens,
- * a length above max_pages pages or a page outside the cache is skipped like padding and reported by
+ * A sequence with descending or outlying bounds, a start below an earlier entry of q_start, more than max_new new
+ * tokens, fewer cached than new tokens, a length above max_pages pages or above 2^31 - 256, or a page outside the cache
+ * is skipped like padding and reported by
  * mlora_seq_status as MLORA_ERR_BAD_SEQUENCE with the first one's number. Caches used with the step have this
  * one's sizes and element type (MLORA_ERR_MISMATCH otherwise).
  * Calls that share a seq must be ordered on one stream. */

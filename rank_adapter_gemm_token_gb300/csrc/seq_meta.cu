@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kCheckThreads = 256;
 constexpr int kPlanThreads = 1024;
+constexpr int kMaxLen = INT_MAX - 255;   // so that a length rounded up to whole pages, units or tiles is an int
 constexpr int kMapSeqs = 8192;      // MLORA_MAX_SEQS: token starts kept in shared memory by the token map
 constexpr int kPlanPre = kMapSeqs / 2;   // prefix sums kept there by the plan
 
@@ -47,7 +48,7 @@ check_seq_kernel(const int32_t* __restrict__ q_start, const int32_t* __restrict_
   top = __reduce_max_sync(0xffffffffu, lane < kSeqs ? max(tops[lane], lane <= warp ? q_start[s0 + lane] : INT_MIN) : INT_MIN);
   const int a = q_start[s], b = q_start[s + 1], L = kv_len[s];
   const int page = 1 << page_log2;
-  bool ok = a >= 0 && a == top && a <= b && b <= v.T && b - a <= max_new && L >= 0 &&
+  bool ok = a >= 0 && a == top && a <= b && b <= v.T && b - a <= max_new && L >= 0 && L <= kMaxLen &&
             static_cast<int64_t>(L) <= static_cast<int64_t>(v.max_pages) * page && (L == 0 || L >= b - a);
   const int used = ok ? (L + page - 1) >> page_log2 : 0;
   bool fine = true;

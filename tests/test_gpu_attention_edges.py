@@ -91,3 +91,20 @@ def test_sequences_that_start_below_an_earlier_one_are_skipped(layer, S, T, star
     for x, dense in zip((cache.k, cache.v), out):
         assert torch.equal(dense[:at], x[good].transpose(1, 2).reshape(at, hkv, hd))
         assert bool((dense[at:] == 7.0).all())
+
+
+def test_length_near_2_31_is_rejected(layer):
+    """Rounded up to whole pages it would pass 2^31; the table has room for it."""
+    from rank_adapter_gemm_token_gb300 import mlora
+    cache = layer.KVCache(2, 256, 1, 64)
+    seq = layer.SeqMeta(2, 2, 1 << 23, 2, 1, 64)
+    table = torch.full((2, 1 << 23), 5, dtype=torch.int32, device="cuda")          # pages that are not there
+    table[1, 0] = 1
+    cache.v[1, 0, :3] = 2.0
+    for L in (2 ** 31 - 1, 2 ** 31 - 255):
+        seq.build(ints([0, 1, 2]), ints([L, 3]), table, 2, cache, 1)
+        o = layer.attention(cache, seq, torch.ones(2, 2, 64, dtype=torch.bfloat16, device="cuda"))
+        with pytest.raises(mlora.MloraError) as e:
+            seq.status()
+        assert e.value.status == mlora.MLORA_ERR_BAD_SEQUENCE and "sequence 0:" in str(e.value)
+        assert not o[0].any() and bool((o[1] == 2.0).all())
