@@ -13,6 +13,7 @@ constexpr int kKvBf16 = 0, kKvE4m3 = 1;
 // it quantises against it, so that every scale is a normal fp32 number with a normal reciprocal.
 constexpr float kAmaxMin = 8.673617379884035e-19f;   // 2^-60
 constexpr float kE4m3Max = 448.0f;
+constexpr float kLeastScale = 0x1p-100f;             // value scales below count as zero (those written here are above 2^-69)
 
 // Device arrays of one layer's paged cache. Row (page, head, offset) of K and V holds hd elements.
 struct KvView {

@@ -17,10 +17,11 @@
 //     128 rows; here the tensor time is a fraction of the load time either way.)
 //   - softmax in one pass in base 2; the running maximum moves only when a score passes it by 2^8, so most
 //     chunks need no shuffles and no rescaling. P is at most 2^8, which f16 and bf16 hold.
-//   - e4m3: codes become f16 (exact) in registers. The key scale multiplies the score, and the value scale goes
-//     into the exponent: with t_j = score_j + log2 vs_j, P_j = 2^(t_j - max t) is the weight times the scale
-//     and at most 2^8 whatever the scales' magnitude; the denominator sums P_j / vs_j. Query rows are divided
-//     by their largest element, so f16 holds them too.
+//   - e4m3: codes become f16 (exact) in registers. The key scale multiplies the score. The weights w_j = 2^(score_j - m)
+//     go into the denominator as they are; for the product with the codes they are multiplied by the value scale and by
+//     u = 2^(m - n), where n follows the largest score_j + log2 vs_j as m follows the largest score: P_j = w_j vs_j u is at
+//     most 2^8 whatever the scales' magnitude. A value scale of 0 leaves its weight in the denominator. Both maxima
+//     are whole numbers, so every rescaling is exact. Query rows are divided by their largest element, so f16 holds them too.
 // Keys at or past a row's limit are replaced by -inf by selection, and rows past the cached length are
 // zero-filled on load, so what lies there (NaN included) has no effect.
 // Measured, 32 heads of 128 on 8, the cache's bytes over the time of a call: 256 sequences of 200-2000 tokens
@@ -39,6 +40,10 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 16;                  // keys of a warp's chunk
 constexpr float kLazy = 8.0f;               // log2 of the largest P
+constexpr float kMostP = 256.0f;
+// A value scale counts as this power of two at least where the maximum is taken: the maximum of value rows of scale 0 alone
+// stays finite, and 2^80 times any number of weights does too.
+constexpr float kLeastLog2 = -80.0f;
 
 template <int HD, int NQ, bool E4M3>
 struct RowsCfg {
@@ -109,6 +114,10 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+// A power of two from its exponent (a whole number in [-126, 127]), and back.
+__device__ __forceinline__ float pow2_of(float x) { return __int_as_float((static_cast<int>(x) + 127) << 23); }
+__device__ __forceinline__ float log2_of(float x) { return static_cast<float>((__float_as_int(x) >> 23) - 127); }
 
 // A place in the list of units: unit u of head kvh of list entry i.
 struct Place {
@@ -272,6 +281,7 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
       }
     }
     float acc[NQ][kSteps][4], m[NQ][2], l[NQ][2];
+    float up[NQ][2];                           // e4m3: 2^(m - n), a power of two
 #pragma unroll
     for (int z = 0; z < NQ; ++z) {
 #pragma unroll
@@ -279,7 +289,7 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[z][i][k] = 0.f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) m[z][c] = -INFINITY, l[z][c] = 0.f;
+      for (int c = 0; c < 2; ++c) m[z][c] = -INFINITY, l[z][c] = 0.f, up[z][c] = 1.f;
     }
 
     for (int u = at.u; u < u_end; ++u, ++done) {
@@ -289,14 +299,13 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
       const int k0 = u * kRowUnit + warp * kChunk;
       if (k0 >= len) continue;
       const uint32_t st = ring + (done % C::kStages) * C::kStage;
-      float ks[2] = {1.f, 1.f}, lvs[2] = {0.f, 0.f}, rvs[2] = {1.f, 1.f};
+      float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
       if (E4M3) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           ks[h] = lds_f(st + 2 * C::kTile + (g + 8 * h) * 4);
-          const float vs = lds_f(st + 2 * C::kTile + 64 + (g + 8 * h) * 4);
-          lvs[h] = __log2f(vs);
-          rvs[h] = vs > 0.f ? __fdividef(1.0f, vs) : 0.f;      // a NaN scale counts in the exponent alone
+          vs[h] = lds_f(st + 2 * C::kTile + 64 + (g + 8 * h) * 4);
+          if (vs[h] < kLeastScale) vs[h] = 0.f;
         }
       }
       float sc[NQ][4], sc1[NQ][4];                // two sums, of the even and odd k-steps: half the chain of products
@@ -339,35 +348,65 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
 #pragma unroll
       for (int z = 0; z < NQ; ++z) {
         bool grow = false;
+        uint32_t hidden = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int c = k & 1, h = k >> 1;
           float x = sc[z][k] + sc1[z][k];
-          x = E4M3 ? fmaf(x * ks[h], cq[z][c], lvs[h]) : x * cq[z][c];
-          if (edge && k0 + g + 8 * h > lim[z][c]) x = -INFINITY;
+          x = E4M3 ? x * ks[h] * cq[z][c] : x * cq[z][c];
+          if (edge && k0 + g + 8 * h > lim[z][c]) x = -INFINITY, hidden |= 1u << k;
           sc[z][k] = x;
           grow = grow || x > m[z][c] + kLazy;
+        }
+        float w[4], p[4];                         // weights, and times scale and u
+        auto weights = [&]() {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int c = k & 1, h = k >> 1;
+            w[k] = exp2_approx(sc[z][k] - (m[z][c] == -INFINITY ? 0.f : m[z][c]));
+            // (what a row does not see counts nothing, also where its scale is NaN)
+            p[k] = !E4M3 ? w[k] : hidden >> k & 1 ? 0.f : w[k] * (vs[h] * up[z][c]);
+          }
+        };
+        if (E4M3) {
+          weights();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) grow = grow || p[k] > kMostP;
         }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float top = fmaxf(sc[z][c], sc[z][2 + c]);
+            auto over_keys = [&](float top) {
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+              for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+              return top;
+            };
+            float top = over_keys(fmaxf(sc[z][c], sc[z][2 + c]));
+            if (E4M3) top = ceilf(top);
             top = fmaxf(top, m[z][c]);
             const float f = top == m[z][c] ? 1.f : exp2_approx(m[z][c] - top);
+            float fp = f;
+            if (E4M3) {
+              float t[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) t[h] = sc[z][2 * h + c] + fmaxf(__log2f(vs[h]), kLeastLog2);
+              const float old = m[z][c] - log2_of(up[z][c]);
+              const float next = fminf(fmaxf(ceilf(over_keys(fmaxf(t[0], t[1]))), old), top + 126.f);
+              fp = next == old ? 1.f : exp2_approx(old - next);
+              if (top != -INFINITY) up[z][c] = pow2_of(top - next);
+            }
             m[z][c] = top;
             l[z][c] *= f;
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) acc[z][i][c] *= f, acc[z][i][2 + c] *= f;
+            for (int i = 0; i < kSteps; ++i) acc[z][i][c] *= fp, acc[z][i][2 + c] *= fp;
           }
+          if (E4M3) weights();
         }
+        if (!E4M3) weights();
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int c = k & 1;
-          const float p = exp2_approx(sc[z][k] - (m[z][c] == -INFINITY ? 0.f : m[z][c]));
-          l[z][c] = E4M3 ? fmaf(p, rvs[k >> 1], l[z][c]) : l[z][c] + p;
-          sc[z][k] = p;
+          l[z][k & 1] += w[k];
+          sc[z][k] = p[k];
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -420,8 +459,9 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
         for (int d = 4; d < 32; d <<= 1) l[z][c] += __shfl_xor_sync(0xffffffffu, l[z][c], d);
         const int r = z * 8 + 2 * t + c;
         if (g == 0) {
-          ml_sh[(warp * C::kRows + r) * 2] = m[z][c];
-          ml_sh[(warp * C::kRows + r) * 2 + 1] = l[z][c];
+          // (e4m3: from here on by the maximum that the value sums go by)
+          ml_sh[(warp * C::kRows + r) * 2] = E4M3 ? m[z][c] - log2_of(up[z][c]) : m[z][c];
+          ml_sh[(warp * C::kRows + r) * 2 + 1] = E4M3 ? l[z][c] * up[z][c] : l[z][c];
         }
         float* row = o_sh + (warp * C::kRows + r) * C::kLd;
 #pragma unroll

@@ -56,7 +56,6 @@ template <bool E4M3>
 constexpr float kUp = E4M3 ? 10.0f : 0.0f;
 constexpr int kLiftLog2 = 6;                  // e4m3: a tile's largest row is scaled to codes of 64 times their value
 constexpr float kLift = 64.0f;
-constexpr float kLeastScale = 0x1p-100f;      // value scales below count as zero (those written here are above 2^-69)
 
 template <int HD, bool E4M3>
 struct TilesCfg {

@@ -108,3 +108,57 @@ def test_length_near_2_31_is_rejected(layer):
             seq.status()
         assert e.value.status == mlora.MLORA_ERR_BAD_SEQUENCE and "sequence 0:" in str(e.value)
         assert not o[0].any() and bool((o[1] == 2.0).all())
+
+
+# ------------------------------------------------------------------------------------------- scales of an e4m3 cache
+def set_scale(st, s, pos, which, value):
+    """The scale of position pos of sequence s (all heads) in the cache and in the step's fp64 rows."""
+    p, off = int(st.table[s, pos // st.page]), pos % st.page
+    z = (st.ks, st.vs)[which]
+    dense = st.rows[s][which]
+    old = z[p, :, off].double().cpu().numpy()[:, None]
+    z[p, :, off] = value
+    dense[pos] = dense[pos] / old * float(np.float32(value))
+
+
+@pytest.mark.parametrize("hq,hkv,hd", [(8, 2, 128), (8, 2, 64), (16, 1, 128)])
+def test_value_scales_of_zero_keep_their_weights(layer, hq, hkv, hd):
+    """Single tokens, short chunks and chunks over caches where a third of the value rows, all of them, and the whole first
+    part have scale 0 (or one so small that it counts as 0): their weights stay in the denominator."""
+    rng = np.random.default_rng(3)
+    for n in ([1, 1, 1], [2, 1, 2], [40, 1, 30]):
+        st = Step(layer, n, [300, 90, 700], hq, hkv, hd, 16, "e4m3", seed=7)
+        for s, L in enumerate(st.len):
+            zero = {0: rng.random(L) < 1 / 3, 1: np.ones(L, bool), 2: np.arange(L) < L // 2}[s]
+            for pos in np.flatnonzero(zero):
+                set_scale(st, s, int(pos), 1, 0.0 if pos % 2 else 2.0 ** -110)
+        o = st.run()
+        st.seq.status()
+        st.check(o)
+        assert not o[st.starts[1]:st.starts[2]].any()
+        assert torch.equal(o, st.run())
+
+
+@pytest.mark.parametrize("n", [1, 33])
+def test_two_equal_scores_one_value_scale_zero(layer, n):
+    """Scores of 0, codes of 448, value scales 1/448 and 0 in turn: the mean of ones and zeros."""
+    st = Step(layer, [n], [64 - n], 4, 1, kind="e4m3")
+    st.q.zero_()
+    for pos in range(64):
+        p, off = int(st.table[0, pos // 16]), pos % 16
+        st.v.view(torch.uint8)[p, :, off] = 0x7E
+        st.vs[p, :, off] = 1 / 448 if pos % 2 else 0.0
+    o = st.run().float()
+    seen = torch.arange(64 - n + 1, 65, device="cuda")
+    want = (seen // 2).float() / seen
+    assert bool(((o - want[:, None]).abs() <= (2.0 ** -8 + 2.0 ** -11) * want[:, None]).all())
+
+
+def test_value_scales_from_tiny_to_large(layer):
+    """Scales of 2^-90 ... 2^40 among the keys of single tokens: each row's sum is that of its largest products."""
+    st = Step(layer, [1, 2], [500, 60], 8, 2, kind="e4m3", seed=2, q_gain=0.2)
+    rng = np.random.default_rng(5)
+    for s, L in enumerate(st.len):
+        for pos in range(L):
+            set_scale(st, s, pos, 1, 2.0 ** rng.integers(-90, 41))
+    st.check(st.run())
