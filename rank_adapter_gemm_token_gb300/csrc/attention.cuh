@@ -116,9 +116,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 // Joining the parts of split attention items.
 constexpr int kPartsAhead = 8;           // parts asked for at once
-__device__ __forceinline__ float inverse(float total) {
-  return total > 0.f ? 1.0f / total : total == 0.f ? 0.f : total;      // an empty row is zero; NaN stays
-}
+// The inverse of a row's sum of weights. Every row that is written sees a key, its own: a sum of 0 is that of scores that
+// are all -inf, and times the products, which are 0 too, gives the softmax's 0 / 0.
+__device__ __forceinline__ float inverse(float total) { return 1.0f / total; }
 
 // Running maximum, sum of weights and four weighted value sums.
 struct Sums {

@@ -474,7 +474,7 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
     __syncthreads();
     constexpr int kGroups = HD / 8;
     auto write_out = [&](int r, int h, const float* x, float total) {
-      const float inv = total > 0.f ? 1.0f / total : total == 0.f ? 0.f : total;   // an empty row is zero; NaN stays
+      const float inv = inverse(total);
       uint4 w;
       w.x = pack_bf16(x[0] * inv, x[1] * inv);
       w.y = pack_bf16(x[2] * inv, x[3] * inv);

@@ -512,7 +512,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       n_sc += it.kb - ka;
       // While the last product runs: where the rows go, and the next item.
       const bool part = it.split != 0 && it.t0 + v.tile_tokens * w < it.n;     // of a split item, to the workspace
-      const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;             // NaN stays
+      const float inv = inverse(l);
       const int64_t own = (static_cast<int64_t>(it.start + tok) * v.Hq + it.kvh * v.G + row_head) * HD;
       uint16_t* dst[4];                               // of the rows of the thread's four lanes, where the thread stores
 #pragma unroll

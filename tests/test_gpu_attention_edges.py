@@ -162,3 +162,49 @@ def test_value_scales_from_tiny_to_large(layer):
         for pos in range(L):
             set_scale(st, s, pos, 1, 2.0 ** rng.integers(-90, 41))
     st.check(st.run())
+
+
+# ------------------------------------------------------------------------------------------- degenerate scores
+@pytest.mark.parametrize("hq,hkv,n", [(4, 2, 1), (4, 2, 2), (4, 1, 60), (2, 2, 200)])
+def test_rows_whose_scores_are_all_minus_infinity_are_nan(layer, hq, hkv, n):
+    """A key with an infinity gives a score of -inf to queries of the other sign there: nothing, beside others; alone, 0 / 0.
+    Keys 0 and 1 of kv head 0 have it; the first new token sees key 0 (and 1, for single tokens) alone."""
+    st = Step(layer, [n], [1 if n == 1 else 0], hq, hkv, 128)
+    st.q[:, :, 0] = -1.0
+    inf = [0, 1] if n == 1 else [0]
+    for pos in inf:
+        st.k[int(st.table[0, 0]), 0, pos, 0] = float("inf")
+    o = st.run()
+    st.seq.status()
+    g = hq // hkv * st.hd
+    assert torch.isnan(o[0, :g]).all()
+    assert torch.isfinite(o[1:]).all() and torch.isfinite(o[0, g:]).all()
+    if n > 1:                                             # elsewhere the key counts nothing
+        keep = st.rows[0][0]
+        keep[0, 0, :] = 0.0
+        st.rows[0][0] = keep
+        want, W, S = attend_without(st, 0, 0)
+        got = o.double().cpu().numpy().reshape(want.shape)[1:]
+        d = (st.hd * 2.0 ** -24 + 2.0 ** -20) * S[..., None]
+        assert (np.abs(got - want[1:]) <= (2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2 * d) * (W + np.abs(want)) + 1e-30)[1:]).all()
+
+
+def attend_without(st, head, pos):
+    """The step's only sequence in fp64, key `pos` left out for kv head `head`."""
+    from oracle import attention as ref
+    k, v = st.rows[0]
+    q = st.q.double().cpu().numpy()
+    G = st.hq // st.hkv
+    out, W, S = ref.attention(q, [k], [v], st.starts, G, st.hd ** -0.5)
+    L, n = len(k), st.n[0]
+    for t in range(n):
+        seen = L - n + t + 1
+        keys = [j for j in range(seen) if j != pos]
+        if not keys:
+            continue
+        for h in range(head * G, head * G + G):
+            z = st.hd ** -0.5 * (k[keys, head] @ q[t, h])
+            p = np.exp(z - z.max())
+            p /= p.sum()
+            out[t, h], W[t, h] = p @ v[keys, head], p @ np.abs(v[keys, head])
+    return out, W, S
