@@ -125,7 +125,10 @@ struct Sums {
   float top, total;
   float4 x;
   __device__ __forceinline__ void add(float m, float l, const float4& y) {
-    if (m == -INFINITY) return;       // (a part that saw none of the row's keys has no sums)
+    if (m == -INFINITY) {             // a part without a score above -inf: its sum of weights is 0, or NaN where a score is
+      total += l;
+      return;
+    }
     const float up = fmaxf(top, m);
     const float f = exp2_approx(top - up), g = exp2_approx(m - up);
     top = up;

@@ -208,3 +208,16 @@ def attend_without(st, head, pos):
             p /= p.sum()
             out[t, h], W[t, h] = p @ v[keys, head], p @ np.abs(v[keys, head])
     return out, W, S
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,ctx", [(1, 20000), (9, 6000)])
+def test_a_part_of_nan_alone_is_not_lost(layer, n, ctx, kind):
+    """A long axis in parts, all keys from one on NaN: wherever a part begins with it, the joined rows are NaN."""
+    st = Step(layer, [n], [ctx], 4, 1, 64, 64, kind, seed=6)
+    assert torch.isfinite(st.run()).all()
+    for i in range((ctx + n - 1) // 64, -1, -1):
+        (st.k if kind == "bf16" else st.ks)[int(st.table[0, i])] = float("nan")
+        seen = min(n, max(0, 64 * i - ctx))               # new tokens before key 64 i
+        o = st.run()
+        assert torch.isnan(o[seen:]).all() and torch.isfinite(o[:seen]).all(), i
