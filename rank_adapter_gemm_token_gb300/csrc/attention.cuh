@@ -63,6 +63,15 @@ __device__ __forceinline__ uint4 e4m3_times(uint2 c, float scale) {
   return out;
 }
 
+// Query rows in f16: the power of two that lifts a row whose largest magnitude is `most` (bf16) to [2^14, 2^15), and its
+// inverse. bf16 numbers stay exact down to 2^-31 of the row's largest. (Rows below 2^-112 are lifted by 2^126, the largest
+// power whose inverse is a normal number.)
+__device__ __forceinline__ float query_lift(float most, float* back) {
+  const int e = __float_as_int(most) >> 23;              // biased; 0 for subnormal numbers and 0
+  *back = __int_as_float(max(1, e - 14) << 23);
+  return __int_as_float(min(253, 268 - e) << 23);
+}
+
 // The last i in [0, n) with pre[i] <= x, for ascending prefix sums with pre[0] <= x (one warp, all lanes).
 template <typename T>
 __device__ __forceinline__ int last_at_most(const T* pre, int n, T x) {

@@ -21,7 +21,7 @@
 //     go into the denominator as they are; for the product with the codes they are multiplied by the value scale and by
 //     u = 2^(m - n), where n follows the largest score_j + log2 vs_j as m follows the largest score: P_j = w_j vs_j u is at
 //     most 2^8 whatever the scales' magnitude. A value scale of 0 leaves its weight in the denominator. Both maxima
-//     are whole numbers, so every rescaling is exact. Query rows are divided by their largest element, so f16 holds them too.
+//     are whole numbers, so every rescaling is exact. Query rows are lifted by a power of two into f16's range.
 // Keys at or past a row's limit are replaced by -inf by selection, and rows past the cached length are
 // zero-filled on load, so what lies there (NaN included) has no effect.
 // Measured, 32 heads of 128 on 8, the cache's bytes over the time of a call: 256 sequences of 200-2000 tokens
@@ -256,16 +256,16 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
         }
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        if (!(most > 0.f)) most = 1.f;
-        const float inv = 1.0f / most;
+        float back;
+        const float lift = query_lift(most, &back);
 #pragma unroll
         for (int i = 0; i < kSteps / 2; ++i) {
           const uint32_t* p = &w[i].x;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) bq[z][2 * i + (k >> 1)][k & 1] = pack_f16(ptx::bf16_lo(p[k]) * inv, ptx::bf16_hi(p[k]) * inv);
+          for (int k = 0; k < 4; ++k) bq[z][2 * i + (k >> 1)][k & 1] = pack_f16(ptx::bf16_lo(p[k]) * lift, ptx::bf16_hi(p[k]) * lift);
         }
-        cq[z][0] = scale_log2 * __shfl_sync(0xffffffffu, most, (2 * t) * 4);
-        cq[z][1] = scale_log2 * __shfl_sync(0xffffffffu, most, (2 * t + 1) * 4);
+        cq[z][0] = scale_log2 * __shfl_sync(0xffffffffu, back, (2 * t) * 4);
+        cq[z][1] = scale_log2 * __shfl_sync(0xffffffffu, back, (2 * t + 1) * 4);
       } else {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {

@@ -16,14 +16,14 @@
 //                   with a warp for each tile, their instructions alternate and the rate falls by a third.
 //   warps 15, 13    the next item's queries of one tile each by TMA, while the last products of this one run (e4m3: and
 //                   their f16 form).
-// e4m3: a tile's key rows become f16 as code * 64 (scale / largest scale of the tile), rounded once (2^-12 on average, as
-// the queries are), and 1/64 of that largest scale multiplies the tile's scores. Its value rows become code * 2^k, exact:
+// e4m3: a tile's key rows become f16 as code * 64 (scale / largest scale of the tile), the factor and the product rounded,
+// and 1/64 of that largest scale multiplies the tile's scores. Its value rows become code * 2^k, exact:
 // with scale = f 2^(E + k), 1 <= f < 2 and 2^E 1/64 of the binary power of the tile's largest scale, f multiplies P before
 // its rounding, E is added to the scores (P then is the weight times the scale, below 2^15 whatever the scales) and 2^-E
 // multiplies the sum. So the softmax reads one factor a key from shared memory; with both scales and the sum's factor of
 // each key it took 5000 cycles a tile against 1400 for bf16. The 64 puts a tile's largest row at the top of f16's range:
 // rows of scales 2^20 below it, which may be all that an early token sees of the tile, keep their bits. Query rows are
-// divided by their largest element so that f16 holds them.
+// lifted by a power of two into f16's range.
 // Work: (block, key/value head) items of 128-key tiles, dealt out whole or in equal shares, a list for each CTA (seq_meta.cu);
 // parts of a split item are joined by attention_join.cu.
 // Measured, 32 heads of 128 on 8: one prompt of 8000 tokens 335 us, 1565 TFLOP/s (tcgen05 busy for 0.6 to 0.7 of the cycles; the
@@ -761,7 +761,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         }
         __syncwarp();
         if (E4M3) {
-          // to f16, each row divided by its largest element: two lanes to a row
+          // to f16, each row lifted by a power of two: two lanes to a row
           constexpr int kN = HD / 16;                 // a lane's 16-byte segments
           wait(full, par);
 #pragma unroll 1
@@ -779,16 +779,16 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               for (int k = 0; k < 4; ++k) most = fmaxf(most, fmaxf(fabsf(ptx::bf16_lo(y[k])), fabsf(ptx::bf16_hi(y[k]))));
             }
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-            if (!(most > 0.f)) most = 1.f;
-            const float inv = 1.0f / most;
+            float back;
+            const float lift = query_lift(most, &back);
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
               uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-              for (int k = 0; k < 4; ++k) y[k] = pack_f16(ptx::bf16_lo(y[k]) * inv, ptx::bf16_hi(y[k]) * inv);
+              for (int k = 0; k < 4; ++k) y[k] = pack_f16(ptx::bf16_lo(y[k]) * lift, ptx::bf16_hi(y[k]) * lift);
               *seg(i) = make_uint4(y[0], y[1], y[2], y[3]);
             }
-            if (side == 0) q_scale[(par * 2 + w) * 128 + row] = most;
+            if (side == 0) q_scale[(par * 2 + w) * 128 + row] = back;
           }
           ptx::fence_proxy_async_smem();
           ptx::mbar_arrive(&q_full[w]);

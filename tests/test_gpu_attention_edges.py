@@ -221,3 +221,14 @@ def test_a_part_of_nan_alone_is_not_lost(layer, n, ctx, kind):
         seen = min(n, max(0, 64 * i - ctx))               # new tokens before key 64 i
         o = st.run()
         assert torch.isnan(o[seen:]).all() and torch.isfinite(o[:seen]).all(), i
+
+
+@pytest.mark.parametrize("n", [[1, 1], [3], [50, 20]])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_tiny_queries_over_e4m3(layer, n, hd):
+    """Queries of subnormal bf16 numbers, of which f16 cannot hold the inverse of the largest, and of the largest magnitudes."""
+    for gain in (2.0 ** -132, 2.0 ** -127, 2.0 ** -20, 2.0 ** 100):
+        st = Step(layer, n, [70] * len(n), 4, 2, hd, kind="e4m3", seed=4)
+        st.q = (st.q.double() * gain).to(torch.bfloat16)
+        scale = 0.1 if gain < 1 else 0.1 / gain
+        st.check(st.run(scale=scale), scale=scale)
