@@ -13,7 +13,8 @@ constexpr int kKvBf16 = 0, kKvE4m3 = 1;
 // it quantises against it, so that every scale is a normal fp32 number with a normal reciprocal.
 constexpr float kAmaxMin = 8.673617379884035e-19f;   // 2^-60
 constexpr float kE4m3Max = 448.0f;
-constexpr float kLeastScale = 0x1p-100f;             // value scales below count as zero (those written here are above 2^-69)
+// Scales below this count as zero, those from the other one on as NaN (those written here lie between 2^-69 and 2^120).
+constexpr float kLeastScale = 0x1p-100f, kMostScale = 0x1p120f;
 
 // Device arrays of one layer's paged cache. Row (page, head, offset) of K and V holds hd elements.
 struct KvView {

@@ -16,14 +16,17 @@
 //                   with a warp for each tile, their instructions alternate and the rate falls by a third.
 //   warps 15, 13    the next item's queries of one tile each by TMA, while the last products of this one run (e4m3: and
 //                   their f16 form).
-// e4m3: a tile's key rows become f16 as code * 64 (scale / largest scale of the tile), the factor and the product rounded,
-// and 1/64 of that largest scale multiplies the tile's scores. Its value rows become code * 2^k, exact:
-// with scale = f 2^(E + k), 1 <= f < 2 and 2^E 1/64 of the binary power of the tile's largest scale, f multiplies P before
-// its rounding, E is added to the scores (P then is the weight times the scale, below 2^15 whatever the scales) and 2^-E
-// multiplies the sum. So the softmax reads one factor a key from shared memory; with both scales and the sum's factor of
-// each key it took 5000 cycles a tile against 1400 for bf16. The 64 puts a tile's largest row at the top of f16's range:
-// rows of scales 2^20 below it, which may be all that an early token sees of the tile, keep their bits. Query rows are
-// lifted by a power of two into f16's range.
+// e4m3: codes become f16 times their scale's first 7 bits and a power of two, which is exact, so that S is a sum of exact products.
+// What is left of the key's scale (1 +- 2^-7) multiplies the score in fp32, to 2^-16, and what is left of the value's (up to
+// 1 + 2^-6) the weight, to 2^-14, before its one rounding to f16. (With scales rounded to f16, and the products with the codes again,
+// every score of a key was off by up to 2^-10: at scores of 60 its weight by 6 %.) 2^E, the binary power of the tile's largest
+// value scale, is added to the scores (P then is the weight times that power, at most 2^15 whatever the scales) and 2^-E
+// multiplies the sum. The largest row of a tile is lifted by 64 to the top of f16's range: rows of scales 2^20 below it,
+// which may be all that an early token sees of the tile, keep their bits. Query rows are lifted by a power of two, most by the
+// same one. So one word a key, from shared memory, is all that the softmax reads, and only where it takes the exponentials:
+// the maximum is taken of S without it and raised by its bound (scores above 100 in base 2 are gone through again with it).
+// A word read by all lanes of a warp costs the shared memory a cycle and the warp a quarter of an instruction: 8000 tokens took
+// 712 us with a factor of the key in both passes and one of the value beside the second, 650 without the first of them, 600 so.
 // Work: (block, key/value head) items of 128-key tiles, dealt out whole or in equal shares, a list for each CTA (seq_meta.cu);
 // parts of a split item are joined by attention_join.cu.
 // Measured, 32 heads of 128 on 8: one prompt of 8000 tokens 335 us, 1565 TFLOP/s (tcgen05 busy for 0.6 to 0.7 of the cycles; the
@@ -35,6 +38,8 @@
 // runs on to the end.
 #include <algorithm>
 #include <climits>
+#include <cmath>
+#include <type_traits>
 
 #include "attention.h"
 #include "attention.cuh"
@@ -48,14 +53,18 @@ constexpr int kThreads = 512;               // 128 registers each at launch, sha
 constexpr int kKeys = kTileKeys;              // 128
 constexpr int kHalf = kKeys * 128;            // bytes of 128 rows of 64 16-bit elements (one swizzled half tile)
 // log2 of the largest exponential; e4m3: and of the factor that lifts P in f16, whose normal numbers then reach down to
-// weights of 2^-24 (their values may be that much larger than the others), while P, a scale's mantissa in it, stays below
-// 2^15. (A limit of 4 in place of 8 rescales O more often: 552 us against 548 at 8000 tokens; one of 2 573.)
+// weights of 2^-25 (their values may be that much larger than the others), while P stays at 2^15 at most. (A limit of 4 in place of 8 rescales O more often: 552 us against 548 at 8000 tokens; one of 2 573.)
 template <bool E4M3>
 constexpr float kLazy = E4M3 ? 4.0f : 8.0f;
 template <bool E4M3>
-constexpr float kUp = E4M3 ? 10.0f : 0.0f;
+constexpr float kUp = E4M3 ? 11.0f : 0.0f;
 constexpr int kLiftLog2 = 6;                  // e4m3: a tile's largest row is scaled to codes of 64 times their value
 constexpr float kLift = 64.0f;
+constexpr float kKeyBound = 0.0079f;          // of what a key's factor leaves of its scale, from 1: a little above 2^-7
+constexpr float kBoundedScore = 100.0f;       // largest score that the bound is used for
+// Query rows whose largest element lies in [2^-6, 2^10) are lifted by 2^5: elements down to 2^-16 of the row's largest stay exact
+// in f16, and the others are off by 2^-24 of it at most. Other rows have a power of their own.
+constexpr float kCommonLift = 32.0f, kCommonLeast = 0x1p-6f, kCommonMost = 0x1p10f;
 
 template <int HD, bool E4M3>
 struct TilesCfg {
@@ -73,8 +82,8 @@ struct TilesCfg {
   static constexpr int kCodeOff = kRingOff + kRing * kTile;
   static constexpr int kRawScaleOff = kCodeOff + (E4M3 ? kStages * kCodes : 0);  // scales on their way: [kStages][2][128]
   static constexpr int kScaleOff = kRawScaleOff + (E4M3 ? kStages * 2 * kKeys * 4 : 0);   // float4 of each scale buffer
-  static constexpr int kMantOff = kScaleOff + (E4M3 ? kScaleBufs * 16 : 0);                // [kScaleBufs][128] f of the value rows
-  static constexpr int kFactorOff = kMantOff + (E4M3 ? kScaleBufs * kKeys * 4 : 0);        // [2][128] half2, [8] maxima
+  static constexpr int kKeyOff = kScaleOff + (E4M3 ? kScaleBufs * 16 : 0);                 // [kScaleBufs][128] keys' words
+  static constexpr int kFactorOff = kKeyOff + (E4M3 ? kScaleBufs * kKeys * 4 : 0);         // [2][128] half2, [8] maxima
   static constexpr int kBarOff = kFactorOff + (E4M3 ? 2 * kKeys * 4 + 32 : 0);
   static constexpr int kQScaleOff = kBarOff + 512;                 // e4m3: [2][tile][128] scales of the query rows
   static constexpr int kWalkOff = kQScaleOff + (E4M3 ? 2 * 2 * 128 * 4 : 0);
@@ -151,11 +160,6 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t pair_u(uint32_t x, uint32_t y) { return pair(__uint_as_float(x), __uint_as_float(y)); }
 
 // One step (BIT 1, then 2) of a turn within four lanes: from a row of four 32-byte pieces in each lane to piece k of row
@@ -176,6 +180,9 @@ __device__ __forceinline__ void turn4(uint32_t (&z)[32], int lane) {
     }
   }
 }
+// A key's word is the factor of its scores; its last byte says what is left of its value's scale: here -(2 + byte 2^-14), so
+// that P (1 + byte 2^-14) is -(P + P times it).
+__device__ __forceinline__ float value_rest(float word) { return __uint_as_float(__byte_perm(__float_as_uint(word), 0xc0000000u, 0x7504)); }
 // Barrier of the four warps that turn codes into f16.
 __device__ __forceinline__ void converters_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // Eight e4m3 codes as f16, times a factor.
@@ -214,7 +221,8 @@ struct alignas(64) Walk {
 template <int HD, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                       const __grid_constant__ CUtensorMap tmap_q, uint16_t* __restrict__ o, float scale_log2, KvView kv, SeqView v) {
+                       const __grid_constant__ CUtensorMap tmap_q, uint16_t* __restrict__ o, float scale_log2, float scale_power, KvView kv,
+                       SeqView v) {
   using C = TilesCfg<HD, E4M3>;
   constexpr int kSteps = HD / 16;
   extern __shared__ uint8_t smem_raw[];
@@ -361,11 +369,13 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       // the fewest and the most keys that a row of the warp sees (rows of no token see none)
       const int low = __reduce_min_sync(0xffffffffu, valid ? lim : INT_MAX), high = __reduce_max_sync(0xffffffffu, lim);
       const int ka = it.ka, end = it.end[w];
-      float c = scale_log2;
+      float c = scale_log2;                           // e4m3: the query row's power of two beside the common one
+      bool plain = true;                              // e4m3: 1 in all rows of the warp
       float m = -INFINITY, l = 0.f;
       for (int j = ka; j < end; ++j) {
-        float ct = c, off = 0.f, rv = 1.f;            // score = S ct + off; the sum takes rv times the exponentials
-        const float* mant = nullptr;
+        // score = S c + off; e4m3: S c key[column] + off, key[] near cs; the sum takes rv times the exponentials
+        float off = 0.f, rv = 1.f, cs = 1.f;
+        const float* key = nullptr;
         wait(&s_full[w], n_s & 1);
         ++n_s;
         ptx::tc_fence_after();
@@ -376,12 +386,14 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           const uint32_t t = n_sc + (j - ka);
           wait(&sc_full[t % C::kScaleBufs], (t / C::kScaleBufs) & 1);
           const float4 f = reinterpret_cast<const float4*>(smem + C::kScaleOff)[t % C::kScaleBufs];
-          ct = f.x, off = f.y, rv = f.z;
-          mant = reinterpret_cast<const float*>(smem + C::kMantOff) + (t % C::kScaleBufs) * kKeys;
-          if (j == ka) c *= q_scale[((n_o & 1) * 2 + w) * 128 + row];
-          ct *= c;
+          cs = f.x, off = f.y, rv = f.z;
+          key = reinterpret_cast<const float*>(smem + C::kKeyOff) + (t % C::kScaleBufs) * kKeys;
+          if (j == ka) {
+            c = valid ? q_scale[((n_o & 1) * 2 + w) * 128 + row] * scale_power : 1.f;
+            plain = __all_sync(0xffffffffu, c == 1.f);
+          }
         }
-        const uint64_t cc = pair(ct, ct);
+        const uint64_t cc = pair(c, c);
         const int seen = lim - j * kKeys, seen_low = low - j * kKeys, seen_high = high - j * kKeys;   // keys 0 .. seen are visible
         constexpr int W = 32;                         // columns at a time
         auto mask = [&](uint32_t (&x)[W], int h) {    // of columns W h ...
@@ -414,20 +426,21 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             tmem_st(to + W * i, xb);
           }
         };
-        // the weights of columns W h ... against the maximum m, into p
-        auto weights = [&](uint32_t (&x)[W], int h, uint64_t neg, uint32_t* p) {
+        // the weights of columns W h ... against the maximum m, into p; e4m3: kf: the columns' words
+        auto weights = [&](uint32_t (&x)[W], uint64_t neg, uint32_t* p, const float4* kf) {
 #pragma unroll
           for (int i = 0; i < W; i += 4) {
-            float2 e0 = unpair(fma_pair(pair_u(x[i], x[i + 1]), cc, neg));
-            float2 e1 = unpair(fma_pair(pair_u(x[i + 2], x[i + 3]), cc, neg));
+            const uint64_t c0 = E4M3 ? pair(kf[i / 4].x, kf[i / 4].y) : cc, c1 = E4M3 ? pair(kf[i / 4].z, kf[i / 4].w) : cc;
+            float2 e0 = unpair(fma_pair(pair_u(x[i], x[i + 1]), c0, neg));
+            float2 e1 = unpair(fma_pair(pair_u(x[i + 2], x[i + 3]), c1, neg));
             e0.x = exp2_approx(e0.x), e0.y = exp2_approx(e0.y);
             e1.x = exp2_approx(e1.x), e1.y = exp2_approx(e1.y);
-            sum = add_pair(sum, pair(e0.x, e0.y));
-            sum1 = add_pair(sum1, pair(e1.x, e1.y));
-            if (E4M3) {
-              const float4 f = *reinterpret_cast<const float4*>(mant + W * h + i);
-              e0 = unpair(mul_pair(pair(e0.x, e0.y), pair(f.x, f.y)));
-              e1 = unpair(mul_pair(pair(e1.x, e1.y), pair(f.z, f.w)));
+            const uint64_t y0 = pair(e0.x, e0.y), y1 = pair(e1.x, e1.y);
+            sum = add_pair(sum, y0);
+            sum1 = add_pair(sum1, y1);
+            if (E4M3) {                               // -P: the value rows are negative too
+              e0 = unpair(fma_pair(y0, pair(value_rest(kf[i / 4].x), value_rest(kf[i / 4].y)), y0));
+              e1 = unpair(fma_pair(y1, pair(value_rest(kf[i / 4].z), value_rest(kf[i / 4].w)), y1));
             }
             p[i / 2] = E4M3 ? pack_f16(e0.x, e0.y) : pack_bf16(e0.x, e0.y);
             p[i / 2 + 1] = E4M3 ? pack_f16(e1.x, e1.y) : pack_bf16(e1.x, e1.y);
@@ -440,17 +453,33 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           // against 568; two pieces a turn, the next loaded ahead, 625). bf16: for the tiles that some row of the warp
           // does not see whole, at most two of an item, where a second unrolled copy cost registers (347 us against 335).
           const int pieces = max(0, min(kKeys / W, (seen_high + W) / W));         // that some row of the warp sees
-          auto pass = [&](auto&& work) {
+          auto load_keys = [&](float4 (&f)[W / 4], int h) {
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) f[i] = reinterpret_cast<const float4*>(key + W * h)[i];
+          };
+          auto maximum = [&](auto exact) {            // of S, or of S times the keys' factors
+            float t = -INFINITY;
 #pragma unroll 1
             for (int h = 0; h < pieces; ++h) {
               tmem_ld(ts + W * h, xa);
               ptx::tmem_ld_wait();
+              if (exact.value) {
+                float4 f[W / 4];
+                load_keys(f, h);
+#pragma unroll
+                for (int i = 0; i < W; ++i) xa[i] = __float_as_uint(__uint_as_float(xa[i]) * (&f[i / 4].x)[i & 3]);
+              }
               if (edge) mask(xa, h);
-              work(xa, h);
+              t = largest(xa, t);
             }
+            return t;
           };
-          pass([&](uint32_t (&x)[W], int) { top = largest(x, top); });
-          top = fmaf(top, ct, off);
+          top = maximum(std::false_type{}) * (E4M3 ? c * cs : c);
+          if (E4M3) {
+            const bool far = fabsf(top) > kBoundedScore && top != -INFINITY;
+            top = fmaf(kKeyBound, fminf(fabsf(top), kBoundedScore), top) + off;
+            if (__any_sync(0xffffffffu, far)) top = fmaf(maximum(std::true_type{}), c, off);
+          }
           if (j == ka)
             m = top;
           else if (__any_sync(0xffffffffu, top > m + kLazy<E4M3>))
@@ -458,10 +487,26 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           const float mm = m == -INFINITY ? 0.f : m;
           const uint64_t neg = pair(off - mm + kUp<E4M3>, off - mm + kUp<E4M3>);
           uint32_t p[W / 2];
-          pass([&](uint32_t (&x)[W], int h) {
-            weights(x, h, neg, p);
-            tmem_st(ts + W / 2 * h, p);
-          });
+          auto second = [&](auto scaled) {
+#pragma unroll 1
+            for (int h = 0; h < pieces; ++h) {
+              float4 f[W / 4];
+              tmem_ld(ts + W * h, xa);
+              if (E4M3) load_keys(f, h);              // (on their way together)
+              ptx::tmem_ld_wait();
+              if (scaled.value) {
+#pragma unroll
+                for (int i = 0; i < W; ++i) xa[i] = __float_as_uint(__uint_as_float(xa[i]) * c);
+              }
+              if (edge) mask(xa, h);
+              weights(xa, neg, p, f);
+              tmem_st(ts + W / 2 * h, p);
+            }
+          };
+          if (!E4M3 || plain)
+            second(std::false_type{});
+          else
+            second(std::bool_constant<E4M3>{});
           if (pieces < kKeys / W) {
 #pragma unroll
             for (int i = 0; i < W / 2; ++i) p[i] = 0u;
@@ -472,7 +517,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           if (j == ka) {                              // a first maximum: that of the first columns
             tmem_ld(ts, xa);
             ptx::tmem_ld_wait();
-            m = fmaf(largest(xa, top), ct, off);
+            m = fmaf(largest(xa, top), c, off);
           }
           // One pass over S, W columns at a time: weights against the maximum so far, and the tile's own maximum. P
           // waits in registers: where the tile's maximum is above the lazy limit, S is still there for another pass.
@@ -484,7 +529,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             sum = 0, sum1 = 0;
             auto piece = [&](uint32_t (&x)[W], int h) {
               top = largest(x, top);
-              weights(x, h, neg, p + W / 2 * h);
+              weights(x, neg, p + W / 2 * h, nullptr);
             };
             tmem_ld(ts, xa);
 #pragma unroll
@@ -496,7 +541,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               if (h + 2 < kKeys / W) tmem_ld(ts + W * h + 2 * W, xa);
               piece(xb, h + 1);
             }
-            top = fmaf(top, ct, off);
+            top = fmaf(top, c, off);
             if (!__any_sync(0xffffffffu, top > m + kLazy<E4M3>)) break;
             rescale(top > m + kLazy<E4M3> ? top : m);
           }
@@ -608,10 +653,13 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             const int st = n % C::kRing, cs = n % C::kStages;
             wait(&raw_full[cs], (n / C::kStages) & 1);
             if (h == 0) {
-              // the tile's largest scales, and every row's share of them
+              // the tile's largest scales, and every row's share of them. A row with a NaN scale is NaN in its
+              // scores alone: its values would reach rows that do not see it.
               const float* rw = reinterpret_cast<const float*>(smem + C::kRawScaleOff) + cs * 2 * kKeys + tid;
-              const float ks = tid < cut ? rw[0] : 0.f, vs = tid < cut ? rw[kKeys] : 0.f;
-              float km = ks, vm = vs;                 // (the maximum passes over NaN)
+              float ks = tid < cut ? rw[0] : 0.f, vs = tid < cut ? rw[kKeys] : 0.f;
+              const bool none = !(fabsf(ks) < kMostScale) || !(fabsf(vs) < kMostScale);
+              if (none) ks = vs = 0.f;
+              float km = fabsf(ks), vm = vs;
 #pragma unroll
               for (int d = 16; d > 0; d >>= 1) {
                 km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, d));
@@ -621,19 +669,24 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               converters_sync();
               km = fmaxf(fmaxf(maxima[0], maxima[1]), fmaxf(maxima[2], maxima[3]));
               vm = fmaxf(fmaxf(maxima[4], maxima[5]), fmaxf(maxima[6], maxima[7]));
-              if (!(km > 0.f)) km = 1.f;
+              if (!(km >= kLeastScale)) km = 1.f;
               if (!(vm >= kLeastScale)) vm = 1.f;
-              // a row with a NaN scale is NaN in its scores alone: its values would reach rows that do not see it
-              factors[tid] = __half2half2(__float2half_rn(ks != ks || vs != vs ? __int_as_float(0x7fffffff) : kLift * __fdividef(ks, km)));
+              const uint32_t kp = __float_as_uint(km) & 0x7f800000, vp = __float_as_uint(vm) & 0x7f800000;   // the powers below
+              const float ki = __uint_as_float((254u << 23) - kp), vi = __uint_as_float((254u << 23) - vp);   // their inverses
               const uint32_t t = n / 2;
-              const float top2 = __int_as_float(__float_as_int(vm) & 0x7f800000);               // 2^E
-              const float row2 = vs >= kLeastScale ? __int_as_float(__float_as_int(vs) & 0x7f800000) : 0.f;
-              const float inv2 = 1.0f / top2;
-              factors[kKeys + tid] = __half2half2(__float2half_rn(kLift * row2 * inv2));
-              (reinterpret_cast<float*>(smem + C::kMantOff) + (t % C::kScaleBufs) * kKeys)[tid] = row2 > 0.f ? vs / row2 : 1.f;
+              // the scales to 7 bits, the key's to the nearest, as shares of those powers; what is left of the value's scale,
+              // 1 + byte 2^-14, lies in the last bits of what is left of the key's
+              const float k7 = __int_as_float((__float_as_int(ks) + 0x10000) & 0xfffe0000);
+              const float v7 = vs >= kLeastScale ? __int_as_float(__float_as_int(vs) & 0xfffe0000) : 0.f;
+              factors[tid] = __half2half2(__float2half_rn(none ? __int_as_float(0x7fffffff) : kLift * (k7 * ki)));
+              factors[kKeys + tid] = __half2half2(__float2half_rn(-kLift * (v7 * vi)));
+              const float common = scale_log2 * (__uint_as_float(kp) * (1.0f / (kLift * kCommonLift)));
+              const int key = __float_as_int(fabsf(ks) >= kLeastScale ? common * __fdividef(ks, k7) : common);
+              const int byte = v7 > 0.f ? min(255, __float2int_rn(__fdividef(vs - v7, v7) * 16384.f)) : 0;
+              (reinterpret_cast<int*>(smem + C::kKeyOff) + (t % C::kScaleBufs) * kKeys)[tid] = ((key - byte + 128) & ~255) | byte;
               if (tid == 0)
                 reinterpret_cast<float4*>(smem + C::kScaleOff)[t % C::kScaleBufs] =
-                    make_float4(km / kLift, static_cast<float>((__float_as_int(vm) >> 23) - 127 - kLiftLog2), inv2 * kLift, 0.f);
+                    make_float4(common, static_cast<float>((__float_as_int(vm) >> 23) - 127 - kLiftLog2), vi * kLift, 0.f);
               ptx::mbar_arrive(&sc_full[t % C::kScaleBufs]);
               converters_sync();
             }
@@ -779,8 +832,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               for (int k = 0; k < 4; ++k) most = fmaxf(most, fmaxf(fabsf(ptx::bf16_lo(y[k])), fabsf(ptx::bf16_hi(y[k]))));
             }
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-            float back;
-            const float lift = query_lift(most, &back);
+            float back, lift = query_lift(most, &back);
+            if (most == 0.f || (most >= kCommonLeast && most < kCommonMost)) lift = kCommonLift, back = 1.0f / kCommonLift;
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
               uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -788,7 +841,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               for (int k = 0; k < 4; ++k) y[k] = pack_f16(ptx::bf16_lo(y[k]) * lift, ptx::bf16_hi(y[k]) * lift);
               *seg(i) = make_uint4(y[0], y[1], y[2], y[3]);
             }
-            if (side == 0) q_scale[(par * 2 + w) * 128 + row] = back;
+            if (side == 0) q_scale[(par * 2 + w) * 128 + row] = back * kCommonLift;
           }
           ptx::fence_proxy_async_smem();
           ptx::mbar_arrive(&q_full[w]);
@@ -815,6 +868,9 @@ cudaError_t launch_as(const CUtensorMap& tk, const CUtensorMap& tv, const uint16
   static cudaError_t once = cudaFuncSetAttribute(attention_tiles_kernel<HD, E4M3>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (once != cudaSuccess) return once;
+  // e4m3: an unusual scale's power of two goes with the query rows, so that the keys' factors are normal numbers
+  float power = 1.0f;
+  if (E4M3 && !(scale_log2 > 0x1p-16f && scale_log2 < 0x1p16f)) power = std::ldexp(1.0f, std::max(-126, std::ilogb(scale_log2)));
   note_launch_begin(kKindAttn, st);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(s.tile_ctas);
@@ -826,7 +882,7 @@ cudaError_t launch_as(const CUtensorMap& tk, const CUtensorMap& tv, const uint16
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_tiles_kernel<HD, E4M3>, tk, tv, tq, o, scale_log2, kv, s);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_tiles_kernel<HD, E4M3>, tk, tv, tq, o, scale_log2 / power, power, kv, s);
   note_launch_end(kKindAttn, st);
   return e;
 }

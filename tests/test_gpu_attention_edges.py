@@ -232,3 +232,39 @@ def test_tiny_queries_over_e4m3(layer, n, hd):
         st.q = (st.q.double() * gain).to(torch.bfloat16)
         scale = 0.1 if gain < 1 else 0.1 / gain
         st.check(st.run(scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("n,hq,hkv,hd", [([1, 1, 1], 8, 2, 128), ([1, 2], 8, 2, 64), ([4, 3], 4, 1, 128), ([150], 4, 2, 128), ([90, 40], 2, 1, 64)])
+def test_sharp_scores_over_e4m3(layer, n, hq, hkv, hd):
+    """Queries along one key each, with scores of 30 to 60 there: relative errors of scores show whole. Scores are fp32 sums of exact
+    products (queries, lifted by a power of two, and codes times at most 7 bits of their scale are f16 numbers), times what is left of
+    the scale to 2^-16; weights take what is left of the value's scale to 2^-14 and are rounded once to f16, 2^-11, and below
+    2^-24 of the largest to 2^-35 of it."""
+    from oracle import attention as ref
+    st = Step(layer, n, [200] * len(n), hq, hkv, hd, 16, "e4m3", seed=11)
+    rng = np.random.default_rng(8)
+    for s, L in enumerate(st.len):
+        for pos in range(L):
+            for which in (0, 1):
+                set_scale(st, s, pos, which, float(2.0 ** rng.uniform(-8.0, -6.0)))
+    G = hq // hkv
+    q = torch.zeros_like(st.q)
+    for s in range(len(n)):
+        for i in range(n[s]):
+            for h in range(hq):
+                pos = int(rng.integers(0, st.len[s] - n[s] + i + 1))
+                key = st.rows[s][0][pos, h // G]
+                q[st.starts[s] + i, h] = torch.from_numpy(key * rng.uniform(30, 60) / (key @ key * hd ** -0.5)).to(torch.bfloat16)
+    st.q = q
+    o = st.run()
+    st.seq.status()
+    want, W, S = ref.attention(q.double().cpu().numpy(), [r[0] for r in st.rows], [r[1] for r in st.rows], st.starts, G, hd ** -0.5)
+    got = o.double().cpu().numpy().reshape(want.shape)
+    d = (hd * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -16) * S[..., None]
+    lost = np.zeros_like(want)
+    for s in range(len(n)):
+        a, b = st.starts[s], st.starts[s + 1]
+        lost[a:b] = 2.0 ** -35 * 4 * np.repeat(np.abs(st.rows[s][1]).sum(0), G, 0)      # (weight times scale: scales differ by 4)
+    tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -14 + 2 * d) * (W + np.abs(want)) + lost
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), bad.size, float(np.nanmax(np.abs(got - want) / tol)))
