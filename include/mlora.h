@@ -336,7 +336,9 @@ enum { MLORA_KV_BF16 = 0, MLORA_KV_E4M3 = 1 };
 /* Creates the paged cache of one attention layer: n_pages pages of page_size tokens (8, 16, 32, 64, 128 or
  * 256), n_kv_heads heads of head_dim (64 or 128) elements.
  *   K, V: [n_pages, n_kv_heads, page_size, head_dim], bf16, or e4m3 codes with one fp32 scale for each
- *   token and head (k_scale, v_scale: [n_pages, n_kv_heads, page_size]; an element is code * scale).
+ *   token and head (k_scale, v_scale: [n_pages, n_kv_heads, page_size]; an element is code * scale). A scale is
+ *   positive, zero, or NaN for a row that is to read as NaN; the attention takes scales below 2^-100 for zero and may take
+ *   those from 2^120 on for NaN (mlora_qkv_write makes scales between 2^-69 and 2^120).
  * The arrays are the caller's (device, 16-byte aligned, valid until the cache is destroyed; the scales NULL
  * for MLORA_KV_BF16), or, with all four NULL, allocated here and zeroed.
  * n_pages * page_size * n_kv_heads must stay below 2^31. Other sizes: MLORA_ERR_INVALID_ARG. */
@@ -419,7 +421,7 @@ MLORA_API mlora_status mlora_qkv_write(mlora_kv_t kv, mlora_seq_t seq, const flo
  * G = n_q_heads / n_kv_heads; query, out: device bf16 [T, n_q_heads, head_dim], 16-byte aligned, not the same
  * array; scale positive. Rows of tokens in no sequence are zero. Scores, maxima and sums are fp32; the weights are rounded to
  * bf16 (f16 over an e4m3 cache) for the product with V. f16 has no room below: a key whose weight, or weight times its
- * value row's scale, is less than 2^-14 of the row's largest counts with fewer bits, and below 2^-24 it may count as zero.
+ * value row's scale, is less than 2^-21 of the row's largest counts with fewer bits, and below 2^-31 it may count as zero.
  * Cache rows past a sequence's length have no effect, whatever they hold. Deterministic: a repeated call gives the same bits. */
 MLORA_API mlora_status mlora_attention(mlora_kv_t kv, mlora_seq_t seq, const mlora_bf16* query, float scale,
                                        mlora_bf16* out, void* stream);

@@ -19,8 +19,8 @@
 //     chunks need no shuffles and no rescaling. P is at most 2^8, which f16 and bf16 hold.
 //   - e4m3: codes become f16 (exact) in registers. The key scale multiplies the score. The weights w_j = 2^(score_j - m)
 //     go into the denominator as they are; for the product with the codes they are multiplied by the value scale and by
-//     u = 2^(m - n), where n follows the largest score_j + log2 vs_j as m follows the largest score: P_j = w_j vs_j u is at
-//     most 2^8 whatever the scales' magnitude. A value scale of 0 leaves its weight in the denominator. Both maxima
+//     u = 2^(m - n), where n + 7 follows the largest score_j + log2 vs_j as m follows the largest score: P_j = w_j vs_j u is at
+//     most 2^15 whatever the scales' magnitude. A value scale of 0 leaves its weight in the denominator. Both maxima
 //     are whole numbers, so every rescaling is exact. Query rows are lifted by a power of two into f16's range.
 // Keys at or past a row's limit are replaced by -inf by selection, and rows past the cached length are
 // zero-filled on load, so what lies there (NaN included) has no effect.
@@ -39,8 +39,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 16;                  // keys of a warp's chunk
-constexpr float kLazy = 8.0f;               // log2 of the largest P
-constexpr float kMostP = 256.0f;
+constexpr float kLazy = 8.0f;               // log2 of the largest weight; e4m3: of the largest weight times scale, before
+constexpr float kUp = 7.0f;                 // P is lifted to the top of f16's range: its normal numbers then reach down to 2^-21
+constexpr float kMostP = 32768.0f;          // of the row's largest
 // A value scale counts as this power of two at least where the maximum is taken: the maximum of value rows of scale 0 alone
 // stays finite, and 2^80 times any number of weights does too.
 constexpr float kLeastLog2 = -80.0f;
@@ -391,7 +392,7 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
 #pragma unroll
               for (int h = 0; h < 2; ++h) t[h] = sc[z][2 * h + c] + fmaxf(__log2f(vs[h]), kLeastLog2);
               const float old = m[z][c] - log2_of(up[z][c]);
-              const float next = fminf(fmaxf(ceilf(over_keys(fmaxf(t[0], t[1]))), old), top + 126.f);
+              const float next = fminf(fmaxf(ceilf(over_keys(fmaxf(t[0], t[1]))) - kUp, old), top + 126.f);
               fp = next == old ? 1.f : exp2_approx(old - next);
               if (top != -INFINITY) up[z][c] = pow2_of(top - next);
             }

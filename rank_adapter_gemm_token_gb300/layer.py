@@ -302,7 +302,7 @@ def attention(cache: KVCache, seq: SeqMeta, q: torch.Tensor, o: torch.Tensor | N
               stream=None) -> torch.Tensor:
     """Causal attention of the step's queries (bf16 [T, Hq, hd]) over the cache: bf16 [T, Hq * hd], the o linear's
     input. scale: 1 / sqrt(hd) by default. Over an e4m3 cache keys whose weight (or weight times value scale) is less than
-    2^-14 of the row's largest count with fewer bits, below 2^-24 they may count as zero."""
+    2^-21 of the row's largest count with fewer bits, below 2^-31 they may count as zero."""
     hq, hd = seq.n_q_heads, seq.head_dim
     assert q.is_cuda and q.dtype == torch.bfloat16 and q.shape == (seq.T, hq, hd) and q.is_contiguous()
     if o is None:

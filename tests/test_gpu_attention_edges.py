@@ -268,3 +268,27 @@ def test_sharp_scores_over_e4m3(layer, n, hq, hkv, hd):
     tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -14 + 2 * d) * (W + np.abs(want)) + lost
     bad = ~(np.abs(got - want) <= tol)
     assert not bad.any(), (int(bad.sum()), bad.size, float(np.nanmax(np.abs(got - want) / tol)))
+
+
+@pytest.mark.parametrize("n", [1, 2, 40])
+@pytest.mark.parametrize("ratio", [2.0 ** -20.37, 2.0 ** -15.6])
+def test_small_weights_over_e4m3_keep_their_bits(layer, n, ratio):
+    """Key 0 has nearly all of the weight and no value in the upper half of the head, where the others, of weight `ratio` each,
+    have ones: weights down to 2^-21 of the largest are rounded to f16 like the others (2^-11)."""
+    L = 64
+    st = Step(layer, [n], [L - n], 4, 1, kind="e4m3")
+    st.q.zero_()
+    st.q[..., 0] = 1.0
+    p = [int(st.table[0, i]) for i in range(L // 16)]
+    for c, z in ((st.k, st.ks), (st.v, st.vs)):
+        c.view(torch.uint8)[p] = 0
+        z[p] = 1 / 448
+    st.k.view(torch.uint8)[p[0], 0, 0, 0] = 0x7E          # 448: one, with its scale
+    st.v.view(torch.uint8)[p, 0, :, 64:] = 0x7E
+    st.v.view(torch.uint8)[p[0], 0, 0, 64:] = 0
+    o = st.run(scale=-float(np.log(ratio))).double().cpu().numpy().reshape(n, 4, 128)
+    others = np.arange(L - n, L)[:, None, None] * ratio
+    want = np.broadcast_to(others / (1 + others), (n, 4, 64))
+    # the product's one at 448 / 448 (2^-23 of a score of 20), the output's bf16 beside the weights
+    assert (np.abs(o[..., 64:] - want) <= (2.0 ** -8 + 2.0 ** -11 + 1e-4) * want).all()
+    assert not o[..., :64].any()
