@@ -134,6 +134,25 @@ def _stream(stream):
     return stream
 
 
+def _torch_stream(stream, device: torch.device):
+    """The torch stream of a torch stream or raw handle."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+
+
+def _output(shape, dtype, device: torch.device, stream) -> torch.Tensor:
+    """A new tensor for a call on `stream`. It is made there, so that nothing queued earlier on the current stream still works in
+    its memory, and, once released, kept from reuse until what the current stream then has queued is done with it too."""
+    here = None if stream is None else torch.cuda.current_stream(device)
+    if here is None or here.cuda_stream == getattr(stream, "cuda_stream", stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        y = torch.empty(shape, dtype=dtype, device=device)
+    y.record_stream(here)
+    return y
+
+
 # The current stream's raw handle. The attention step's calls take a few microseconds on the GPU for small batches, where
 # making a Stream object for each (about 3 us) is felt.
 _raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -154,7 +173,7 @@ def linear(pool: AdapterPool, meta: StepMeta, x: torch.Tensor, W: torch.Tensor, 
     T = meta.T
     assert x.shape == (T, pool.K) and W.shape == (pool.D, pool.K)
     if y is None:
-        y = torch.empty((T, pool.D), dtype=torch.float32, device=x.device)
+        y = _output((T, pool.D), torch.float32, x.device, stream)
     mlora.mlora_linear(pool.handle, meta.handle, x, W, y, _stream(stream))
     return y
 
@@ -166,7 +185,7 @@ def embedding(pool: EmbeddingPool, meta: StepMeta, ids: torch.Tensor, E: torch.T
     T = meta.T
     assert ids.shape == (T,) and E.shape == (pool.K, pool.D)
     if y is None:
-        y = torch.empty((T, pool.D), dtype=torch.float32, device=E.device)
+        y = _output((T, pool.D), torch.float32, E.device, stream)
     mlora.mlora_embedding(pool.handle, meta.handle, ids, E, y, _stream(stream))
     return y
 
@@ -175,7 +194,7 @@ def base_gemm(x: torch.Tensor, W: torch.Tensor, y: torch.Tensor | None = None, s
     T, K = x.shape
     D = W.shape[0]
     if y is None:
-        y = torch.empty((T, D), dtype=torch.float32, device=x.device)
+        y = _output((T, D), torch.float32, x.device, stream)
     mlora.mlora_base_gemm(x, W, y, T, K, D, _stream(stream))
     return y
 
@@ -290,7 +309,7 @@ def qkv_write(cache: KVCache, seq: SeqMeta, qkv: torch.Tensor, q: torch.Tensor |
     assert positions is None or (positions.is_cuda and positions.dtype == torch.int32 and positions.shape == (seq.T,)
                                  and positions.is_contiguous())
     if q is None:
-        q = torch.empty((seq.T, hq, hd), dtype=torch.bfloat16, device=seq.device)
+        q = _output((seq.T, hq, hd), torch.bfloat16, seq.device, stream)
     else:
         assert q.dtype == torch.bfloat16 and q.shape == (seq.T, hq, hd) and q.is_contiguous()
     mlora.mlora_qkv_write(cache.handle, seq.handle, qkv, qkv.stride(0) if seq.T > 1 else qkv.shape[1], q_norm, k_norm,
@@ -306,7 +325,7 @@ def attention(cache: KVCache, seq: SeqMeta, q: torch.Tensor, o: torch.Tensor | N
     hq, hd = seq.n_q_heads, seq.head_dim
     assert q.is_cuda and q.dtype == torch.bfloat16 and q.shape == (seq.T, hq, hd) and q.is_contiguous()
     if o is None:
-        o = torch.empty((seq.T, hq * hd), dtype=torch.bfloat16, device=seq.device)
+        o = _output((seq.T, hq * hd), torch.bfloat16, seq.device, stream)
     else:
         assert o.dtype == torch.bfloat16 and o.shape == (seq.T, hq * hd) and o.is_contiguous()
     mlora.mlora_attention(cache.handle, seq.handle, q, hd ** -0.5 if scale is None else scale, o, _raw_stream(stream, seq.device))
@@ -320,9 +339,9 @@ def kv_read(cache: KVCache, seq: SeqMeta, row_start: torch.Tensor, rows: int, k=
     assert row_start.numel() >= seq.n_seqs
     shape = (rows, cache.n_kv_heads, cache.head_dim)
     if k is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=seq.device)
+        k = _output(shape, torch.bfloat16, seq.device, stream)
     if v is None:
-        v = torch.empty(shape, dtype=torch.bfloat16, device=seq.device)
+        v = _output(shape, torch.bfloat16, seq.device, stream)
     assert k.shape == shape and v.shape == shape and k.dtype == v.dtype == torch.bfloat16
     assert k.is_contiguous() and v.is_contiguous()
     mlora.mlora_kv_read(cache.handle, seq.handle, row_start, rows, k, v, _raw_stream(stream, seq.device))
@@ -334,7 +353,13 @@ def attention_block(meta: StepMeta, seq: SeqMeta, cache: KVCache, x: torch.Tenso
                     rope: Rope | None = None, scale: float | None = None, stream=None) -> torch.Tensor:
     """One layer's attention for the step that `meta` (adapters) and `seq` (sequences) describe: the adapted qkv linear of
     x (bf16 [T, hidden]), the write of its rows, the attention over the cache, and the adapted o linear: fp32
-    [T, W_o.shape[0]]."""
-    qkv = linear(qkv_pool, meta, x, W_qkv, stream=stream)
-    q = qkv_write(cache, seq, qkv, q_norm=q_norm, k_norm=k_norm, eps=eps, rope=rope, stream=stream)
-    return linear(o_pool, meta, attention(cache, seq, q, scale=scale, stream=stream), W_o, stream=stream)
+    [T, W_o.shape[0]]. With `stream` all of it runs there, what lies between the operators included."""
+    if stream is not None:
+        here = torch.cuda.current_stream(seq.device)
+        with torch.cuda.stream(_torch_stream(stream, seq.device)):
+            y = attention_block(meta, seq, cache, x, qkv_pool, W_qkv, o_pool, W_o, q_norm, k_norm, eps, rope, scale)
+        y.record_stream(here)
+        return y
+    qkv = linear(qkv_pool, meta, x, W_qkv)
+    q = qkv_write(cache, seq, qkv, q_norm=q_norm, k_norm=k_norm, eps=eps, rope=rope)
+    return linear(o_pool, meta, attention(cache, seq, q, scale=scale), W_o)

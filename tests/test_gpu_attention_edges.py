@@ -292,3 +292,93 @@ def test_small_weights_over_e4m3_keep_their_bits(layer, n, ratio):
     # the product's one at 448 / 448 (2^-23 of a score of 20), the output's bf16 beside the weights
     assert (np.abs(o[..., 64:] - want) <= (2.0 ** -8 + 2.0 ** -11 + 1e-4) * want).all()
     assert not o[..., :64].any()
+
+
+# ------------------------------------------------------------------------------------------- another stream
+def busy(stream, milliseconds=100):
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(int(2e6 * milliseconds))
+
+
+class Block:
+    """A small adapted layer and a step of prompts and single tokens for it."""
+
+    def __init__(self, layer):
+        g = torch.Generator(device="cuda").manual_seed(4)
+        rand = lambda *shape, std=1.0: (std * torch.randn(*shape, generator=g, device="cuda")).to(torch.bfloat16)  # noqa: E731
+        hidden, self.hq, self.hkv, self.hd = 512, 8, 2, 64
+        self.layer = layer
+        self.W_qkv, self.W_o = rand((self.hq + 2 * self.hkv) * self.hd, hidden, std=0.04), rand(hidden, self.hq * self.hd, std=0.04)
+        self.pools = layer.AdapterPool(2, 8, hidden, self.W_qkv.shape[0]), layer.AdapterPool(2, 8, self.hq * self.hd, hidden)
+        for p in self.pools:
+            p.load(0, rand(8, p.K, std=0.05), rand(p.D, 8, std=0.05), 8, 16.0)
+            p.sync()
+        n, ctx = [40, 1, 1, 7], [0, 30, 100, 12]
+        self.T = sum(n)
+        self.cache = layer.KVCache(40, 16, self.hkv, self.hd)
+        self.cache.k.normal_(generator=g)
+        self.cache.v.normal_(generator=g)
+        self.table = torch.arange(40, dtype=torch.int32, device="cuda").reshape(4, 10)
+        self.meta, self.seq = layer.StepMeta(self.T, 1, 8), layer.SeqMeta(4, self.T, 10, self.hq, self.hkv, self.hd)
+        self.slots, self.q_start = ints([0] * 30 + [-1] * (self.T - 30)), ints([0, 40, 41, 42, 49])
+        self.kv_len = ints([a + b for a, b in zip(n, ctx)])
+        self.rope, self.x = layer.Rope(self.hd), rand(self.T, hidden)
+        self.build()
+
+    def build(self):
+        self.meta.build(self.slots, None, self.pools[0])
+        self.seq.build(self.q_start, self.kv_len, self.table, self.T, self.cache, 40)
+
+    def run(self, stream=None):
+        return self.layer.attention_block(self.meta, self.seq, self.cache, self.x, self.pools[0], self.W_qkv, self.pools[1],
+                                          self.W_o, rope=self.rope, stream=stream)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_attention_block_on_another_stream(layer, raw):
+    """The block waits on its stream while the current one makes and fills tensors of its temporaries' sizes; and it runs at
+    once while the current stream still has work in memory that was released before the call."""
+    b = Block(layer)
+    want = b.run()
+    sizes = [(b.T * (b.hq + 2 * b.hkv) * b.hd, torch.float32), (b.T * b.hq * b.hd, torch.bfloat16), (b.T * 512, torch.float32)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for late in (True, False):
+        if late:
+            busy(s)
+        else:
+            busy(torch.cuda.current_stream())
+            for size, dtype in sizes * 3:
+                torch.full((size,), float("nan"), dtype=dtype, device="cuda")
+        y = b.run(stream=s.cuda_stream if raw else s)
+        if late:
+            kept = [torch.full((size,), float("nan"), dtype=dtype, device="cuda") for size, dtype in sizes * 3]
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), late
+        del y
+    del kept
+
+
+def test_outputs_made_for_another_stream(layer):
+    """Outputs that the calls make while the current stream still has work in memory of their size that was just released."""
+    b = Block(layer)
+    qkv, rs = torch.randn(b.T, (b.hq + 2 * b.hkv) * b.hd, device="cuda"), ints([0, 40, 71, 172])
+    q = layer.qkv_write(b.cache, b.seq, qkv)
+    calls = [lambda st: layer.linear(b.pools[0], b.meta, b.x, b.W_qkv, stream=st),
+             lambda st: layer.base_gemm(b.x, b.W_qkv, stream=st),
+             lambda st: layer.qkv_write(b.cache, b.seq, qkv, stream=st),
+             lambda st: layer.attention(b.cache, b.seq, q, stream=st),
+             lambda st: layer.kv_read(b.cache, b.seq, rs, 191, stream=st)]
+    s = torch.cuda.Stream()
+    for call in calls:
+        want = call(None)
+        want = want if isinstance(want, tuple) else (want,)
+        torch.cuda.synchronize()
+        busy(torch.cuda.current_stream())
+        for x in want * 4:
+            torch.full_like(x, float("nan"))
+        got = call(s)
+        torch.cuda.synchronize()
+        for x, y in zip(want, got if isinstance(got, tuple) else (got,)):
+            assert torch.equal(x, y)
