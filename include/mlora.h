@@ -411,7 +411,8 @@ MLORA_API mlora_status mlora_seq_status(mlora_seq_t seq);
  *   q_out: device bf16 [T, n_q_heads, head_dim], overwritten (zero rows for tokens in no sequence).
  * Keys and values go to the tokens' rows of the cache: rounded to bf16, or as e4m3 with the scale
  * max(largest magnitude, 2^-60) / 448 (a row with an infinity or a NaN: scale NaN, so that it reads as NaN).
- * qkv, q_out and the weights are 16-byte aligned. All arithmetic is fp32; angles are accurate to about 1e-7. Every value is a fixed sequence of operations. */
+ * qkv, q_out and the weights are 16-byte aligned. All arithmetic is fp32; angles are accurate to 2e-7 of a
+ * radian (5e-7 for frequencies above 1). Every value is a fixed sequence of operations. */
 MLORA_API mlora_status mlora_qkv_write(mlora_kv_t kv, mlora_seq_t seq, const float* qkv, int64_t ld,
                                        const mlora_bf16* q_norm, const mlora_bf16* k_norm, float eps,
                                        mlora_rope_t rope, const int32_t* positions, mlora_bf16* q_out, void* stream);

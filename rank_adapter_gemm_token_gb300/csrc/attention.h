@@ -94,9 +94,9 @@ constexpr int kTileHead = 3;          // key tiles that an item's fixed costs (q
 // CTAs of the row kernel on an SM: by the row limit (16 rather than 8) and the cache's type.
 __host__ __device__ constexpr int rows_ctas_per_sm(bool sixteen, bool e4m3) { return e4m3 && !sixteen ? 3 : 2; }
 
-// Per-pair rotation frequencies in turns per position, each as a sum of two floats.
+// Per-pair rotation frequencies in turns per position, each as a sum of three floats.
 struct RopeView {
-  const float2* freq;   // [rot / 2]
+  const float4* freq;   // [rot / 2]
   int rot;              // rotated elements of a head (0: none)
   int interleaved;      // pairs (2i, 2i + 1) instead of (i, i + rot / 2)
   float mscale;         // factor on cos and sin

@@ -58,7 +58,7 @@ struct mlora_kv {
 };
 
 struct mlora_rope {
-  float2* freq = nullptr;
+  float4* freq = nullptr;
   int rot = 0, interleaved = 0;
   float mscale = 1.f;
 };
@@ -205,20 +205,26 @@ mlora_status mlora_rope_create(int rot_dim, int interleaved, const double* freq,
   if (rot_dim < 8 || rot_dim % 8 || rot_dim > 128) return fail(MLORA_ERR_INVALID_ARG, "rot_dim %d must be a multiple of 8 in [8, 128]", rot_dim);
   if (!freq) return fail(MLORA_ERR_INVALID_ARG, "freq is NULL");
   if (!std::isfinite(mscale)) return fail(MLORA_ERR_INVALID_ARG, "mscale must be finite");
-  float2 host[64];
+  // Turns per position, freq / (2 pi), to twice a double's bits, as a sum of three floats: positions up to 2^24 times frequencies
+  // up to 1e6 are 2^42 turns, of which the kernel wants 2^-24.
+  constexpr double kTwoPi = 6.283185307179586476925286766559, kTwoPiRest = 2.4492935982947064e-16;      // their sum
+  float4 host[64];
   for (int i = 0; i < rot_dim / 2; ++i) {
     if (!(std::fabs(freq[i]) <= 1e6)) return fail(MLORA_ERR_INVALID_ARG, "frequency %d is not a number of magnitude up to 1e6", i);
-    const double turns = freq[i] / 6.283185307179586476925286766559;
+    const double turns = freq[i] / kTwoPi, rest = (std::fma(-turns, kTwoPi, freq[i]) - turns * kTwoPiRest) / kTwoPi;
     host[i].x = static_cast<float>(turns);
-    host[i].y = static_cast<float>(turns - static_cast<double>(host[i].x));
+    const double y = (turns - static_cast<double>(host[i].x)) + rest;
+    host[i].y = static_cast<float>(y);
+    host[i].z = static_cast<float>(y - static_cast<double>(host[i].y));
+    host[i].w = 0.f;
   }
   mlora_rope* r = new (std::nothrow) mlora_rope();
   if (!r) return fail(MLORA_ERR_OOM, "host allocation failed");
   r->rot = rot_dim;
   r->interleaved = interleaved != 0;
   r->mscale = mscale;
-  cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&r->freq), sizeof(float2) * rot_dim / 2);
-  if (e == cudaSuccess) e = cudaMemcpy(r->freq, host, sizeof(float2) * rot_dim / 2, cudaMemcpyHostToDevice);
+  cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&r->freq), sizeof(float4) * rot_dim / 2);
+  if (e == cudaSuccess) e = cudaMemcpy(r->freq, host, sizeof(float4) * rot_dim / 2, cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     mlora_rope_destroy(r);

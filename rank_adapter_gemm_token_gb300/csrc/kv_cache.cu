@@ -7,9 +7,9 @@
 //     queries: bf16 row of q; keys and values: row pos % page of page table[pos / page], as bf16 or as
 //     e4m3 codes rn(x / s) with s = max(max |x|, 2^-60) / 448, one fp32 s for each token and head.
 // A row with an infinity or a NaN gets codes 0 and the scale NaN, so that all of it reads back as NaN.
-// Angles are taken in turns: pos * f with f a sum of two floats, the whole turns dropped exactly
-// (product and its rounding error by fma), then sin and cos of the fraction: about 1e-7 for every
-// position up to 2^24, where an fp32 angle in radians would be off by pos * 6e-8.
+// Angles are taken in turns: pos * f with f a sum of three floats, the whole turns of each product and of its
+// rounding error (by fma) dropped exactly, then sin and cos of the fraction: 2e-7 for every position up to 2^24 and
+// frequency up to 1 (5e-7 up to 1e6), where an fp32 angle in radians would be off by pos * 6e-8.
 // Bound: HBM, each value read once and written once, and close behind it the instructions: a row (one head of one token)
 // lies in the registers of hd / 8 lanes, eight elements each, so that norm, rotation and maximum are a few shuffles for two
 // (four) rows at a time, and the angles of a CTA's few tokens are made once, in shared memory. Each thread has two rows on
@@ -90,10 +90,10 @@ qkv_write_kernel(const float* __restrict__ qkv, int64_t ld, const uint16_t* __re
   }
   if (half > 0) {
     while (at < tokens) {
-      const float2 f = __ldg(rope.freq + ak);
-      const float p = pos * f.x;
+      const float4 f = __ldg(rope.freq + ak);
+      const float p = pos * f.x, p1 = pos * f.y, r = fmaf(pos, f.x, -p);
       float frac = p - rintf(p);
-      frac += fmaf(pos, f.x, -p) + pos * f.y;
+      frac += (r - rintf(r)) + (p1 - rintf(p1)) + (fmaf(pos, f.y, -p1) + pos * f.z);
       float sn, cs;
       sincospif(2.0f * frac, &sn, &cs);
       angle[at][ak] = make_float2(cs * rope.mscale, sn * rope.mscale);

@@ -382,3 +382,25 @@ def test_outputs_made_for_another_stream(layer):
         torch.cuda.synchronize()
         for x, y in zip(want, got if isinstance(got, tuple) else (got,)):
             assert torch.equal(x, y)
+
+
+# ------------------------------------------------------------------------------------------- angles
+def test_angles_of_fast_frequencies_and_far_positions(layer):
+    """Angles of pos * freq radians, freq up to 1e6 and positions up to 2^24, against exact arithmetic: 5e-7 of a radian and a
+    few roundings of the fp32 rotation (6e-8 each), in bf16 half a step, 2^-8."""
+    from fractions import Fraction
+    two_pi = Fraction("6.283185307179586476925286766559005768394338798750211641949889184615632812572417997256069650684234136")
+    freq = [1e6, 654321.987, 3.0e5, 77777.7, 1234.5678, 31.4, 6.283185, 3.14159, 1.0, 0.7, 0.01, 1e-3, 1e-5, -2.5e5, -1.0, 999999.999]
+    rope = layer.Rope(32, freq=freq)
+    pos = [0, 1, 2, 3, 1000, 65537, 1 << 20, 16777215, 16777216, 12345678, -5, -16777216]
+    T = len(pos)
+    st = Step(layer, [T], [0], 1, 1, 128)
+    qkv = torch.zeros(T, 3 * 128, device="cuda")
+    qkv[:, :16] = 1.0                                     # (1, 0) turned is (cos, sin)
+    q = layer.qkv_write(st.cache, st.seq, qkv, rope=rope, positions=ints(pos)).double().cpu().numpy()[:, 0]
+    for t, p in enumerate(pos):
+        for i, f in enumerate(freq):
+            turns = Fraction(p) * Fraction(f) / two_pi
+            a = float((turns - round(turns)) * two_pi)
+            for got, want in ((q[t, i], np.cos(a)), (q[t, i + 16], np.sin(a))):
+                assert abs(got - want) <= 2.0 ** -8 * abs(want) + 1e-6, (p, f, got, want)
