@@ -8,8 +8,20 @@
 #include <cstdint>
 
 #include "attention.h"
+#include "per_device.h"
 
 namespace mlora {
+
+// Allows a kernel's launches on the current device this many bytes of dynamic shared memory.
+template <auto Kernel>
+cudaError_t allow_shared_memory(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int device = 0;
+  if (cudaError_t e = cudaGetDevice(&device)) return e;
+  return once_per_device<cudaError_t>(done, device, [&] {
+    return cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;

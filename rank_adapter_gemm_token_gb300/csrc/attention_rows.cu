@@ -553,9 +553,7 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
 template <int HD, int NQ, bool E4M3>
 cudaError_t launch_as(const uint16_t* q, uint16_t* o, float scale_log2, const KvView& kv, const SeqView& s, cudaStream_t st) {
   using C = RowsCfg<HD, NQ, E4M3>;
-  static cudaError_t once = cudaFuncSetAttribute(attention_rows_kernel<HD, NQ, E4M3>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
-  if (once != cudaSuccess) return once;
+  if (cudaError_t e = allow_shared_memory<attention_rows_kernel<HD, NQ, E4M3>>(C::kBytes)) return e;
   note_launch_begin(kKindAttn, st);
   attention_rows_kernel<HD, NQ, E4M3><<<s.row_ctas, kThreads, C::kBytes, st>>>(q, o, scale_log2, kv, s);
   const cudaError_t e = cudaGetLastError();

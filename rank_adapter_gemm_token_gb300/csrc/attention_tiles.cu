@@ -865,9 +865,7 @@ cudaError_t launch_as(const CUtensorMap& tk, const CUtensorMap& tv, const uint16
   CUtensorMap tq;
   if (!make_tmap_heads_bf16(&tq, q, s.T, s.Hq, HD, s.tile_tokens, s.G)) return cudaErrorInvalidValue;
   using C = TilesCfg<HD, E4M3>;
-  static cudaError_t once = cudaFuncSetAttribute(attention_tiles_kernel<HD, E4M3>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
-  if (once != cudaSuccess) return once;
+  if (cudaError_t e = allow_shared_memory<attention_tiles_kernel<HD, E4M3>>(C::kBytes)) return e;
   // e4m3: an unusual scale's power of two goes with the query rows, so that the keys' factors are normal numbers
   float power = 1.0f;
   if (E4M3 && !(scale_log2 > 0x1p-16f && scale_log2 < 0x1p16f)) power = std::ldexp(1.0f, std::max(-126, std::ilogb(scale_log2)));
