@@ -430,6 +430,9 @@ mlora_status mlora_attention(mlora_kv_t kv, mlora_seq_t q, const mlora_bf16* que
   if (v.T > 0 && (!query || !out)) return fail(MLORA_ERR_INVALID_ARG, "query or out is NULL");
   if (!aligned(query, 16) || !aligned(out, 16)) return fail(MLORA_ERR_INVALID_ARG, "query and out must be 16-byte aligned");
   if (!(scale > 0.f && std::isfinite(scale))) return fail(MLORA_ERR_INVALID_ARG, "scale must be positive and finite");
+  const uintptr_t qa = reinterpret_cast<uintptr_t>(query), oa = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t bytes = static_cast<uintptr_t>(v.T) * v.Hq * v.hd * 2;
+  if (qa < oa + bytes && oa < qa + bytes) return fail(MLORA_ERR_INVALID_ARG, "query and out must not overlap");
   if (v.T == 0) return MLORA_OK;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_attention_rows(query, out, scale, kv->view, v, s);

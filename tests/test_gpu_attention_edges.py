@@ -404,3 +404,21 @@ def test_angles_of_fast_frequencies_and_far_positions(layer):
             a = float((turns - round(turns)) * two_pi)
             for got, want in ((q[t, i], np.cos(a)), (q[t, i + 16], np.sin(a))):
                 assert abs(got - want) <= 2.0 ** -8 * abs(want) + 1e-6, (p, f, got, want)
+
+
+# ------------------------------------------------------------------------------------------- refusals
+def test_query_and_output_must_not_overlap(layer):
+    from rank_adapter_gemm_token_gb300 import mlora
+    st = Step(layer, [1, 30], [50, 20])
+    both = torch.zeros(2 * st.q.numel(), dtype=torch.bfloat16, device="cuda")
+    n = st.q.numel() * 2
+    call = lambda q, o: mlora.mlora_attention(st.cache.handle, st.seq.handle, q, 1.0, o)  # noqa: E731
+    a = both.data_ptr()
+    for q, o in ((a, a), (a, a + 16), (a + n - 16, a), (a, a + n - 16)):
+        with pytest.raises(mlora.MloraError) as e:
+            call(q, o)
+        assert e.value.status == mlora.MLORA_ERR_INVALID_ARG
+    both[:st.q.numel()] = st.q.flatten()
+    call(a, a + n)                                        # side by side
+    torch.cuda.synchronize()
+    assert torch.equal(both[st.q.numel():].view_as(st.run()), st.run(scale=1.0))
