@@ -311,7 +311,7 @@ def qkv_write(cache: KVCache, seq: SeqMeta, qkv: torch.Tensor, q: torch.Tensor |
     if q is None:
         q = _output((seq.T, hq, hd), torch.bfloat16, seq.device, stream)
     else:
-        assert q.dtype == torch.bfloat16 and q.shape == (seq.T, hq, hd) and q.is_contiguous()
+        assert q.is_cuda and q.dtype == torch.bfloat16 and q.shape == (seq.T, hq, hd) and q.is_contiguous()
     mlora.mlora_qkv_write(cache.handle, seq.handle, qkv, qkv.stride(0) if seq.T > 1 else qkv.shape[1], q_norm, k_norm,
                           eps, rope.handle if rope is not None else None, positions, q, _raw_stream(stream, seq.device))
     return q
@@ -327,7 +327,7 @@ def attention(cache: KVCache, seq: SeqMeta, q: torch.Tensor, o: torch.Tensor | N
     if o is None:
         o = _output((seq.T, hq * hd), torch.bfloat16, seq.device, stream)
     else:
-        assert o.dtype == torch.bfloat16 and o.shape == (seq.T, hq * hd) and o.is_contiguous()
+        assert o.is_cuda and o.dtype == torch.bfloat16 and o.shape == (seq.T, hq * hd) and o.is_contiguous()
     mlora.mlora_attention(cache.handle, seq.handle, q, hd ** -0.5 if scale is None else scale, o, _raw_stream(stream, seq.device))
     return o
 
@@ -342,7 +342,7 @@ def kv_read(cache: KVCache, seq: SeqMeta, row_start: torch.Tensor, rows: int, k=
         k = _output(shape, torch.bfloat16, seq.device, stream)
     if v is None:
         v = _output(shape, torch.bfloat16, seq.device, stream)
-    assert k.shape == shape and v.shape == shape and k.dtype == v.dtype == torch.bfloat16
+    assert k.is_cuda and v.is_cuda and k.shape == shape and v.shape == shape and k.dtype == v.dtype == torch.bfloat16
     assert k.is_contiguous() and v.is_contiguous()
     mlora.mlora_kv_read(cache.handle, seq.handle, row_start, rows, k, v, _raw_stream(stream, seq.device))
     return k, v

@@ -422,3 +422,17 @@ def test_query_and_output_must_not_overlap(layer):
     call(a, a + n)                                        # side by side
     torch.cuda.synchronize()
     assert torch.equal(both[st.q.numel():].view_as(st.run()), st.run(scale=1.0))
+
+
+def test_outputs_of_the_host_are_refused(layer):
+    st = Step(layer, [1, 30], [50, 20])
+    host = lambda x: torch.empty(x, dtype=torch.bfloat16)  # noqa: E731
+    on = lambda x: host(x).cuda()  # noqa: E731
+    with pytest.raises(AssertionError):
+        layer.attention(st.cache, st.seq, st.q, host((st.T, st.hq * st.hd)))
+    with pytest.raises(AssertionError):
+        layer.qkv_write(st.cache, st.seq, torch.zeros(st.T, 12 * 128, device="cuda"), host((st.T, st.hq, st.hd)))
+    rows = (sum(st.len), st.hkv, st.hd)
+    for k, v in ((host(rows), on(rows)), (on(rows), host(rows))):
+        with pytest.raises(AssertionError):
+            layer.kv_read(st.cache, st.seq, ints([0, st.len[0]]), rows[0], k, v)
