@@ -423,7 +423,12 @@ MLORA_API mlora_status mlora_qkv_write(mlora_kv_t kv, mlora_seq_t seq, const flo
  * overlapping; scale positive. Rows of tokens in no sequence are zero. Scores, maxima and sums are fp32; the weights are rounded to
  * bf16 (f16 over an e4m3 cache) for the product with V. f16 has no room below: a key whose weight, or weight times its
  * value row's scale, is less than 2^-21 of the row's largest counts with fewer bits, and below 2^-31 it may count as zero.
- * Cache rows past a sequence's length have no effect, whatever they hold. Deterministic: a repeated call gives the same bits. */
+ * Cache rows past a sequence's length have no effect, whatever they hold, and a key row's infinities and NaN reach the rows that see
+ * it alone (over an e4m3 cache a row with a NaN scale is such a row). Two limits among the new tokens of one sequence, whose
+ * keys some rows see and others do not yet: a value row with an infinity or a NaN, bf16, may make earlier new tokens' rows
+ * NaN too (0 times it is NaN); and over an e4m3 cache the 128 keys of a tile of a chunk or prompt share f16's range,
+ * seen or not: a key or value row whose scale lies 2^20 below the tile's largest loses bits, from 2^38 below on it counts as zero.
+ * Deterministic: a repeated call gives the same bits. */
 MLORA_API mlora_status mlora_attention(mlora_kv_t kv, mlora_seq_t seq, const mlora_bf16* query, float scale,
                                        mlora_bf16* out, void* stream);
 
