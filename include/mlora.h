@@ -420,8 +420,9 @@ MLORA_API mlora_status mlora_qkv_write(mlora_kv_t kv, mlora_seq_t seq, const flo
 /* Causal attention of the step's new tokens over the cache, which already holds them:
  *     out[t, h, :] = sum_{j <= p} softmax_j(scale query[t, h] . K[j, h / G]) V[j, h / G],  p = position of t,
  * G = n_q_heads / n_kv_heads; query, out: device bf16 [T, n_q_heads, head_dim], 16-byte aligned, not
- * overlapping; scale positive. Rows of tokens in no sequence are zero. Scores, maxima and sums are fp32; the weights are rounded to
- * bf16 (f16 over an e4m3 cache) for the product with V. f16 has no room below: a key whose weight, or weight times its
+ * overlapping; scale positive. Rows of tokens in no sequence are zero. Scores, maxima and sums are fp32; the weights are rounded
+ * for the product with V: to f16 over an e4m3 cache, else to bf16 in chunks and prompts and to 16 bits for single tokens and
+ * other sequences of few rows (at most 8, or 16, to a key/value head). f16 has no room below: a key whose weight, or weight times its
  * value row's scale, is less than 2^-21 of the row's largest counts with fewer bits, and below 2^-31 it may count as zero.
  * Cache rows past a sequence's length have no effect, whatever they hold, and a key row's infinities and NaN reach the rows that see
  * it alone (over an e4m3 cache a row with a NaN scale is such a row). Two limits among the new tokens of one sequence, whose

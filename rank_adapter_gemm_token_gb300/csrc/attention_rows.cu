@@ -16,7 +16,9 @@
 //     O^T = V^T P^T with the query rows as N = 8 (or 16), so few rows waste few lanes. (The tcgen05 shapes need
 //     128 rows; here the tensor time is a fraction of the load time either way.)
 //   - softmax in one pass in base 2; the running maximum moves only when a score passes it by 2^8, so most
-//     chunks need no shuffles and no rescaling. P is at most 2^8, which f16 and bf16 hold.
+//     chunks need no shuffles and no rescaling. bf16: P meets the values in two pieces of 8 bits, which costs a second
+//     product where the tensor cores wait for loads anyway (256 sequences 168.5 us without it, 169.8 with). e4m3: one piece, f16's 11
+//     bits (a second would cost 4 %: 105.8 us, 109.9).
 //   - e4m3: codes become f16 (exact) in registers. The key scale multiplies the score. The weights w_j = 2^(score_j - m)
 //     go into the denominator as they are; for the product with the codes they are multiplied by the value scale and by
 //     u = 2^(m - n), where n + 7 follows the largest score_j + log2 vs_j as m follows the largest score: P_j = w_j vs_j u is at
@@ -344,7 +346,7 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
           for (int z = 0; z < NQ; ++z) mma<false>(i & 1 ? sc1[z] : sc[z], a, bq[z][i][0], bq[z][i][1]);
         }
       }
-      uint32_t pb[NQ][2];
+      uint32_t pb[NQ][2], pr[NQ][2];              // P in 16 bits, and (bf16) what that leaves, in 16 more
       const bool edge = k0 + kChunk > base + 1;
 #pragma unroll
       for (int z = 0; z < NQ; ++z) {
@@ -410,8 +412,12 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
           sc[z][k] = p[k];
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          pb[z][h] = mat_trans(E4M3 ? pack_f16(sc[z][2 * h], sc[z][2 * h + 1]) : pack_bf16(sc[z][2 * h], sc[z][2 * h + 1]));
+        for (int h = 0; h < 2; ++h) {
+          const float p0 = sc[z][2 * h], p1 = sc[z][2 * h + 1];
+          const uint32_t x = E4M3 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+          pb[z][h] = mat_trans(x);
+          if (!E4M3) pr[z][h] = mat_trans(pack_bf16(p0 - ptx::bf16_lo(x), p1 - ptx::bf16_hi(x)));
+        }
       }
       const uint32_t vt = st + C::kTile;
       if (E4M3) {
@@ -446,7 +452,10 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
           const int r = (lane & 7) + ((lane >> 4) & 1) * 8, seg = 2 * i + ((lane >> 3) & 1);
           ldsm4t(a, vt + r * C::kRowBytes + (seg ^ (r & 7)) * 16);
 #pragma unroll
-          for (int z = 0; z < NQ; ++z) mma<false>(acc[z][i], a, pb[z][0], pb[z][1]);
+          for (int z = 0; z < NQ; ++z) {
+            mma<false>(acc[z][i], a, pb[z][0], pb[z][1]);
+            mma<false>(acc[z][i], a, pr[z][0], pr[z][1]);
+          }
         }
       }
     }

@@ -436,3 +436,20 @@ def test_outputs_of_the_host_are_refused(layer):
     for k, v in ((host(rows), on(rows)), (on(rows), host(rows))):
         with pytest.raises(AssertionError):
             layer.kv_read(st.cache, st.seq, ints([0, st.len[0]]), rows[0], k, v)
+
+
+# ------------------------------------------------------------------------------------------- weights
+@pytest.mark.parametrize("n,ctx,hq,hkv,hd", [([1] * 5, [700, 64, 3, 2000, 150], 8, 2, 128), ([1, 1], [300, 9000], 4, 1, 64),
+                                             ([2, 1, 2], [500, 90, 1200], 8, 2, 128), ([3, 4, 1], [100, 900, 200], 8, 2, 64),
+                                             ([1, 1], [700, 40], 16, 1, 128)])
+def test_weights_of_few_rows_keep_16_bits(layer, n, ctx, hq, hkv, hd):
+    """bf16, sequences of few rows: the weights are two bf16 numbers, the second rounded at 2^-8 of 2^-8 of the first."""
+    from oracle import attention as ref
+    st = Step(layer, n, ctx, hq, hkv, hd, seed=13)
+    o = st.run()
+    want, W, S = ref.attention(st.q.double().cpu().numpy(), [r[0] for r in st.rows], [r[1] for r in st.rows], st.starts, hq // hkv, hd ** -0.5)
+    got = o.double().cpu().numpy().reshape(want.shape)
+    d = (hd * 2.0 ** -24 + 2.0 ** -20) * S[..., None]
+    tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -16 + 2 * d) * (W + np.abs(want)) + 1e-30
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), bad.size, float(np.nanmax(np.abs(got - want) / tol)))
