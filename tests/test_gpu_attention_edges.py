@@ -453,3 +453,30 @@ def test_weights_of_few_rows_keep_16_bits(layer, n, ctx, hq, hkv, hd):
     tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -16 + 2 * d) * (W + np.abs(want)) + 1e-30
     bad = ~(np.abs(got - want) <= tol)
     assert not bad.any(), (int(bad.sum()), bad.size, float(np.nanmax(np.abs(got - want) / tol)))
+
+
+def test_whole_blocks_dealt_out_over_e4m3(layer):
+    """200 short chunks, dealt out whole, head size 64, over e4m3 with scores (checked here) that leave every weight above 2^-24 of
+    its row's largest, and value scales that differ by at most 2^6: nothing rests on what is below f16's range."""
+    from tests.test_gpu_attention import DEALT
+    n, ctx, hq, hkv, hd = DEALT[1]
+    assert hq == hkv
+    st = Step(layer, n, ctx, hq, hkv, hd, 32, "e4m3", seed=21)
+    rng = np.random.default_rng(2)
+    table = st.table.cpu().numpy()
+    for which, (x, z, lo, hi) in enumerate(((st.k, st.ks, -10.0, -7.5), (st.v, st.vs, -8.0, -2.0))):
+        z.copy_(torch.where(torch.isnan(z), z, torch.from_numpy(2.0 ** rng.uniform(lo, hi, tuple(z.shape))).to(z)))
+        code, scale = x.double().cpu().numpy(), z.double().cpu().numpy()
+        for s, L in enumerate(st.len):
+            p, off = table[s, np.arange(L) // 32], np.arange(L) % 32
+            st.rows[s][which] = code[p, :, off] * scale[p, :, off][..., None]
+    q = st.q.double().cpu().numpy()
+    for s in range(len(n)):
+        z = np.einsum("thd,jhd->thj", q[st.starts[s]:st.starts[s + 1]], st.rows[s][0]) * hd ** -0.5
+        assert np.ptp(z, axis=-1).max() < 24 * np.log(2)
+    o = st.run()
+    st.seq.status()
+    st.check(o)
+    for _ in range(2):
+        st.build()
+        assert torch.equal(o, st.run())
