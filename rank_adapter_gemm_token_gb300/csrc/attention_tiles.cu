@@ -34,8 +34,8 @@
 // 8 x 512 tokens 33 us, 520: of an item's first and last tile about 4400 cycles, 1.5 tiles, overlap with nothing. e4m3:
 // 8000 tokens 540 us, 970.
 // Value rows past the cached length are zeroed in shared memory, scores past a row's limit are replaced by -inf:
-// what lies there has no effect. Every wait is bounded: after 2 s a role records the timeout, stops waiting and
-// runs on to the end.
+// what lies there has no effect. Every wait is bounded: after 2 s a role records the timeout, brings no more
+// copies and products (its copies are 2 s old by then, its products are waited for), stops waiting and runs on to the end.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -241,7 +241,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
   uint64_t* v_clean = v_short + 1;                    // those rows are zero
   uint64_t* raw_full = v_clean + 1;                   // [kStages], e4m3
   uint64_t* raw_empty = raw_full + C::kStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_empty + C::kStages);
+  uint64_t* drained = raw_empty + C::kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
   float* q_scale = reinterpret_cast<float*>(smem + C::kQScaleOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* err = v.err;
@@ -261,6 +262,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     }
     for (int i = 0; i < C::kScaleBufs; ++i) ptx::mbar_init(&sc_full[i], 128);
     ptx::mbar_init(v_short, 1);
+    ptx::mbar_init(drained, 1);
     ptx::mbar_init(v_clean, 32);
     for (int i = 0; i < C::kStages; ++i) {
       ptx::mbar_init(&raw_full[i], 1);
@@ -330,6 +332,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         for (int h = 0; h < 2; ++h, ++n) {            // the keys (and both scales), then the values
           const int st = n % kDepth;
           wait(&empty[st], ((n / kDepth) & 1) ^ 1);
+          if (__any_sync(0xffffffffu, dead)) return;
           if (lane == 0)
             ptx::mbar_arrive_expect_tx(&full[st], count * box * (!E4M3 ? 2 * HD : h == 0 ? HD + 8 : HD));
           __syncwarp();
@@ -748,6 +751,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               ks = vs, ks_par = vs_par;
               if (++ks == C::kRing) ks = 0, ks_par ^= 1;
               wait(&kv_full[vs], vs_par);
+              if (dead) break;
               if (short_tile && j == kb) {
                 ptx::mbar_arrive(v_short);
                 wait(v_clean, clean_par);
@@ -788,7 +792,12 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             if (j > ka) ptx::umma_commit(&kv_empty[vs]);
             if (j < kb) ptx::umma_commit(&kv_empty[ks]);
           }
+          if (dead) break;
           // (ks is now the slot of the next item's first key tile)
+        }
+        if (dead) {                                   // the products under way
+          ptx::umma_commit(drained);
+          ptx::mbar_wait(drained, 0, err);
         }
       }
       __syncwarp();
@@ -806,6 +815,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       for (bool go = any; go; go = advance()) {
           if (it.end[w] <= it.ka) continue;
         wait(&q_empty[w], par ^ 1);
+        if (__any_sync(0xffffffffu, dead)) break;
         if (lane == 0) {
           ptx::mbar_arrive_expect_tx(full, bytes);
 #pragma unroll
