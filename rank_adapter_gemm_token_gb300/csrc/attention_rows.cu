@@ -9,7 +9,7 @@
 //     equal share of the units whatever the sequences' lengths (Shares), so one long sequence and many short
 //     ones both fill the GPU. An item across a cut leaves partial sums (with their maximum) in the step's
 //     workspace, and the CTA that comes last with one joins them in their order: the result does not depend on who it is.
-//     (As a launch of its own that took as long on the GPU, and a small call 2 us more: 10.4 us against 8.5 for one token.)
+//     (As a launch of its own that took as long on the GPU, and a small call 2 us more.)
 //   - a warp takes 16 keys of each unit, through its own ring of stages filled by cp.async (the next item's
 //     keys are already on their way while one item is finished), with no barrier between warps inside an item.
 //   - the products run on the warp-level tensor instructions with the keys as the M side: S^T = K Q^T and
@@ -26,8 +26,9 @@
 //     are whole numbers, so every rescaling is exact. Query rows are lifted by a power of two into f16's range.
 // Keys at or past a row's limit are replaced by -inf by selection, and rows past the cached length are
 // zero-filled on load, so what lies there (NaN included) has no effect.
-// Measured, 32 heads of 128 on 8, the cache's bytes over the time of a call: 256 sequences of 200-2000 tokens
-// bf16 171 us, 6.5 TB/s; e4m3 106 us, 5.8 TB/s; one of 131000 tokens 85 us, 6.3 TB/s (copy: 6.8); one of 500 tokens 8.5 us.
+// Measured on the GPU, 32 heads of 128 on 8, all bytes over the time: 256 sequences of 200-2000 tokens bf16 168 us, 6.6 TB/s;
+// e4m3 105 us, 5.8 TB/s; one of 131000 tokens 84 us, 6.4 TB/s (copy: 6.8), e4m3 51 us, 5.4; one of 500 tokens 7.5 us. 9 to 16 rows
+// (64 sequences of 3 tokens on 1000): 54 us, 4.9 TB/s; e4m3 46 us, 3.0.
 #include <algorithm>
 
 #include "attention.h"

@@ -26,13 +26,14 @@
 // same one. So one word a key, from shared memory, is all that the softmax reads, and only where it takes the exponentials:
 // the maximum is taken of S without it and raised by its bound (scores above 100 in base 2 are gone through again with it).
 // A word read by all lanes of a warp costs the shared memory a cycle and the warp a quarter of an instruction: 8000 tokens took
-// 712 us with a factor of the key in both passes and one of the value beside the second, 650 without the first of them, 600 so.
+// 712 us with a factor of the key in both passes and one of the value beside the second, 650 without the first of them, 600 so
+// (and 546 with the rounded scales, whose one factor a key came after the exponential).
 // Work: (block, key/value head) items of 128-key tiles, dealt out whole or in equal shares, a list for each CTA (seq_meta.cu);
 // parts of a split item are joined by attention_join.cu.
-// Measured, 32 heads of 128 on 8: one prompt of 8000 tokens 335 us, 1565 TFLOP/s (tcgen05 busy for 0.6 to 0.7 of the cycles; the
-// rest is a softmax that its own products wait for, TMEM being full with two tiles); 512 tokens on 32000 195 us, 1390;
-// 8 x 512 tokens 33 us, 520: of an item's first and last tile about 4400 cycles, 1.5 tiles, overlap with nothing. e4m3:
-// 8000 tokens 540 us, 970.
+// Measured on the GPU, 32 heads of 128 on 8: one prompt of 8000 tokens 331 us, 1580 TFLOP/s, at 2070 MHz (357 us in calls for
+// seconds on end, when the power cap holds 1935 MHz; tcgen05 busy for 0.6 to 0.7 of the cycles; the rest is a softmax that its own
+// products wait for, TMEM being full with two tiles); 512 tokens on 32000 191 us, 1415; 8 x 512 tokens 32 us, 540: of an item's first
+// and last tile about 4400 cycles, 1.5 tiles, overlap with nothing. e4m3: 8000 tokens 600 us, 875; 8 x 512 tokens 50 us.
 // Value rows past the cached length are zeroed in shared memory, scores past a row's limit are replaced by -inf:
 // what lies there has no effect. Every wait is bounded: after 2 s a role records the timeout, brings no more
 // copies and products (its copies are 2 s old by then, its products are waited for), stops waiting and runs on to the end.

@@ -14,8 +14,9 @@
 // lies in the registers of hd / 8 lanes, eight elements each, so that norm, rotation and maximum are a few shuffles for two
 // (four) rows at a time, and the angles of a CTA's few tokens are made once, in shared memory. Each thread has two rows on
 // their way before it works on the first, five CTAs an SM: with three rows and three CTAs fewer loads were on their way
-// beside the arithmetic (40 us against 34 for 4096 tokens of 48 heads of 128, e4m3). One row for a small step. Measured: those
-// 4096 tokens 33 us, 4.3 TB/s, instructions issued in 0.76 of the cycles; 256 tokens 15 us, a call's launch.
+// beside the arithmetic (40 us against 34 for 4096 tokens of 48 heads of 128, e4m3). One row for a small step. Measured on the GPU: those
+// 4096 tokens 31 us, 4.6 TB/s, instructions issued in 0.76 of the cycles (bf16 with norms 35 us, 4.3 TB/s); 256 tokens 6 us. The
+// two-step forms spill 68 bytes at 48 registers.
 //
 // kv_read: whole sequences' cached rows as dense bf16 rows [token, head, hd]; a copy (bf16) or code * scale
 // rounded once (e4m3). Bound: HBM. A warp takes a run of consecutive (page, head) units, so that only its first one
