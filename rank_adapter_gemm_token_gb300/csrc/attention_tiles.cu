@@ -482,7 +482,10 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           if (E4M3) {
             const bool far = fabsf(top) > kBoundedScore && top != -INFINITY;
             top = fmaf(kKeyBound, fminf(fabsf(top), kBoundedScore), top) + off;
-            if (__any_sync(0xffffffffu, far)) top = fmaf(maximum(std::true_type{}), c, off);
+            if (__any_sync(0xffffffffu, far)) {       // (for those rows alone: a row's result is its own)
+              const float exact = fmaf(maximum(std::true_type{}), c, off);
+              top = far ? exact : top;
+            }
           }
           if (j == ka)
             m = top;

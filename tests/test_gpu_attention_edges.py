@@ -480,3 +480,19 @@ def test_whole_blocks_dealt_out_over_e4m3(layer):
     for _ in range(2):
         st.build()
         assert torch.equal(o, st.run())
+
+
+@pytest.mark.parametrize("n,ctx,hq,hkv,hd", [([366, 127, 33], [0, 0, 0], 6, 2, 128), ([23, 1, 60], [42, 7, 2904], 7, 1, 64), ([368], [0], 99, 3, 128)])
+def test_chunks_of_odd_groups_repeat_their_bits(layer, n, ctx, hq, hkv, hd):
+    """Groups that do not divide a tile of 128 rows leave rows of it without a token, in which the shared memory's earlier content
+    stays: whatever other calls have left there, a call over e4m3 repeats its bits."""
+    st = Step(layer, n, ctx, hq, hkv, hd, kind="e4m3", seed=3, q_gain=0.002)
+    o = st.run()
+    st.seq.status()
+    st.check(o)
+    other = Step(layer, [300], [200], 8, 2, hd, kind="e4m3", seed=4, q_gain=300.0)
+    for _ in range(6):
+        other.run()
+        assert torch.equal(o, st.run())
+        other.q.neg_()
+        assert torch.equal(o, st.run())
