@@ -228,6 +228,23 @@ MLORA_API mlora_status mlora_meta_read(mlora_meta_t meta, int32_t* order, int32_
 MLORA_API mlora_status mlora_linear(mlora_pool_t pool, mlora_meta_t meta, const mlora_bf16* x, const mlora_bf16* W, float* y,
                           void* stream);
 
+/* The gated half of a feed-forward block, h = act(g) * u, with [g u] = x W^T + sum_j s c B(A x) the layer above over the
+ * stacked gate and up projections (an addition with no counterpart on the pages):
+ *   pool: D = 2 F, F a multiple of 8; rows 0 .. F - 1 of W (and of every B) are the gate's, rows F .. 2 F - 1 the up
+ *   projection's (per-slice adapters: mlora_load_adapter_sliced). x: device bf16 [T, K]; W: device bf16 [2 F, K];
+ *   h: device bf16 [T, F], 16-byte aligned, overwritten: the down linear's input.
+ *   act: MLORA_ACT_SILU g / (1 + e^-g), MLORA_ACT_GELU_TANH g / 2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))),
+ *   MLORA_ACT_GELU g / 2 erfc(-g / sqrt(2)).
+ *   workspace: device, 16-byte aligned, mlora_gated_workspace_bytes(pool, meta) bytes, free again when the call has run;
+ *   NULL where that is 0.
+ * g, u and the activation are fp32; h is rounded once. Orders itself after the pool's queued loads; calls that share a meta or
+ * a pool must be ordered on one stream. */
+enum { MLORA_ACT_SILU = 0, MLORA_ACT_GELU_TANH = 1, MLORA_ACT_GELU = 2 };
+MLORA_API mlora_status mlora_gated_linear(mlora_pool_t pool, mlora_meta_t meta, const mlora_bf16* x, const mlora_bf16* W,
+                                          int act, mlora_bf16* h, void* workspace, void* stream);
+/* Bytes of workspace that mlora_gated_linear needs for the meta's last build; 0 also for arguments that it refuses. */
+MLORA_API size_t mlora_gated_workspace_bytes(mlora_pool_t pool, mlora_meta_t meta);
+
 /* The same kernels one at a time (for per-kernel tests and timing):
  *   mlora_base_gemm:   y[T, D] = x[T, K] W[D, K]^T (fp32 out, tcgen05 tensor cores);
  *   mlora_lora_shrink: v = A_slot x per active pair into the meta's workspace;
@@ -504,7 +521,7 @@ MLORA_API mlora_status mlora_check_wait_timeout(void* stream);
  * on its own stream (at most `capacity` launches are kept). mlora_trace_read synchronises
  * and returns, for each kernel kind, the number of launches and their summed device time in
  * milliseconds; kinds: 0 meta, 1 base GEMM, 2 shrink, 3 expand, 4 slot bookkeeping, 5 embedding
- * lookup, 6 sequence metadata, 7 cache write and read, 8 attention. */
+ * lookup, 6 sequence metadata, 7 cache write and read, 8 attention, 9 activation. */
 MLORA_API mlora_status mlora_trace_enable(int capacity);
 MLORA_API mlora_status mlora_trace_disable(void);
 MLORA_API mlora_status mlora_trace_read(int n_kinds, int* launches, double* total_ms);

@@ -95,7 +95,7 @@ constexpr int kVfullMaxAct = 512;
 // Kernel kinds for the launch counter and the optional per-kernel event trace.
 enum KernelKind : int {
   kKindMeta = 0, kKindGemm = 1, kKindShrink = 2, kKindExpand = 3, kKindSlot = 4, kKindEmbed = 5, kKindSeq = 6, kKindKv = 7,
-  kKindAttn = 8, kNumKinds = 9
+  kKindAttn = 8, kKindAct = 9, kNumKinds = 10
 };
 
 // Records the thread's last-error message and returns the status (mlora_runtime.cu).
@@ -154,6 +154,8 @@ cudaError_t launch_lora_shrink_tc(const uint16_t* x, const PoolView& pool, const
 cudaError_t launch_base_gemm_lora(const uint16_t* x, const uint16_t* W, float* y, int T, int K, int D,
                                   uint32_t* err, int num_sms, const PoolView* pool, const MetaView* meta,
                                   cudaStream_t s);
+// h[T, F] (bf16) = act(y[:, :F]) * y[:, F:] of fp32 rows y [T, 2 F] (gated.cu); F a multiple of 8.
+cudaError_t launch_gated_activation(const float* y, uint16_t* h, int T, int F, int act, int num_sms, cudaStream_t s);
 // One block waiting on an mbarrier nothing arrives on (wait_check.cu): exercises the bounded
 // wait, which sets ptx::kErrWaitTimeout in *err after the limit and returns.
 cudaError_t launch_wait_check(uint32_t* err, cudaStream_t s);

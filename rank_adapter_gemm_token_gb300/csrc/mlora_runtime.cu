@@ -338,7 +338,7 @@ const char* mlora_status_string(mlora_status s) {
 
 const char* mlora_kernel_kind_name(int kind) {
   static const char* names[kNumKinds] = {"meta", "base_gemm", "shrink", "expand", "slot", "embedding",
-                                          "sequences", "kv_cache", "attention"};
+                                          "sequences", "kv_cache", "attention", "activation"};
   return (kind >= 0 && kind < kNumKinds) ? names[kind] : "?";
 }
 
@@ -982,6 +982,29 @@ mlora_status mlora_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, c
     }
   }
   m->last_stream = s;
+  return MLORA_OK;
+}
+
+size_t mlora_gated_workspace_bytes(mlora_pool_t p, mlora_meta_t m) {
+  if (!p || !m || p->embed || !m->built) return 0;
+  return static_cast<size_t>(m->T) * p->D * sizeof(float);
+}
+
+mlora_status mlora_gated_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, const mlora_bf16* W, int act,
+                                mlora_bf16* h, void* workspace, void* stream) {
+  if (p && p->embed) return fail(MLORA_ERR_INVALID_ARG, "an embedding pool: use mlora_embedding");
+  if (mlora_status st = check_pair(p, m)) return st;
+  if (p->D % 16) return fail(MLORA_ERR_INVALID_ARG, "D %d must be twice a multiple of 8", p->D);
+  if (act < MLORA_ACT_SILU || act > MLORA_ACT_GELU) return fail(MLORA_ERR_INVALID_ARG, "unknown activation %d", act);
+  if (mlora_status st = check_operands(x, W, h, m->T, p->K, p->D)) return st;
+  if (m->T == 0) return MLORA_OK;
+  if (!workspace || !aligned16(workspace)) return fail(MLORA_ERR_INVALID_ARG, "workspace is NULL or misaligned");
+  float* y = static_cast<float*>(workspace);
+  if (mlora_status st = mlora_linear(p, m, x, W, y, stream)) return st;
+  DeviceState* ds = nullptr;
+  if (mlora_status st = device_state(&ds)) return st;
+  const cudaError_t e = launch_gated_activation(y, h, m->T, p->D / 2, act, ds->num_sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "activation launch");
   return MLORA_OK;
 }
 

@@ -178,6 +178,26 @@ def linear(pool: AdapterPool, meta: StepMeta, x: torch.Tensor, W: torch.Tensor, 
     return y
 
 
+ACTIVATIONS = {"silu": mlora.MLORA_ACT_SILU, "gelu_tanh": mlora.MLORA_ACT_GELU_TANH, "gelu": mlora.MLORA_ACT_GELU}
+
+
+def gated_linear(pool: AdapterPool, meta: StepMeta, x: torch.Tensor, W: torch.Tensor, act: str = "silu",
+                 h: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """h[T, F] bf16 = act(g) * u, where [g u] = x W^T + the step's LoRA side path (x [T, K] and W [2 F, K] bf16 on the GPU, the
+    gate's rows first); act: one of ACTIVATIONS."""
+    assert x.is_cuda and x.dtype == torch.bfloat16 and W.dtype == torch.bfloat16 and x.is_contiguous() and W.is_contiguous()
+    T, F = meta.T, pool.D // 2
+    assert x.shape == (T, pool.K) and W.shape == (pool.D, pool.K) and W.device == x.device
+    if h is None:
+        h = _output((T, F), torch.bfloat16, x.device, stream)
+    else:
+        assert h.device == x.device and h.dtype == torch.bfloat16 and h.shape == (T, F) and h.is_contiguous()
+    need = mlora.mlora_gated_workspace_bytes(pool.handle, meta.handle)
+    work = _output((need,), torch.uint8, x.device, stream) if need else None
+    mlora.mlora_gated_linear(pool.handle, meta.handle, x, W, ACTIVATIONS[act], h, work, _raw_stream(stream, x.device))
+    return h
+
+
 def embedding(pool: EmbeddingPool, meta: StepMeta, ids: torch.Tensor, E: torch.Tensor, y: torch.Tensor | None = None,
               stream=None) -> torch.Tensor:
     """y[T, dim] fp32 = E[ids] + the step's LoRA side path (ids int32 [T], E [vocab, dim] bf16 on the GPU)."""
@@ -363,3 +383,16 @@ def attention_block(meta: StepMeta, seq: SeqMeta, cache: KVCache, x: torch.Tenso
     qkv = linear(qkv_pool, meta, x, W_qkv)
     q = qkv_write(cache, seq, qkv, q_norm=q_norm, k_norm=k_norm, eps=eps, rope=rope)
     return linear(o_pool, meta, attention(cache, seq, q, scale=scale), W_o)
+
+
+def feed_forward(meta: StepMeta, x: torch.Tensor, gate_up_pool: AdapterPool, W_gate_up: torch.Tensor, down_pool: AdapterPool,
+                 W_down: torch.Tensor, act: str = "silu", stream=None) -> torch.Tensor:
+    """One layer's gated feed-forward block for the step that `meta` describes: the adapted gate_up linear of x (bf16
+    [T, hidden]) with its activation, and the adapted down linear: fp32 [T, W_down.shape[0]]. With `stream` all of it runs there."""
+    if stream is not None:
+        here = torch.cuda.current_stream(x.device)
+        with torch.cuda.stream(_torch_stream(stream, x.device)):
+            y = feed_forward(meta, x, gate_up_pool, W_gate_up, down_pool, W_down, act)
+        y.record_stream(here)
+        return y
+    return linear(down_pool, meta, gated_linear(gate_up_pool, meta, x, W_gate_up, act=act), W_down)

@@ -31,13 +31,17 @@ MLORA_ERR_BAD_SEQUENCE = 13
 
 MLORA_KV_BF16 = 0
 MLORA_KV_E4M3 = 1
+MLORA_ACT_SILU = 0
+MLORA_ACT_GELU_TANH = 1
+MLORA_ACT_GELU = 2
 MLORA_ROPE_PLAIN = 0
 MLORA_ROPE_LINEAR = 1
 MLORA_ROPE_BASE = 2
 MLORA_ROPE_WAVES = 3
 MLORA_ROPE_RAMP = 4
 
-KERNEL_KINDS = ("meta", "base_gemm", "shrink", "expand", "slot", "embedding", "sequences", "kv_cache", "attention")
+KERNEL_KINDS = ("meta", "base_gemm", "shrink", "expand", "slot", "embedding", "sequences", "kv_cache", "attention",
+                "activation")
 
 EXPORTS = (
     "mlora_pool_create", "mlora_pool_destroy", "mlora_load_adapter", "mlora_clear_slot", "mlora_pool_sync",
@@ -54,6 +58,7 @@ EXPORTS = (
     "mlora_kv_create", "mlora_kv_destroy", "mlora_kv_info", "mlora_kv_bytes", "mlora_rope_frequencies",
     "mlora_rope_create", "mlora_rope_destroy", "mlora_seq_create", "mlora_seq_destroy", "mlora_build_seq",
     "mlora_seq_status", "mlora_qkv_write", "mlora_attention", "mlora_kv_read",
+    "mlora_gated_linear", "mlora_gated_workspace_bytes",
 )
 
 
@@ -103,6 +108,7 @@ def load(path: str | None = None):
             "mlora_meta_status": [vp],
             "mlora_meta_read": [vp, vp, vp, vp, vp, vp],
             "mlora_linear": [vp, vp, vp, vp, vp, vp],
+            "mlora_gated_linear": [vp, vp, vp, vp, i32, vp, vp, vp],
             "mlora_base_gemm": [vp, vp, vp, i32, i32, i32, vp],
             "mlora_lora_shrink": [vp, vp, vp, vp],
             "mlora_lora_expand": [vp, vp, vp, vp],
@@ -148,6 +154,8 @@ def load(path: str | None = None):
         lib.mlora_pool_bytes.restype = ctypes.c_size_t
         lib.mlora_kv_bytes.argtypes = [i32, i32, i32, i32, i32]
         lib.mlora_kv_bytes.restype = ctypes.c_size_t
+        lib.mlora_gated_workspace_bytes.argtypes = [vp, vp]
+        lib.mlora_gated_workspace_bytes.restype = ctypes.c_size_t
         lib.mlora_status_string.argtypes = [i32]
         lib.mlora_status_string.restype = ctypes.c_char_p
         lib.mlora_last_error.argtypes = []
@@ -316,6 +324,15 @@ def mlora_linear(pool: int, meta: int, x, W, y, stream=None) -> None:
 def mlora_embedding(pool: int, meta: int, ids, E, y, stream=None) -> None:
     """y[t] = E[ids[t]] + the step's LoRA side path on the lookup (ids int32 [T], E bf16 [vocab, dim], y fp32 [T, dim])."""
     _check(load().mlora_embedding(pool, meta, _ptr(ids), _ptr(E), _ptr(y), _stream(stream)), "mlora_embedding")
+
+
+def mlora_gated_linear(pool: int, meta: int, x, W, act: int, h, workspace=None, stream=None) -> None:
+    _check(load().mlora_gated_linear(pool, meta, _ptr(x), _ptr(W), act, _ptr(h), _ptr(workspace), _stream(stream)),
+           "mlora_gated_linear")
+
+
+def mlora_gated_workspace_bytes(pool: int, meta: int) -> int:
+    return int(load().mlora_gated_workspace_bytes(pool, meta))
 
 
 def mlora_base_gemm(x, W, y, T: int, K: int, D: int, stream=None) -> None:
