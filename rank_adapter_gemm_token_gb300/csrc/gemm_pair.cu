@@ -40,6 +40,7 @@
 #include <algorithm>
 #include <climits>
 
+#include "gated.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -159,14 +160,16 @@ __device__ __forceinline__ PairTile pair_tile(int t, int S, int per, int num_mp,
   return pt;
 }
 
-template <int BN, int STAGES>
+template <int BN, int STAGES, bool GATED>
 __global__ void __launch_bounds__(kPairThreads, 1)
 gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                       const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_b,
                       const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_y,
                       const PairSide sp, float* __restrict__ y, int y_tma, int T, int D, int K,
-                      uint32_t* __restrict__ err) {
+                      uint32_t* __restrict__ err, int act) {
   using L = PairCfg<BN, STAGES>;
+  constexpr int kOut = GATED ? BN / 2 : BN;              // output columns of a tile
+  const int F = GATED ? D / 2 : D;                       // and of the whole output
   constexpr int kPer = L::kBRows >= 2 * kBlockCols ? 4 : 2;   // entries per shrink sub-tile (N <= 2 kBRows)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -186,7 +189,7 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
   const int n_pairs = gridDim.x >> 1;
   const int num_m = (T + kHalf - 1) / kHalf;             // 128-row M-tiles
   const int num_mp = (num_m + 1) / 2;                    // pair tiles along M
-  const int num_n = (D + BN - 1) / BN;
+  const int num_n = (F + kOut - 1) / kOut;
   const int num_kb = (K + kPK - 1) / kPK;
 
   if (threadIdx.x == 0) {
@@ -293,7 +296,7 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
           }
           continue;
         }
-        const int n0 = pt.n_idx * BN + static_cast<int>(rank) * L::kBRows;
+        const int n0 = pt.n_idx * kOut + static_cast<int>(rank) * (GATED ? F : L::kBRows);
         const int n_extra = pair_extra(sp.ptile_off, pt.mp);
         // the tile's K blocks of x and W (kept free of other work: a branch in this loop slows it)
         for (int kb = 0; kb < num_kb; ++kb) {
@@ -468,11 +471,43 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
         __syncwarp();
         if (lane == 0) atomicAdd(&sp.sync[2 + pt.mp], 1u);
       } else {
-        const int n0 = pt.n_idx * BN;
+        const int n0 = pt.n_idx * kOut;
+        if (GATED) {
+          // columns c of the accumulator are the gate's, BN / 2 + c the up projection's: both of one output in one thread. A
+          // box of 32 rows x 32 columns of h, 64 bytes a row (16-byte chunk v of row r at v ^ (r / 2 % 4)), as below.
+#pragma unroll 1
+          for (int c = 0; c < kOut; c += 32) {
+            const int col = n0 + c;
+            if (col >= F || m0 + quarter * 32 >= T) break;
+            uint32_t g[32], u[32], w[16];
+            ptx::tmem_ld_32x32b_x32(lane_tmem + static_cast<uint32_t>(c), g);
+            ptx::tmem_ld_32x32b_x32(lane_tmem + static_cast<uint32_t>(kOut + c), u);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(gate(__uint_as_float(g[2 * i]), act) * __uint_as_float(u[2 * i]),
+                                                              gate(__uint_as_float(g[2 * i + 1]), act) * __uint_as_float(u[2 * i + 1]));
+              w[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            uint8_t* b = stage_box + box * kEpiBoxBytes;
+            if (lane == 0) ptx::bulk_wait_group_read<1>();
+            __syncwarp();
+            uint4* rowp = reinterpret_cast<uint4*>(b + lane * 64);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) rowp[v ^ (lane >> 1 & 3)] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              ptx::tma_store_2d(&tmap_y, b, col, m0 + quarter * 32);
+              ptx::bulk_commit_group();
+            }
+            box ^= 1;
+          }
+        }
         const int row = m0 + row_in_half;
         float* yrow = y + static_cast<size_t>(row) * D;
 #pragma unroll 1
-        for (int c = 0; c < BN; c += 32) {
+        for (int c = 0; c < (GATED ? 0 : BN); c += 32) {
           uint32_t r[32];
           ptx::tmem_ld_32x32b_x32(lane_tmem + static_cast<uint32_t>(c), r);
           ptx::tmem_ld_wait();
@@ -541,15 +576,16 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
 // The N tiles the pair kernel is built for, each with the deepest ring that fits.
 using Pair256 = PairCfg<256, 6>;
 
-template <int BN, int STAGES>
+template <int BN, int STAGES, bool GATED = false>
 cudaError_t configure_pair() {
-  return cudaFuncSetAttribute(gemm_bf16_pair_kernel<BN, STAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(gemm_bf16_pair_kernel<BN, STAGES, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               PairCfg<BN, STAGES>::kBytes);
 }
 
-template <int BN, int STAGES>
-cudaError_t launch_pair_bn(const uint16_t* x, const uint16_t* W, float* y, int T, int K, int D, uint32_t* err,
-                           const PoolView* pool, const MetaView* meta, int max_pairs, bool fuse, cudaStream_t s) {
+// y: fp32 [T, D], or, GATED, h: bf16 [T, D / 2] after the activation `act`.
+template <int BN, int STAGES, bool GATED = false>
+cudaError_t launch_pair_bn(const uint16_t* x, const uint16_t* W, void* y, int T, int K, int D, uint32_t* err,
+                           const PoolView* pool, const MetaView* meta, int max_pairs, bool fuse, cudaStream_t s, int act = 0) {
   using L = PairCfg<BN, STAGES>;
   CUtensorMap mx, mw, mv, mb, ma;
   if (!make_tmap_bf16(&mx, x, T, K, kHalf, kPK) || !make_tmap_bf16(&mw, W, D, K, L::kBRows, kPK))
@@ -591,11 +627,12 @@ cudaError_t launch_pair_bn(const uint16_t* x, const uint16_t* W, float* y, int T
     ma = mx;
   }
   CUtensorMap my;
-  const int y_tma = make_tmap_f32_sw128(&my, y, T, D, 32) ? 1 : 0;   // else plain row stores
-  if (!y_tma) my = mx;
+  const int y_tma = (GATED ? make_tmap_bf16_store(&my, y, T, D / 2, 32) : make_tmap_f32_sw128(&my, y, T, D, 32)) ? 1 : 0;
+  if (GATED && !y_tma) return cudaErrorInvalidValue;
+  if (!y_tma) my = mx;                                                 // plain row stores
   // with the side path every resident pair is launched (the shrink sub-tiles are counted on the
   // device); otherwise no more pairs than tiles
-  const int tiles = ((num_m + 1) / 2) * ((D + BN - 1) / BN);
+  const int tiles = ((num_m + 1) / 2) * (GATED ? (D / 2 + BN / 2 - 1) / (BN / 2) : (D + BN - 1) / BN);
   const int pairs = sp.fused ? max_pairs : (tiles < max_pairs ? tiles : max_pairs);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs, 1, 1);
@@ -612,8 +649,8 @@ cudaError_t launch_pair_bn(const uint16_t* x, const uint16_t* W, float* y, int T
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   note_launch_begin(kKindGemm, s);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_bf16_pair_kernel<BN, STAGES>, mx, mw, mv, mb, ma, my, sp, y, y_tma, T,
-                                     D, K, err);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_bf16_pair_kernel<BN, STAGES, GATED>, mx, mw, mv, mb, ma, my, sp,
+                                     static_cast<float*>(GATED ? nullptr : y), y_tma, T, D, K, err, act);
   note_launch_end(kKindGemm, s);
   return e;
 }
@@ -647,7 +684,9 @@ int pair_gemm_max_pairs() {
   cudaGetDevice(&dev);
   if (cached_device == dev) return cached;
   if (configure_pair<256, 6>() != cudaSuccess || configure_pair<224, 6>() != cudaSuccess ||
-      configure_pair<192, 6>() != cudaSuccess || configure_pair<128, 8>() != cudaSuccess) {
+      configure_pair<192, 6>() != cudaSuccess || configure_pair<128, 8>() != cudaSuccess ||
+      configure_pair<256, 6, true>() != cudaSuccess || configure_pair<192, 6, true>() != cudaSuccess ||
+      configure_pair<128, 8, true>() != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -665,7 +704,7 @@ int pair_gemm_max_pairs() {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int clusters = 0;
-  if (cudaOccupancyMaxActiveClusters(&clusters, gemm_bf16_pair_kernel<256, 6>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&clusters, gemm_bf16_pair_kernel<256, 6, false>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     clusters = 0;
   }
@@ -704,6 +743,27 @@ cudaError_t launch_pair_gemm(const uint16_t* x, const uint16_t* W, float* y, int
     case 192: return launch_pair_bn<192, 6>(x, W, y, T, K, D, err, pool, meta, max_pairs, fuse, s);
     case 128: return launch_pair_bn<128, 8>(x, W, y, T, K, D, err, pool, meta, max_pairs, fuse, s);
     default: return cudaErrorInvalidValue;
+  }
+}
+
+// Tiles of 256 rows x bn / 2 columns of h; the widths that whole boxes of 32 columns fill. By the estimates above, over tiles of
+// bn rows of W.
+cudaError_t launch_pair_gemm_gated(const uint16_t* x, const uint16_t* W, uint16_t* h, int T, int K, int D, int act, uint32_t* err,
+                                   const PoolView* pool, const MetaView* meta, int bn, cudaStream_t s) {
+  const bool fuse = pair_gemm_fuses_shrink(K);
+  const int max_pairs = pair_gemm_max_pairs();
+  if (max_pairs < 1) return cudaErrorNotSupported;
+  if (bn != 256 && bn != 192 && bn != 128) {
+    double best = 0.0;
+    for (int n : {256, 192, 128}) {
+      const double time = fuse ? pair_time_dynamic(T, D, n, max_pairs) : pair_time(T, D, n, max_pairs);
+      if (n == 256 || time < best - 1e-9 || (fuse && time <= best + 1e-9)) best = time, bn = n;
+    }
+  }
+  switch (bn) {
+    case 256: return launch_pair_bn<256, 6, true>(x, W, h, T, K, D, err, pool, meta, max_pairs, fuse, s, act);
+    case 192: return launch_pair_bn<192, 6, true>(x, W, h, T, K, D, err, pool, meta, max_pairs, fuse, s, act);
+    default: return launch_pair_bn<128, 8, true>(x, W, h, T, K, D, err, pool, meta, max_pairs, fuse, s, act);
   }
 }
 

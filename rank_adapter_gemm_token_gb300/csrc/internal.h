@@ -118,6 +118,9 @@ bool make_tmap_u8(CUtensorMap* map, const void* base, long rows, int cols, int b
 // Row-major fp32 matrix [rows, cols] with a box of box_rows x 32 columns (128 bytes, 128-byte
 // swizzle), for tiled stores. False unless cols is a multiple of 4 and base 16-byte aligned.
 bool make_tmap_f32_sw128(CUtensorMap* map, const void* base, long rows, int cols, int box_rows);
+// Row-major bf16 matrix [rows, cols] with a box of box_rows x 32 columns (64 bytes, 64-byte swizzle), for tiled stores. False
+// unless cols is a multiple of 8 and base 16-byte aligned.
+bool make_tmap_bf16_store(CUtensorMap* map, const void* base, long rows, int cols, int box_rows);
 
 // Launchers. Each returns the cudaError_t of its launch.
 // The step's metadata: sorted pairs, segments, pair-blocks, active slots and, for the tensor-core
@@ -177,6 +180,10 @@ bool pair_gemm_fuses_shrink(int K);
 int pair_gemm_pick_n(int T, int D, int max_pairs, bool dynamic);
 cudaError_t launch_pair_gemm(const uint16_t* x, const uint16_t* W, float* y, int T, int K, int D, uint32_t* err,
                              const PoolView* pool, const MetaView* meta, int bn, cudaStream_t s);
+// The same kernel over the stacked gate and up projections (D = 2 F rows of W, the gate's first), with the activation and the
+// product in its epilogue: h bf16 [T, F] (gated.cuh); bn: 256, 192, 128, or any other value for the estimated best.
+cudaError_t launch_pair_gemm_gated(const uint16_t* x, const uint16_t* W, uint16_t* h, int T, int K, int D, int act, uint32_t* err,
+                                   const PoolView* pool, const MetaView* meta, int bn, cudaStream_t s);
 int gemm_tile_n();
 
 // K elements per shrink split and the number of splits for a pool of width R.

@@ -926,6 +926,23 @@ mlora_status mlora_lora_expand(mlora_pool_t p, mlora_meta_t m, float* y, void* s
   return MLORA_OK;
 }
 
+// The unit lists of the tensor-core side path, which the first linear of a step that takes it builds.
+static cudaError_t build_units(mlora_pool_t p, mlora_meta_t m, cudaStream_t s) {
+  if (m->units_built) return cudaSuccess;
+  const cudaError_t e = launch_build_meta(nullptr, nullptr, m->T, m->J, p->view(), m->view(), s, kMetaUnitsOnly);
+  m->units_built = e == cudaSuccess;
+  return e;
+}
+
+// Whether the step's sizes allow an M-tile to pass the unit limits, so that its pairs take the CUDA-core kernels.
+static bool units_may_overflow(mlora_pool_t p, mlora_meta_t m) {
+  const long n_blocks = (p->C + kBlockCols - 1) / kBlockCols;
+  const long per_tile = std::min(128L * m->J * p->max_span, n_blocks);
+  const long n_tiles = (m->T + 127) / 128;
+  return per_tile > kMaxTileUnits ||
+         (n_tiles * per_tile > m->unit_cap && static_cast<long>(m->T) * m->J * p->max_span > m->unit_cap);
+}
+
 mlora_status mlora_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, const mlora_bf16* W, float* y,
                           void* stream) {
   if (p && p->embed) return fail(MLORA_ERR_INVALID_ARG, "an embedding pool: use mlora_embedding");
@@ -960,23 +977,14 @@ mlora_status mlora_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, c
     // tensor-core side path: the shrink of every unit (M-tile, column block), then the base GEMM
     // with the expand as extra K blocks; the CUDA-core kernels take the pairs of M-tiles that
     // overflow the unit lists, and are launched only when the sizes allow an overflow
-    if (!m->units_built) {
-      if ((e = launch_build_meta(nullptr, nullptr, m->T, m->J, pv, mv, s, kMetaUnitsOnly)) != cudaSuccess)
-        return cuda_fail(e, "unit lists launch");
-      m->units_built = true;
-    }
+    if ((e = build_units(p, m, s)) != cudaSuccess) return cuda_fail(e, "unit lists launch");
     // (the CTA-pair GEMM computes the shrink itself, as tiles of its own schedule, for K <= 8192)
     const bool fused_shrink = base_gemm_uses_pair(m->T) && pair_gemm_fuses_shrink(p->K);
     if (!fused_shrink && (e = launch_lora_shrink_tc(x, pv, mv, ds->err, ds->num_sms, s)) != cudaSuccess)
       return cuda_fail(e, "tensor-core shrink launch");
     if ((e = launch_base_gemm_lora(x, W, y, m->T, p->K, p->D, ds->err, ds->num_sms, &pv, &mv, s)) != cudaSuccess)
       return cuda_fail(e, "base GEMM launch");
-    const long n_blocks = (p->C + kBlockCols - 1) / kBlockCols;
-    const long per_tile = std::min(128L * m->J * p->max_span, n_blocks);
-    const long n_tiles = (m->T + 127) / 128;
-    const bool overflow = per_tile > kMaxTileUnits ||
-                          (n_tiles * per_tile > m->unit_cap && static_cast<long>(m->T) * m->J * p->max_span > m->unit_cap);
-    if (overflow) {
+    if (units_may_overflow(p, m)) {
       if ((e = launch_lora_shrink(x, pv, mv, ds->num_sms, s, true)) != cudaSuccess) return cuda_fail(e, "shrink launch");
       if ((e = launch_lora_expand(y, pv, mv, ds->num_sms, s, true)) != cudaSuccess) return cuda_fail(e, "expand launch");
     }
@@ -985,8 +993,14 @@ mlora_status mlora_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, c
   return MLORA_OK;
 }
 
+// The activation runs in the CTA-pair GEMM's epilogue, except where the output is not complete there (pairs that the
+// CUDA-core kernels add), or where the controls ask for another GEMM.
+static bool gated_fuses(mlora_pool_t p, mlora_meta_t m) {
+  return g_path.load(std::memory_order_relaxed) != 1 && gemm_tile_n() >= 0 && pair_gemm_max_pairs() > 0 && !units_may_overflow(p, m);
+}
+
 size_t mlora_gated_workspace_bytes(mlora_pool_t p, mlora_meta_t m) {
-  if (!p || !m || p->embed || !m->built) return 0;
+  if (!p || !m || p->embed || !m->built || gated_fuses(p, m)) return 0;
   return static_cast<size_t>(m->T) * p->D * sizeof(float);
 }
 
@@ -998,13 +1012,26 @@ mlora_status mlora_gated_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16
   if (act < MLORA_ACT_SILU || act > MLORA_ACT_GELU) return fail(MLORA_ERR_INVALID_ARG, "unknown activation %d", act);
   if (mlora_status st = check_operands(x, W, h, m->T, p->K, p->D)) return st;
   if (m->T == 0) return MLORA_OK;
-  if (!workspace || !aligned16(workspace)) return fail(MLORA_ERR_INVALID_ARG, "workspace is NULL or misaligned");
-  float* y = static_cast<float*>(workspace);
-  if (mlora_status st = mlora_linear(p, m, x, W, y, stream)) return st;
   DeviceState* ds = nullptr;
   if (mlora_status st = device_state(&ds)) return st;
-  const cudaError_t e = launch_gated_activation(y, h, m->T, p->D / 2, act, ds->num_sms, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "activation launch");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (!gated_fuses(p, m)) {
+    if (!workspace || !aligned16(workspace)) return fail(MLORA_ERR_INVALID_ARG, "workspace is NULL or misaligned");
+    float* y = static_cast<float*>(workspace);
+    if (mlora_status st = mlora_linear(p, m, x, W, y, stream)) return st;
+    if ((e = launch_gated_activation(y, h, m->T, p->D / 2, act, ds->num_sms, s)) != cudaSuccess) return cuda_fail(e, "activation launch");
+    return MLORA_OK;
+  }
+  if (mlora_status st = pool_use(p, s)) return st;
+  const MetaView mv = m->view();
+  const PoolView pv = p->view();
+  if ((e = build_units(p, m, s)) != cudaSuccess) return cuda_fail(e, "unit lists launch");
+  if (!pair_gemm_fuses_shrink(p->K) && (e = launch_lora_shrink_tc(x, pv, mv, ds->err, ds->num_sms, s)) != cudaSuccess)
+    return cuda_fail(e, "tensor-core shrink launch");
+  if ((e = launch_pair_gemm_gated(x, W, h, m->T, p->K, p->D, act, ds->err, &pv, &mv, gemm_tile_n(), s)) != cudaSuccess)
+    return cuda_fail(e, "gated GEMM launch");
+  m->last_stream = s;
   return MLORA_OK;
 }
 
