@@ -82,6 +82,7 @@ enum {
 #define MLORA_MAX_CLASSES 8           /* rank classes of one pool (mlora_pool_create_classes) */
 #define MLORA_MAX_SEQS 8192           /* sequences of one step (mlora_seq_create) */
 #define MLORA_MAX_HEADS 256           /* query heads, key/value heads of one attention layer */
+#define MLORA_MAX_SINKS 1048576       /* first tokens that stay visible (mlora_build_seq_window) */
 
 /* ------------------------------------------------------------------ adapter pool ----- */
 
@@ -395,6 +396,10 @@ MLORA_API mlora_status mlora_rope_destroy(mlora_rope_t rope);
  * 128 query heads) of head_dim. */
 MLORA_API mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n_q_heads, int n_kv_heads,
                                         int head_dim, mlora_seq_t* out);
+/* The same, with room for max_groups groups of sequences that share a prefix (mlora_build_seq_groups; at most max_seqs). Their
+ * workspace takes about 4 n_q_heads (head_dim + 2) bytes for each token of the step and 512 n_kv_heads (head_dim + 2) * 2 for each group. */
+MLORA_API mlora_status mlora_seq_create_groups(int max_seqs, int max_tokens, int max_pages, int n_q_heads, int n_kv_heads,
+                                               int head_dim, int max_groups, mlora_seq_t* out);
 MLORA_API mlora_status mlora_seq_destroy(mlora_seq_t seq);
 
 /* Describes one step (asynchronous on `stream`; the arrays may change once it has run there):
@@ -416,6 +421,30 @@ MLORA_API mlora_status mlora_seq_destroy(mlora_seq_t seq);
 MLORA_API mlora_status mlora_build_seq(mlora_seq_t seq, const int32_t* q_start, const int32_t* kv_len,
                                        const int32_t* pages, int pages_ld, int n_seqs, int T, int max_new,
                                        mlora_kv_t kv, void* stream);
+/* The same step for layers whose tokens see a window of the last tokens and a few first ones: the token at position p sees
+ * positions j <= p with j < sinks or j > p - window (window >= 1: its own among them; 0 <= sinks <= MLORA_MAX_SINKS).
+ * Pages that hold no position which a new token of their sequence sees (nor, for a sequence without new tokens, its next one)
+ * are not read: they may have been given back, and their entries hold anything. mlora_kv_read leaves the rows of such pages
+ * as they are. A model whose layers differ in this has a mlora_seq for each kind. */
+MLORA_API mlora_status mlora_build_seq_window(mlora_seq_t seq, const int32_t* q_start, const int32_t* kv_len,
+                                              const int32_t* pages, int pages_ld, int n_seqs, int T, int max_new, int window,
+                                              int sinks, mlora_kv_t kv, void* stream);
+/* The same step where groups of sequences begin with the same cached tokens: the attention reads those once for a group, all of
+ * whose query rows meet them together, and joins the result with that over each sequence's own tokens. What it computes is that
+ * of mlora_build_seq, but for the order of the sums.
+ *   group_start: device int32 [n_groups + 1], ascending, within [0, n_seqs]: group g is the sequences group_start[g] ..
+ *                group_start[g + 1] - 1 (sequences outside stand alone).
+ *   prefix_len:  device int32 [n_groups]: the group's sequences share their first prefix_len[g] positions, that is, the pages that
+ *                these fill (whole pages, at least 128 positions, are shared; the rest is read for each).
+ *   n_groups:    at most the seq's max_groups (MLORA_ERR_TOO_MANY_TOKENS otherwise).
+ *   max_prefix:  an upper bound of prefix_len known to the host: where the groups cannot save enough by it, they are not used.
+ * The groups are a hint: a sequence whose pages are not those of its group's first sequence, or with fewer earlier tokens than
+ * the prefix, is attended by itself. Bounds that do not ascend within the sequences: no group is used, and mlora_seq_status
+ * reports MLORA_ERR_INVALID_ARG. */
+MLORA_API mlora_status mlora_build_seq_groups(mlora_seq_t seq, const int32_t* q_start, const int32_t* kv_len,
+                                              const int32_t* pages, int pages_ld, int n_seqs, int T, int max_new,
+                                              const int32_t* group_start, const int32_t* prefix_len, int n_groups,
+                                              int max_prefix, mlora_kv_t kv, void* stream);
 /* Synchronises with the last call that used this object and reports its device-side errors, which it clears. */
 MLORA_API mlora_status mlora_seq_status(mlora_seq_t seq);
 

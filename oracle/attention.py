@@ -36,7 +36,14 @@ def row_scale(x: np.ndarray) -> np.ndarray:
     return np.maximum(np.abs(x).max(-1), AMAX_MIN) / E4M3_MAX
 
 
-def attention(q, keys, values, starts, group: int, scale: float) -> tuple:
+def seen_keys(position: int, window=None, sinks: int = 0) -> np.ndarray:
+    """The keys that the token at `position` sees: all up to its own, or, with a window, the first `sinks` ones and the last
+    `window` ones."""
+    j = np.arange(position + 1)
+    return j if window is None else j[(j < sinks) | (j > position - window)]
+
+
+def attention(q, keys, values, starts, group: int, scale: float, window=None, sinks: int = 0) -> tuple:
     """q [T, Hq, hd]; keys, values: for each sequence [L, Hkv, hd]; its queries are rows starts[s] .. starts[s + 1] - 1
     and its last positions. Returns the output [T, Hq, hd] and two bounds' ingredients of each element or row:
     sum_j p_j |v_j| and max_j scale sum_i |q_i k_ji|. Rows of no sequence, or with no key, are zero."""
@@ -45,11 +52,11 @@ def attention(q, keys, values, starts, group: int, scale: float) -> tuple:
     for s, (k, v) in enumerate(zip(keys, values)):
         a, b = starts[s], starts[s + 1]
         for t in range(a, b):
-            seen = len(k) - (b - a) + (t - a) + 1
-            if seen <= 0:
+            if len(k) - (b - a) + (t - a) < 0:
                 continue
+            seen = seen_keys(len(k) - (b - a) + (t - a), window, sinks)
             for h in range(hq):
-                kk, vv = k[:seen, h // group], v[:seen, h // group]
+                kk, vv = k[seen, h // group], v[seen, h // group]
                 z = scale * (kk @ q[t, h])
                 p = np.exp(z - z.max())
                 p /= p.sum()

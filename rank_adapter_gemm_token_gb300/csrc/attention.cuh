@@ -161,12 +161,26 @@ struct Sums {
   }
 };
 
+// A row's sums over its group's shared prefix: the (token, head of the group) row r of a sequence whose place there is `at`.
+struct PreRow {
+  const float* slot;
+  int row;
+  __device__ __forceinline__ PreRow(const SeqView& v, int2 at, int kvh, int r) {
+    const int tok = at.y + r / v.G, tile = tok / v.tile_tokens;
+    slot = v.pre_part + ((static_cast<int64_t>(at.x + (tile >> 1)) * v.Hkv + kvh) * 2 + (tile & 1)) * tile_slot(v);
+    row = (tok - tile * v.tile_tokens) * v.G + r % v.G;
+  }
+  __device__ __forceinline__ float top(int hd) const { return slot[128 * hd + row]; }
+  __device__ __forceinline__ float total(int hd) const { return slot[128 * hd + 128 + row]; }
+  __device__ __forceinline__ float4 quad(int q) const { return reinterpret_cast<const float4*>(slot)[q * 128 + row]; }
+};
+
 // Joins `count` parts of a row kernel's item of `rows` rows (token, head of the group): those from part `from` on, `step` apart,
-// of the item whose first part CTA `cta` has. The result goes to the output rows from o on, or, without o, to the place of part
-// `from`. All threads of the block; sx, sm: a place for each.
+// of the item whose first part CTA `cta` has. The result goes to the output rows from o on (pre: with the rows' sums over their
+// prefix, at pre_at in head kvh), or, without o, to the place of part `from`. All threads of the block; sx, sm: a place for each.
 template <int HD, int THREADS>
 __device__ __forceinline__ void join_rows(uint16_t* o, const SeqView& v, int rows, int cta, int from, int step, int count,
-                                          float4* sx, float2* sm) {
+                                          float4* sx, float2* sm, bool pre = false, int2 pre_at = make_int2(0, 0), int kvh = 0) {
   constexpr int kQuads = HD / 4;         // groups of four columns
   const int elements = rows * kQuads;
   const int64_t slot = row_slot(v);
@@ -215,6 +229,10 @@ __device__ __forceinline__ void join_rows(uint16_t* o, const SeqView& v, int row
       *reinterpret_cast<float4*>(part(0) + r * HD + h) = z.x;                  // (no other thread reads this element)
       if (h == 0) done[r] = make_float2(z.top, z.total);
     } else {
+      if (pre) {
+        const PreRow p(v, pre_at, kvh, r);
+        z.add(p.top(HD), p.total(HD), p.quad(h / 4));
+      }
       const float inv = inverse(z.total);
       *reinterpret_cast<uint2*>(o + (static_cast<int64_t>(r / v.G) * v.Hq + r % v.G) * HD + h) =
           make_uint2(pack_bf16(z.x.x * inv, z.x.y * inv), pack_bf16(z.x.z * inv, z.x.w * inv));

@@ -39,19 +39,30 @@ struct alignas(16) RowShare {
 // A block of the tile kernel's list: tokens t0 ... (two tiles of SeqView::tile_tokens) of sequence seq, `tiles` key
 // tiles.
 struct alignas(32) TileBlk {
-  int32_t seq, n, len, start, t0, tiles;
+  int32_t seq, n, len, start, t0, tiles, gap;
 };
 // What a CTA of the tile kernel does next: key tiles [ka, kb) of head kvh of such a block, of which its tile w sees
-// [ka, end[w]); split: not the whole item. A CTA's list begins at tile_share.x and holds tile_share.y of them.
+// [ka, end[w]); split: not the whole item; gap: as below, or, in a prefix pass, the block's number. A CTA's list begins at
+// tile_share.x and holds tile_share.y of them.
 struct alignas(16) TileWork {
   int32_t ka, kb, end[2];
   int32_t len, n, start, t0;
-  int32_t seq, kvh, split, unused;
+  int32_t seq, kvh, split, gap;
 };
 // An item (list entry, head) that lies across cuts: CTAs cta ... cta + parts - 1 each hold a part.
 struct JoinTask {
   int32_t item, kvh, cta, parts;
 };
+
+// Which keys the rows of a step's sequences see, as the kernels are compiled for it:
+//   kSeeAll     a row at position p all keys up to p;
+//   kSeeRanges  with a window, keys j <= p with j < sinks or j > p - window; behind a shared prefix, keys up to p from the end of
+//               the prefix on, the rows' sums over the prefix's keys joined from SeqView::pre_part. The units (key tiles) of a
+//               sequence that some row sees are counted without the gap between the first ones and the window (or without
+//               the prefix): unit u is unit u + gap of the cache from gap_unit on (key tile: from gap_tile on);
+//   kSeePrefix  the pass over the shared prefixes: a "sequence" is a group, every row of it sees all `len` keys, a multiple
+//               of kTileKeys, and its sums go to pre_part.
+constexpr int kSeeAll = 0, kSeeRanges = 1, kSeePrefix = 2;
 
 // Device arrays of one step's sequences, written by launch_build_seq.
 struct SeqView {
@@ -75,12 +86,32 @@ struct SeqView {
   JoinTask* tile_join;  // [counts[2]] the tile kernel's split items
   int32_t* counts;      // [1] first rejected sequence (INT32_MAX if none), [2] split items
   uint32_t* err;        // device error word (ptx::kErr* bits)
+  int32_t* row_gap;     // [S] kSeeRanges: gap of each of the row kernel's sequences, in units
+  int32_t* skip;        // [S] keys of each sequence that its group's prefix pass takes (0: none)
+  int32_t* group;       // [S] its group
+  int2* pre_at;         // [S] first block of its group in the prefix pass (-1: none), its first token among the group's
+  int32_t* rep;         // [S] prefix pass: a sequence that has the group's table
+  int32_t* first_blk;   // [S] prefix pass: the group's first block
+  float* pre_part;      // sums over the prefix of block b's rows: slot (b * Hkv + head) * 2 + tile, as tile_part's
   float* row_part;      // partial results of the row kernel's split items
   float* tile_part;     // of the tile kernel's
   int S, T, max_pages, Hq, Hkv, G, hd;
   int tile_tokens;      // tokens of one 128-row tile of the tile kernel (128 / G)
   int row_limit;        // rows (new tokens * G) up to which a sequence takes the row kernel
   int row_ctas, tile_ctas;
+  int see;              // kSee*
+  int window, sinks;    // kSeeRanges (without a window: INT_MAX, 0)
+  int gap_unit, gap_tile;
+};
+
+// What a step's rows see beside plain causal attention, for launch_build_seq: a window (0: none), or groups of sequences that
+// share a prefix (device arrays; the prefix pass's own view).
+struct SeqReuse {
+  int window, sinks;
+  const int32_t* group_start;   // [n_groups + 1]
+  const int32_t* prefix_len;    // [n_groups]
+  int n_groups;
+  SeqView prefix;
 };
 
 // Keys of one unit of the row kernel (four warps x 16 keys) and of one tile of the tile kernel.
@@ -90,6 +121,9 @@ constexpr int kTileKeys = 128;
 constexpr int kTileSnap = 2;          // key tiles that a split costs at least (1 and 0: a prompt of 3000 tokens in shares 93, 97 us for 87)
 constexpr int kTileDeal = 12;         // key tiles above the mean up to which whole items are dealt out (6: 6 chunks of 300 on 4000 137 us for 108)
 constexpr int kTileHead = 3;          // key tiles that an item's fixed costs (queries, first products, output) are worth
+
+constexpr int64_t kShareBytes = 32 << 20;      // bytes that a step's groups must be able to save for a prefix pass
+constexpr int kShareSeqs = 2;         // sequences of a group from which on its prefix is attended once for all
 
 // CTAs of the row kernel on an SM: by the row limit (16 rather than 8) and the cache's type.
 __host__ __device__ constexpr int rows_ctas_per_sm(bool sixteen, bool e4m3) { return e4m3 && !sixteen ? 3 : 2; }
@@ -103,7 +137,7 @@ struct RopeView {
 };
 
 cudaError_t launch_build_seq(const int32_t* q_start, const int32_t* kv_len, const int32_t* pages, int table_ld,
-                             const SeqView& s, int max_new, const KvView& kv, cudaStream_t st);
+                             const SeqView& s, int max_new, const KvView& kv, const SeqReuse& reuse, cudaStream_t st);
 cudaError_t launch_qkv_write(const float* qkv, int64_t ld, const uint16_t* q_norm, const uint16_t* k_norm, float eps,
                              const RopeView& rope, const int32_t* positions, uint16_t* q, const KvView& kv,
                              const SeqView& s, int num_sms, cudaStream_t st);
@@ -111,7 +145,9 @@ cudaError_t launch_kv_read(const int32_t* row_start, int64_t rows, uint16_t* k, 
                            const SeqView& s, int num_sms, cudaStream_t st);
 // Attention in up to three launches, each a programmatic dependent of the one before: the row kernel (sequences of at
 // most SeqView::row_limit rows, and the zero rows of tokens in no sequence), with `tiles` the tile kernel (the other
-// sequences; tk and tv: the maps of the cache's K and V), and the join of the items that were split among CTAs.
+// sequences; tk and tv: the maps of the cache's K and V), and the join of the items that were split among CTAs. Where groups
+// share prefixes, the tile kernel and the join run over those first (kSeePrefix; the first of a step's launches waits for the
+// work before it as a whole).
 cudaError_t launch_attention_rows(const uint16_t* q, uint16_t* o, float scale, const KvView& kv, const SeqView& s,
                                   cudaStream_t st);
 cudaError_t launch_attention_tiles(const CUtensorMap& tk, const CUtensorMap& tv, const uint16_t* q, uint16_t* o,
@@ -125,6 +161,10 @@ bool make_kv_maps(const KvView& kv, CUtensorMap* k, CUtensorMap* v);
 // Tile kernel: two 128-row tiles, each [hd / 4][128] four sums, then [128] maxima and [128] sums of weights.
 __host__ __device__ inline int64_t row_slot(const SeqView& s) { return static_cast<int64_t>(s.row_limit) * (s.hd + 2); }
 __host__ __device__ inline int64_t tile_slot(const SeqView& s) { return static_cast<int64_t>(128) * (s.hd + 2); }
+// The most blocks that n tokens of s sequences make in the tile kernel's list.
+inline int64_t most_blocks(const SeqView& v, int64_t n, int64_t s) { return n / (2 * v.tile_tokens) + s; }
+// The first key behind the sinks that the row at position p sees.
+__host__ __device__ inline int first_seen(int p, int window) { return p - window + 1 > 0 ? p - window + 1 : 0; }
 inline size_t row_part_bytes(const SeqView& s) { return static_cast<size_t>(s.row_ctas) * 2 * 16 * (s.hd + 2) * 4; }
 inline size_t tile_part_bytes(const SeqView& s) { return static_cast<size_t>(s.tile_ctas) * 2 * 2 * tile_slot(s) * 4; }
 

@@ -6,6 +6,8 @@
 // context) still spread over the SMs. (The row kernel's items are joined by its own last CTAs.) Launched as a programmatic
 // dependent: it reads its first task while the attention still runs. Bound by the latency of the parts' reads (from L2):
 // eight parts are asked for at once. 3 to 4 us alone and cold with little to join, most of it beside the attention's end.
+#include <type_traits>
+
 #include "attention.h"
 #include "attention.cuh"
 #include "internal.h"
@@ -18,7 +20,7 @@ constexpr int kThreads = 256;
 constexpr int kRows = 8;              // rows of a unit of a tile item
 constexpr int kSlices = 256 / kRows;  // units of a block
 
-template <int HD>
+template <int HD, int SEE>
 __global__ void __launch_bounds__(kThreads)
 attention_join_kernel(uint16_t* __restrict__ o, SeqView v) {
   constexpr int kQuads = HD / 4;       // groups of four columns
@@ -55,6 +57,19 @@ attention_join_kernel(uint16_t* __restrict__ o, SeqView v) {
       for (int k = 0; k < kPartsAhead; ++k)
         if (k0 + k < parts) z.add(m[k], l[k], y[k]);
     }
+    if (SEE == kSeePrefix) {                          // to the block's own place: the join with the sequences' own keys is still to come
+      float* p = v.pre_part + ((static_cast<int64_t>(task.x) * v.Hkv + kvh) * 2 + w) * slot;
+      reinterpret_cast<float4*>(p)[quad * 128 + r] = z.x;
+      if (quad == 0) p[128 * HD + r] = z.top, p[128 * HD + 128 + r] = z.total;
+      continue;
+    }
+    if (SEE == kSeeRanges && v.pre_at != nullptr) {
+      const int2 at = v.pre_at[b.seq];
+      if (at.x >= 0) {
+        const PreRow p(v, at, kvh, (b.t0 + v.tile_tokens * w) * v.G + r);
+        z.add(p.top(HD), p.total(HD), p.quad(quad));
+      }
+    }
     const float inv = inverse(z.total);
     *reinterpret_cast<uint2*>(o + (static_cast<int64_t>(b.start + tok) * v.Hq + kvh * v.G + r % v.G) * HD + 4 * quad) =
         make_uint2(pack_bf16(z.x.x * inv, z.x.y * inv), pack_bf16(z.x.z * inv, z.x.w * inv));
@@ -75,8 +90,13 @@ cudaError_t launch_attention_join(uint16_t* o, const SeqView& s, cudaStream_t st
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = s.hd == 128 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<128>, o, s)
-                                    : cudaLaunchKernelEx(&cfg, attention_join_kernel<64>, o, s);
+  auto launch = [&](auto see) {
+    return s.hd == 128 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<128, see.value>, o, s)
+                       : cudaLaunchKernelEx(&cfg, attention_join_kernel<64, see.value>, o, s);
+  };
+  const cudaError_t e = s.see == kSeeAll ? launch(std::integral_constant<int, kSeeAll>())
+                        : s.see == kSeeRanges ? launch(std::integral_constant<int, kSeeRanges>())
+                                              : launch(std::integral_constant<int, kSeePrefix>());
   note_launch_end(kKindAttn, st);
   return e;
 }

@@ -124,15 +124,27 @@ __device__ __forceinline__ float pow2_of(float x) { return __int_as_float((stati
 __device__ __forceinline__ float log2_of(float x) { return static_cast<float>((__float_as_int(x) >> 23) - 127); }
 
 // A place in the list of units: unit u of head kvh of list entry i.
+template <bool RANGES>
 struct Place {
   int i, kvh, u, units;
   RowSeq s;
   const int32_t* table;
+  int gap;                                    // RANGES: units u from v.gap_unit on are units u + gap of the cache
   __device__ __forceinline__ void load(const SeqView& v) {
     const int4 x = *reinterpret_cast<const int4*>(v.row_seq + i);
     s = RowSeq{x.x, x.y, x.z, x.w};
     units = (s.len + kRowUnit - 1) / kRowUnit;
+    if (RANGES) units -= gap = v.row_gap[i];
     table = v.table + static_cast<size_t>(s.seq) * v.max_pages;
+  }
+  // The first key of the warp's chunk of unit x, and whether no row sees any of the chunk (RANGES; keys before
+  // first_seen() of the first row that are not among the first ones are brought as zeros).
+  __device__ __forceinline__ int key(const SeqView& v, int x, int warp) const {
+    return (RANGES && x >= v.gap_unit ? x + gap : x) * kRowUnit + warp * kChunk;
+  }
+  __device__ __forceinline__ int first(const SeqView& v) const { return RANGES ? first_seen(s.len - s.n, v.window) : 0; }
+  __device__ __forceinline__ bool unseen(const SeqView& v, int k0) const {
+    return k0 >= s.len || (RANGES && k0 >= v.sinks && k0 + kChunk <= first(v));
   }
   // the next unit; the caller knows that there is one
   __device__ __forceinline__ void next(const SeqView& v) {
@@ -145,7 +157,7 @@ struct Place {
   }
 };
 
-template <int HD, int NQ, bool E4M3>
+template <int HD, int NQ, bool E4M3, bool RANGES>
 __global__ void __launch_bounds__(kThreads, RowsCfg<HD, NQ, E4M3>::kCtas)
 attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, float scale_log2, KvView kv, SeqView v) {
   using C = RowsCfg<HD, NQ, E4M3>;
@@ -161,13 +173,14 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
   const int n_chunks = share.w;
   // ---- the warp's loads: chunk i of the CTA's share goes to stage i % kStages
   const uint32_t ring = ptx::smem_u32(smem) + warp * (C::kStages * C::kStage);
-  Place src{share.x, share.y, share.z, 0, {}, nullptr};
+  Place<RANGES> src{share.x, share.y, share.z, 0, {}, nullptr, 0};
   int issued = 0;
   int page_a = 0, page_b = 0;                 // pages of the next chunk's first and second 8 keys
   auto look = [&]() {
-    const int k0 = src.u * kRowUnit + warp * kChunk;
+    const int k0 = src.key(v, src.u, warp);
     page_a = src.table[min(k0, src.s.len - 1) >> kv.page_log2];
     page_b = kv.page_log2 < 4 ? src.table[min(k0 + 8, src.s.len - 1) >> kv.page_log2] : page_a;
+    if (RANGES) page_a = max(page_a, 0), page_b = max(page_b, 0);        // (a page that no row sees: nothing is read there)
   };
   if (n_chunks > 0) {
     src.load(v);
@@ -175,8 +188,8 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
   }
   auto issue = [&]() {
     if (issued < n_chunks) {
-      const int k0 = src.u * kRowUnit + warp * kChunk;
-      if (k0 < src.s.len) {
+      const int k0 = src.key(v, src.u, warp);
+      if (!src.unseen(v, k0)) {
         const uint32_t st = ring + (issued % C::kStages) * C::kStage;
         constexpr int kStep = 32 / C::kSegs;  // rows of one copy of all lanes
         constexpr int kHalf = kChunk / 2 / kStep;                                // copies of eight rows
@@ -186,7 +199,9 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
         const int64_t row_b = (static_cast<int64_t>(page_b) * v.Hkv + src.kvh) << kv.page_log2;
         const int off_a = k0 & (kv.page - 1), off_b = (k0 + 8) & (kv.page - 1);
         const int lr = lane / C::kSegs, seg = lane % C::kSegs;
-        const bool full = k0 + kChunk <= src.s.len;
+        const int seen0 = src.first(v);
+        const bool full = k0 + kChunk <= src.s.len && (!RANGES || k0 + kChunk <= v.sinks || k0 >= seen0);
+        auto inside = [&](int key) { return full || (key < src.s.len && (!RANGES || key < v.sinks || key >= seen0)); };
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int64_t at = ((half ? row_b + off_b : row_a + off_a) + lr) * C::kRowBytes + seg * 16;
@@ -197,7 +212,7 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
             const int r = half * 8 + i * kStep + lr;
             const int phys = C::kSegs >= 8 ? seg ^ (r & 7) : seg ^ ((r >> 1) & 3);
             const uint32_t dst = st + r * C::kRowBytes + phys * 16;
-            const bool in = full || k0 + r < src.s.len;
+            const bool in = inside(k0 + r);
             cp16(dst, pk + i * kStep * C::kRowBytes, in);
             cp16(dst + C::kTile, pv + i * kStep * C::kRowBytes, in);
           }
@@ -205,7 +220,7 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
         if (E4M3) {
           const int r = lane & 15;
           const int64_t at = (r < 8 ? row_a + off_a : row_b + off_b) + (r & 7);
-          cp4(st + 2 * C::kTile + lane * 4, (lane < 16 ? kv.k_scale : kv.v_scale) + at, full || k0 + r < src.s.len);
+          cp4(st + 2 * C::kTile + lane * 4, (lane < 16 ? kv.k_scale : kv.v_scale) + at, inside(k0 + r));
         }
       }
       ++issued;
@@ -233,7 +248,7 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
   }
 
   // ---- the CTA's items
-  Place at{share.x, share.y, share.z, 0, {}, nullptr};
+  Place<RANGES> at{share.x, share.y, share.z, 0, {}, nullptr, 0};
   if (n_chunks > 0) at.load(v);
   int done = 0;
   while (done < n_chunks) {
@@ -300,8 +315,8 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
       cp_wait<C::kStages - 2>();
       __syncwarp();
       issue();
-      const int k0 = u * kRowUnit + warp * kChunk;
-      if (k0 >= len) continue;
+      const int k0 = at.key(v, u, warp);
+      if (at.unseen(v, k0)) continue;
       const uint32_t st = ring + (done % C::kStages) * C::kStage;
       float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
       if (E4M3) {
@@ -348,7 +363,7 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
         }
       }
       uint32_t pb[NQ][2], pr[NQ][2];              // P in 16 bits, and (bf16) what that leaves, in 16 more
-      const bool edge = k0 + kChunk > base + 1;
+      const bool edge = k0 + kChunk > base + 1 || (RANGES && k0 + kChunk > v.sinks && k0 <= len - 1 - v.window);
 #pragma unroll
       for (int z = 0; z < NQ; ++z) {
         bool grow = false;
@@ -358,7 +373,8 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
           const int c = k & 1, h = k >> 1;
           float x = sc[z][k] + sc1[z][k];
           x = E4M3 ? x * ks[h] * cq[z][c] : x * cq[z][c];
-          if (edge && k0 + g + 8 * h > lim[z][c]) x = -INFINITY, hidden |= 1u << k;
+          const int key = k0 + g + 8 * h;
+          if (edge && (key > lim[z][c] || (RANGES && key >= v.sinks && key <= lim[z][c] - v.window))) x = -INFINITY, hidden |= 1u << k;
           sc[z][k] = x;
           grow = grow || x > m[z][c] + kLazy;
         }
@@ -493,6 +509,8 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
       w.w = pack_bf16(x[6] * inv, x[7] * inv);
       *reinterpret_cast<uint4*>(o + (static_cast<int64_t>(first + r / v.G) * v.Hq + at.kvh * v.G + r % v.G) * HD + h) = w;
     };
+    const int2 pre_at = RANGES && v.pre_at != nullptr ? v.pre_at[at.s.seq] : make_int2(-1, 0);
+    const bool pre = RANGES && pre_at.x >= 0;
     const bool whole = at.u == 0 && u_end == at.units;
     float* slot = v.row_part + (2 * static_cast<int64_t>(blockIdx.x) + (at.u == 0 ? 1 : 0)) * row_slot(v);
     for (int i = threadIdx.x; i < rows * kGroups; i += kThreads) {
@@ -511,6 +529,15 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
         for (int k = 0; k < 8; ++k) x[k] = fmaf(f, row[k], x[k]);
       }
       if (whole) {
+        if (pre) {                                    // joined with the row's sums over its prefix
+          const PreRow p(v, pre_at, at.kvh, r);
+          Sums z0{top, total, make_float4(x[0], x[1], x[2], x[3])}, z1{top, total, make_float4(x[4], x[5], x[6], x[7])};
+          z0.add(p.top(HD), p.total(HD), p.quad(h / 4));
+          z1.add(p.top(HD), p.total(HD), p.quad(h / 4 + 1));
+          x[0] = z0.x.x, x[1] = z0.x.y, x[2] = z0.x.z, x[3] = z0.x.w;
+          x[4] = z1.x.x, x[5] = z1.x.y, x[6] = z1.x.z, x[7] = z1.x.w;
+          total = z0.total;
+        }
         write_out(r, h, x, total);
       } else {
         float4* p = reinterpret_cast<float4*>(slot + r * HD + h);
@@ -545,10 +572,10 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
       // (an item's first run and the last of the item before may begin in the same CTA: counters of their own)
       if (is_last(v.row_there + (run == 0 ? 0 : 2 * v.row_ctas) + cta + run, in_run)) {
         const bool all = parts <= kPartsAhead;
-        join_rows<HD, kThreads>(all ? out : nullptr, v, rows, cta, run, 1, in_run, sx, sm);
+        join_rows<HD, kThreads>(all ? out : nullptr, v, rows, cta, run, 1, in_run, sx, sm, pre, pre_at, at.kvh);
         const int runs = (parts + kPartsAhead - 1) / kPartsAhead;
         if (!all && is_last(v.row_there + v.row_ctas + cta, runs))
-          join_rows<HD, kThreads>(out, v, rows, cta, 0, kPartsAhead, runs, sx, sm);
+          join_rows<HD, kThreads>(out, v, rows, cta, 0, kPartsAhead, runs, sx, sm, pre, pre_at, at.kvh);
       }
       __syncthreads();
     }
@@ -560,15 +587,21 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
   cp_wait<0>();
 }
 
-template <int HD, int NQ, bool E4M3>
-cudaError_t launch_as(const uint16_t* q, uint16_t* o, float scale_log2, const KvView& kv, const SeqView& s, cudaStream_t st) {
+template <int HD, int NQ, bool E4M3, bool RANGES>
+cudaError_t launch_seeing(const uint16_t* q, uint16_t* o, float scale_log2, const KvView& kv, const SeqView& s, cudaStream_t st) {
   using C = RowsCfg<HD, NQ, E4M3>;
-  if (cudaError_t e = allow_shared_memory<attention_rows_kernel<HD, NQ, E4M3>>(C::kBytes)) return e;
+  if (cudaError_t e = allow_shared_memory<attention_rows_kernel<HD, NQ, E4M3, RANGES>>(C::kBytes)) return e;
   note_launch_begin(kKindAttn, st);
-  attention_rows_kernel<HD, NQ, E4M3><<<s.row_ctas, kThreads, C::kBytes, st>>>(q, o, scale_log2, kv, s);
+  attention_rows_kernel<HD, NQ, E4M3, RANGES><<<s.row_ctas, kThreads, C::kBytes, st>>>(q, o, scale_log2, kv, s);
   const cudaError_t e = cudaGetLastError();
   note_launch_end(kKindAttn, st);
   return e;
+}
+
+template <int HD, int NQ, bool E4M3>
+cudaError_t launch_as(const uint16_t* q, uint16_t* o, float scale_log2, const KvView& kv, const SeqView& s, cudaStream_t st) {
+  return s.see == kSeeRanges ? launch_seeing<HD, NQ, E4M3, true>(q, o, scale_log2, kv, s, st)
+                             : launch_seeing<HD, NQ, E4M3, false>(q, o, scale_log2, kv, s, st);
 }
 
 }  // namespace

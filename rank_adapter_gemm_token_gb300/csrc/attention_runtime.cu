@@ -1,5 +1,6 @@
 // Host side of the attention step behind mlora.h: the paged KV cache, the rotation, a step's
 // sequences, argument checks and dispatch.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdio>
@@ -65,6 +66,11 @@ struct mlora_rope {
 
 struct mlora_seq {
   SeqView view{};
+  SeqView prefix{};                   // of the pass over shared prefixes: its lists beside the step's
+  int max_groups = 0;
+  bool prefixes = false;              // the last build has such a pass
+  int32_t *skip = nullptr, *group = nullptr;
+  int2* pre_at = nullptr;
   int max_seqs = 0, max_tokens = 0, num_sms = 0;
   int64_t max_blocks = 0;
   void* mem = nullptr;
@@ -244,6 +250,11 @@ mlora_status mlora_rope_destroy(mlora_rope_t r) {
 // ---------------------------------------------------------------- a step's sequences
 mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n_q_heads, int n_kv_heads, int head_dim,
                               mlora_seq_t* out) {
+  return mlora_seq_create_groups(max_seqs, max_tokens, max_pages, n_q_heads, n_kv_heads, head_dim, 0, out);
+}
+
+mlora_status mlora_seq_create_groups(int max_seqs, int max_tokens, int max_pages, int n_q_heads, int n_kv_heads, int head_dim,
+                                     int max_groups, mlora_seq_t* out) {
   if (!out) return fail(MLORA_ERR_INVALID_ARG, "out is NULL");
   *out = nullptr;
   if (max_seqs < 1 || max_seqs > MLORA_MAX_SEQS)
@@ -257,6 +268,8 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
     return fail(MLORA_ERR_INVALID_ARG, "%d query heads must be a multiple of %d key/value heads, both in [1, %d]", n_q_heads, n_kv_heads, MLORA_MAX_HEADS);
   if (n_q_heads / n_kv_heads > 128)
     return fail(MLORA_ERR_INVALID_ARG, "%d query heads for each key/value head, at most 128", n_q_heads / n_kv_heads);
+  if (max_groups < 0 || max_groups > max_seqs)
+    return fail(MLORA_ERR_INVALID_ARG, "max_groups %d outside [0, max_seqs = %d]", max_groups, max_seqs);
   int sms = 0;
   if (mlora_status st = device_sms(&sms)) return st;
   mlora_seq* q = new (std::nothrow) mlora_seq();
@@ -273,9 +286,10 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
   v.hd = head_dim;
   v.row_ctas = 3 * sms;               // at most (mlora_build_seq)
   v.tile_ctas = sms;
-  const size_t S = max_seqs, T = max_tokens;
-  q->max_blocks = static_cast<int64_t>(T) / (2 * v.tile_tokens) + static_cast<int64_t>(S);
-  const size_t J = q->max_blocks;
+  q->max_groups = max_groups;
+  const size_t S = max_seqs, T = max_tokens, N = max_groups;
+  q->max_blocks = most_blocks(v, T, S);
+  const size_t J = q->max_blocks, P = N > 0 ? most_blocks(v, T, N) : 0;      // P: blocks of the prefix pass
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -288,7 +302,12 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
                o_rs = take(S * sizeof(RowSeq)), o_rp = take((S + 1) * 8), o_blk = take(J * sizeof(TileBlk)),
                o_bp = take((J + 1) * 8), o_rsh = take(R * sizeof(RowShare)), o_tsh = take(C * sizeof(int2)), o_tw = take((J * n_kv_heads + C) * sizeof(TileWork)),
                o_there = take(3 * R * 4), o_tj = take(C * sizeof(JoinTask)), o_counts = take(8 * 4),
-               o_err = take(4), o_part = take(row_part_bytes(v)), o_tile_part = take(tile_part_bytes(v));
+               o_err = take(4), o_gap = take(S * 4), o_part = take(row_part_bytes(v)), o_tile_part = take(tile_part_bytes(v));
+  const size_t o_skip = take(N ? S * 4 : 0), o_group = take(N ? S * 4 : 0), o_at = take(N ? S * sizeof(int2) : 0), o_gs = take(N * 4),
+               o_gn = take(N * 4), o_gl = take(N * 4), o_rep = take(N * 4), o_gb = take(N * 4), o_pblk = take(P * sizeof(TileBlk)),
+               o_pbp = take((P + 1) * 8), o_ptsh = take(C * sizeof(int2)), o_ptw = take((P * n_kv_heads + C) * sizeof(TileWork)),
+               o_ptj = take(C * sizeof(JoinTask)), o_pcounts = take(8 * 4),
+               o_pre = take(P * n_kv_heads * 2 * static_cast<size_t>(tile_slot(v)) * 4);
   cudaError_t e = cudaMalloc(&q->mem, at);
   if (e == cudaSuccess) {
     char* b = static_cast<char*>(q->mem);
@@ -313,6 +332,28 @@ mlora_status mlora_seq_create(int max_seqs, int max_tokens, int max_pages, int n
     v.err = reinterpret_cast<uint32_t*>(b + o_err);
     v.row_part = reinterpret_cast<float*>(b + o_part);
     v.tile_part = reinterpret_cast<float*>(b + o_tile_part);
+    v.row_gap = reinterpret_cast<int32_t*>(b + o_gap);
+    if (N > 0) {
+      q->skip = reinterpret_cast<int32_t*>(b + o_skip);
+      q->group = reinterpret_cast<int32_t*>(b + o_group);
+      q->pre_at = reinterpret_cast<int2*>(b + o_at);
+      v.pre_part = reinterpret_cast<float*>(b + o_pre);
+      SeqView& p = q->prefix = v;
+      p.start = reinterpret_cast<int32_t*>(b + o_gs);
+      p.n = reinterpret_cast<int32_t*>(b + o_gn);
+      p.len = reinterpret_cast<int32_t*>(b + o_gl);
+      p.rep = reinterpret_cast<int32_t*>(b + o_rep);
+      p.first_blk = reinterpret_cast<int32_t*>(b + o_gb);
+      p.blk = reinterpret_cast<TileBlk*>(b + o_pblk);
+      p.blk_pre = reinterpret_cast<int64_t*>(b + o_pbp);
+      p.tile_share = reinterpret_cast<int2*>(b + o_ptsh);
+      p.tile_work = reinterpret_cast<TileWork*>(b + o_ptw);
+      p.tile_join = reinterpret_cast<JoinTask*>(b + o_ptj);
+      p.counts = reinterpret_cast<int32_t*>(b + o_pcounts);
+      p.see = kSeePrefix;
+      p.window = INT_MAX;
+      p.sinks = p.gap_unit = p.gap_tile = 0;
+    }
     const int32_t counts[8] = {0, INT32_MAX, 0, 0, 0, 0, 0, 0};
     e = cudaMemset(v.err, 0, 4);
     if (e == cudaSuccess) e = cudaMemcpy(v.counts, counts, sizeof counts, cudaMemcpyHostToDevice);
@@ -338,9 +379,9 @@ mlora_status mlora_seq_destroy(mlora_seq_t q) {
   return MLORA_OK;
 }
 
-mlora_status mlora_build_seq(mlora_seq_t q, const int32_t* q_start, const int32_t* kv_len, const int32_t* pages,
-                             int pages_ld, int n_seqs, int T, int max_new, mlora_kv_t kv, void* stream) {
-  if (!q || !kv) return fail(MLORA_ERR_INVALID_ARG, "seq or cache is NULL");
+static mlora_status build_seq(mlora_seq_t q, const int32_t* q_start, const int32_t* kv_len, const int32_t* pages, int pages_ld,
+                              int n_seqs, int T, int max_new, int window, int sinks, const int32_t* group_start,
+                              const int32_t* prefix_len, int n_groups, mlora_kv_t kv, void* stream) {
   if (n_seqs < 0 || T < 0 || max_new < 0) return fail(MLORA_ERR_INVALID_ARG, "n_seqs %d, T %d and max_new %d must be >= 0", n_seqs, T, max_new);
   if (n_seqs > q->max_seqs || T > q->max_tokens)
     return fail(MLORA_ERR_TOO_MANY_TOKENS, "%d sequences, %d tokens exceed the object's %d and %d", n_seqs, T, q->max_seqs, q->max_tokens);
@@ -359,15 +400,60 @@ mlora_status mlora_build_seq(mlora_seq_t q, const int32_t* q_start, const int32_
   const int64_t most = static_cast<int64_t>(max_new) * v.G;
   v.row_limit = most <= 8 ? 8 : most <= 16 || v.G > 8 ? 16 : 8;
   v.row_ctas = rows_ctas_per_sm(v.row_limit > 8, w.type == kKvE4m3) * q->num_sms;
+  v.see = window > 0 || n_groups > 0 ? kSeeRanges : kSeeAll;
+  v.window = window > 0 ? window : INT_MAX;
+  v.sinks = sinks;
+  v.gap_unit = (sinks + kRowUnit - 1) / kRowUnit;
+  v.gap_tile = (sinks + kTileKeys - 1) / kTileKeys;
+  v.skip = n_groups > 0 ? q->skip : nullptr;
+  v.group = n_groups > 0 ? q->group : nullptr;
+  v.pre_at = n_groups > 0 ? q->pre_at : nullptr;
+  SeqReuse reuse{window, sinks, group_start, prefix_len, n_groups, q->prefix};
+  reuse.prefix.S = n_groups;
+  reuse.prefix.T = T;
+  reuse.prefix.row_limit = v.row_limit;
+  q->prefix = reuse.prefix;
+  q->prefixes = n_groups > 0;
   q->tiles = most > v.row_limit;
   q->page = w.page;
   q->n_pages = w.n_pages;
   q->type = w.type;
-  const cudaError_t e = launch_build_seq(q_start, kv_len, pages, pages_ld, v, max_new, w, s);
+  const cudaError_t e = launch_build_seq(q_start, kv_len, pages, pages_ld, v, max_new, w, reuse, s);
   if (e != cudaSuccess) return report_cuda_error(e, "build_seq launch");
   q->last_stream = s;
   q->built = true;
   return MLORA_OK;
+}
+
+mlora_status mlora_build_seq(mlora_seq_t q, const int32_t* q_start, const int32_t* kv_len, const int32_t* pages,
+                             int pages_ld, int n_seqs, int T, int max_new, mlora_kv_t kv, void* stream) {
+  if (!q || !kv) return fail(MLORA_ERR_INVALID_ARG, "seq or cache is NULL");
+  return build_seq(q, q_start, kv_len, pages, pages_ld, n_seqs, T, max_new, 0, 0, nullptr, nullptr, 0, kv, stream);
+}
+
+mlora_status mlora_build_seq_window(mlora_seq_t q, const int32_t* q_start, const int32_t* kv_len, const int32_t* pages,
+                                    int pages_ld, int n_seqs, int T, int max_new, int window, int sinks, mlora_kv_t kv,
+                                    void* stream) {
+  if (!q || !kv) return fail(MLORA_ERR_INVALID_ARG, "seq or cache is NULL");
+  if (window < 1) return fail(MLORA_ERR_INVALID_ARG, "window %d must be positive", window);
+  if (sinks < 0 || sinks > MLORA_MAX_SINKS) return fail(MLORA_ERR_INVALID_ARG, "sinks %d outside [0, %d]", sinks, MLORA_MAX_SINKS);
+  return build_seq(q, q_start, kv_len, pages, pages_ld, n_seqs, T, max_new, window, sinks, nullptr, nullptr, 0, kv, stream);
+}
+
+mlora_status mlora_build_seq_groups(mlora_seq_t q, const int32_t* q_start, const int32_t* kv_len, const int32_t* pages,
+                                    int pages_ld, int n_seqs, int T, int max_new, const int32_t* group_start,
+                                    const int32_t* prefix_len, int n_groups, int max_prefix, mlora_kv_t kv, void* stream) {
+  if (!q || !kv) return fail(MLORA_ERR_INVALID_ARG, "seq or cache is NULL");
+  if (n_groups < 0 || max_prefix < 0) return fail(MLORA_ERR_INVALID_ARG, "n_groups %d and max_prefix %d must be >= 0", n_groups, max_prefix);
+  if (n_groups > q->max_groups)
+    return fail(MLORA_ERR_TOO_MANY_TOKENS, "%d groups exceed the object's %d", n_groups, q->max_groups);
+  if (n_groups > 0 && (!group_start || !prefix_len)) return fail(MLORA_ERR_INVALID_ARG, "group_start or prefix_len is NULL");
+  // The pass over the prefixes costs two launches; where the groups cannot save the reads that those take, there is none.
+  const KvView& w = kv->view;
+  const int64_t keys = std::min(static_cast<int64_t>(max_prefix), static_cast<int64_t>(q->view.max_pages) * w.page);
+  const int64_t saved = std::max(n_seqs - n_groups, 0) * keys * w.Hkv * 2 * w.hd * (w.type == kKvBf16 ? 2 : 1);
+  if (saved < kShareBytes || T == 0) n_groups = 0;
+  return build_seq(q, q_start, kv_len, pages, pages_ld, n_seqs, T, max_new, 0, 0, group_start, prefix_len, n_groups, kv, stream);
 }
 
 mlora_status mlora_seq_status(mlora_seq_t q) {
@@ -386,6 +472,8 @@ mlora_status mlora_seq_status(mlora_seq_t q) {
   if (err & ptx::kErrWaitTimeout) return fail(MLORA_ERR_DEVICE_TIMEOUT, "a kernel's bounded wait timed out");
   if (err & ptx::kErrBadSeq)
     return fail(MLORA_ERR_BAD_SEQUENCE, "sequence %d: its tokens, length or pages do not hold; it was skipped", first);
+  if (err & ptx::kErrBadGroups)
+    return fail(MLORA_ERR_INVALID_ARG, "the groups' bounds do not ascend within the sequences: none was shared");
   return fail(MLORA_ERR_INVALID_ARG, "a cache read's rows lie outside its output");
 }
 
@@ -435,7 +523,12 @@ mlora_status mlora_attention(mlora_kv_t kv, mlora_seq_t q, const mlora_bf16* que
   if (qa < oa + bytes && oa < qa + bytes) return fail(MLORA_ERR_INVALID_ARG, "query and out must not overlap");
   if (v.T == 0) return MLORA_OK;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_attention_rows(query, out, scale, kv->view, v, s);
+  cudaError_t e = cudaSuccess;
+  if (q->prefixes) {
+    e = launch_attention_tiles(kv->map_k, kv->map_v, query, out, scale, kv->view, q->prefix, s);
+    if (e == cudaSuccess) e = launch_attention_join(out, q->prefix, s);
+  }
+  if (e == cudaSuccess) e = launch_attention_rows(query, out, scale, kv->view, v, s);
   if (e == cudaSuccess && q->tiles) e = launch_attention_tiles(kv->map_k, kv->map_v, query, out, scale, kv->view, v, s);
   if (e == cudaSuccess && q->tiles) e = launch_attention_join(out, v, s);
   if (e != cudaSuccess) return report_cuda_error(e, "attention launch");

@@ -219,7 +219,28 @@ struct alignas(64) Walk {
   int at, last;
 };
 
-template <int HD, bool E4M3>
+// Rows [from, to) of key tile j (of the cache) that no row of an item sees, beside those from the sequence's length on: a
+// window's gap (kSeeRanges). They may lie on pages that are gone: their boxes are not brought.
+__device__ __forceinline__ int2 unseen_rows(const SeqView& v, const TileWork& it, int j) {
+  return make_int2(max(v.sinks - j * kKeys, 0), min(first_seen(it.len - it.n + it.t0, v.window) - j * kKeys, kKeys));
+}
+template <int SEE>
+__device__ __forceinline__ int cache_tile(const SeqView& v, const TileWork& it, int j) {
+  return SEE == kSeeRanges && j >= v.gap_tile ? j + it.gap : j;
+}
+// Whether a value tile has rows to clear: tile j (of the item) holds some that no row of the item sees.
+template <int SEE>
+__device__ __forceinline__ bool short_tile(const SeqView& v, const TileWork& it, int j) {
+  if (SEE == kSeePrefix) return false;
+  const int tile = cache_tile<SEE>(v, it, j);
+  if (SEE == kSeeRanges) {
+    const int2 none = unseen_rows(v, it, tile);
+    if (none.x < none.y) return true;
+  }
+  return (tile + 1) * kKeys > it.len;
+}
+
+template <int HD, bool E4M3, int SEE>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                        const __grid_constant__ CUtensorMap tmap_q, uint16_t* __restrict__ o, float scale_log2, float scale_power, KvView kv,
@@ -324,10 +345,14 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     for (bool go = any; go; go = advance()) {
       const int32_t* table = v.table + static_cast<size_t>(it.seq) * v.max_pages;
       for (int j = it.ka; j < it.kb; ++j) {
-        const int key = j * kKeys + lane * box;
-        const bool mine = lane < boxes && key < it.len;
+        const int key = cache_tile<SEE>(v, it, j) * kKeys + lane * box;
+        bool mine = lane < boxes && key < it.len;
         int at = 0;
-        if (mine) at = ((table[key >> kv.page_log2] * v.Hkv + it.kvh) << kv.page_log2) + (key & (kv.page - 1));
+        if (mine) {
+          const int page = table[key >> kv.page_log2];
+          at = ((page * v.Hkv + it.kvh) << kv.page_log2) + (key & (kv.page - 1));
+          if (SEE == kSeeRanges) mine = page >= 0;
+        }
         const int count = __popc(__ballot_sync(0xffffffffu, mine));
 #pragma unroll
         for (int h = 0; h < 2; ++h, ++n) {            // the keys (and both scales), then the values
@@ -369,7 +394,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     for (bool go = any; go;) {
       const int tok = it.t0 + v.tile_tokens * w + row_tok;
       const bool valid = row_tok < v.tile_tokens && tok < it.n;
-      const int lim = valid ? it.len - it.n + tok : -1;
+      const int lim = !valid ? -1 : SEE == kSeePrefix ? it.len - 1 : it.len - it.n + tok;
       // the fewest and the most keys that a row of the warp sees (rows of no token see none)
       const int low = __reduce_min_sync(0xffffffffu, valid ? lim : INT_MAX), high = __reduce_max_sync(0xffffffffu, lim);
       const int ka = it.ka, end = it.end[w];
@@ -398,13 +423,21 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           }
         }
         const uint64_t cc = pair(c, c);
-        const int seen = lim - j * kKeys, seen_low = low - j * kKeys, seen_high = high - j * kKeys;   // keys 0 .. seen are visible
+        const int first = cache_tile<SEE>(v, it, j) * kKeys;
+        const int seen = lim - first, seen_low = low - first, seen_high = high - first;   // keys 0 .. seen are visible
+        // kSeeRanges: but not keys gone .. from - 1, before the window and behind the first ones
+        const int from = SEE == kSeeRanges && seen >= 0 ? seen - v.window + 1 : 0, gone = SEE == kSeeRanges ? max(v.sinks - first, 0) : 0;
         constexpr int W = 32;                         // columns at a time
         auto mask = [&](uint32_t (&x)[W], int h) {    // of columns W h ...
 #pragma unroll
           for (int i = 0; i < W; ++i) x[i] = W * h + i > seen ? 0xff800000u : x[i];
+          if (SEE == kSeeRanges && gone < from) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) x[i] = W * h + i >= gone && W * h + i < from ? 0xff800000u : x[i];
+          }
         };
-        const bool edge = seen_low < kKeys - 1;       // some row of the warp does not see the whole tile
+        // some row of the warp does not see the whole tile
+        const bool edge = seen_low < kKeys - 1 || (SEE == kSeeRanges && seen_high - v.window >= gone && gone < kKeys);
         auto largest = [&](const uint32_t (&x)[W], float t) {
           float u = __uint_as_float(x[0]);
 #pragma unroll
@@ -563,7 +596,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       }
       n_sc += it.kb - ka;
       // While the last product runs: where the rows go, and the next item.
-      const bool part = it.split != 0 && it.t0 + v.tile_tokens * w < it.n;     // of a split item, to the workspace
+      // of a split item, to the workspace; of a prefix pass, to its block's place, if not there
+      const bool part = (SEE == kSeePrefix || it.split != 0) && it.t0 + v.tile_tokens * w < it.n;
       const float inv = inverse(l);
       const int64_t own = (static_cast<int64_t>(it.start + tok) * v.Hq + it.kvh * v.G + row_head) * HD;
       uint16_t* dst[4];                               // of the rows of the thread's four lanes, where the thread stores
@@ -573,7 +607,24 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         dst[k] = of < 0 ? nullptr : o + of + 16 * (lane & 3);
       }
       float* mine = v.tile_part + ((2 * static_cast<int64_t>(blockIdx.x) + (ka == 0)) * 2 + w) * tile_slot(v);
+      if (SEE == kSeePrefix && it.split == 0) mine = v.pre_part + ((static_cast<int64_t>(it.gap) * v.Hkv + it.kvh) * 2 + w) * tile_slot(v);
+      // (beside sums of the row kernel, or of a call before: from here on by the maximum that the weights' sum goes by)
+      if (SEE != kSeeAll) m -= kUp<E4M3>;
       const bool worked = end > ka;
+      float keep = inv, add = 0.f;                    // O and the sums over the prefix, as shares of the output
+      const float4* pre = nullptr;
+      if (SEE == kSeeRanges && v.pre_at != nullptr && !part && valid) {
+        const int2 at = v.pre_at[it.seq];
+        if (at.x >= 0) {
+          const PreRow p(v, at, it.kvh, tok * v.G + row_head);
+          const float pm = p.top(HD), pl = p.total(HD), up = fmaxf(m, pm);
+          const float f = m == -INFINITY ? 0.f : exp2_approx(m - up), g = pm == -INFINITY ? 0.f : exp2_approx(pm - up);
+          // (a sum over scores that are all -inf is 0, or NaN where one of them is)
+          const float all = inverse((m == -INFINITY ? l : l * f) + (pm == -INFINITY ? pl : pl * g));
+          keep = f * all, add = g * all;
+          pre = reinterpret_cast<const float4*>(p.slot) + p.row;
+        }
+      }
       go = advance();
       if (worked) {
         wait(&o_full[w], n_o & 1);
@@ -604,6 +655,13 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           ptx::tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
+            if (SEE == kSeeRanges && pre != nullptr) {
+              const float4 a = pre[(16 * i + k / 2) * 128], b = pre[(16 * i + 8 + k / 2) * 128];
+              const float2 a2 = k % 2 ? make_float2(a.z, a.w) : make_float2(a.x, a.y), b2 = k % 2 ? make_float2(b.z, b.w) : make_float2(b.x, b.y);
+              z[k] = pack_bf16(fmaf(__uint_as_float(y0[2 * k]), keep, a2.x * add), fmaf(__uint_as_float(y0[2 * k + 1]), keep, a2.y * add));
+              z[16 + k] = pack_bf16(fmaf(__uint_as_float(y1[2 * k]), keep, b2.x * add), fmaf(__uint_as_float(y1[2 * k + 1]), keep, b2.y * add));
+              continue;
+            }
             z[k] = pack_bf16(__uint_as_float(y0[2 * k]) * inv, __uint_as_float(y0[2 * k + 1]) * inv);
             z[16 + k] = pack_bf16(__uint_as_float(y1[2 * k]) * inv, __uint_as_float(y1[2 * k + 1]) * inv);
           }
@@ -627,15 +685,25 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       if (warp == 8) {
         bring();
       } else if (warp == 9) {
-        // value rows past the length, in the one tile of an item that may hold any, when the products have come to it
+        // value rows past the length, in the one tile of an item that may hold any (kSeeRanges: and rows in a window's gap, in up to
+        // two more), when the products have come to it
         uint32_t n = 1, par = 0;                      // ring position of the item's first value tile; tiles so far
-        for (bool go = any; go; go = advance()) {
-          if (it.kb * kKeys > it.len) {
+        for (bool go = any && SEE != kSeePrefix; go; go = advance()) {
+          for (int j = SEE == kSeeAll ? it.kb - 1 : it.ka; j < it.kb; ++j) {
+            if (!short_tile<SEE>(v, it, j)) continue;
             wait(v_short, par);
             par ^= 1;
-            uint8_t* t = smem + C::kRingOff + (n + 2 * (it.kb - 1 - it.ka)) % C::kRing * C::kTile;
-            for (int i = (it.len - (it.kb - 1) * kKeys) * (HD / 8) + lane; i < kKeys * (HD / 8); i += 32)
-              *reinterpret_cast<uint4*>(t + (i % (HD / 8) >> 3) * kHalf + i / (HD / 8) * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            uint8_t* t = smem + C::kRingOff + (n + 2 * (j - it.ka)) % C::kRing * C::kTile;
+            auto clear = [&](int a, int b) {
+              for (int i = a * (HD / 8) + lane; i < b * (HD / 8); i += 32)
+                *reinterpret_cast<uint4*>(t + (i % (HD / 8) >> 3) * kHalf + i / (HD / 8) * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            };
+            const int tile = cache_tile<SEE>(v, it, j);
+            clear(max(min(it.len - tile * kKeys, kKeys), 0), kKeys);
+            if (SEE == kSeeRanges) {
+              const int2 none = unseen_rows(v, it, tile);
+              clear(none.x, none.y);
+            }
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(v_clean);
           }
@@ -654,7 +722,10 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       uint32_t n = 0;
       for (bool go = any; go; go = advance()) {
         for (int j = it.ka; j < it.kb; ++j) {
-          const int cut = it.len - j * kKeys;         // rows of the tile inside the sequence (any number)
+          const int tile = cache_tile<SEE>(v, it, j);
+          const int cut = it.len - tile * kKeys;      // rows of the tile inside the sequence (any number)
+          const int2 none_seen = SEE == kSeeRanges ? unseen_rows(v, it, tile) : make_int2(0, 0);
+          auto outside = [&](int r) { return r >= cut || (SEE == kSeeRanges && r >= none_seen.x && r < none_seen.y); };
 #pragma unroll 1
           for (int h = 0; h < 2; ++h, ++n) {
             const int st = n % C::kRing, cs = n % C::kStages;
@@ -663,7 +734,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               // the tile's largest scales, and every row's share of them. A row with a NaN scale is NaN in its
               // scores alone: its values would reach rows that do not see it.
               const float* rw = reinterpret_cast<const float*>(smem + C::kRawScaleOff) + cs * 2 * kKeys + tid;
-              float ks = tid < cut ? rw[0] : 0.f, vs = tid < cut ? rw[kKeys] : 0.f;
+              float ks = outside(tid) ? 0.f : rw[0], vs = outside(tid) ? 0.f : rw[kKeys];
               const bool none = !(fabsf(ks) < kMostScale) || !(fabsf(vs) < kMostScale);
               if (none) ks = vs = 0.f;
               float km = fabsf(ks), vm = vs;
@@ -718,7 +789,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                   uint4 y = scaled(cd[i][x].x, cd[i][x].y, f[i]);
-                  if (r >= cut) y = make_uint4(0u, 0u, 0u, 0u);
+                  if (outside(r)) y = make_uint4(0u, 0u, 0u, 0u);
                   *reinterpret_cast<uint4*>(dst + r * 128 + (((even + (x ^ (odd ? 1 : 0))) ^ (r & 7)) * 16)) = y;
                 }
               }
@@ -741,9 +812,12 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         int at = any ? walk.at : 0, len = it.len;
         const int last = any ? walk.last : -1;
         int4 next = *reinterpret_cast<const int4*>(&it);
+        TileWork now;                                 // kSeeRanges, bf16: what short_tile() reads
+        constexpr bool kGaps = !E4M3 && SEE == kSeeRanges;
         while (at <= last) {
           const int ka = next.x, kb = next.y, end0 = next.z, end1 = next.w;
-          const bool short_tile = !E4M3 && kb * kKeys > len;
+          const bool short_last = !E4M3 && SEE == kSeeAll && kb * kKeys > len;
+          if (kGaps) now = v.tile_work[at];
           if (++at <= last) {                         // the next item, long before it is wanted
             next = *reinterpret_cast<const int4*>(v.tile_work + at);
             len = v.tile_work[at].len;
@@ -756,7 +830,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               if (++ks == C::kRing) ks = 0, ks_par ^= 1;
               wait(&kv_full[vs], vs_par);
               if (dead) break;
-              if (short_tile && j == kb) {
+              if ((short_last && j == kb) || (kGaps && short_tile<SEE>(v, now, j - 1))) {
                 ptx::mbar_arrive(v_short);
                 wait(v_clean, clean_par);
                 clean_par ^= 1;
@@ -873,13 +947,13 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
   }
 }
 
-template <int HD, bool E4M3>
-cudaError_t launch_as(const CUtensorMap& tk, const CUtensorMap& tv, const uint16_t* q, uint16_t* o, float scale_log2,
+template <int HD, bool E4M3, int SEE>
+cudaError_t launch_seeing(const CUtensorMap& tk, const CUtensorMap& tv, const uint16_t* q, uint16_t* o, float scale_log2,
                       const KvView& kv, const SeqView& s, cudaStream_t st) {
   CUtensorMap tq;
   if (!make_tmap_heads_bf16(&tq, q, s.T, s.Hq, HD, s.tile_tokens, s.G)) return cudaErrorInvalidValue;
   using C = TilesCfg<HD, E4M3>;
-  if (cudaError_t e = allow_shared_memory<attention_tiles_kernel<HD, E4M3>>(C::kBytes)) return e;
+  if (cudaError_t e = allow_shared_memory<attention_tiles_kernel<HD, E4M3, SEE>>(C::kBytes)) return e;
   // e4m3: an unusual scale's power of two goes with the query rows, so that the keys' factors are normal numbers
   float power = 1.0f;
   if (E4M3 && !(scale_log2 > 0x1p-16f && scale_log2 < 0x1p16f)) power = std::ldexp(1.0f, std::max(-126, std::ilogb(scale_log2)));
@@ -893,10 +967,18 @@ cudaError_t launch_as(const CUtensorMap& tk, const CUtensorMap& tv, const uint16
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_tiles_kernel<HD, E4M3>, tk, tv, tq, o, scale_log2 / power, power, kv, s);
+  cfg.numAttrs = SEE == kSeePrefix ? 0 : 1;           // (the prefix pass comes first in a step)
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_tiles_kernel<HD, E4M3, SEE>, tk, tv, tq, o, scale_log2 / power, power, kv, s);
   note_launch_end(kKindAttn, st);
   return e;
+}
+
+template <int HD, bool E4M3>
+cudaError_t launch_as(const CUtensorMap& tk, const CUtensorMap& tv, const uint16_t* q, uint16_t* o, float scale_log2,
+                      const KvView& kv, const SeqView& s, cudaStream_t st) {
+  return s.see == kSeeAll      ? launch_seeing<HD, E4M3, kSeeAll>(tk, tv, q, o, scale_log2, kv, s, st)
+         : s.see == kSeeRanges ? launch_seeing<HD, E4M3, kSeeRanges>(tk, tv, q, o, scale_log2, kv, s, st)
+                               : launch_seeing<HD, E4M3, kSeePrefix>(tk, tv, q, o, scale_log2, kv, s, st);
 }
 
 }  // namespace

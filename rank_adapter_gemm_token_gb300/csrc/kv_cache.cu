@@ -258,7 +258,7 @@ kv_read_kernel(const int32_t* __restrict__ row_start, int64_t rows, uint16_t* __
       const bool fits = dst >= 0 && dst + cnt <= rows;
       if (!fits && lane == 0) atomicOr(s.err, ptx::kErrBadRow);
       for (; h < kv.Hkv && u < end; ++h, ++u) {
-        if (!fits) continue;
+        if (!fits || page < 0) continue;                  // (a page that has gone out of every window)
         const int64_t at = (page * kv.Hkv + h) << kv.page_log2;
         for (int b = r0; b < cnt; b += kStep * kAhead) {
           uint4 a[kAhead], c[kAhead];

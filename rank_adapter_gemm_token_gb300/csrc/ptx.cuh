@@ -15,6 +15,7 @@ constexpr uint32_t kErrShape = 1u << 2;         // a launch saw sizes it cannot 
 constexpr uint32_t kErrBadId = 1u << 3;         // a token id outside the embedding table
 constexpr uint32_t kErrBadSeq = 1u << 4;        // a sequence's bounds or page table do not hold
 constexpr uint32_t kErrBadRow = 1u << 5;        // a cache read's rows lie outside its output
+constexpr uint32_t kErrBadGroups = 1u << 6;     // the bounds of a step's groups do not ascend within its sequences
 
 // A wait gives up after this many nanoseconds of %globaltimer (2 s): far above any
 // legitimate wait of these kernels, short enough to leave the GPU usable.

@@ -5,10 +5,13 @@
 //           copied into the step's own storage, so that the caller's may change as soon as this kernel
 //           has run. A sequence that fails is skipped
 //           (length 0: nothing is read or written for it, its rows of the attention are zero) and
-//           recorded;
+//           recorded. With a window, pages that none of a sequence's new tokens sees are neither checked nor kept (-1).
+//           Where groups share prefixes, a sequence's first pages are compared with those of its group's first sequence: a
+//           group is no more than a hint, and a sequence that does not share its prefix is attended by itself;
 //   plan    blocks 0 and 1: the work of the row kernel and of the tile kernel as prefix sums, over which their CTAs take
-//           equal shares, or whole items dealt out, where there are enough (tile kernel, whose CTAs get lists); the other
-//           blocks: sequence, position and cache row of each token.
+//           equal shares, or whole items dealt out, where there are enough (tile kernel, whose CTAs get lists); with groups,
+//           block 2: the same for the pass over their prefixes; the other blocks: sequence, position and cache row of each
+//           token.
 // Bound by latency: a few dependent loads, block scans and searches; the table is read once. Measured on the GPU: 7.4 us for 256
 // single tokens, 9.8 with four chunks beside them, 25 for 300 prompts of 100 tokens (4800 items), once for all layers of a step.
 #include <algorithm>
@@ -31,7 +34,8 @@ constexpr int kPlanPre = kMapSeqs / 2;   // prefix sums kept there by the plan
 
 __global__ void __launch_bounds__(kCheckThreads)
 check_seq_kernel(const int32_t* __restrict__ q_start, const int32_t* __restrict__ kv_len,
-                 const int32_t* __restrict__ pages, int table_ld, SeqView v, int max_new, int n_pages, int page_log2) {
+                 const int32_t* __restrict__ pages, int table_ld, SeqView v, int max_new, int n_pages, int page_log2,
+                 const int32_t* __restrict__ group_start, const int32_t* __restrict__ prefix_len, int n_groups) {
   constexpr int kSeqs = kCheckThreads / 32;
   __shared__ int32_t tops[kSeqs];
   ptx::grid_dependents_launch();
@@ -52,12 +56,42 @@ check_seq_kernel(const int32_t* __restrict__ q_start, const int32_t* __restrict_
             static_cast<int64_t>(L) <= static_cast<int64_t>(v.max_pages) * page && (L == 0 || L >= b - a);
   const int used = ok ? (L + page - 1) >> page_log2 : 0;
   bool fine = true;
+  const int first = ok ? first_seen(L - (b - a), v.window) : 0;      // of the first new token, or of the next one
   for (int i = lane; i < used; i += 32) {
-    const int p = pages[static_cast<size_t>(s) * table_ld + i];
-    fine = fine && p >= 0 && p < n_pages;
+    int p = pages[static_cast<size_t>(s) * table_ld + i];
+    if (static_cast<int64_t>(i) << page_log2 >= v.sinks && static_cast<int64_t>(i + 1) << page_log2 <= first)
+      p = -1;                            // (without a window, first is 0)
+    else
+      fine = fine && p >= 0 && p < n_pages;
     v.table[static_cast<size_t>(s) * v.max_pages + i] = p;
   }
   ok = __all_sync(0xffffffffu, fine) && ok;
+  if (n_groups > 0) {
+    bool ascend = true;
+    int g = -1;
+    for (int i = lane; i < n_groups; i += 32) {
+      const int g0 = group_start[i], g1 = group_start[i + 1];
+      ascend = ascend && g0 >= 0 && g0 <= g1 && g1 <= v.S;
+      if (g0 <= s && s < g1) g = i;
+    }
+    ascend = __all_sync(0xffffffffu, ascend);
+    g = ascend ? __reduce_max_sync(0xffffffffu, g) : -1;
+    int keys = 0;                        // of the prefix, in whole pages and key tiles
+    if (g >= 0 && ok && b > a) {
+      const int leader = group_start[g], whole = max(page, kTileKeys);
+      if (group_start[g + 1] - leader >= kShareSeqs) keys = max(prefix_len[g], 0) / whole * whole;
+      if (keys > L - (b - a)) keys = 0;  // not cached yet, or not seen by the first new token
+      bool same = true;
+      for (int i = lane; i < keys >> page_log2; i += 32)
+        same = same && pages[static_cast<size_t>(s) * table_ld + i] == pages[static_cast<size_t>(leader) * table_ld + i];
+      if (!__all_sync(0xffffffffu, same)) keys = 0;
+    }
+    if (lane == 0) {
+      v.skip[s] = keys;
+      v.group[s] = g;
+      if (!ascend) atomicOr(v.err, ptx::kErrBadGroups);
+    }
+  }
   if (lane == 0) {
     v.start[s] = ok ? a : 0;
     v.n[s] = ok ? b - a : 0;
@@ -159,12 +193,13 @@ __device__ __forceinline__ void put_work(const SeqView& v, int64_t place, const 
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     const int from = b.t0 + v.tile_tokens * w, last = min(from + v.tile_tokens, b.n) - 1;
-    end[w] = from < b.n ? max(ka, min(kb, (b.len - b.n + last) / kTileKeys + 1)) : ka;
+    const int seen = v.see == kSeePrefix ? b.tiles : (b.len - b.n + last) / kTileKeys + 1 - b.gap;
+    end[w] = from < b.n ? max(ka, min(kb, seen)) : ka;
   }
   int4* to = reinterpret_cast<int4*>(v.tile_work + place);
   to[0] = make_int4(ka, kb, end[0], end[1]);
   to[1] = make_int4(b.len, b.n, b.start, b.t0);
-  to[2] = make_int4(b.seq, kvh, ka > 0 || kb < b.tiles, 0);
+  to[2] = make_int4(b.seq, kvh, ka > 0 || kb < b.tiles, b.gap);
 }
 static_assert(sizeof(TileWork) == 48 && offsetof(TileWork, len) == 16 && offsetof(TileWork, seq) == 32, "written in this order");
 
@@ -212,7 +247,7 @@ __device__ __forceinline__ void share_out(const SeqView& v, const int64_t* pre, 
 
 // The row kernel's work, or the tile kernel's (TILES).
 template <bool TILES>
-__device__ void plan(const SeqView& v, int page_log2, int64_t* pre, int64_t* cuts) {
+__device__ __forceinline__ void plan(const SeqView& v, int page_log2, int64_t* pre, int64_t* cuts) {
   __shared__ int64_t sums[4][32];
   __shared__ int joins;                           // split items so far (their order in the lists does not matter)
   __shared__ int most, deepest;                   // key tiles of the largest block; units of the fullest hands
@@ -222,9 +257,13 @@ __device__ void plan(const SeqView& v, int page_log2, int64_t* pre, int64_t* cut
     const int s = s0 + threadIdx.x;
     const int n = s < v.S ? v.n[s] : 0, L = s < v.S ? v.len[s] : 0, start = s < v.S ? v.start[s] : 0;
     const int64_t rows = static_cast<int64_t>(n) * v.G;
-    const bool some = rows > 0 && L > 0, few = rows <= v.row_limit;
+    const bool some = rows > 0 && L > 0, few = v.see != kSeePrefix && rows <= v.row_limit;
     const int per = 2 * v.tile_tokens;              // tokens of a block
-    const int64_t u = some && few ? kRowHead + (L + kRowUnit - 1) / kRowUnit : 0;
+    const int skip = v.skip != nullptr && v.see == kSeeRanges && s < v.S ? v.skip[s] : 0;
+    // units, or tiles of `size` keys, that the rows from position p on do not see
+    auto gap = [&](int p, int keys, int size, int from) { return keys > 0 ? keys / size : max(0, first_seen(p, v.window) / size - from); };
+    const int row_gap = v.see == kSeeRanges ? gap(L - n, skip, kRowUnit, v.gap_unit) : 0;
+    const int64_t u = some && few ? kRowHead + (L + kRowUnit - 1) / kRowUnit - row_gap : 0;
     const int64_t b = some && !few ? (n + per - 1) / per : 0;
     int64_t x[4] = {u, u > 0, (static_cast<int64_t>(L) + (1 << page_log2) - 1) >> page_log2, b}, t[4];
     block_scan(x, sums, t);
@@ -233,6 +272,7 @@ __device__ void plan(const SeqView& v, int page_log2, int64_t* pre, int64_t* cut
       const int64_t e = entries + x[1];
       v.row_seq[e - 1] = RowSeq{s, n, L, start};
       v.row_pre[e] = (units + x[0]) * v.Hkv;
+      if (v.see == kSeeRanges) v.row_gap[e - 1] = row_gap;
     }
     // the chunk's tile blocks, a warp for each sequence
     const int64_t first = blocks + x[3] - b;
@@ -241,11 +281,20 @@ __device__ void plan(const SeqView& v, int page_log2, int64_t* pre, int64_t* cut
       const int i = __ffs(has) - 1;
       has &= has - 1;
       const int nb = static_cast<int>(__shfl_sync(0xffffffffu, b, i)), bn = __shfl_sync(0xffffffffu, n, i),
-                bl = __shfl_sync(0xffffffffu, L, i), bstart = __shfl_sync(0xffffffffu, start, i);
+                bl = __shfl_sync(0xffffffffu, L, i), bstart = __shfl_sync(0xffffffffu, start, i),
+                bskip = __shfl_sync(0xffffffffu, skip, i);
       const int64_t f = __shfl_sync(0xffffffffu, first, i);
+      const int bs = s0 + warp * 32 + i;
+      if (v.see == kSeePrefix) {
+        if (lane == 0) v.first_blk[bs] = static_cast<int32_t>(f);
+        for (int k = lane; k < nb; k += 32)
+          v.blk[f + k] = TileBlk{v.rep[bs], bn, bl, bstart, k * per, bl / kTileKeys, static_cast<int32_t>(f + k)};
+        continue;
+      }
       for (int k = lane; k < nb; k += 32) {
-        const int tiles = (bl - bn + min((k + 1) * per, bn) - 1) / kTileKeys + 1;
-        v.blk[f + k] = TileBlk{s0 + warp * 32 + i, bn, bl, bstart, k * per, tiles};
+        const int bgap = v.see == kSeeRanges ? gap(bl - bn + k * per, bskip, kTileKeys, v.gap_tile) : 0;
+        const int tiles = (bl - bn + min((k + 1) * per, bn) - 1) / kTileKeys + 1 - bgap;
+        v.blk[f + k] = TileBlk{bs, bn, bl, bstart, k * per, tiles, bgap};
       }
     }
     units += t[0];
@@ -369,29 +418,75 @@ __device__ void plan(const SeqView& v, int page_log2, int64_t* pre, int64_t* cut
   if (threadIdx.x == 0) v.counts[2] = joins;
 }
 
+// The prefix pass's work: its groups' tokens (from the first to the last sequence that shares the prefix; what lies between
+// comes along), before their list is made; and after it where each sequence's sums will lie.
+__device__ __forceinline__ void groups_as_sequences(const SeqView& v, const SeqView& p, const int32_t* group_start) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int g = warp; g < p.S; g += kPlanThreads / 32) {
+    int count = 0, keys = 0, rep = INT_MAX, from = INT_MAX, to = 0;
+    const int g1 = min(group_start[g + 1], v.S);
+    for (int s = max(group_start[g], 0) + lane; s < g1; s += 32) {
+      if (v.skip[s] == 0 || v.group[s] != g) continue;
+      ++count;
+      keys = v.skip[s];                             // (the same for all of them)
+      rep = min(rep, s);
+      from = min(from, v.start[s]);
+      to = max(to, v.start[s] + v.n[s]);
+    }
+    count = __reduce_add_sync(0xffffffffu, count);
+    keys = __reduce_max_sync(0xffffffffu, keys);
+    rep = __reduce_min_sync(0xffffffffu, rep);
+    from = __reduce_min_sync(0xffffffffu, from);
+    to = __reduce_max_sync(0xffffffffu, to);
+    if (lane == 0) {
+      p.start[g] = count > 0 ? from : 0;
+      p.n[g] = count > 0 ? to - from : 0;
+      p.len[g] = count > 0 ? keys : 0;
+      p.rep[g] = count > 0 ? rep : 0;
+    }
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ void places_of_sums(const SeqView& v, const SeqView& p) {
+  __syncthreads();
+  for (int s = threadIdx.x; s < v.S; s += kPlanThreads) {
+    const int g = v.skip[s] > 0 ? v.group[s] : -1;
+    v.pre_at[s] = g >= 0 ? make_int2(p.first_blk[g], v.start[s] - p.start[g]) : make_int2(-1, 0);
+  }
+}
+
+template <bool GROUPS>
 __global__ void __launch_bounds__(kPlanThreads)
-plan_seq_kernel(const int32_t* __restrict__ q_start, SeqView v, int page_log2) {
+plan_seq_kernel(const int32_t* __restrict__ q_start, const __grid_constant__ SeqView v, int page_log2,
+                const int32_t* __restrict__ group_start, const __grid_constant__ SeqView p) {
   __shared__ alignas(16) int32_t begin[kMapSeqs + 1];
   __shared__ int64_t cuts[kPlanThreads];
   const int S = v.S;
+  constexpr int planners = GROUPS ? 3 : 2;
   bool falls = false;
-  if (blockIdx.x > 1)
+  if (static_cast<int>(blockIdx.x) >= planners)
     for (int i = threadIdx.x; i <= S && S > 0; i += kPlanThreads) {
       begin[i] = q_start[i];
       falls = falls || (i > 0 && q_start[i - 1] > begin[i]);
     }
   ptx::grid_dependency_wait();        // the check's results
-  if (blockIdx.x < 2) {
+  if (static_cast<int>(blockIdx.x) < planners) {
     int64_t* pre = reinterpret_cast<int64_t*>(begin);
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0) {
       plan<false>(v, page_log2, pre, cuts);
-    else
+    } else if (!GROUPS) {
       plan<true>(v, page_log2, pre, cuts);
+    } else {
+      const bool prefixes = blockIdx.x == 2;
+      if (prefixes) groups_as_sequences(v, p, group_start);
+      plan<true>(prefixes ? p : v, page_log2, pre, cuts);
+      if (prefixes) places_of_sums(v, p);
+    }
     return;
   }
   // Starts that fall somewhere: their running maximum takes their place, which is an accepted sequence's own start and its end.
   if (__syncthreads_or(falls)) running_max(begin, S + 1, reinterpret_cast<int32_t*>(cuts));
-  const int t = (blockIdx.x - 2) * kPlanThreads + threadIdx.x;
+  const int t = (blockIdx.x - planners) * kPlanThreads + threadIdx.x;
   if (t >= v.T) return;
   int lo = 0, hi = S;                 // the last s with begin[s] <= t
   while (hi - lo > 1) {
@@ -416,17 +511,17 @@ plan_seq_kernel(const int32_t* __restrict__ q_start, SeqView v, int page_log2) {
 }  // namespace
 
 cudaError_t launch_build_seq(const int32_t* q_start, const int32_t* kv_len, const int32_t* pages, int table_ld,
-                             const SeqView& s, int max_new, const KvView& kv, cudaStream_t st) {
+                             const SeqView& s, int max_new, const KvView& kv, const SeqReuse& reuse, cudaStream_t st) {
   const int check = std::max(1, (s.S + kCheckThreads / 32 - 1) / (kCheckThreads / 32));
   note_launch_begin(kKindSeq, st);
   check_seq_kernel<<<check, kCheckThreads, 0, st>>>(q_start, kv_len, pages, table_ld, s, max_new, kv.n_pages,
-                                                    kv.page_log2);
+                                                    kv.page_log2, reuse.group_start, reuse.prefix_len, reuse.n_groups);
   cudaError_t e = cudaGetLastError();
   note_launch_end(kKindSeq, st);
   if (e != cudaSuccess) return e;
   note_launch_begin(kKindSeq, st);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 + (s.T + kPlanThreads - 1) / kPlanThreads);
+  cfg.gridDim = dim3((reuse.n_groups > 0 ? 3 : 2) + (s.T + kPlanThreads - 1) / kPlanThreads);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
@@ -434,7 +529,8 @@ cudaError_t launch_build_seq(const int32_t* q_start, const int32_t* kv_len, cons
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, plan_seq_kernel, q_start, s, kv.page_log2);
+  e = reuse.n_groups > 0 ? cudaLaunchKernelEx(&cfg, plan_seq_kernel<true>, q_start, s, kv.page_log2, reuse.group_start, reuse.prefix)
+                         : cudaLaunchKernelEx(&cfg, plan_seq_kernel<false>, q_start, s, kv.page_log2, reuse.group_start, reuse.prefix);
   note_launch_end(kKindSeq, st);
   return e;
 }

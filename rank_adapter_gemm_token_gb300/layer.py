@@ -283,24 +283,45 @@ class Rope:
 
 class SeqMeta:
     """One step's sequences (token rows, cached lengths, page tables) and the attention's workspace, for layers of
-    n_q_heads query heads over n_kv_heads key/value heads."""
+    n_q_heads query heads over n_kv_heads key/value heads; max_groups: groups of sequences behind a shared prefix that a step
+    may have."""
 
-    def __init__(self, max_seqs: int, max_tokens: int, max_pages: int, n_q_heads: int, n_kv_heads: int, head_dim: int):
+    def __init__(self, max_seqs: int, max_tokens: int, max_pages: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                 max_groups: int = 0):
         self.n_q_heads, self.n_kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
         self.device = torch.device("cuda", torch.cuda.current_device())
-        self.handle = mlora.mlora_seq_create(max_seqs, max_tokens, max_pages, n_q_heads, n_kv_heads, head_dim)
+        self.handle = mlora.mlora_seq_create_groups(max_seqs, max_tokens, max_pages, n_q_heads, n_kv_heads, head_dim, max_groups)
         self.T = 0
         self.n_seqs = 0
 
     def build(self, q_start: torch.Tensor, kv_len: torch.Tensor, pages: torch.Tensor, T: int, cache: KVCache,
-              max_new: int, stream=None) -> None:
-        """q_start int32 [n_seqs + 1], kv_len int32 [n_seqs], pages int32 [n_seqs, >= max_pages], all on the GPU."""
+              max_new: int, stream=None, window: int | None = None, sinks: int = 0, group_start: torch.Tensor | None = None,
+              prefix_len: torch.Tensor | None = None, max_prefix: int | None = None) -> None:
+        """q_start int32 [n_seqs + 1], kv_len int32 [n_seqs], pages int32 [n_seqs, >= max_pages], all on the GPU.
+        window, sinks: a token sees the last `window` positions, its own among them, and the first `sinks` ones; pages without
+        any that a new token sees may be gone. group_start int32 [n_groups + 1], prefix_len int32 [n_groups], on the GPU:
+        sequences group_start[g] .. group_start[g + 1] - 1 have the pages of their first prefix_len[g] (at most max_prefix)
+        positions in common. A step has a window or groups, not both."""
         for x in (q_start, kv_len, pages):
             assert x.is_cuda and x.dtype == torch.int32 and x.is_contiguous()
         n = kv_len.shape[0]
         assert q_start.shape == (n + 1,) and pages.dim() == 2 and pages.shape[0] == n
-        mlora.mlora_build_seq(self.handle, q_start, kv_len, pages, pages.shape[1], n, T, max_new, cache.handle,
-                              _raw_stream(stream, self.device))
+        args = self.handle, q_start, kv_len, pages, pages.shape[1], n, T, max_new
+        s = _raw_stream(stream, self.device)
+        if group_start is not None:
+            assert window is None and sinks == 0 and prefix_len is not None
+            for x in (group_start, prefix_len):
+                assert x.is_cuda and x.dtype == torch.int32 and x.is_contiguous()
+            groups = prefix_len.numel()
+            assert group_start.shape == (groups + 1,) and prefix_len.dim() == 1
+            bound = (1 << 31) - 1 if max_prefix is None else max_prefix
+            mlora.mlora_build_seq_groups(*args, group_start, prefix_len, groups, bound, cache.handle, s)
+        elif window is not None:
+            assert prefix_len is None and max_prefix is None
+            mlora.mlora_build_seq_window(*args, window, sinks, cache.handle, s)
+        else:
+            assert sinks == 0 and prefix_len is None and max_prefix is None
+            mlora.mlora_build_seq(*args, cache.handle, s)
         self.T, self.n_seqs = T, n
 
     def status(self) -> None:

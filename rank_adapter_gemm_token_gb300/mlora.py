@@ -29,6 +29,8 @@ MLORA_ERR_NO_FREE_SLOT = 11
 MLORA_ERR_BAD_TOKEN_ID = 12
 MLORA_ERR_BAD_SEQUENCE = 13
 
+MLORA_MAX_SINKS = 1048576
+
 MLORA_KV_BF16 = 0
 MLORA_KV_E4M3 = 1
 MLORA_ACT_SILU = 0
@@ -58,7 +60,7 @@ EXPORTS = (
     "mlora_kv_create", "mlora_kv_destroy", "mlora_kv_info", "mlora_kv_bytes", "mlora_rope_frequencies",
     "mlora_rope_create", "mlora_rope_destroy", "mlora_seq_create", "mlora_seq_destroy", "mlora_build_seq",
     "mlora_seq_status", "mlora_qkv_write", "mlora_attention", "mlora_kv_read",
-    "mlora_gated_linear", "mlora_gated_workspace_bytes",
+    "mlora_seq_create_groups", "mlora_build_seq_window", "mlora_build_seq_groups", "mlora_gated_linear", "mlora_gated_workspace_bytes",
 )
 
 
@@ -141,6 +143,9 @@ def load(path: str | None = None):
             "mlora_seq_create": [i32, i32, i32, i32, i32, i32, vp],
             "mlora_seq_destroy": [vp],
             "mlora_build_seq": [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp],
+            "mlora_seq_create_groups": [i32, i32, i32, i32, i32, i32, i32, vp],
+            "mlora_build_seq_window": [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp],
+            "mlora_build_seq_groups": [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, i32, vp, vp],
             "mlora_seq_status": [vp],
             "mlora_qkv_write": [vp, vp, vp, i64, vp, vp, f32, vp, vp, vp, vp],
             "mlora_attention": [vp, vp, vp, f32, vp, vp],
@@ -427,6 +432,14 @@ def mlora_seq_create(max_seqs: int, max_tokens: int, max_pages: int, n_q_heads: 
     return out.value
 
 
+def mlora_seq_create_groups(max_seqs: int, max_tokens: int, max_pages: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                            max_groups: int) -> int:
+    out = ctypes.c_void_p()
+    _check(load().mlora_seq_create_groups(max_seqs, max_tokens, max_pages, n_q_heads, n_kv_heads, head_dim, max_groups,
+                                          ctypes.byref(out)), "mlora_seq_create_groups")
+    return out.value
+
+
 def mlora_seq_destroy(seq: int) -> None:
     _check(load().mlora_seq_destroy(seq), "mlora_seq_destroy")
 
@@ -435,6 +448,19 @@ def mlora_build_seq(seq: int, q_start, kv_len, pages, pages_ld: int, n_seqs: int
                     stream=None) -> None:
     _check(load().mlora_build_seq(seq, _ptr(q_start), _ptr(kv_len), _ptr(pages), pages_ld, n_seqs, T, max_new, kv,
                                   _stream(stream)), "mlora_build_seq")
+
+
+def mlora_build_seq_window(seq: int, q_start, kv_len, pages, pages_ld: int, n_seqs: int, T: int, max_new: int, window: int,
+                           sinks: int, kv: int, stream=None) -> None:
+    _check(load().mlora_build_seq_window(seq, _ptr(q_start), _ptr(kv_len), _ptr(pages), pages_ld, n_seqs, T, max_new, window,
+                                         sinks, kv, _stream(stream)), "mlora_build_seq_window")
+
+
+def mlora_build_seq_groups(seq: int, q_start, kv_len, pages, pages_ld: int, n_seqs: int, T: int, max_new: int, group_start,
+                           prefix_len, n_groups: int, max_prefix: int, kv: int, stream=None) -> None:
+    _check(load().mlora_build_seq_groups(seq, _ptr(q_start), _ptr(kv_len), _ptr(pages), pages_ld, n_seqs, T, max_new,
+                                         _ptr(group_start), _ptr(prefix_len), n_groups, max_prefix, kv, _stream(stream)),
+           "mlora_build_seq_groups")
 
 
 def mlora_seq_status(seq: int) -> None:

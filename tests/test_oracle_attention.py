@@ -121,3 +121,23 @@ def test_refusals_need_no_device(mlora):
     assert mlora.mlora_kv_bytes(10, 16, 8, 128, 0) == 2 * 10 * 16 * 8 * 128 * 2
     assert mlora.mlora_kv_bytes(10, 16, 8, 128, 1) == 2 * 10 * 16 * 8 * (128 + 4)
     assert mlora.mlora_kv_bytes(10, 17, 8, 128, 1) == 0
+
+
+def test_window_and_first_tokens():
+    """Which keys a token sees, by hand; a window as long as the sequence changes nothing; and the attention over a window is
+    that over the seen rows alone."""
+    assert ref.seen_keys(0, 1, 0).tolist() == [0]
+    assert ref.seen_keys(5, 2, 0).tolist() == [4, 5]
+    assert ref.seen_keys(5, 2, 1).tolist() == [0, 4, 5]
+    assert ref.seen_keys(5, 3, 4).tolist() == [0, 1, 2, 3, 4, 5]
+    assert ref.seen_keys(2, 9, 1).tolist() == [0, 1, 2]
+    assert ref.seen_keys(3, 1, 9).tolist() == [0, 1, 2, 3]
+    rng = np.random.default_rng(0)
+    k, v, q = rng.standard_normal((9, 1, 4)), rng.standard_normal((9, 1, 4)), rng.standard_normal((2, 2, 4))
+    whole = ref.attention(q, [k], [v], [0, 2], 2, 0.5)
+    for a, b in zip(whole, ref.attention(q, [k], [v], [0, 2], 2, 0.5, window=9, sinks=3)):
+        assert np.array_equal(a, b)
+    rows = [0, 1, 6, 7, 8]
+    got = ref.attention(q[1:], [k], [v], [0, 1], 2, 0.5, window=3, sinks=2)[0]
+    want = ref.attention(q[1:], [k[rows]], [v[rows]], [0, 1], 2, 0.5)[0]
+    assert np.allclose(got, want, rtol=1e-14)
