@@ -57,9 +57,9 @@ struct JoinTask {
 // Which keys the rows of a step's sequences see, as the kernels are compiled for it:
 //   kSeeAll     a row at position p all keys up to p;
 //   kSeeRanges  with a window, keys j <= p with j < sinks or j > p - window; behind a shared prefix, keys up to p from the end of
-//               the prefix on, the rows' sums over the prefix's keys joined from SeqView::pre_part. The units (key tiles) of a
+//               the prefix on, the rows' sums over the prefix's keys joined from SeqView::pre_part. The chunks (key tiles) of a
 //               sequence that some row sees are counted without the gap between the first ones and the window (or without
-//               the prefix): unit u is unit u + gap of the cache from gap_unit on (key tile: from gap_tile on);
+//               the prefix): chunk c is chunk c + gap of the cache from gap_chunk on (key tile: from gap_tile on);
 //   kSeePrefix  the pass over the shared prefixes: a "sequence" is a group, every row of it sees all `len` keys, a multiple
 //               of kTileKeys, and its sums go to pre_part.
 constexpr int kSeeAll = 0, kSeeRanges = 1, kSeePrefix = 2;
@@ -86,7 +86,7 @@ struct SeqView {
   JoinTask* tile_join;  // [counts[2]] the tile kernel's split items
   int32_t* counts;      // [1] first rejected sequence (INT32_MAX if none), [2] split items
   uint32_t* err;        // device error word (ptx::kErr* bits)
-  int32_t* row_gap;     // [S] kSeeRanges: gap of each of the row kernel's sequences, in units
+  int32_t* row_gap;     // [S] kSeeRanges: gap of each of the row kernel's sequences, in chunks
   int32_t* skip;        // [S] keys of each sequence that its group's prefix pass takes (0: none)
   int32_t* group;       // [S] its group
   int2* pre_at;         // [S] first block of its group in the prefix pass (-1: none), its first token among the group's
@@ -101,7 +101,7 @@ struct SeqView {
   int row_ctas, tile_ctas;
   int see;              // kSee*
   int window, sinks;    // kSeeRanges (without a window: INT_MAX, 0)
-  int gap_unit, gap_tile;
+  int gap_chunk, gap_tile;
 };
 
 // What a step's rows see beside plain causal attention, for launch_build_seq: a window (0: none), or groups of sequences that
@@ -115,14 +115,18 @@ struct SeqReuse {
 };
 
 // Keys of one unit of the row kernel (four warps x 16 keys) and of one tile of the tile kernel.
-constexpr int kRowUnit = 64;
+constexpr int kRowUnit = 64, kRowChunk = 16;
 constexpr int kRowHead = 3;           // units that an item's fixed costs (queries, joining the warps' sums) are worth
+constexpr int kRowShort = 48;         // units up to which an item is not cut into more parts than are joined in one go
 constexpr int kTileKeys = 128;
 constexpr int kTileSnap = 2;          // key tiles that a split costs at least (1 and 0: a prompt of 3000 tokens in shares 93, 97 us for 87)
 constexpr int kTileDeal = 12;         // key tiles above the mean up to which whole items are dealt out (6: 6 chunks of 300 on 4000 137 us for 108)
 constexpr int kTileHead = 3;          // key tiles that an item's fixed costs (queries, first products, output) are worth
 
-constexpr int64_t kShareBytes = 32 << 20;      // bytes that a step's groups must be able to save for a prefix pass
+// Bytes that a step's groups must be able to save for a prefix pass: what the sequences read again comes from L2 where the
+// prefix fits there, and two launches cost 10 us. (Tokens behind a prefix of 4100, 8 heads of 128, with the pass and without: 8 of
+// them, bf16, 120 MB, 20.6 and 17.6 us; 16, 250 MB, 20.5 and 26.3; e4m3 16, 126 MB, 27.9 and 25.7; 64, 530 MB, 34.5 and 77.6.)
+constexpr int64_t kShareBytes = 144 << 20;
 constexpr int kShareSeqs = 2;         // sequences of a group from which on its prefix is attended once for all
 
 // CTAs of the row kernel on an SM: by the row limit (16 rather than 8) and the cache's type.
@@ -163,6 +167,10 @@ __host__ __device__ inline int64_t row_slot(const SeqView& s) { return static_ca
 __host__ __device__ inline int64_t tile_slot(const SeqView& s) { return static_cast<int64_t>(128) * (s.hd + 2); }
 // The most blocks that n tokens of s sequences make in the tile kernel's list.
 inline int64_t most_blocks(const SeqView& v, int64_t n, int64_t s) { return n / (2 * v.tile_tokens) + s; }
+// Units of the row kernel over `len` keys without a gap of so many chunks.
+__host__ __device__ inline int row_units(int len, int gap) {
+  return ((len + kRowChunk - 1) / kRowChunk - gap + kRowUnit / kRowChunk - 1) / (kRowUnit / kRowChunk);
+}
 // The first key behind the sinks that the row at position p sees.
 __host__ __device__ inline int first_seen(int p, int window) { return p - window + 1 > 0 ? p - window + 1 : 0; }
 inline size_t row_part_bytes(const SeqView& s) { return static_cast<size_t>(s.row_ctas) * 2 * 16 * (s.hd + 2) * 4; }

@@ -41,7 +41,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kChunk = 16;                  // keys of a warp's chunk
+constexpr int kChunk = kRowChunk;           // keys of a warp's chunk
 constexpr float kLazy = 8.0f;               // log2 of the largest weight; e4m3: of the largest weight times scale, before
 constexpr float kUp = 7.0f;                 // P is lifted to the top of f16's range: its normal numbers then reach down to 2^-21
 constexpr float kMostP = 32768.0f;          // of the row's largest
@@ -129,18 +129,22 @@ struct Place {
   int i, kvh, u, units;
   RowSeq s;
   const int32_t* table;
-  int gap;                                    // RANGES: units u from v.gap_unit on are units u + gap of the cache
+  int gap;                                    // RANGES: chunks c from v.gap_chunk on are chunks c + gap of the cache
   __device__ __forceinline__ void load(const SeqView& v) {
     const int4 x = *reinterpret_cast<const int4*>(v.row_seq + i);
     s = RowSeq{x.x, x.y, x.z, x.w};
     units = (s.len + kRowUnit - 1) / kRowUnit;
-    if (RANGES) units -= gap = v.row_gap[i];
+    if (RANGES) {
+      gap = v.row_gap[i];
+      units = row_units(s.len, gap);
+    }
     table = v.table + static_cast<size_t>(s.seq) * v.max_pages;
   }
   // The first key of the warp's chunk of unit x, and whether no row sees any of the chunk (RANGES; keys before
   // first_seen() of the first row that are not among the first ones are brought as zeros).
   __device__ __forceinline__ int key(const SeqView& v, int x, int warp) const {
-    return (RANGES && x >= v.gap_unit ? x + gap : x) * kRowUnit + warp * kChunk;
+    const int c = x * kWarps + warp;
+    return (RANGES && c >= v.gap_chunk ? c + gap : c) * kChunk;
   }
   __device__ __forceinline__ int first(const SeqView& v) const { return RANGES ? first_seen(s.len - s.n, v.window) : 0; }
   __device__ __forceinline__ bool unseen(const SeqView& v, int k0) const {

@@ -352,7 +352,7 @@ mlora_status mlora_seq_create_groups(int max_seqs, int max_tokens, int max_pages
       p.counts = reinterpret_cast<int32_t*>(b + o_pcounts);
       p.see = kSeePrefix;
       p.window = INT_MAX;
-      p.sinks = p.gap_unit = p.gap_tile = 0;
+      p.sinks = p.gap_chunk = p.gap_tile = 0;
     }
     const int32_t counts[8] = {0, INT32_MAX, 0, 0, 0, 0, 0, 0};
     e = cudaMemset(v.err, 0, 4);
@@ -403,7 +403,7 @@ static mlora_status build_seq(mlora_seq_t q, const int32_t* q_start, const int32
   v.see = window > 0 || n_groups > 0 ? kSeeRanges : kSeeAll;
   v.window = window > 0 ? window : INT_MAX;
   v.sinks = sinks;
-  v.gap_unit = (sinks + kRowUnit - 1) / kRowUnit;
+  v.gap_chunk = (sinks + kRowChunk - 1) / kRowChunk;
   v.gap_tile = (sinks + kTileKeys - 1) / kTileKeys;
   v.skip = n_groups > 0 ? q->skip : nullptr;
   v.group = n_groups > 0 ? q->group : nullptr;

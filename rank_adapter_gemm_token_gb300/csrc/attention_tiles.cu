@@ -184,6 +184,12 @@ __device__ __forceinline__ void turn4(uint32_t (&z)[32], int lane) {
 // A key's word is the factor of its scores; its last byte says what is left of its value's scale: here -(2 + byte 2^-14), so
 // that P (1 + byte 2^-14) is -(P + P times it).
 __device__ __forceinline__ float value_rest(float word) { return __uint_as_float(__byte_perm(__float_as_uint(word), 0xc0000000u, 0x7504)); }
+// Rows [a, b) of a value tile become zero (a warp).
+template <int HD>
+__device__ __forceinline__ void clear_rows(uint8_t* t, int a, int b, int lane) {
+  for (int i = a * (HD / 8) + lane; i < b * (HD / 8); i += 32)
+    *reinterpret_cast<uint4*>(t + (i % (HD / 8) >> 3) * kHalf + i / (HD / 8) * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+}
 // Barrier of the four warps that turn codes into f16.
 __device__ __forceinline__ void converters_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // Eight e4m3 codes as f16, times a factor.
@@ -219,25 +225,34 @@ struct alignas(64) Walk {
   int at, last;
 };
 
-// Rows [from, to) of key tile j (of the cache) that no row of an item sees, beside those from the sequence's length on: a
-// window's gap (kSeeRanges). They may lie on pages that are gone: their boxes are not brought.
-__device__ __forceinline__ int2 unseen_rows(const SeqView& v, const TileWork& it, int j) {
-  return make_int2(max(v.sinks - j * kKeys, 0), min(first_seen(it.len - it.n + it.t0, v.window) - j * kKeys, kKeys));
-}
 template <int SEE>
 __device__ __forceinline__ int cache_tile(const SeqView& v, const TileWork& it, int j) {
   return SEE == kSeeRanges && j >= v.gap_tile ? j + it.gap : j;
 }
-// Whether a value tile has rows to clear: tile j (of the item) holds some that no row of the item sees.
-template <int SEE>
-__device__ __forceinline__ bool short_tile(const SeqView& v, const TileWork& it, int j) {
-  if (SEE == kSeePrefix) return false;
-  const int tile = cache_tile<SEE>(v, it, j);
-  if (SEE == kSeeRanges) {
-    const int2 none = unseen_rows(v, it, tile);
-    if (none.x < none.y) return true;
+// What the rows of an item see of key tile j (of the cache), kSeeRanges: rows [0, first) and [from, to). Only the 16-row steps
+// that hold some of them (steps: a bit for each) meet the weights, so that of a tile with a few first tokens one step is
+// multiplied, and the rows in between are cleared in those steps alone (ragged: there are some).
+struct TileSeen {
+  int first, from, to;
+  __device__ __forceinline__ TileSeen(const SeqView& v, const TileWork& it, int j) {
+    const int start = j * kKeys, base = it.len - it.n + it.t0, rows = min(2 * v.tile_tokens, it.n - it.t0);
+    to = min(base + rows - start, kKeys);
+    first = min(max(v.sinks - start, 0), to);
+    from = min(max(first_seen(base, v.window) - start, first), to);
   }
-  return (tile + 1) * kKeys > it.len;
+  __device__ __forceinline__ uint32_t steps() const {
+    return ((1u << ((first + 15) >> 4)) - 1) | (((1u << ((to + 15) >> 4)) - 1) & ~((1u << (from >> 4)) - 1));
+  }
+  // rows of those steps that nothing sees: [first, a), [b, from) and [to, c)
+  __device__ __forceinline__ int a() const { return min((first + 15) & ~15, from); }
+  __device__ __forceinline__ int b() const { return max(from & ~15, first); }
+  __device__ __forceinline__ int c() const { return (to + 15) & ~15; }
+  __device__ __forceinline__ bool ragged() const { return first < a() || b() < from || to < c(); }
+};
+// The columns below x (any number) of the 32 that begin at `at`, as bits.
+__device__ __forceinline__ uint32_t columns_below(int x, int at) {
+  const int n = min(max(x - at, 0), 32);
+  return n == 32 ? 0xffffffffu : (1u << n) - 1;
 }
 
 template <int HD, bool E4M3, int SEE>
@@ -261,7 +276,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
   uint64_t* sc_full = o_full + 2;                     // [kScaleBufs]
   uint64_t* v_short = sc_full + C::kScaleBufs;        // bf16: a value tile with rows past the length is there, and
   uint64_t* v_clean = v_short + 1;                    // those rows are zero
-  uint64_t* raw_full = v_clean + 1;                   // [kStages], e4m3
+  uint64_t* v_ready = v_clean + 1;                    // [kRing], bf16, kSeeRanges: a value tile is there, rows that nothing sees zero
+  uint64_t* raw_full = v_ready + C::kRing;            // [kStages], e4m3
   uint64_t* raw_empty = raw_full + C::kStages;
   uint64_t* drained = raw_empty + C::kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
@@ -273,6 +289,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     for (int i = 0; i < C::kRing; ++i) {
       ptx::mbar_init(&kv_full[i], E4M3 ? 128 : 1);
       ptx::mbar_init(&kv_empty[i], 1);
+      ptx::mbar_init(&v_ready[i], 32);
     }
     for (int w = 0; w < 2; ++w) {
       ptx::mbar_init(&q_full[w], E4M3 ? 32 : 1);
@@ -349,9 +366,9 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         bool mine = lane < boxes && key < it.len;
         int at = 0;
         if (mine) {
-          const int page = table[key >> kv.page_log2];
-          at = ((page * v.Hkv + it.kvh) << kv.page_log2) + (key & (kv.page - 1));
-          if (SEE == kSeeRanges) mine = page >= 0;
+          at = ((table[key >> kv.page_log2] * v.Hkv + it.kvh) << kv.page_log2) + (key & (kv.page - 1));
+          // (a box that no row sees may lie on a page that is gone)
+          if (SEE == kSeeRanges) mine = key < v.sinks || key + box > first_seen(it.len - it.n + it.t0, v.window);
         }
         const int count = __popc(__ballot_sync(0xffffffffu, mine));
 #pragma unroll
@@ -431,10 +448,14 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         auto mask = [&](uint32_t (&x)[W], int h) {    // of columns W h ...
 #pragma unroll
           for (int i = 0; i < W; ++i) x[i] = W * h + i > seen ? 0xff800000u : x[i];
-          if (SEE == kSeeRanges && gone < from) {
+        };
+        auto mask_ranges = [&](uint32_t (&x)[W], int h) {
+          const uint32_t on = columns_below(seen + 1, W * h) & ~(columns_below(from, W * h) & ~columns_below(gone, W * h));
 #pragma unroll
-            for (int i = 0; i < W; ++i) x[i] = W * h + i >= gone && W * h + i < from ? 0xff800000u : x[i];
-          }
+          for (int i = 0; i < W; ++i) x[i] = on >> i & 1 ? x[i] : 0xff800000u;
+        };
+        auto hide = [&](uint32_t (&x)[W], int h) {
+          if (SEE == kSeeRanges) mask_ranges(x, h); else mask(x, h);
         };
         // some row of the warp does not see the whole tile
         const bool edge = seen_low < kKeys - 1 || (SEE == kSeeRanges && seen_high - v.window >= gone && gone < kKeys);
@@ -490,6 +511,9 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           // against 568; two pieces a turn, the next loaded ahead, 625). bf16: for the tiles that some row of the warp
           // does not see whole, at most two of an item, where a second unrolled copy cost registers (347 us against 335).
           const int pieces = max(0, min(kKeys / W, (seen_high + W) / W));         // that some row of the warp sees
+          // kSeeRanges: the pieces whose steps meet the weights; the others' weights are not read
+          const uint32_t steps = SEE == kSeeRanges && edge ? TileSeen(v, it, cache_tile<SEE>(v, it, j)).steps() : 0xffu;
+          auto met = [&](int h) { return SEE != kSeeRanges || (steps >> (W / 16 * h) & ((1 << W / 16) - 1)) != 0; };
           auto load_keys = [&](float4 (&f)[W / 4], int h) {
 #pragma unroll
             for (int i = 0; i < W / 4; ++i) f[i] = reinterpret_cast<const float4*>(key + W * h)[i];
@@ -498,6 +522,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             float t = -INFINITY;
 #pragma unroll 1
             for (int h = 0; h < pieces; ++h) {
+              if (!met(h)) continue;
               tmem_ld(ts + W * h, xa);
               ptx::tmem_ld_wait();
               if (exact.value) {
@@ -506,7 +531,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
 #pragma unroll
                 for (int i = 0; i < W; ++i) xa[i] = __float_as_uint(__uint_as_float(xa[i]) * (&f[i / 4].x)[i & 3]);
               }
-              if (edge) mask(xa, h);
+              if (edge) hide(xa, h);
               t = largest(xa, t);
             }
             return t;
@@ -520,9 +545,13 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               top = far ? exact : top;
             }
           }
+          // kSeeRanges: a first tile of which a row sees a few keys says little about the others: bf16 has room for a maximum
+          // that much higher, and saves going through the next tile twice. A row that has seen nothing yet has no sums.
           if (j == ka)
+            m = SEE == kSeeRanges && !E4M3 ? top + kLazy<E4M3> : top;
+          else if (SEE == kSeeRanges && m == -INFINITY)
             m = top;
-          else if (__any_sync(0xffffffffu, top > m + kLazy<E4M3>))
+          if (j > ka && __any_sync(0xffffffffu, top > m + kLazy<E4M3>))
             rescale(top > m + kLazy<E4M3> ? top : m);
           const float mm = m == -INFINITY ? 0.f : m;
           const uint64_t neg = pair(off - mm + kUp<E4M3>, off - mm + kUp<E4M3>);
@@ -530,6 +559,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
           auto second = [&](auto scaled) {
 #pragma unroll 1
             for (int h = 0; h < pieces; ++h) {
+              if (!met(h)) continue;
               float4 f[W / 4];
               tmem_ld(ts + W * h, xa);
               if (E4M3) load_keys(f, h);              // (on their way together)
@@ -538,7 +568,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
 #pragma unroll
                 for (int i = 0; i < W; ++i) xa[i] = __float_as_uint(__uint_as_float(xa[i]) * c);
               }
-              if (edge) mask(xa, h);
+              if (edge) hide(xa, h);
               weights(xa, neg, p, f);
               tmem_st(ts + W / 2 * h, p);
             }
@@ -554,10 +584,10 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             for (int h = max(pieces, 0); h < kKeys / W; ++h) tmem_st(ts + W / 2 * h, p);
           }
         } else {
-          if (j == ka) {                              // a first maximum: that of the first columns
-            tmem_ld(ts, xa);
+          if (j == ka || (SEE == kSeeRanges && __any_sync(0xffffffffu, m == -INFINITY))) {
+            tmem_ld(ts, xa);                          // a first maximum: that of the first columns
             ptx::tmem_ld_wait();
-            m = fmaf(largest(xa, top), c, off);
+            if (SEE != kSeeRanges || j == ka || m == -INFINITY) m = fmaf(largest(xa, top), c, off);
           }
           // One pass over S, W columns at a time: weights against the maximum so far, and the tile's own maximum. P
           // waits in registers: where the tile's maximum is above the lazy limit, S is still there for another pass.
@@ -685,29 +715,40 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
       if (warp == 8) {
         bring();
       } else if (warp == 9) {
-        // value rows past the length, in the one tile of an item that may hold any (kSeeRanges: and rows in a window's gap, in up to
-        // two more), when the products have come to it
-        uint32_t n = 1, par = 0;                      // ring position of the item's first value tile; tiles so far
-        for (bool go = any && SEE != kSeePrefix; go; go = advance()) {
-          for (int j = SEE == kSeeAll ? it.kb - 1 : it.ka; j < it.kb; ++j) {
-            if (!short_tile<SEE>(v, it, j)) continue;
-            wait(v_short, par);
-            par ^= 1;
-            uint8_t* t = smem + C::kRingOff + (n + 2 * (j - it.ka)) % C::kRing * C::kTile;
-            auto clear = [&](int a, int b) {
-              for (int i = a * (HD / 8) + lane; i < b * (HD / 8); i += 32)
-                *reinterpret_cast<uint4*>(t + (i % (HD / 8) >> 3) * kHalf + i / (HD / 8) * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            };
-            const int tile = cache_tile<SEE>(v, it, j);
-            clear(max(min(it.len - tile * kKeys, kKeys), 0), kKeys);
-            if (SEE == kSeeRanges) {
-              const int2 none = unseen_rows(v, it, tile);
-              clear(none.x, none.y);
+        uint32_t n = 1;                               // ring position of the item's first value tile
+        if (SEE == kSeeAll) {
+          // value rows past the length, in the one tile of an item that may hold any, when the products have come to it
+          uint32_t par = 0;                           // tiles so far
+          for (bool go = any; go; go = advance()) {
+            if (it.kb * kKeys > it.len) {
+              wait(v_short, par);
+              par ^= 1;
+              uint8_t* t = smem + C::kRingOff + (n + 2 * (it.kb - 1 - it.ka)) % C::kRing * C::kTile;
+              clear_rows<HD>(t, it.len - (it.kb - 1) * kKeys, kKeys, lane);
+              ptx::fence_proxy_async_smem();
+              ptx::mbar_arrive(v_clean);
             }
-            ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(v_clean);
+            n += 2 * (it.kb - it.ka);
           }
-          n += 2 * (it.kb - it.ka);
+        } else if (SEE == kSeeRanges) {
+          // Value rows that nothing sees, in up to three tiles of an item, as soon as a tile is there: every value tile goes
+          // through here on its way to the products, so that this warp is at most a turn of the ring behind. (With the
+          // exchange above, a prompt of 8000 tokens in a window of 1024 took 164 us, 139 without its 4 first tokens.)
+          for (bool go = any; go; go = advance()) {
+            for (int j = it.ka; j < it.kb; ++j, n += 2) {
+              const TileSeen seen(v, it, cache_tile<SEE>(v, it, j));
+              const uint32_t st = n % C::kRing;
+              wait(&kv_full[st], (n / C::kRing) & 1);
+              if (seen.ragged()) {
+                uint8_t* t = smem + C::kRingOff + st * C::kTile;
+                clear_rows<HD>(t, seen.first, seen.a(), lane);
+                clear_rows<HD>(t, seen.b(), seen.from, lane);
+                clear_rows<HD>(t, seen.to, seen.c(), lane);
+                ptx::fence_proxy_async_smem();
+              }
+              ptx::mbar_arrive(&v_ready[st]);
+            }
+          }
         }
       }
     } else {
@@ -724,8 +765,9 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         for (int j = it.ka; j < it.kb; ++j) {
           const int tile = cache_tile<SEE>(v, it, j);
           const int cut = it.len - tile * kKeys;      // rows of the tile inside the sequence (any number)
-          const int2 none_seen = SEE == kSeeRanges ? unseen_rows(v, it, tile) : make_int2(0, 0);
-          auto outside = [&](int r) { return r >= cut || (SEE == kSeeRanges && r >= none_seen.x && r < none_seen.y); };
+          const TileSeen some(v, it, tile);
+          auto outside = [&](int r) { return SEE == kSeeRanges ? r >= some.to || (r >= some.first && r < some.from) : r >= cut; };
+          const uint32_t steps = SEE == kSeeRanges ? some.steps() : 0xffu;        // those that are wanted
 #pragma unroll 1
           for (int h = 0; h < 2; ++h, ++n) {
             const int st = n % C::kRing, cs = n % C::kStages;
@@ -774,6 +816,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             constexpr int kAtOnce = 4;                // (2: 597 us at 8000 tokens, 8 the same as 4)
 #pragma unroll 1
             for (int i0 = 0; i0 < kCopies; i0 += kAtOnce) {
+              if (SEE == kSeeRanges && (steps >> (i0 * kStep / 16) & ((1u << (kAtOnce * kStep / 16)) - 1)) == 0) continue;
               uint2 cd[kAtOnce][2];
               __half2 f[kAtOnce];
 #pragma unroll
@@ -812,17 +855,21 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         int at = any ? walk.at : 0, len = it.len;
         const int last = any ? walk.last : -1;
         int4 next = *reinterpret_cast<const int4*>(&it);
-        TileWork now;                                 // kSeeRanges, bf16: what short_tile() reads
-        constexpr bool kGaps = !E4M3 && SEE == kSeeRanges;
+        TileWork ahead{};                             // kSeeRanges: of the next item, what TileSeen reads
+        if (SEE == kSeeRanges) ahead = it;
         while (at <= last) {
           const int ka = next.x, kb = next.y, end0 = next.z, end1 = next.w;
           const bool short_last = !E4M3 && SEE == kSeeAll && kb * kKeys > len;
-          if (kGaps) now = v.tile_work[at];
+          const TileWork now = ahead;                 // (tiles between these keys are seen whole)
+          const int all_from = SEE == kSeeRanges ? first_seen(now.len - now.n + now.t0, v.window) : 0;
+          const int all_to = now.len - now.n + now.t0 + min(2 * v.tile_tokens, now.n - now.t0);
           if (++at <= last) {                         // the next item, long before it is wanted
             next = *reinterpret_cast<const int4*>(v.tile_work + at);
             len = v.tile_work[at].len;
+            if (SEE == kSeeRanges) ahead = v.tile_work[at];
           }
           for (int j = ka; j <= kb; ++j) {
+            uint32_t steps = 0xffu;                   // of the value tile that meet the weights
             if (j > ka) {
               vs = ks, vs_par = ks_par;               // the tile after K_{j-1}
               if (++vs == C::kRing) vs = 0, vs_par ^= 1;
@@ -830,7 +877,12 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
               if (++ks == C::kRing) ks = 0, ks_par ^= 1;
               wait(&kv_full[vs], vs_par);
               if (dead) break;
-              if ((short_last && j == kb) || (kGaps && short_tile<SEE>(v, now, j - 1))) {
+              if (SEE == kSeeRanges) {
+                if (!E4M3) wait(&v_ready[vs], vs_par);
+                const int at0 = cache_tile<SEE>(v, now, j - 1) * kKeys;
+                if ((at0 < all_from && at0 + kKeys > v.sinks) || at0 + kKeys > all_to) steps = TileSeen(v, now, at0 / kKeys).steps();
+              }
+              if (short_last && j == kb) {
                 ptx::mbar_arrive(v_short);
                 wait(v_clean, clean_par);
                 clean_par ^= 1;
@@ -846,9 +898,18 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                 wait(&p_full[w], p_par[w]);
                 p_par[w] ^= 1;
                 ptx::tc_fence_after();
+                if (SEE == kSeeRanges && steps != 0xffu) {
+                  bool more = j - 1 > ka;
+#pragma unroll 1
+                  for (uint32_t left = steps; left != 0; left &= left - 1, more = true) {
+                    const int k = __ffs(left) - 1;
+                    umma_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k, dv + k * (2048 >> 4), id_o, more);
+                  }
+                } else {
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                  umma_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k, dv + k * (2048 >> 4), id_o, j - 1 > ka || k > 0);
+                  for (int k = 0; k < kKeys / 16; ++k)
+                    umma_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * k, dv + k * (2048 >> 4), id_o, j - 1 > ka || k > 0);
+                }
                 if (j == end) ptx::umma_commit(&o_full[w]);
               }
               if (j < end) {

@@ -253,6 +253,7 @@ __device__ __forceinline__ void plan(const SeqView& v, int page_log2, int64_t* p
   __shared__ int most, deepest;                   // key tiles of the largest block; units of the fullest hands
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t units = 0, entries = 0, cached = 0, blocks = 0;      // totals of the sequences before this chunk
+  int longest = 0;                                // units of the thread's longest item
   for (int s0 = 0; s0 < v.S; s0 += kPlanThreads) {
     const int s = s0 + threadIdx.x;
     const int n = s < v.S ? v.n[s] : 0, L = s < v.S ? v.len[s] : 0, start = s < v.S ? v.start[s] : 0;
@@ -260,10 +261,11 @@ __device__ __forceinline__ void plan(const SeqView& v, int page_log2, int64_t* p
     const bool some = rows > 0 && L > 0, few = v.see != kSeePrefix && rows <= v.row_limit;
     const int per = 2 * v.tile_tokens;              // tokens of a block
     const int skip = v.skip != nullptr && v.see == kSeeRanges && s < v.S ? v.skip[s] : 0;
-    // units, or tiles of `size` keys, that the rows from position p on do not see
+    // chunks, or tiles, of `size` keys that the rows from position p on do not see
     auto gap = [&](int p, int keys, int size, int from) { return keys > 0 ? keys / size : max(0, first_seen(p, v.window) / size - from); };
-    const int row_gap = v.see == kSeeRanges ? gap(L - n, skip, kRowUnit, v.gap_unit) : 0;
-    const int64_t u = some && few ? kRowHead + (L + kRowUnit - 1) / kRowUnit - row_gap : 0;
+    const int row_gap = v.see == kSeeRanges ? gap(L - n, skip, kRowChunk, v.gap_chunk) : 0;
+    const int64_t u = some && few ? kRowHead + row_units(L, row_gap) : 0;
+    if (!TILES && v.see == kSeeRanges) longest = max(longest, static_cast<int>(u));
     const int64_t b = some && !few ? (n + per - 1) / per : 0;
     int64_t x[4] = {u, u > 0, (static_cast<int64_t>(L) + (1 << page_log2) - 1) >> page_log2, b}, t[4];
     block_scan(x, sums, t);
@@ -315,8 +317,15 @@ __device__ __forceinline__ void plan(const SeqView& v, int page_log2, int64_t* p
       for (int64_t i = threadIdx.x; i <= entries; i += kPlanThreads) pre[i] = v.row_pre[i];
     __syncthreads();
     const int64_t row_total = units * v.Hkv;
+    int64_t ctas = min(static_cast<int64_t>(v.row_ctas), row_total);
+    if (v.see == kSeeRanges) {
+      // Short items in at most kPartsAhead parts, which are joined in one go: fewer CTAs for few of them.
+      atomicMax(&most, longest);
+      __syncthreads();
+      if (most <= kRowShort && most > 0) ctas = min(ctas, (kPartsAhead - 1) * row_total / most);
+    }
     share_out<false>(v, small_rows ? pre : v.row_pre, static_cast<int>(entries),
-                     Shares{row_total, static_cast<int>(min(static_cast<int64_t>(v.row_ctas), row_total)), kRowHead, 0}, v.row_ctas,
+                     Shares{row_total, static_cast<int>(ctas), kRowHead, 0}, v.row_ctas,
                      cuts, pre, &joins);
     return;
   }

@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-WIDE = 1 << 14          # entries of a page table's row: by them the prefixes might be long enough to be worth a pass
+WIDE = 1 << 15          # entries of a page table's row: by them the prefixes might be long enough to be worth a pass
 
 
 @pytest.fixture(scope="module")
