@@ -747,7 +747,8 @@ cudaError_t launch_pair_gemm(const uint16_t* x, const uint16_t* W, float* y, int
 }
 
 // Tiles of 256 rows x bn / 2 columns of h; the widths that whole boxes of 32 columns fill. By the estimates above, over tiles of
-// bn rows of W.
+// bn rows of W; of at most 256 tokens, which are bound by the bytes that an SM takes in, by those: whole waves times 128 rows of x
+// and bn / 2 of W (256 tokens, 4096 -> 2 x 14336, no adapters: widths 256, 192, 128 take 61, 56, 62 us).
 cudaError_t launch_pair_gemm_gated(const uint16_t* x, const uint16_t* W, uint16_t* h, int T, int K, int D, int act, uint32_t* err,
                                    const PoolView* pool, const MetaView* meta, int bn, cudaStream_t s) {
   const bool fuse = pair_gemm_fuses_shrink(K);
@@ -756,7 +757,10 @@ cudaError_t launch_pair_gemm_gated(const uint16_t* x, const uint16_t* W, uint16_
   if (bn != 256 && bn != 192 && bn != 128) {
     double best = 0.0;
     for (int n : {256, 192, 128}) {
-      const double time = fuse ? pair_time_dynamic(T, D, n, max_pairs) : pair_time(T, D, n, max_pairs);
+      const int tiles = (D / 2 + n / 2 - 1) / (n / 2);
+      const double time = T <= kPairM ? static_cast<double>((tiles + max_pairs - 1) / max_pairs) * (kHalf + n / 2)
+                          : fuse      ? pair_time_dynamic(T, D, n, max_pairs)
+                                      : pair_time(T, D, n, max_pairs);
       if (n == 256 || time < best - 1e-9 || (fuse && time <= best + 1e-9)) best = time, bn = n;
     }
   }

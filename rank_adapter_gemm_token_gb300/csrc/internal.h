@@ -76,7 +76,7 @@ struct MetaView {
   int32_t* pent_u0;       // [U] unit of M-tile 2mp with that block (-1: none)
   int32_t* pent_u1;       // [U] unit of M-tile 2mp + 1 with that block (-1: none)
   int32_t* ptile_order;   // [pair tiles] pair tiles by entry count, most first (ties ascending)
-  uint32_t* sync;         // [2 + pair tiles] the pair GEMM's counters: [0] next tile ticket, [1] clusters
+  uint32_t* sync;         // [2 + pair tiles] the pair GEMM's counters (and the few tokens' gated linear's: tickets, CTAs done, shares): [0] next tile ticket, [1] clusters
                           //   done, [2 + mp] shrink sub-tiles of pair tile mp written (one per epilogue
                           //   warp); zero between launches (the last cluster of a launch resets them)
   int32_t* pair_fused;    // [n] 1: the pair's side path runs on the tensor cores inside the GEMM
@@ -159,6 +159,14 @@ cudaError_t launch_base_gemm_lora(const uint16_t* x, const uint16_t* W, float* y
                                   cudaStream_t s);
 // h[T, F] (bf16) = act(y[:, :F]) * y[:, F:] of fp32 rows y [T, 2 F] (gated.cu); F a multiple of 8.
 cudaError_t launch_gated_activation(const float* y, uint16_t* h, int T, int F, int act, int num_sms, cudaStream_t s);
+// The gated linear of a few tokens, W streamed through registers (gated_stream.cu).
+constexpr int kStreamTokens = 32;
+// Shared memory up to which a step's tokens and side path take this kernel: what it leaves of an SM's 256 KB is where the loads on
+// their way lie (4096 -> 2 x 14336, pair GEMM 85 us: 16 tokens, 133 KB, 51 us; 20, 167 KB, 64; 24, 200 KB, 88).
+constexpr int kStreamBytes = 176 * 1024;
+bool gated_streams(int T, int J, int K, int F, const PoolView& pool, int num_sms);
+cudaError_t launch_gated_stream(const uint16_t* x, const uint16_t* W, uint16_t* h, int K, int F, int act, const PoolView& pool,
+                                const MetaView& m, int num_sms, uint32_t* err, cudaStream_t s);
 // One block waiting on an mbarrier nothing arrives on (wait_check.cu): exercises the bounded
 // wait, which sets ptx::kErrWaitTimeout in *err after the limit and returns.
 cudaError_t launch_wait_check(uint32_t* err, cudaStream_t s);

@@ -943,6 +943,17 @@ static bool units_may_overflow(mlora_pool_t p, mlora_meta_t m) {
          (n_tiles * per_tile > m->unit_cap && static_cast<long>(m->T) * m->J * p->max_span > m->unit_cap);
 }
 
+// Whether mlora_linear takes the small-batch path.
+static bool takes_small_path(mlora_pool_t p, mlora_meta_t m, int num_sms) {
+  const int path = g_path.load(std::memory_order_relaxed);
+  const bool small_ok = p->uniform() && skinny_shrink_fusable(m->T, m->J, p->S, p->R, m->vfull_ld) &&
+                        (p->D + 127) / 128 <= num_sms;
+  // the small-batch kernel multiplies every token by every active slot's rows: worth it while
+  // those rows add at most half of the output's 128-row blocks
+  const long act_blocks = (static_cast<long>(std::min(p->S, m->T * m->J)) * p->R + 127) / 128;
+  return small_ok && (path == 1 || (path == 0 && 2 * act_blocks <= (p->D + 127) / 128));
+}
+
 mlora_status mlora_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, const mlora_bf16* W, float* y,
                           void* stream) {
   if (p && p->embed) return fail(MLORA_ERR_INVALID_ARG, "an embedding pool: use mlora_embedding");
@@ -959,14 +970,7 @@ mlora_status mlora_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, c
     m->last_stream = s;
     return MLORA_OK;
   }
-  const int path = g_path.load(std::memory_order_relaxed);
-  const bool small_ok = p->uniform() && skinny_shrink_fusable(m->T, m->J, p->S, p->R, m->vfull_ld) &&
-                        (p->D + 127) / 128 <= ds->num_sms;
-  // the small-batch kernel multiplies every token by every active slot's rows: worth it while
-  // those rows add at most half of the output's 128-row blocks
-  const long act_blocks = (static_cast<long>(std::min(p->S, m->T * m->J)) * p->R + 127) / 128;
-  const bool small = small_ok && (path == 1 || (path == 0 && 2 * act_blocks <= (p->D + 127) / 128));
-  if (small) {
+  if (takes_small_path(p, m, ds->num_sms)) {
     // small batch whose 128-column output blocks fit in one wave: one split-K tensor-core kernel
     // for the base product and the shrink of every active slot, then the expand as its
     // programmatic dependent
@@ -993,14 +997,26 @@ mlora_status mlora_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, c
   return MLORA_OK;
 }
 
-// The activation runs in the CTA-pair GEMM's epilogue, except where the output is not complete there (pairs that the
-// CUDA-core kernels add), or where the controls ask for another GEMM.
-static bool gated_fuses(mlora_pool_t p, mlora_meta_t m) {
-  return g_path.load(std::memory_order_relaxed) != 1 && gemm_tile_n() >= 0 && pair_gemm_max_pairs() > 0 && !units_may_overflow(p, m);
+// How mlora_gated_linear runs a step: a few tokens in a kernel of their own (gated_stream.cu); with the activation in the CTA-pair
+// GEMM's epilogue; or mlora_linear, into the workspace, and the activation after it: where the output is not complete in that
+// epilogue (pairs that the CUDA-core kernels add), where the controls ask for another GEMM, and for small batches with an output
+// so small that the split-K kernel's shorter K loop counts for more than the second pass (GB300, cold, 8 and 100 adapters of rank 16, us
+// unfused and fused: 40 tokens 1024 -> 2 x 512 16 and 24, 15 and 30; 128 tokens 4096 -> 2 x 2048 26 and 37, 31 and 44, -> 2 x 5632 51 and
+// 49, 60 and 58; 256 tokens 1024 -> 2 x 2048 27 and 27, 30 and 33, -> 2 x 5632 43 and 31, 52 and 40).
+enum { kGatedStream, kGatedFused, kGatedApart };
+static int gated_form(mlora_pool_t p, mlora_meta_t m, int num_sms) {
+  constexpr int64_t kApartOutputs = 1 << 19;
+  constexpr int kApartWidth = 6144;
+  const int path = g_path.load(std::memory_order_relaxed), F = p->D / 2;
+  if (path == 0 && gemm_tile_n() == 0 && gated_streams(m->T, m->J, p->K, F, p->view(), num_sms)) return kGatedStream;
+  if (path == 1 || gemm_tile_n() < 0 || pair_gemm_max_pairs() < 1 || units_may_overflow(p, m)) return kGatedApart;
+  const bool little = F <= kApartWidth && static_cast<int64_t>(m->T) * F <= kApartOutputs;
+  return gemm_tile_n() == 0 && little && takes_small_path(p, m, num_sms) ? kGatedApart : kGatedFused;
 }
 
 size_t mlora_gated_workspace_bytes(mlora_pool_t p, mlora_meta_t m) {
-  if (!p || !m || p->embed || !m->built || gated_fuses(p, m)) return 0;
+  int sms = 0;
+  if (!p || !m || p->embed || !m->built || device_sms(&sms) || gated_form(p, m, sms) != kGatedApart) return 0;
   return static_cast<size_t>(m->T) * p->D * sizeof(float);
 }
 
@@ -1016,7 +1032,8 @@ mlora_status mlora_gated_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16
   if (mlora_status st = device_state(&ds)) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
-  if (!gated_fuses(p, m)) {
+  const int form = gated_form(p, m, ds->num_sms);
+  if (form == kGatedApart) {
     if (!workspace || !aligned16(workspace)) return fail(MLORA_ERR_INVALID_ARG, "workspace is NULL or misaligned");
     float* y = static_cast<float*>(workspace);
     if (mlora_status st = mlora_linear(p, m, x, W, y, stream)) return st;
@@ -1026,6 +1043,12 @@ mlora_status mlora_gated_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16
   if (mlora_status st = pool_use(p, s)) return st;
   const MetaView mv = m->view();
   const PoolView pv = p->view();
+  if (form == kGatedStream) {
+    if ((e = launch_gated_stream(x, W, h, p->K, p->D / 2, act, pv, mv, ds->num_sms, ds->err, s)) != cudaSuccess)
+      return cuda_fail(e, "gated linear launch");
+    m->last_stream = s;
+    return MLORA_OK;
+  }
   if ((e = build_units(p, m, s)) != cudaSuccess) return cuda_fail(e, "unit lists launch");
   if (!pair_gemm_fuses_shrink(p->K) && (e = launch_lora_shrink_tc(x, pv, mv, ds->err, ds->num_sms, s)) != cudaSuccess)
     return cuda_fail(e, "tensor-core shrink launch");
