@@ -56,14 +56,16 @@ check_seq_kernel(const int32_t* __restrict__ q_start, const int32_t* __restrict_
             static_cast<int64_t>(L) <= static_cast<int64_t>(v.max_pages) * page && (L == 0 || L >= b - a);
   const int used = ok ? (L + page - 1) >> page_log2 : 0;
   bool fine = true;
-  const int first = ok ? first_seen(L - (b - a), v.window) : 0;      // of the first new token, or of the next one
-  for (int i = lane; i < used; i += 32) {
-    int p = pages[static_cast<size_t>(s) * table_ld + i];
-    if (static_cast<int64_t>(i) << page_log2 >= v.sinks && static_cast<int64_t>(i + 1) << page_log2 <= first)
-      p = -1;                            // (without a window, first is 0)
-    else
-      fine = fine && p >= 0 && p < n_pages;
-    v.table[static_cast<size_t>(s) * v.max_pages + i] = p;
+  // Pages [gone0, gone1) are seen by none: they end before the window of the first new token, or of the next one, begins.
+  const int gone1 = ok ? first_seen(L - (b - a), v.window) >> page_log2 : 0, gone0 = min((v.sinks + page - 1) >> page_log2, gone1);
+  const int32_t* row = pages + static_cast<size_t>(s) * table_ld;
+  int32_t* to = v.table + static_cast<size_t>(s) * v.max_pages;
+  for (int i = gone0 + lane; i < min(gone1, used); i += 32) to[i] = -1;
+#pragma unroll 4
+  for (int i = lane; i < used - (gone1 - gone0); i += 32) {
+    const int at = i < gone0 ? i : i + gone1 - gone0, p = row[at];
+    fine = fine && p >= 0 && p < n_pages;
+    to[at] = p;
   }
   ok = __all_sync(0xffffffffu, fine) && ok;
   if (n_groups > 0) {
@@ -82,8 +84,9 @@ check_seq_kernel(const int32_t* __restrict__ q_start, const int32_t* __restrict_
       if (group_start[g + 1] - leader >= kShareSeqs) keys = max(prefix_len[g], 0) / whole * whole;
       if (keys > L - (b - a)) keys = 0;  // not cached yet, or not seen by the first new token
       bool same = true;
-      for (int i = lane; i < keys >> page_log2; i += 32)
-        same = same && pages[static_cast<size_t>(s) * table_ld + i] == pages[static_cast<size_t>(leader) * table_ld + i];
+      const int32_t* first_row = pages + static_cast<size_t>(leader) * table_ld;
+#pragma unroll 4
+      for (int i = lane; i < keys >> page_log2; i += 32) same = (row[i] == first_row[i]) & same;
       if (!__all_sync(0xffffffffu, same)) keys = 0;
     }
     if (lane == 0) {
@@ -434,13 +437,15 @@ __device__ __forceinline__ void groups_as_sequences(const SeqView& v, const SeqV
   for (int g = warp; g < p.S; g += kPlanThreads / 32) {
     int count = 0, keys = 0, rep = INT_MAX, from = INT_MAX, to = 0;
     const int g1 = min(group_start[g + 1], v.S);
+#pragma unroll 4
     for (int s = max(group_start[g], 0) + lane; s < g1; s += 32) {
-      if (v.skip[s] == 0 || v.group[s] != g) continue;
+      const int skip = v.skip[s], of = v.group[s], start = v.start[s], n = v.n[s];
+      if (skip == 0 || of != g) continue;
       ++count;
-      keys = v.skip[s];                             // (the same for all of them)
+      keys = skip;                                  // (the same for all of them)
       rep = min(rep, s);
-      from = min(from, v.start[s]);
-      to = max(to, v.start[s] + v.n[s]);
+      from = min(from, start);
+      to = max(to, start + n);
     }
     count = __reduce_add_sync(0xffffffffu, count);
     keys = __reduce_max_sync(0xffffffffu, keys);
