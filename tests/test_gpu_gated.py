@@ -325,3 +325,62 @@ def test_refusals(layer):
     meta.build(torch.arange(128, dtype=torch.int32, device="cuda") % 100, None, over)
     x, W, h = (torch.zeros(n, dtype=torch.bfloat16, device="cuda") for n in (128 * 64, 272 * 64, 128 * 136))
     refused(bad, over.handle, meta.handle, x, W, 0, h, None)
+
+
+FEW = [(T, J) for T in (1, 2, 8, 9, 16, 17, 31, 32) for J in (1, 3)] + [(5, 8), (32, 8)]
+
+
+@pytest.mark.parametrize("T,J", FEW)
+def test_few_tokens(layer, T, J):
+    """The kernel of a few tokens: from one share of the side path to more than there are CTAs, slots named twice by a token, K
+    that ends inside a step, one group of columns and many."""
+    for K, F, slots, rank in ((8, 8, 1, 8), (1000, 72, 5, 40), (264, 9000, 40, 16), (64, 136, 300, 64)):
+        c = Case(layer, T, K, F, slots, rank, J, seed=T + J)
+        h = c.run("gelu")
+        c.meta.status()
+        c.check(h, "gelu")
+        assert torch.equal(h, c.run("gelu")), "a repeated call differs"
+
+
+def test_few_tokens_between_other_kernels_on_their_metadata(layer):
+    """The linear's tensor-core path and the few tokens' kernel count in the same places: each leaves them as it found them."""
+    c = Case(layer, 20, 256, 512, classes=[(9, 8), (5, 16), (3, 64)], J=2, seed=5)
+    down = Case(layer, 20, 512, 128, classes=[(9, 8), (5, 16), (3, 64)], J=2, seed=6)
+    first = c.run()
+    c.check(first)
+    for _ in range(3):
+        y = layer.feed_forward(c.meta, c.x, c.pool, c.W, down.pool, down.W)
+        assert torch.equal(c.run(), first)
+        assert torch.equal(y, layer.feed_forward(c.meta, c.x, c.pool, c.W, down.pool, down.W))
+    c.meta.status()
+
+
+def test_slots_cleared_behind_the_metadata(layer):
+    """Slots that were loaded when the metadata was built and are empty when the linear runs add nothing, and nothing waits."""
+    for T in (1, 12, 200):
+        c = Case(layer, T, 128, 264, slots=6, seed=T)
+        for s in range(6):
+            c.pool.clear(s)
+        c.pool.sync()
+        for _ in range(2):
+            h = c.run()
+        c.meta.status()
+        c.A, c.B = [a * 0 for a in c.A], [b * 0 for b in c.B]
+        c.check(h)
+
+
+def test_two_streams_at_once(layer):
+    """Steps with metadata and pools of their own, side by side on two streams: CTAs of both share the GPU."""
+    cases = [Case(layer, T, 2048, 4096, slots=30, rank=64, seed=T) for T in (30, 31)]
+    want = [c.run() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (c, s) in enumerate(zip(cases, streams)):
+            got[i].append(layer.gated_linear(c.pool, c.meta, c.x, c.W, stream=s))
+    torch.cuda.synchronize()
+    for i, c in enumerate(cases):
+        c.check(want[i])
+        assert all(torch.equal(h, want[i]) for h in got[i])
+        c.meta.status()
