@@ -787,6 +787,17 @@ mlora_status mlora_meta_destroy(mlora_meta_t m) {
   return MLORA_OK;
 }
 
+// Whether mlora_linear takes the small-batch path.
+static bool takes_small_path(mlora_pool_t p, mlora_meta_t m, int num_sms) {
+  const int path = g_path.load(std::memory_order_relaxed);
+  const bool small_ok = p->uniform() && skinny_shrink_fusable(m->T, m->J, p->S, p->R, m->vfull_ld) &&
+                        (p->D + 127) / 128 <= num_sms;
+  // the small-batch kernel multiplies every token by every active slot's rows: worth it while
+  // those rows add at most half of the output's 128-row blocks
+  const long act_blocks = (static_cast<long>(std::min(p->S, m->T * m->J)) * p->R + 127) / 128;
+  return small_ok && (path == 1 || (path == 0 && 2 * act_blocks <= (p->D + 127) / 128));
+}
+
 mlora_status mlora_build_meta(mlora_meta_t m, const int32_t* token_slots, const float* scales, int T, int J,
                               mlora_pool_t pool, void* stream) {
   if (!m || !pool) return fail(MLORA_ERR_INVALID_ARG, "meta or pool is NULL");
@@ -805,13 +816,17 @@ mlora_status mlora_build_meta(mlora_meta_t m, const int32_t* token_slots, const 
   m->class_slots = pool->class_slots;
   m->class_rank = pool->class_rank;
   MetaView v = m->view();
-  // the sort only: the tensor-core side path's unit lists are built by the first linear that
-  // takes that path (small-batch steps never need them)
-  cudaError_t e = launch_build_meta(token_slots, scales, T, J, pool->view(), v, s, kMetaSortOnly);
+  // the sort only, for small batches: the tensor-core side path's unit lists are built by the first
+  // linear that takes that path (small-batch steps never need them). Where this pool's linear will
+  // take it, both at once
+  DeviceState* ds = nullptr;
+  if (mlora_status st = device_state(&ds)) return st;
+  const bool units = T > kStreamTokens && !pool->embed && !takes_small_path(pool, m, ds->num_sms);
+  cudaError_t e = launch_build_meta(token_slots, scales, T, J, pool->view(), v, s, units ? kMetaAll : kMetaSortOnly);
   if (e != cudaSuccess) return cuda_fail(e, "build_meta launch");
   m->last_stream = s;
   m->built = true;
-  m->units_built = false;
+  m->units_built = units;
   return MLORA_OK;
 }
 
@@ -941,17 +956,6 @@ static bool units_may_overflow(mlora_pool_t p, mlora_meta_t m) {
   const long n_tiles = (m->T + 127) / 128;
   return per_tile > kMaxTileUnits ||
          (n_tiles * per_tile > m->unit_cap && static_cast<long>(m->T) * m->J * p->max_span > m->unit_cap);
-}
-
-// Whether mlora_linear takes the small-batch path.
-static bool takes_small_path(mlora_pool_t p, mlora_meta_t m, int num_sms) {
-  const int path = g_path.load(std::memory_order_relaxed);
-  const bool small_ok = p->uniform() && skinny_shrink_fusable(m->T, m->J, p->S, p->R, m->vfull_ld) &&
-                        (p->D + 127) / 128 <= num_sms;
-  // the small-batch kernel multiplies every token by every active slot's rows: worth it while
-  // those rows add at most half of the output's 128-row blocks
-  const long act_blocks = (static_cast<long>(std::min(p->S, m->T * m->J)) * p->R + 127) / 128;
-  return small_ok && (path == 1 || (path == 0 && 2 * act_blocks <= (p->D + 127) / 128));
 }
 
 mlora_status mlora_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, const mlora_bf16* W, float* y,
