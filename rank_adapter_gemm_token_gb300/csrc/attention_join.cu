@@ -24,6 +24,7 @@ template <int HD, int SEE>
 __global__ void __launch_bounds__(kThreads)
 attention_join_kernel(uint16_t* __restrict__ o, SeqView v) {
   constexpr int kQuads = HD / 4;       // groups of four columns
+  if (SEE == kSeePrefix) ptx::grid_dependents_launch();
   const int units = v.counts[2] * kSlices;
   bool waited = false;
   auto wait = [&]() {

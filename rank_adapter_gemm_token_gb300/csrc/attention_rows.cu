@@ -515,6 +515,7 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
     };
     const int2 pre_at = RANGES && v.pre_at != nullptr ? v.pre_at[at.s.seq] : make_int2(-1, 0);
     const bool pre = RANGES && pre_at.x >= 0;
+    if (pre) ptx::grid_dependency_wait();      // the prefixes' sums, whose pass may still be at its end until here
     const bool whole = at.u == 0 && u_end == at.units;
     float* slot = v.row_part + (2 * static_cast<int64_t>(blockIdx.x) + (at.u == 0 ? 1 : 0)) * row_slot(v);
     for (int i = threadIdx.x; i < rows * kGroups; i += kThreads) {
@@ -589,6 +590,7 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
     }
   }
   cp_wait<0>();
+  if (RANGES) ptx::grid_dependency_wait();     // this grid's end stands for the prefix pass's too
 }
 
 template <int HD, int NQ, bool E4M3, bool RANGES>
@@ -596,8 +598,17 @@ cudaError_t launch_seeing(const uint16_t* q, uint16_t* o, float scale_log2, cons
   using C = RowsCfg<HD, NQ, E4M3>;
   if (cudaError_t e = allow_shared_memory<attention_rows_kernel<HD, NQ, E4M3, RANGES>>(C::kBytes)) return e;
   note_launch_begin(kKindAttn, st);
-  attention_rows_kernel<HD, NQ, E4M3, RANGES><<<s.row_ctas, kThreads, C::kBytes, st>>>(q, o, scale_log2, kv, s);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(s.row_ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = RANGES && s.pre_at != nullptr ? 1 : 0;        // beside the end of the prefix pass; else the step's first launch
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_rows_kernel<HD, NQ, E4M3, RANGES>, q, o, scale_log2, kv, s);
   note_launch_end(kKindAttn, st);
   return e;
 }

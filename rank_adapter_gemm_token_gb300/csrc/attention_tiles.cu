@@ -315,6 +315,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     ptx::tmem_relinquish();
   }
   ptx::grid_dependents_launch();
+  // behind a prefix pass: its join may still be reading the parts' places, or writing the sums that are read here
+  if (SEE == kSeeRanges && v.pre_at != nullptr) ptx::grid_dependency_wait();
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
