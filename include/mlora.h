@@ -233,12 +233,15 @@ MLORA_API mlora_status mlora_linear(mlora_pool_t pool, mlora_meta_t meta, const 
  * stacked gate and up projections (an addition with no counterpart on the pages):
  *   pool: D = 2 F, F a multiple of 8; rows 0 .. F - 1 of W (and of every B) are the gate's, rows F .. 2 F - 1 the up
  *   projection's (per-slice adapters: mlora_load_adapter_sliced). x: device bf16 [T, K]; W: device bf16 [2 F, K];
- *   h: device bf16 [T, F], 16-byte aligned, overwritten: the down linear's input.
+ *   h: device bf16 [T, F], 16-byte aligned, overwritten (not x's or W's memory): the down linear's input.
  *   act: MLORA_ACT_SILU g / (1 + e^-g), MLORA_ACT_GELU_TANH g / 2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))),
  *   MLORA_ACT_GELU g / 2 erfc(-g / sqrt(2)).
  *   workspace: device, 16-byte aligned, mlora_gated_workspace_bytes(pool, meta) bytes, free again when the call has run;
  *   NULL where that is 0.
- * g, u and the activation are fp32; h is rounded once. Orders itself after the pool's queued loads; calls that share a meta or
+ * g, u and the activation are fp32 (the side path's scaled v is rounded to bf16, but in the small-batch path); h is rounded once.
+ * Three forms: up to 32 tokens (as far as they fit in shared memory) a kernel that streams W; otherwise the CTA-pair GEMM with the
+ * activation in its epilogue; or, with a workspace, mlora_linear and the activation after it, where pairs take the CUDA-core
+ * kernels, where the tuning controls ask for another GEMM, and for small batches with a small F. Orders itself after the pool's queued loads; calls that share a meta or
  * a pool must be ordered on one stream. */
 enum { MLORA_ACT_SILU = 0, MLORA_ACT_GELU_TANH = 1, MLORA_ACT_GELU = 2 };
 MLORA_API mlora_status mlora_gated_linear(mlora_pool_t pool, mlora_meta_t meta, const mlora_bf16* x, const mlora_bf16* W,
@@ -425,13 +428,15 @@ MLORA_API mlora_status mlora_build_seq(mlora_seq_t seq, const int32_t* q_start, 
  * positions j <= p with j < sinks or j > p - window (window >= 1: its own among them; 0 <= sinks <= MLORA_MAX_SINKS).
  * Pages that hold no position which a new token of their sequence sees (nor, for a sequence without new tokens, its next one)
  * are not read: they may have been given back, and their entries hold anything. mlora_kv_read leaves the rows of such pages
- * as they are. A model whose layers differ in this has a mlora_seq for each kind. */
+ * as they are. A model whose layers differ in this has a mlora_seq for each kind. What no token of a sequence's step sees has
+ * no effect, whatever it holds; the limits stated at mlora_attention, for keys that some rows of a step see and others do not yet,
+ * hold for keys that some rows do not see any more as well. */
 MLORA_API mlora_status mlora_build_seq_window(mlora_seq_t seq, const int32_t* q_start, const int32_t* kv_len,
                                               const int32_t* pages, int pages_ld, int n_seqs, int T, int max_new, int window,
                                               int sinks, mlora_kv_t kv, void* stream);
 /* The same step where groups of sequences begin with the same cached tokens: the attention reads those once for a group, all of
  * whose query rows meet them together, and joins the result with that over each sequence's own tokens. What it computes is that
- * of mlora_build_seq, but for the order of the sums.
+ * of mlora_build_seq, but for the order of the sums and the rounding of the prefix's weights, which is that of chunks and prompts.
  *   group_start: device int32 [n_groups + 1], ascending, within [0, n_seqs]: group g is the sequences group_start[g] ..
  *                group_start[g + 1] - 1 (sequences outside stand alone).
  *   prefix_len:  device int32 [n_groups]: the group's sequences share their first prefix_len[g] positions, that is, the pages that

@@ -1031,6 +1031,10 @@ mlora_status mlora_gated_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16
   if (p->D % 16) return fail(MLORA_ERR_INVALID_ARG, "D %d must be twice a multiple of 8", p->D);
   if (act < MLORA_ACT_SILU || act > MLORA_ACT_GELU) return fail(MLORA_ERR_INVALID_ARG, "unknown activation %d", act);
   if (mlora_status st = check_operands(x, W, h, m->T, p->K, p->D)) return st;
+  const uintptr_t h0 = reinterpret_cast<uintptr_t>(h), h1 = h0 + static_cast<uintptr_t>(m->T) * p->D;
+  auto overlaps = [&](const void* at, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(at) < h1 && h0 < reinterpret_cast<uintptr_t>(at) + bytes; };
+  if (overlaps(x, static_cast<uintptr_t>(m->T) * p->K * 2) || overlaps(W, static_cast<uintptr_t>(p->D) * p->K * 2))
+    return fail(MLORA_ERR_INVALID_ARG, "h must not overlap x or W");
   if (m->T == 0) return MLORA_OK;
   DeviceState* ds = nullptr;
   if (mlora_status st = device_state(&ds)) return st;

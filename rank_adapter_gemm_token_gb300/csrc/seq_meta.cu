@@ -35,7 +35,7 @@ constexpr int kPlanPre = kMapSeqs / 2;   // prefix sums kept there by the plan
 __global__ void __launch_bounds__(kCheckThreads)
 check_seq_kernel(const int32_t* __restrict__ q_start, const int32_t* __restrict__ kv_len,
                  const int32_t* __restrict__ pages, int table_ld, SeqView v, int max_new, int n_pages, int page_log2,
-                 const int32_t* __restrict__ group_start, const int32_t* __restrict__ prefix_len, int n_groups) {
+                 const int32_t* __restrict__ group_start, const int32_t* __restrict__ prefix_len, int n_groups, int least_seqs) {
   constexpr int kSeqs = kCheckThreads / 32;
   __shared__ int32_t tops[kSeqs];
   ptx::grid_dependents_launch();
@@ -81,7 +81,7 @@ check_seq_kernel(const int32_t* __restrict__ q_start, const int32_t* __restrict_
     int keys = 0;                        // of the prefix, in whole pages and key tiles
     if (g >= 0 && ok && b > a) {
       const int leader = group_start[g], whole = max(page, kTileKeys);
-      if (group_start[g + 1] - leader >= kShareSeqs) keys = max(prefix_len[g], 0) / whole * whole;
+      if (group_start[g + 1] - leader >= least_seqs) keys = max(prefix_len[g], 0) / whole * whole;
       if (keys > L - (b - a)) keys = 0;  // not cached yet, or not seen by the first new token
       bool same = true;
       const int32_t* first_row = pages + static_cast<size_t>(leader) * table_ld;
@@ -529,7 +529,8 @@ cudaError_t launch_build_seq(const int32_t* q_start, const int32_t* kv_len, cons
   const int check = std::max(1, (s.S + kCheckThreads / 32 - 1) / (kCheckThreads / 32));
   note_launch_begin(kKindSeq, st);
   check_seq_kernel<<<check, kCheckThreads, 0, st>>>(q_start, kv_len, pages, table_ld, s, max_new, kv.n_pages,
-                                                    kv.page_log2, reuse.group_start, reuse.prefix_len, reuse.n_groups);
+                                                    kv.page_log2, reuse.group_start, reuse.prefix_len, reuse.n_groups,
+                                                    share_seqs(kv.type == kKvE4m3));
   cudaError_t e = cudaGetLastError();
   note_launch_end(kKindSeq, st);
   if (e != cudaSuccess) return e;

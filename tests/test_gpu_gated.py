@@ -301,6 +301,8 @@ def test_refusals(layer):
     refused(bad, p, m, c.x, c.W, 3, h, work)
     refused(bad, p, m, c.x.data_ptr() + 2, c.W, 0, h, work)
     refused(bad, p, m, c.x, c.W, 0, h.data_ptr() + 8, work)
+    refused(bad, p, m, c.x, c.W, 0, c.x, work)
+    refused(bad, p, m, c.x, c.W, 0, c.W.data_ptr() + 16, work)
     odd = layer.AdapterPool(4, 16, 64, 136)            # half of 136 is no multiple of 8
     refused(bad, odd.handle, m, c.x, c.W, 0, h, work)
     other = layer.AdapterPool(5, 16, 64, 128)
