@@ -239,7 +239,7 @@ MLORA_API mlora_status mlora_linear(mlora_pool_t pool, mlora_meta_t meta, const 
  *   workspace: device, 16-byte aligned, mlora_gated_workspace_bytes(pool, meta) bytes, free again when the call has run;
  *   NULL where that is 0.
  * g, u and the activation are fp32 (the side path's scaled v is rounded to bf16, but in the small-batch path); h is rounded once.
- * Three forms: up to 32 tokens (as far as they fit in shared memory) a kernel that streams W; otherwise the CTA-pair GEMM with the
+ * Three forms: up to 64 tokens (as far as they fit in shared memory) a kernel that streams W; otherwise the CTA-pair GEMM with the
  * activation in its epilogue; or, with a workspace, mlora_linear and the activation after it, where pairs take the CUDA-core
  * kernels, where the tuning controls ask for another GEMM, and for small batches with a small F. Orders itself after the pool's queued loads; calls that share a meta or
  * a pool must be ordered on one stream. */

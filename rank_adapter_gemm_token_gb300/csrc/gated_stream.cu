@@ -1,6 +1,6 @@
-// The gated linear of a few tokens (T <= 32): h = act(g) * u with [g u] = x W^T + the side path, in one launch that reads W once.
+// The gated linear of a few tokens (T <= 64): h = act(g) * u with [g u] = x W^T + the side path, in one launch that reads W once.
 //
-// Bound: HBM, the bytes of W (and of the adapters' rows in use): 2 to 64 flops a byte. So W goes from memory straight to registers,
+// Bound: HBM, the bytes of W (and of the adapters' rows in use): 2 to 128 flops a byte. So W goes from memory straight to registers,
 // 16 bytes a lane and up to 8 steps ahead, and meets the tokens on the warp-level tensor instructions as their M side:
 //   - a warp's 16 rows are 8 rows of the gate and the same 8 of the up projection, so that both values of an output lie in one
 //     thread, which applies the activation. A quad's four lanes hold 32 consecutive k, eight each: the order of k inside a
@@ -29,7 +29,7 @@ constexpr int kStreamers = kWarps * 32, kThreads = kStreamers + kBuilders;
 constexpr int kStep = 32;                   // k of a step: two products
 constexpr int kWarpsWanted = 6;             // of an SM: 48 KB on their way, what the memory's latency asks for
 template <int NT>
-constexpr int kAhead = NT <= 2 ? 8 : 6;     // steps on their way to a warp, 1 KB each, as far as the registers go
+constexpr int kAhead = NT <= 2 ? 8 : NT <= 4 ? 6 : 4;     // steps on their way to a warp, 1 KB each, as far as the registers go
 constexpr int kFetchPieces = 8;             // (of more, asking for them takes longer than it saves: 16 tokens 53.7 us, 58.4 with)
 constexpr int kOwnShares = 2;               // shares of the side path up to which each CTA does all of them
 // Named barriers: 1 ... kWarps / 2 of warps that share a group; the streaming warps', both sides', the side path's, and of the three of its warps that
@@ -48,7 +48,7 @@ StreamPlan stream_plan(int T, int J, int K, int F, const PoolView& pool, int num
   p.split = kWarps;
   for (int s : {6, 4, 3, 2, 1})
     if (static_cast<int64_t>(F / 8) * s >= static_cast<int64_t>(kWarpsWanted) * num_sms) p.split = s;
-  const int tiles = T <= 8 ? 1 : T <= 16 ? 2 : 4;
+  const int tiles = T <= 8 ? 1 : T <= 16 ? 2 : T <= 32 ? 4 : 8;
   const int64_t n = static_cast<int64_t>(T) * J;
   p.x_row = (K + 63) / 64 * 128 + 64;
   p.act = static_cast<int>(std::min<int64_t>(n, pool.S));
@@ -394,7 +394,8 @@ cudaError_t launch_gated_stream(const uint16_t* x, const uint16_t* W, uint16_t* 
   const int grid = static_cast<int>(std::min<int64_t>(num_sms, std::max<int64_t>(groups, p.shares <= kOwnShares ? 0 : p.shares)));
   if (m.T <= 8) return launch_nt<1>(x, W, h, K, F, act, pool, m, p, grid, err, s);
   if (m.T <= 16) return launch_nt<2>(x, W, h, K, F, act, pool, m, p, grid, err, s);
-  return launch_nt<4>(x, W, h, K, F, act, pool, m, p, grid, err, s);
+  if (m.T <= 32) return launch_nt<4>(x, W, h, K, F, act, pool, m, p, grid, err, s);
+  return launch_nt<8>(x, W, h, K, F, act, pool, m, p, grid, err, s);
 }
 
 }  // namespace mlora

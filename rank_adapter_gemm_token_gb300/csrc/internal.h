@@ -160,7 +160,7 @@ cudaError_t launch_base_gemm_lora(const uint16_t* x, const uint16_t* W, float* y
 // h[T, F] (bf16) = act(y[:, :F]) * y[:, F:] of fp32 rows y [T, 2 F] (gated.cu); F a multiple of 8.
 cudaError_t launch_gated_activation(const float* y, uint16_t* h, int T, int F, int act, int num_sms, cudaStream_t s);
 // The gated linear of a few tokens, W streamed through registers (gated_stream.cu).
-constexpr int kStreamTokens = 32;
+constexpr int kStreamTokens = 64;
 // Shared memory up to which a step's tokens and side path take this kernel: what it leaves of an SM's 256 KB is where the loads on
 // their way lie (4096 -> 2 x 14336, pair GEMM 85 us: 16 tokens, 133 KB, 51 us; 20, 167 KB, 64; 24, 200 KB, 88).
 constexpr int kStreamBytes = 176 * 1024;

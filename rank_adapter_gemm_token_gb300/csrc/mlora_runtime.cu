@@ -787,15 +787,18 @@ mlora_status mlora_meta_destroy(mlora_meta_t m) {
   return MLORA_OK;
 }
 
-// Whether mlora_linear takes the small-batch path.
+// Whether the small-batch path can run the step's linear; its 128-row blocks of active slots' rows, which it multiplies by every token.
+static bool small_path_fits(mlora_pool_t p, mlora_meta_t m, int num_sms) {
+  return p->uniform() && skinny_shrink_fusable(m->T, m->J, p->S, p->R, m->vfull_ld) && (p->D + 127) / 128 <= num_sms;
+}
+static long active_blocks(mlora_pool_t p, mlora_meta_t m) {
+  return (static_cast<long>(std::min(p->S, m->T * m->J)) * p->R + 127) / 128;
+}
+// Whether mlora_linear takes the small-batch path: worth it while those rows add at most half of
+// the output's 128-row blocks.
 static bool takes_small_path(mlora_pool_t p, mlora_meta_t m, int num_sms) {
   const int path = g_path.load(std::memory_order_relaxed);
-  const bool small_ok = p->uniform() && skinny_shrink_fusable(m->T, m->J, p->S, p->R, m->vfull_ld) &&
-                        (p->D + 127) / 128 <= num_sms;
-  // the small-batch kernel multiplies every token by every active slot's rows: worth it while
-  // those rows add at most half of the output's 128-row blocks
-  const long act_blocks = (static_cast<long>(std::min(p->S, m->T * m->J)) * p->R + 127) / 128;
-  return small_ok && (path == 1 || (path == 0 && 2 * act_blocks <= (p->D + 127) / 128));
+  return small_path_fits(p, m, num_sms) && (path == 1 || (path == 0 && 2 * active_blocks(p, m) <= (p->D + 127) / 128));
 }
 
 mlora_status mlora_build_meta(mlora_meta_t m, const int32_t* token_slots, const float* scales, int T, int J,
@@ -958,14 +961,9 @@ static bool units_may_overflow(mlora_pool_t p, mlora_meta_t m) {
          (n_tiles * per_tile > m->unit_cap && static_cast<long>(m->T) * m->J * p->max_span > m->unit_cap);
 }
 
-mlora_status mlora_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, const mlora_bf16* W, float* y,
-                          void* stream) {
-  if (p && p->embed) return fail(MLORA_ERR_INVALID_ARG, "an embedding pool: use mlora_embedding");
-  if (mlora_status st = check_pair(p, m)) return st;
-  if (mlora_status st = check_operands(x, W, y, m->T, p->K, p->D)) return st;
-  DeviceState* ds = nullptr;
-  if (mlora_status st = device_state(&ds)) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
+// mlora_linear behind its checks, on the small-batch path or the tensor-core side path.
+static mlora_status run_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, const mlora_bf16* W, float* y, cudaStream_t s,
+                               DeviceState* ds, bool small) {
   if (mlora_status st = pool_use(p, s)) return st;
   const MetaView mv = m->view();
   const PoolView pv = p->view();
@@ -974,7 +972,7 @@ mlora_status mlora_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, c
     m->last_stream = s;
     return MLORA_OK;
   }
-  if (takes_small_path(p, m, ds->num_sms)) {
+  if (small) {
     // small batch whose 128-column output blocks fit in one wave: one split-K tensor-core kernel
     // for the base product and the shrink of every active slot, then the expand as its
     // programmatic dependent
@@ -1001,6 +999,16 @@ mlora_status mlora_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, c
   return MLORA_OK;
 }
 
+mlora_status mlora_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, const mlora_bf16* W, float* y,
+                          void* stream) {
+  if (p && p->embed) return fail(MLORA_ERR_INVALID_ARG, "an embedding pool: use mlora_embedding");
+  if (mlora_status st = check_pair(p, m)) return st;
+  if (mlora_status st = check_operands(x, W, y, m->T, p->K, p->D)) return st;
+  DeviceState* ds = nullptr;
+  if (mlora_status st = device_state(&ds)) return st;
+  return run_linear(p, m, x, W, y, static_cast<cudaStream_t>(stream), ds, takes_small_path(p, m, ds->num_sms));
+}
+
 // How mlora_gated_linear runs a step: a few tokens in a kernel of their own (gated_stream.cu); with the activation in the CTA-pair
 // GEMM's epilogue; or mlora_linear, into the workspace, and the activation after it: where the output is not complete in that
 // epilogue (pairs that the CUDA-core kernels add), where the controls ask for another GEMM, and for small batches with an output
@@ -1008,14 +1016,18 @@ mlora_status mlora_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, c
 // unfused and fused: 40 tokens 1024 -> 2 x 512 16 and 24, 15 and 30; 128 tokens 4096 -> 2 x 2048 26 and 37, 31 and 44, -> 2 x 5632 51 and
 // 49, 60 and 58; 256 tokens 1024 -> 2 x 2048 27 and 27, 30 and 33, -> 2 x 5632 43 and 31, 52 and 40).
 enum { kGatedStream, kGatedFused, kGatedApart };
+static bool gated_small(mlora_pool_t p, mlora_meta_t m, int num_sms) {
+  constexpr int64_t kOutputs = 1 << 19;
+  constexpr int kWidth = 6144;
+  const int F = p->D / 2;
+  return g_path.load(std::memory_order_relaxed) == 0 && gemm_tile_n() == 0 && F <= kWidth && static_cast<int64_t>(m->T) * F <= kOutputs &&
+         small_path_fits(p, m, num_sms) && active_blocks(p, m) + (p->D + 127) / 128 <= num_sms;
+}
 static int gated_form(mlora_pool_t p, mlora_meta_t m, int num_sms) {
-  constexpr int64_t kApartOutputs = 1 << 19;
-  constexpr int kApartWidth = 6144;
-  const int path = g_path.load(std::memory_order_relaxed), F = p->D / 2;
-  if (path == 0 && gemm_tile_n() == 0 && gated_streams(m->T, m->J, p->K, F, p->view(), num_sms)) return kGatedStream;
+  const int path = g_path.load(std::memory_order_relaxed);
+  if (path == 0 && gemm_tile_n() == 0 && gated_streams(m->T, m->J, p->K, p->D / 2, p->view(), num_sms)) return kGatedStream;
   if (path == 1 || gemm_tile_n() < 0 || pair_gemm_max_pairs() < 1 || units_may_overflow(p, m)) return kGatedApart;
-  const bool little = F <= kApartWidth && static_cast<int64_t>(m->T) * F <= kApartOutputs;
-  return gemm_tile_n() == 0 && little && takes_small_path(p, m, num_sms) ? kGatedApart : kGatedFused;
+  return gated_small(p, m, num_sms) ? kGatedApart : kGatedFused;
 }
 
 size_t mlora_gated_workspace_bytes(mlora_pool_t p, mlora_meta_t m) {
@@ -1044,7 +1056,7 @@ mlora_status mlora_gated_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16
   if (form == kGatedApart) {
     if (!workspace || !aligned16(workspace)) return fail(MLORA_ERR_INVALID_ARG, "workspace is NULL or misaligned");
     float* y = static_cast<float*>(workspace);
-    if (mlora_status st = mlora_linear(p, m, x, W, y, stream)) return st;
+    if (mlora_status st = run_linear(p, m, x, W, y, s, ds, gated_small(p, m, ds->num_sms) || takes_small_path(p, m, ds->num_sms))) return st;
     if ((e = launch_gated_activation(y, h, m->T, p->D / 2, act, ds->num_sms, s)) != cudaSuccess) return cuda_fail(e, "activation launch");
     return MLORA_OK;
   }

@@ -329,7 +329,7 @@ def test_refusals(layer):
     refused(bad, over.handle, meta.handle, x, W, 0, h, None)
 
 
-FEW = [(T, J) for T in (1, 2, 8, 9, 16, 17, 31, 32) for J in (1, 3)] + [(5, 8), (32, 8)]
+FEW = [(T, J) for T in (1, 2, 8, 9, 16, 17, 31, 32, 33, 64) for J in (1, 3)] + [(5, 8), (32, 8)]
 
 
 @pytest.mark.parametrize("T,J", FEW)
