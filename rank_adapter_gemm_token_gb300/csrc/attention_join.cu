@@ -5,7 +5,8 @@
 // plan lists the split items; a unit of work is 8 rows of one, so that a few items with many parts (a chunk on a long
 // context) still spread over the SMs. (The row kernel's items are joined by its own last CTAs.) Launched as a programmatic
 // dependent: it reads its first task while the attention still runs. Bound by the latency of the parts' reads (from L2):
-// eight parts are asked for at once. 3 to 4 us alone and cold with little to join, most of it beside the attention's end.
+// eight parts are asked for at once. The prefix pass's parts (kSeePrefix) are joined to a row's sums over the prefix, in fp32; behind
+// such a pass (kSeeRanges) those join the parts as one more. 3 to 4 us alone and cold with little to join, most of it beside the attention's end.
 #include <type_traits>
 
 #include "attention.h"

@@ -26,9 +26,15 @@
 //     are whole numbers, so every rescaling is exact. Query rows are lifted by a power of two into f16's range.
 // Keys at or past a row's limit are replaced by -inf by selection, and rows past the cached length are
 // zero-filled on load, so what lies there (NaN included) has no effect.
+// RANGES (kSeeRanges): with a window, the chunks of 16 keys between the first ones and the window are not counted as units at all
+// (Place::key), keys that no row of an item sees are zero-filled on load like those past the length, and the others' masks have a
+// lower edge; behind a shared prefix the chunks begin at its end, and the rows' sums over it join the item's at its end. Compiled
+// apart, so that plain causal steps do not carry it (193 registers for 180).
 // Measured on the GPU, 32 heads of 128 on 8, all bytes over the time: 256 sequences of 200-2000 tokens bf16 168 us, 6.6 TB/s;
 // e4m3 105 us, 5.8 TB/s; one of 131000 tokens 84 us, 6.4 TB/s (copy: 6.8), e4m3 51 us, 5.4; one of 500 tokens 7.5 us. 9 to 16 rows
-// (64 sequences of 3 tokens on 1000): 54 us, 4.9 TB/s; e4m3 46 us, 3.0.
+// (64 sequences of 3 tokens on 1000): 54 us, 4.9 TB/s; e4m3 46 us, 3.0. A window of 1024 and 4 first keys, 256 sequences of
+// 200-30000: 162 us, 6.6 TB/s; 64 of 2000-120000 in 4001 and 70, e4m3: 100 us, 5.4. Short items lose more: 256 sequences of 10-500
+// keys behind a prefix 60 us, 4.7 TB/s; 200 of 10-800, e4m3, 51 us, 3.4 (loads alone, in a copy, 38; the epilogue is 1.5 of it).
 #include <algorithm>
 
 #include "attention.h"
