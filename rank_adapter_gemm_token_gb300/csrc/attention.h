@@ -123,10 +123,6 @@ constexpr int kTileSnap = 2;          // key tiles that a split costs at least (
 constexpr int kTileDeal = 12;         // key tiles above the mean up to which whole items are dealt out (6: 6 chunks of 300 on 4000 137 us for 108)
 constexpr int kTileHead = 3;          // key tiles that an item's fixed costs (queries, first products, output) are worth
 
-// Bytes that a step's groups must be able to save for a prefix pass: what the sequences read again comes from L2 where the
-// prefix fits there, and two launches cost 10 us. (Tokens behind a prefix of 4100, 8 heads of 128, with the pass and without: 8 of
-// them, bf16, 120 MB, 20.6 and 17.6 us; 16, 250 MB, 20.5 and 26.3; e4m3 16, 126 MB, 27.9 and 25.7; 64, 530 MB, 34.5 and 77.6.)
-constexpr int64_t kShareBytes = 144 << 20;
 // Sequences of a group from which on its prefix is attended once for all: for a few rows the tile kernel takes 1.5 us an SM for 128
 // keys, 2.8 over e4m3, where the row kernel takes 1.45 and 0.8 us for each sequence.
 __host__ __device__ constexpr int share_seqs(bool e4m3) { return e4m3 ? 4 : 2; }

@@ -440,6 +440,29 @@ mlora_status mlora_build_seq_window(mlora_seq_t q, const int32_t* q_start, const
   return build_seq(q, q_start, kv_len, pages, pages_ld, n_seqs, T, max_new, window, sinks, nullptr, nullptr, 0, kv, stream);
 }
 
+// Whether a pass over prefixes of up to max_prefix keys may save more than it costs: two launches, and the rows' fp32 sums written
+// and read again. What it saves: where single tokens and other few rows take the row kernel, the reads of all sequences of a group
+// but one, mostly from L2; where the rows take the tile kernel, blocks of key tiles, as far as the sequences' own blocks are not
+// full. (Graph times without and with a pass. One token each behind 4100, 8 heads of 128: 8 of them, bf16, 17.6 and 20.6 us; 16, 26.3
+// and 20.5; e4m3 16, 25.7 and 27.9; 64, 77.6 and 34.5. 16 chunks behind 9000, 32 heads on 8: of 8 tokens 108 and 38 us, of 48 126 and
+// 112, of 64, a full block each, 135 and 139, of 96 222 and 194, of 128 229 and 240; e4m3 170 and 53, 196 and 172, 210 and 219, ...)
+static bool sharing_pays(const SeqView& v, const KvView& w, int num_sms, int n_seqs, int T, int max_new, int n_groups, int max_prefix) {
+  constexpr double kL2 = 13e6, kSums = 5e6;                       // bytes a us
+  double cost = 10.0;                                             // us; with few items, whose keys are split finely, more:
+  const bool e4m3 = w.type == kKvE4m3;
+  const double keys = static_cast<double>(std::min(static_cast<int64_t>(max_prefix), static_cast<int64_t>(v.max_pages) * w.page));
+  double saved = 0.0;
+  if (static_cast<int64_t>(max_new) * v.G <= 16) {
+    saved = std::max(n_seqs - n_groups, 0) * keys * w.Hkv * 2 * w.hd * (e4m3 ? 1 : 2) / kL2;
+  } else if (n_seqs > 0) {
+    const double per = 2 * v.tile_tokens, mean = static_cast<double>(T) / n_seqs;
+    const double apart = n_seqs * std::ceil(mean / per), together = T / per + n_groups;
+    cost = 20.0;                                                  // (e4m3, 16 heads on 1, 2 tokens behind 9000: 33 us, 48 with a pass)
+    saved = std::max(apart - together, 0.0) * w.Hkv * keys / kTileKeys * (e4m3 ? 2.8 : 1.45) / num_sms;      // us of a key tile on an SM
+  }
+  return T > 0 && saved > cost + static_cast<double>(T) * v.Hq * (w.hd + 2) * 8 / kSums;
+}
+
 mlora_status mlora_build_seq_groups(mlora_seq_t q, const int32_t* q_start, const int32_t* kv_len, const int32_t* pages,
                                     int pages_ld, int n_seqs, int T, int max_new, const int32_t* group_start,
                                     const int32_t* prefix_len, int n_groups, int max_prefix, mlora_kv_t kv, void* stream) {
@@ -448,11 +471,7 @@ mlora_status mlora_build_seq_groups(mlora_seq_t q, const int32_t* q_start, const
   if (n_groups > q->max_groups)
     return fail(MLORA_ERR_TOO_MANY_TOKENS, "%d groups exceed the object's %d", n_groups, q->max_groups);
   if (n_groups > 0 && (!group_start || !prefix_len)) return fail(MLORA_ERR_INVALID_ARG, "group_start or prefix_len is NULL");
-  // The pass over the prefixes costs two launches; where the groups cannot save the reads that those take, there is none.
-  const KvView& w = kv->view;
-  const int64_t keys = std::min(static_cast<int64_t>(max_prefix), static_cast<int64_t>(q->view.max_pages) * w.page);
-  const int64_t saved = std::max(n_seqs - n_groups, 0) * keys * w.Hkv * 2 * w.hd * (w.type == kKvBf16 ? 2 : 1);
-  if (saved < kShareBytes || T == 0) n_groups = 0;
+  if (n_groups > 0 && !sharing_pays(q->view, kv->view, q->num_sms, n_seqs, T, max_new, n_groups, max_prefix)) n_groups = 0;
   return build_seq(q, q_start, kv_len, pages, pages_ld, n_seqs, T, max_new, 0, 0, group_start, prefix_len, n_groups, kv, stream);
 }
 

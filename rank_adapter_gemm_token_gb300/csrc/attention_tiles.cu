@@ -41,8 +41,8 @@
 // rescaled for nearly every row (a prompt of 8000 in a window of 1024 with 4 first keys 161 us, 136 so, 132 without the 4).
 // kSeePrefix: rows of all a group's tokens see all keys; maximum, sum and O go to their block's place in fp32. kSeeRanges behind it
 // adds those to each row's at the end. Measured: the prompt above 137 us, 920 TFLOP/s of visible pairs (e4m3 242); the window's own
-// edges make a tile of 9 partial at either end; the prefix pass of 256 tokens on 4096 shared keys 23 us, 750; 2756 tokens on 8960
-// 265 us, 1530. A window longer than all keys: 8000 tokens 369 us (kSeeAll 347), e4m3 678 (600).
+// edges make a tile of 9 partial at either end; the prefix pass of 256 tokens on 4096 shared keys 23 us, 750; 3001 tokens on 8960
+// 265 us, 1660. A window longer than all keys: 8000 tokens 369 us (kSeeAll 347), e4m3 678 (600).
 // Value rows past the cached length are zeroed in shared memory, scores past a row's limit are replaced by -inf:
 // what lies there has no effect. Every wait is bounded: after 2 s a role records the timeout, brings no more
 // copies and products (its copies are 2 s old by then, its products are waited for), stops waiting and runs on to the end.

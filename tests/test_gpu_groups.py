@@ -75,6 +75,7 @@ CASES = [
     ([40, 1, 70, 33], [512, 512, 530, 512], 8, 2, 128, 16, [(0, 4, 512)]),              # chunks and a token
     ([200, 300, 64], [384, 400, 390], 28, 4, 128, 128, [(0, 3, 384)]),
     ([130] * 3, [256] * 3, 24, 1, 64, 32, [(0, 3, 256)]),
+    ([12] * 5, [256] * 5, 24, 1, 64, 32, [(0, 5, 256)]),
     ([1] * 130, [140 + i % 7 for i in range(130)], 8, 2, 128, 16, [(0, 2, 128), (2, 100, 140), (100, 101, 130), (101, 130, 139)]),
     ([1] * 3, [5000, 5100, 4999], 8, 2, 128, 64, [(0, 3, 4992)]),                       # the prefix's keys are split among CTAs
     ([3] * 5, [2000] * 5, 12, 12, 64, 16, [(0, 5, 1990)]),
