@@ -31,9 +31,9 @@
 // lower edge; behind a shared prefix the chunks begin at its end, and the rows' sums over it join the item's at its end. Compiled
 // apart, so that plain causal steps do not carry it (193 registers for 180).
 // Measured on the GPU, 32 heads of 128 on 8, all bytes over the time: 256 sequences of 200-2000 tokens bf16 168 us, 6.6 TB/s;
-// e4m3 105 us, 5.8 TB/s; one of 131000 tokens 84 us, 6.4 TB/s (copy: 6.8), e4m3 51 us, 5.4; one of 500 tokens 7.5 us. 9 to 16 rows
+// e4m3 101 us, 6.1 TB/s; one of 131000 tokens 84 us, 6.4 TB/s (copy: 6.8), e4m3 51 us, 5.4; one of 500 tokens 7.5 us. 9 to 16 rows
 // (64 sequences of 3 tokens on 1000): 54 us, 4.9 TB/s; e4m3 46 us, 3.0. A window of 1024 and 4 first keys, 256 sequences of
-// 200-30000: 162 us, 6.6 TB/s; 64 of 2000-120000 in 4001 and 70, e4m3: 100 us, 5.4. Short items lose more: 256 sequences of 10-500
+// 200-30000: 162 us, 6.6 TB/s; 64 of 2000-120000 in 4001 and 70, e4m3: 98 us, 5.6. Short items lose more: 256 sequences of 10-500
 // keys behind a prefix 60 us, 4.7 TB/s; 200 of 10-800, e4m3, 51 us, 3.4 (loads alone, in a copy, 38; the epilogue is 1.5 of it).
 #include <algorithm>
 
@@ -185,12 +185,19 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
   const uint32_t ring = ptx::smem_u32(smem) + warp * (C::kStages * C::kStage);
   Place<RANGES> src{share.x, share.y, share.z, 0, {}, nullptr, 0};
   int issued = 0;
-  int page_a = 0, page_b = 0;                 // pages of the next chunk's first and second 8 keys
+  // The pages of the next chunk's first and second 8 keys, as places in the sequence's table, and 32 entries of the table around
+  // them, one to a lane (both places are among them: the first is even where they differ): the other chunks and heads that lie on
+  // them need no load of their own (e4m3, 256 sequences of 200-2000: 104.5 us with a load for each chunk, 100.5 so; bf16 the same).
+  int place_a = 0, place_b = 0, held = 0, held_from = -1, held_seq = -1;
   auto look = [&]() {
     const int k0 = src.key(v, src.u, warp);
-    page_a = src.table[min(k0, src.s.len - 1) >> kv.page_log2];
-    page_b = kv.page_log2 < 4 ? src.table[min(k0 + 8, src.s.len - 1) >> kv.page_log2] : page_a;
-    if (RANGES) page_a = max(page_a, 0), page_b = max(page_b, 0);        // (a page that no row sees: nothing is read there)
+    place_a = min(k0, src.s.len - 1) >> kv.page_log2;
+    place_b = kv.page_log2 < 4 ? min(k0 + 8, src.s.len - 1) >> kv.page_log2 : place_a;
+    const int from = place_a & ~31;
+    if (from != held_from || src.s.seq != held_seq) {
+      held = src.table[min(from + lane, v.max_pages - 1)];
+      held_from = from, held_seq = src.s.seq;
+    }
   };
   if (n_chunks > 0) {
     src.load(v);
@@ -200,6 +207,8 @@ attention_rows_kernel(const uint16_t* __restrict__ q, uint16_t* __restrict__ o, 
     if (issued < n_chunks) {
       const int k0 = src.key(v, src.u, warp);
       if (!src.unseen(v, k0)) {
+        int page_a = __shfl_sync(0xffffffffu, held, place_a & 31), page_b = __shfl_sync(0xffffffffu, held, place_b & 31);
+        if (RANGES) page_a = max(page_a, 0), page_b = max(page_b, 0);    // (a page that no row sees: nothing is read there)
         const uint32_t st = ring + (issued % C::kStages) * C::kStage;
         constexpr int kStep = 32 / C::kSegs;  // rows of one copy of all lanes
         constexpr int kHalf = kChunk / 2 / kStep;                                // copies of eight rows
