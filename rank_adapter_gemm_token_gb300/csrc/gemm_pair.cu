@@ -110,7 +110,7 @@ struct PairSide {
   const int32_t* grp_cnt;
   const int32_t* n_groups;     // number of groups (device)
   const int32_t* ptile_order;  // pair tiles by entry count, most first
-  uint32_t* sync;              // [0] ticket, [1] pairs done, [2 + mp] shrink sub-tiles written (x kEpiWarps)
+  uint32_t* sync;              // [0] ticket, [1] CTAs past their last wait, [2 + mp] shrink sub-tiles written (x kEpiWarps)
   uint16_t* vtile;             // [units][128][64] bf16 scaled v
   const int32_t* pair_slot;    // [T * J] validated slot per pair
   const float* pair_scale;     // [T * J]
@@ -153,10 +153,10 @@ __device__ __forceinline__ PairTile pair_tile(int t, int S, int per, int num_mp,
   }
   const int b = t - S;
   if (sp.fused && sp.heavy_first) {
-    pt.mp = sp.ptile_order[b / num_n];
+    pt.mp = num_mp > 1 ? sp.ptile_order[b / num_n] : 0;
     pt.n_idx = b % num_n;
   } else if (sp.fused) {
-    pt.mp = sp.ptile_order[b % num_mp];
+    pt.mp = num_mp > 1 ? sp.ptile_order[b % num_mp] : 0;
     pt.n_idx = b / num_mp;
   } else {
     pt.mp = pair_row(b, num_mp);
@@ -228,6 +228,9 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
   // here on its results (x, the metadata) are read. The next kernel may start its own set-up.
   ptx::grid_dependency_wait();
   ptx::grid_dependents_launch();
+  // rank 0's producer draws its first ticket before anything waits for the number of sub-tiles
+  uint32_t ticket = 0;
+  if (sp.fused && warp == 0 && lane == 0 && rank == 0) ticket = atomicAdd(&sp.sync[0], 1u);
   const int S = sp.fused ? *sp.n_groups * (kGroupUnits / kPer) : 0;
   const int total = S + num_mp * num_n;
 
@@ -247,6 +250,19 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
     return t;
   };
 
+  // Counts this CTA off the launch's counters; the last to be so has them zero for the next launch on this metadata. Nothing adds
+  // to them any more by then: every sub-tile was written before the tiles of y that waited for it.
+  auto done_with_counters = [&]() {
+    if (atomicAdd(&sp.sync[1], 1u) == 2u * static_cast<uint32_t>(n_pairs) - 1u) {
+      sp.sync[0] = 0u;
+      sp.sync[1] = 0u;
+      for (int q = 0; q < num_mp; ++q) sp.sync[2 + q] = 0u;
+      __threadfence();
+    }
+    return true;
+  };
+  bool counted = false;
+
   if (warp == 0) {
     if (lane == 0) {
       const int32_t* own_unit = rank == 0 ? sp.pent_u0 : sp.pent_u1;
@@ -264,7 +280,7 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
           if (!ok) {
             t = -1;
           } else if (sp.fused) {
-            const int tk = static_cast<int>(atomicAdd(&sp.sync[0], 1u));
+            const int tk = static_cast<int>(i == 0 ? ticket : atomicAdd(&sp.sync[0], 1u));
             t = tk < total ? tk : -1;
           } else {
             const long tk = pair + static_cast<long>(i) * n_pairs;
@@ -338,6 +354,8 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
+      // all of this CTA's waits on the launch's counters are behind it
+      if (sp.fused && ok) counted = done_with_counters();
       // tail: every stage released, i.e. every commit addressed to this CTA's stage barriers has
       // landed before the CTA may exit
       for (int i = 0; i < STAGES && ok; ++i) {
@@ -573,17 +591,7 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem_base, L::kTmemCols);
   }
-  if (sp.fused && rank == 0 && threadIdx.x == 0) {
-    // the last pair to finish resets the launch's counters for the next launch on this metadata
-    __threadfence();
-    const uint32_t done = atomicAdd(&sp.sync[1], 1u);
-    if (done == static_cast<uint32_t>(n_pairs) - 1u) {
-      sp.sync[0] = 0u;
-      sp.sync[1] = 0u;
-      for (int q = 0; q < num_mp; ++q) sp.sync[2 + q] = 0u;
-      __threadfence();
-    }
-  }
+  if (sp.fused && threadIdx.x == 0 && !counted) done_with_counters();   // after a wait that ran out
 }
 
 // The N tiles the pair kernel is built for, each with the deepest ring that fits.
