@@ -420,22 +420,18 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
       if (t < 0) break;
       const PairTile pt = pair_tile(t, S, kPer, num_mp, num_n, sp);
       if (pt.kind == 2) continue;
-      const int acc = local & 1;
-      const uint32_t acc_phase = static_cast<uint32_t>(local >> 1) & 1u;
-      if (!ptx::mbar_wait_short(&acc_full[acc], acc_phase, err)) break;
-      ptx::tc_fence_after();
-      const uint32_t lane_tmem = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                 static_cast<uint32_t>(acc * L::kAccStride);
       const int m0 = (2 * pt.mp + static_cast<int>(rank)) * kHalf;
+      const int tok = m0 + row_in_half;
+      const bool row_ok = tok < T;
+      int* tab_own = reinterpret_cast<int*>(stage_box);
+      float* tab_fac = reinterpret_cast<float*>(stage_box + 4 * kGroupUnits * kBlockCols);
+      int sl[kMaxJ];
+      float sc[kMaxJ];
       if (pt.kind == 1) {
-        const int tok = m0 + row_in_half;
-        const bool row_ok = tok < T;
-        // per column of the sub-tile's entries: the owning slot and its factor (0 past the rank or
-        // in a gap), in this warp's staging area once its earlier stores have read it
+        // While the sub-tile is still being computed: per column of its entries the owning slot and its factor (0 past the rank or
+        // in a gap), in this warp's staging area once its earlier stores have read it, and the token's slots.
         if (y_tma && lane == 0) ptx::bulk_wait_group_read<0>();
         __syncwarp();
-        int* tab_own = reinterpret_cast<int*>(stage_box);
-        float* tab_fac = reinterpret_cast<float*>(stage_box + 4 * kGroupUnits * kBlockCols);
         for (int c = lane; c < pt.cnt * kBlockCols; c += 32) {
           const int col = sp.pent_blk[pt.e0 + c / kBlockCols] * kBlockCols + c % kBlockCols;
           const int owner = col < sp.C ? sp.col_slot[col] : -1;
@@ -445,14 +441,20 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
           tab_fac[c] = f;
         }
         __syncwarp();
-        int sl[kMaxJ];
-        float sc[kMaxJ];
 #pragma unroll
         for (int j = 0; j < kMaxJ; ++j) {
           const bool in = row_ok && j < sp.J;
           sl[j] = in ? sp.pair_slot[static_cast<size_t>(tok) * sp.J + j] : -1;
           sc[j] = in ? sp.pair_scale[static_cast<size_t>(tok) * sp.J + j] : 0.f;
         }
+      }
+      const int acc = local & 1;
+      const uint32_t acc_phase = static_cast<uint32_t>(local >> 1) & 1u;
+      if (!ptx::mbar_wait_short(&acc_full[acc], acc_phase, err)) break;
+      ptx::tc_fence_after();
+      const uint32_t lane_tmem = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                 static_cast<uint32_t>(acc * L::kAccStride);
+      if (pt.kind == 1) {
         const int32_t* own_unit = rank == 0 ? sp.pent_u0 : sp.pent_u1;
         const bool one_slot = sp.J == 1;
         for (int e = 0; e < pt.cnt; ++e) {
