@@ -305,6 +305,9 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
           // rows (64-row boxes; entries past the sub-tile read zeros)
           const int boxes = pt.cnt <= 2 ? 1 : 2;
           const uint32_t sbytes = static_cast<uint32_t>(kPairABytes + boxes * kABoxBytes);
+          const int ent = static_cast<int>(rank) * boxes;
+          const int row0 = (ent < pt.cnt ? sp.pent_blk[pt.e0 + ent] : blk_out) * kBlockCols;
+          const int row1 = (boxes == 2 && ent + 1 < pt.cnt ? sp.pent_blk[pt.e0 + ent + 1] : blk_out) * kBlockCols;
           for (int kb = 0; kb < num_kb; ++kb) {
             if (!ptx::mbar_wait_short(&empty[stage], phase ^ 1u, err)) { ok = false; break; }
             uint8_t* sa = smem + stage * L::kStageBytes;
@@ -312,11 +315,8 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
             const uint32_t bar = ptx::mapa_shared(ptx::smem_u32(&full[stage]), 0);
             if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * sbytes);
             ptx::tma_load_2d_pair(sa, &tmap_x, bar, kb * kPK, m_blk * kHalf);
-            for (int b = 0; b < boxes; ++b) {
-              const int ent = static_cast<int>(rank) * boxes + b;
-              const int blk = ent < pt.cnt ? sp.pent_blk[pt.e0 + ent] : blk_out;
-              ptx::tma_load_2d_pair(sb + b * kABoxBytes, &tmap_a, bar, kb * kPK, blk * kBlockCols);
-            }
+            ptx::tma_load_2d_pair(sb, &tmap_a, bar, kb * kPK, row0);
+            if (boxes == 2) ptx::tma_load_2d_pair(sb + kABoxBytes, &tmap_a, bar, kb * kPK, row1);
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           }
           continue;
@@ -355,17 +355,18 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
         }
         // then one K block per entry of the pair tile: this M-tile's v tile (or zeros) and the
         // block's 64 columns of B
-        const int e0 = sp.ptile_off[pt.mp];
-        for (int e = e0; e < e0 + n_extra; ++e) {
+        const int e_end = sp.ptile_off[pt.mp] + n_extra;
+        int e = e_end - n_extra, own = own_unit[e], blk = sp.pent_blk[e];
+        while (e < e_end) {
           if (!ptx::mbar_wait_short(&empty[stage], phase ^ 1u, err)) { ok = false; break; }
           uint8_t* sa = smem + stage * L::kStageBytes;
           uint8_t* sb = sa + kPairABytes;
           const uint32_t bar = ptx::mapa_shared(ptx::smem_u32(&full[stage]), 0);
           if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * L::kStageBytes);
-          const int own = own_unit[e];
           const int vrow = own >= 0 ? own * kHalf : sp.v_rows;   // v_rows: past the end, zeros
           ptx::tma_load_2d_pair(sa, &tmap_v, bar, 0, vrow);
-          ptx::tma_load_2d_pair(sb, &tmap_b, bar, sp.pent_blk[e] * kBlockCols, n0);
+          ptx::tma_load_2d_pair(sb, &tmap_b, bar, blk * kBlockCols, n0);
+          if (++e < e_end) own = own_unit[e], blk = sp.pent_blk[e];   // while the next stage is waited for
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
