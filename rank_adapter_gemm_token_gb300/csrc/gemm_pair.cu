@@ -786,8 +786,10 @@ cudaError_t launch_pair_gemm(const uint16_t* x, const uint16_t* W, float* y, int
 }
 
 // Tiles of 256 rows x bn / 2 columns of h; the widths that whole boxes of 32 columns fill. By the estimates above, over tiles of
-// bn rows of W; of at most 256 tokens, which are bound by the bytes that an SM takes in, by those: whole waves times 128 rows of x
-// and bn / 2 of W (256 tokens, 4096 -> 2 x 14336, no adapters: widths 256, 192, 128 take 61, 56, 62 us).
+// bn rows of W; of at most 256 tokens, which are bound by the bytes that an SM takes in, by those: whole waves of tiles and shrink
+// sub-tiles times 128 rows of x and bn / 2 of W (GB300, cold, 256 tokens: 4096 -> 2 x 14336, no adapters, widths 256, 192, 128 take
+// 61, 60, 65 us, with 20 adapters of rank 16 75, 78, 79; 4096 -> 2 x 4096 with 100, where 64 tiles of 128 and 13 sub-tiles are one
+// more than there are pairs, 192 and 128 take 45 and 63).
 cudaError_t launch_pair_gemm_gated(const uint16_t* x, const uint16_t* W, uint16_t* h, int T, int K, int D, int act, uint32_t* err,
                                    const PoolView* pool, const MetaView* meta, int bn, cudaStream_t s) {
   const bool fuse = pair_gemm_fuses_shrink(K);
@@ -795,8 +797,10 @@ cudaError_t launch_pair_gemm_gated(const uint16_t* x, const uint16_t* W, uint16_
   if (max_pairs < 1) return cudaErrorNotSupported;
   if (bn != 256 && bn != 192 && bn != 128) {
     double best = 0.0;
+    const int entries = fuse ? std::min((pool->C + kBlockCols - 1) / kBlockCols, T * meta->J) : 0;
     for (int n : {256, 192, 128}) {
-      const int tiles = (D / 2 + n / 2 - 1) / (n / 2);
+      const int per = n / 2 >= 2 * kBlockCols ? 4 : 2;
+      const int tiles = (D / 2 + n / 2 - 1) / (n / 2) + (entries + per - 1) / per;
       const double time = T <= kPairM ? static_cast<double>((tiles + max_pairs - 1) / max_pairs) * (kHalf + n / 2)
                           : fuse      ? pair_time_dynamic(T, D, n, max_pairs)
                                       : pair_time(T, D, n, max_pairs);

@@ -1013,14 +1013,14 @@ mlora_status mlora_linear(mlora_pool_t p, mlora_meta_t m, const mlora_bf16* x, c
 // GEMM's epilogue; or mlora_linear, into the workspace, and the activation after it: where the output is not complete in that
 // epilogue (pairs that the CUDA-core kernels add), where the controls ask for another GEMM, and for small batches with an output
 // so small that the split-K kernel's shorter K loop counts for more than the second pass (GB300, cold, 8 and 100 adapters of rank 16, us
-// unfused and fused: 40 tokens 1024 -> 2 x 512 16 and 24, 15 and 30; 128 tokens 4096 -> 2 x 2048 26 and 37, 31 and 44, -> 2 x 5632 51 and
-// 49, 60 and 58; 256 tokens 1024 -> 2 x 2048 27 and 27, 30 and 33, -> 2 x 5632 43 and 31, 52 and 40).
+// unfused and fused: 64 tokens 1024 -> 2 x 1024 16 and 17, 16 and 22; 128 tokens 1024 -> 2 x 2048 23 and 19, 23 and 24, 4096 -> 2 x 2048
+// 26 and 30, 31 and 36, -> 2 x 4096 43 and 34, 57 and 41; 256 tokens 1024 -> 2 x 1024 22 and 19, 26 and 24, 4096 -> 2 x 1024 27 and 30,
+// 30 and 35, -> 2 x 2048 34 and 30, 36 and 37).
 enum { kGatedStream, kGatedFused, kGatedApart };
 static bool gated_small(mlora_pool_t p, mlora_meta_t m, int num_sms) {
-  constexpr int64_t kOutputs = 1 << 19;
-  constexpr int kWidth = 6144;
+  constexpr int kWidth = 2048;
   const int F = p->D / 2;
-  return g_path.load(std::memory_order_relaxed) == 0 && gemm_tile_n() == 0 && F <= kWidth && static_cast<int64_t>(m->T) * F <= kOutputs &&
+  return g_path.load(std::memory_order_relaxed) == 0 && gemm_tile_n() == 0 && F <= kWidth && static_cast<int64_t>(m->T) * F <= 64LL * p->K &&
          small_path_fits(p, m, num_sms) && active_blocks(p, m) + (p->D + 127) / 128 <= num_sms;
 }
 static int gated_form(mlora_pool_t p, mlora_meta_t m, int num_sms) {
