@@ -353,13 +353,18 @@ gated_stream_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__
       bar_sync(1 + warp / split, 32 * split);
     }
     if (part == 0) {
+      auto outputs = [&](int a) {                       // one activation's code
 #pragma unroll
-      for (int z = 0; z < NT; ++z)
+        for (int z = 0; z < NT; ++z)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int tok = 8 * z + 2 * t + i;
-          if (tok < T) reinterpret_cast<__nv_bfloat16*>(h)[static_cast<size_t>(tok) * F + out] = __float2bfloat16_rn(gate(acc[z][i], act) * acc[z][2 + i]);
-        }
+          for (int i = 0; i < 2; ++i) {
+            const int tok = 8 * z + 2 * t + i;
+            if (tok < T) reinterpret_cast<__nv_bfloat16*>(h)[static_cast<size_t>(tok) * F + out] = __float2bfloat16_rn(gate(acc[z][i], a) * acc[z][2 + i]);
+          }
+      };
+      if (act == MLORA_ACT_SILU) outputs(MLORA_ACT_SILU);
+      else if (act == MLORA_ACT_GELU_TANH) outputs(MLORA_ACT_GELU_TANH);
+      else outputs(MLORA_ACT_GELU);
     }
   }
   if (!ready) __syncthreads();
