@@ -89,7 +89,6 @@ __device__ __forceinline__ int pair_extra(const int32_t* ptile_off, int mp) {
   return ptile_off ? ptile_off[mp + 1] - ptile_off[mp] : 0;
 }
 
-constexpr int kTicketAhead = 4;         // K blocks before a tile's end at which the next ticket is drawn
 constexpr int kSchedDepth = 4;          // tile ids in flight from the scheduler to the other roles
 constexpr uint32_t kSchedUsers = 10;    // readers of a tile id: rank 0's MMA thread and 4 epilogue
                                         // warps, rank 1's producer and 4 epilogue warps
@@ -270,7 +269,7 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
       const int blk_out = (sp.C + kBlockCols - 1) / kBlockCols + 1;   // an A box past the end: zeros
       int stage = 0;
       uint32_t phase = 0;
-      bool ok = true, drawn = true;
+      bool ok = true;
       for (int i = 0; ok; ++i) {
         int t;
         if (rank == 0) {
@@ -281,9 +280,7 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
           if (!ok) {
             t = -1;
           } else if (sp.fused) {
-            if (!drawn) ticket = atomicAdd(&sp.sync[0], 1u);
-            drawn = false;
-            const int tk = static_cast<int>(ticket);
+            const int tk = static_cast<int>(i == 0 ? ticket : atomicAdd(&sp.sync[0], 1u));
             t = tk < total ? tk : -1;
           } else {
             const long tk = pair + static_cast<long>(i) * n_pairs;
@@ -324,27 +321,15 @@ gemm_bf16_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_c
         const int n0 = pt.n_idx * kOut + static_cast<int>(rank) * (GATED ? F : L::kBRows);
         const int n_extra = pair_extra(sp.ptile_off, pt.mp);
         // the tile's K blocks of x and W (kept free of other work: a branch in this loop slows it)
-        const int late = max(0, num_kb - kTicketAhead);
-        int kb = 0;
-#pragma unroll 1
-        for (int part = 0; part < 2 && ok; ++part) {
-          for (const int end = part ? num_kb : late; kb < end; ++kb) {
-            if (!ptx::mbar_wait_short(&empty[stage], phase ^ 1u, err)) { ok = false; break; }
-            uint8_t* sa = smem + stage * L::kStageBytes;
-            uint8_t* sb = sa + kPairABytes;
-            const uint32_t bar = ptx::mapa_shared(ptx::smem_u32(&full[stage]), 0);   // rank 0's barrier
-            if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * L::kStageBytes);
-            ptx::tma_load_2d_pair(sa, &tmap_x, bar, kb * kPK, m_blk * kHalf);
-            ptx::tma_load_2d_pair(sb, &tmap_w, bar, kb * kPK, n0);
-            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-          }
-          // The next ticket is on its way during the last blocks (GB300, cold, us before and after: 1000 tokens 4096 -> 2 x 4096, 30
-          // adapters 70.1 and 67.9; linear of 256 tokens 4096 -> 28672, 100 adapters 95.6 and 94.1). One held in hand is above
-          // that of the tile it waits in, so never a sub-tile that another waits for.
-          if (part == 0 && ok && sp.fused && rank == 0) {
-            ticket = atomicAdd(&sp.sync[0], 1u);
-            drawn = true;
-          }
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!ptx::mbar_wait_short(&empty[stage], phase ^ 1u, err)) { ok = false; break; }
+          uint8_t* sa = smem + stage * L::kStageBytes;
+          uint8_t* sb = sa + kPairABytes;
+          const uint32_t bar = ptx::mapa_shared(ptx::smem_u32(&full[stage]), 0);   // rank 0's barrier
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * L::kStageBytes);
+          ptx::tma_load_2d_pair(sa, &tmap_x, bar, kb * kPK, m_blk * kHalf);
+          ptx::tma_load_2d_pair(sb, &tmap_w, bar, kb * kPK, n0);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
         if (!ok || n_extra == 0) continue;
         if (sp.fused) {
