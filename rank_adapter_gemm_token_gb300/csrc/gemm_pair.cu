@@ -32,9 +32,10 @@
 // GATED (the gated linear): W's rows are the gate's and then the up projection's; rank 0 stages BN / 2 gate rows of a tile and rank 1
 // the same BN / 2 up rows, so that an accumulator's row holds both values of BN / 2 outputs of one token, and the epilogue's thread
 // applies the activation and the product (gated.cuh) and stages bf16: 2 bytes an output leave the SM in place of 8 that a second
-// kernel would read again. 4096 tokens, 4096 -> 2 x 14336, rank 64: 588 us after an L2 flush (fp32 output and a second kernel 740 in
-// calls one after another, 610 to 650 so), tensor pipe 84 % busy; 256 tokens of 100 adapters 98 us (DRAM 48 %, tensor pipe 46 %:
-// neither, but the ring's turn, 2.6 us of latency with six stages; more stages' worth asked into L2 ahead made it slower).
+// kernel would read again. 4096 tokens, 4096 -> 2 x 14336, rank 64: 567 us after an L2 flush (fp32 output and a second kernel 740 in
+// calls one after another, 607 to 628 so), tensor pipe 84 % busy; 256 tokens of 100 adapters 92 us, 61 without adapters: neither DRAM
+// nor the tensor pipe, but the ring's turn, 2.6 us of latency with six stages (more stages' worth asked into L2 ahead made it slower),
+// and 7 us in which every pair's first tile waits for the shrink's sub-tiles.
 // Tile order: M fastest (the pairs working on one W column block run together, so W comes from
 // HBM once), with the rows of each column rotated by the column index, so that a row with many
 // extra blocks (decode tokens with many slots) is spread over all pairs instead of falling to the

@@ -76,9 +76,9 @@ struct MetaView {
   int32_t* pent_u0;       // [U] unit of M-tile 2mp with that block (-1: none)
   int32_t* pent_u1;       // [U] unit of M-tile 2mp + 1 with that block (-1: none)
   int32_t* ptile_order;   // [pair tiles] pair tiles by entry count, most first (ties ascending)
-  uint32_t* sync;         // [2 + pair tiles] the pair GEMM's counters (and the few tokens' gated linear's: tickets, CTAs done, shares): [0] next tile ticket, [1] clusters
-                          //   done, [2 + mp] shrink sub-tiles of pair tile mp written (one per epilogue
-                          //   warp); zero between launches (the last cluster of a launch resets them)
+  uint32_t* sync;         // [2 + pair tiles] the pair GEMM's counters (and the few tokens' gated linear's: tickets, CTAs done, shares): [0] next tile ticket, [1] CTAs
+                          //   past their last wait, [2 + mp] shrink sub-tiles of pair tile mp written (one per epilogue
+                          //   warp); zero between launches (the last CTA of a launch to be so resets them)
   int32_t* pair_fused;    // [n] 1: the pair's side path runs on the tensor cores inside the GEMM
   int32_t* todo_blk;      // [n] ascending pair-block numbers holding a pair with pair_fused == 0
   uint16_t* vtile;        // [U][128][64] bf16: s c v of the unit's tokens on the block's columns
